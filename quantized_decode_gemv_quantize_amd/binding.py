@@ -1,4 +1,5 @@
-"""Python binding of ``libmmvq.so`` (C ABI in ``include/mmvq.h``).
+"""Python binding of ``libmmvq.so`` (C ABI in ``include/mmvq.h`` and, for the
+operators between the mat-vecs, ``include/mmvq_decode.h``).
 
 Argument marshalling only: every step of the computation runs in the HIP
 library. Functions keep the C names; device buffers may be given as torch
@@ -17,9 +18,12 @@ import re
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB = os.path.join(HERE, "libmmvq.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "mmvq.h")
+DECODE_HEADER = os.path.join(os.path.dirname(HERE), "include", "mmvq_decode.h")
 
 Q4_0, Q8_0, Q8_1, Q4_K, Q6_K = 2, 8, 9, 12, 14
 Q4_1, Q5_0, Q5_1, Q5_K = 3, 6, 7, 13
+F16 = 1
+TARGET_LOGITS, TARGET_WEIGHTS = 0, 1
 GLU_PLAIN, GLU_SWIGLU, GLU_GEGLU, GLU_SWIGLU_OAI, GLU_SWIGLU_CLAMP = 0, 1, 2, 3, 4
 MAX_COLS = 8
 BLOCK = {Q4_0: (32, 18), Q8_0: (32, 34), Q4_K: (256, 144), Q6_K: (256, 210), Q8_1: (32, 36)}
@@ -48,6 +52,35 @@ def epilogue(up_bias=None, gate_bias=None, up_scale=None, gate_scale=None, glu_o
 
 _EP = ctypes.POINTER(Epilogue)
 
+
+class KVCache(ctypes.Structure):
+    """``mmvq_kv_cache`` (made by ``kv_cache()``; holds addresses, not tensors)."""
+    _fields_ = [("k", _p), ("v", _p), ("type", _int), ("n_pages", _int), ("page_size", _int),
+                ("n_kv_heads", _int), ("head_dim", _int)]
+
+
+class KVBatch(ctypes.Structure):
+    """``mmvq_kv_batch`` (made by ``kv_batch()``; holds addresses, not tensors)."""
+    _fields_ = [("token_start", _p), ("seq_len", _p), ("page_table", _p), ("table_stride", _i64),
+                ("n_seqs", _int), ("n_tokens", _int), ("pages_per_seq", _int), ("max_new", _int),
+                ("max_len", _int)]
+
+
+def kv_cache(k, v, kv_type: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int) -> KVCache:
+    return KVCache(_addr(k), _addr(v), kv_type, n_pages, page_size, n_kv_heads, head_dim)
+
+
+def kv_batch(token_start, seq_len, page_table, n_seqs: int, n_tokens: int, max_new: int, max_len: int,
+             pages_per_seq: int, table_stride: int | None = None) -> KVBatch:
+    return KVBatch(_addr(token_start), _addr(seq_len), _addr(page_table),
+                   pages_per_seq if table_stride is None else table_stride, n_seqs, n_tokens, pages_per_seq,
+                   max_new, max_len)
+
+
+_KC, _KB = ctypes.POINTER(KVCache), ctypes.POINTER(KVBatch)
+_pi64 = ctypes.POINTER(_i64)
+_f32 = ctypes.c_float
+
 _SIGS = {
     "mmvq_type_info": (_int, [_int, ctypes.POINTER(_int), ctypes.POINTER(_int)]),
     "mmvq_many_columns_min": (_int, [_int, _int, _int, ctypes.POINTER(_int)]),
@@ -67,6 +100,16 @@ _SIGS = {
     "mmvq_block_dots": (_int, [_p, _int, _i64, _i64, _p, _i64, _p, _p]),
     "mmvq_read_probe": (_int, [_p, _i64, _p, _p]),
     "mmvq_strerror": (ctypes.c_char_p, [_int]),
+    "mmvq_add_rms_norm": (_int, [_p, _i64, _i64, _i64, _p, _i64, _p, _f32, _p, _i64, _p, _i64, _p, _p]),
+    "mmvq_dequantize_q8_1": (_int, [_p, _i64, _i64, _p, _i64, _p]),
+    "mmvq_kv_page_bytes": (_int, [_int, _int, _int, _int, _pi64]),
+    "mmvq_kv_write": (_int, [_KC, _KB, _p, _i64, _p, _i64, _p]),
+    "mmvq_kv_read": (_int, [_KC, _KB, _p, _i64, _p, _i64, _p]),
+    "mmvq_attn_workspace": (_int, [_KC, _KB, _int, _pi64]),
+    "mmvq_attn": (_int, [_KC, _KB, _p, _i64, _int, _f32, _int, _p, _p, _i64, _p, _i64, _p]),
+    "mmvq_verify_workspace": (_int, [_int, _int, _int, _pi64]),
+    "mmvq_verify_draft": (_int, [_p, _i64, _int, _int, _p, _p, _p, _i64, _p, _int, _int, _p, _p, _p, _p, _int,
+                                 _p, _i64, _p]),
 }
 
 _lib = None
@@ -220,6 +263,76 @@ def mmvq_id_ex(W_up, W_gate, expert_stride_bytes: int, n_experts: int, wtype: in
 def mmvq_block_dots(W, wtype: int, M: int, K: int, y_q, n: int, dots, stream=None) -> None:
     _check("mmvq_block_dots", lib().mmvq_block_dots(_addr(W), wtype, M, K, _addr(y_q), n,
                                                     _addr(dots), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Operators between the mat-vecs (include/mmvq_decode.h)
+# ---------------------------------------------------------------------------
+
+def _launch(fn: str, where, stream, *args) -> None:
+    """Calls ``fn`` on ``stream``; without one, on the current stream of the device of ``where``, which
+    need not be the current device."""
+    f = getattr(lib(), fn)
+    if stream is not None:
+        _check(fn, f(*args, _stream(stream)))
+        return
+    import torch
+    index = where.device.index if isinstance(where, torch.Tensor) and where.is_cuda else None
+    if index is None or index == torch.cuda.current_device():
+        _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+    else:
+        with torch.cuda.device(index):
+            _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+
+
+def mmvq_add_rms_norm(x, K: int, n: int, ldx: int, residual, ldr: int, weight, eps: float, sum_out, lds: int,
+                      y, ldy: int, y_q, stream=None) -> None:
+    _launch("mmvq_add_rms_norm", x, stream, _addr(x), K, n, ldx, _addr(residual), ldr, _addr(weight), eps,
+            _addr(sum_out), lds, _addr(y), ldy, _addr(y_q))
+
+
+def mmvq_dequantize_q8_1(y_q, K: int, n: int, x, ldx: int, stream=None) -> None:
+    _launch("mmvq_dequantize_q8_1", x, stream, _addr(y_q), K, n, _addr(x), ldx)
+
+
+def mmvq_kv_page_bytes(kv_type: int, page_size: int, n_kv_heads: int, head_dim: int) -> int:
+    n = _i64()
+    _check("mmvq_kv_page_bytes", lib().mmvq_kv_page_bytes(kv_type, page_size, n_kv_heads, head_dim, n))
+    return n.value
+
+
+def mmvq_kv_write(cache: KVCache, batch: KVBatch, k, ldk: int, v, ldv: int, stream=None) -> None:
+    _launch("mmvq_kv_write", k, stream, cache, batch, _addr(k), ldk, _addr(v), ldv)
+
+
+def mmvq_kv_read(cache: KVCache, batch: KVBatch, k, ldk: int, v, ldv: int, stream=None) -> None:
+    _launch("mmvq_kv_read", v if k is None else k, stream, cache, batch, _addr(k), ldk, _addr(v), ldv)
+
+
+def mmvq_attn_workspace(cache: KVCache, batch: KVBatch, n_heads: int) -> int:
+    n = _i64()
+    _check("mmvq_attn_workspace", lib().mmvq_attn_workspace(cache, batch, n_heads, n))
+    return n.value
+
+
+def mmvq_attn(cache: KVCache, batch: KVBatch, q, ldq: int, n_heads: int, scale: float, window: int, sinks, out,
+              ldo: int, workspace, workspace_bytes: int, stream=None) -> None:
+    _launch("mmvq_attn", q, stream, cache, batch, _addr(q), ldq, n_heads, scale, window, _addr(sinks),
+            _addr(out), ldo, _addr(workspace), workspace_bytes)
+
+
+def mmvq_verify_workspace(n_seqs: int, n_rows: int, vocab: int) -> int:
+    n = _i64()
+    _check("mmvq_verify_workspace", lib().mmvq_verify_workspace(n_seqs, n_rows, vocab, n))
+    return n.value
+
+
+def mmvq_verify_draft(target, ldt: int, vocab: int, kind: int, temperature, draft_tokens, draft_probs, ldd: int,
+                      row_start, n_seqs: int, n_rows: int, u_accept, u_sample, n_accepted, tokens, max_out: int,
+                      workspace, workspace_bytes: int, stream=None) -> None:
+    _launch("mmvq_verify_draft", target, stream, _addr(target), ldt, vocab, kind, _addr(temperature),
+            _addr(draft_tokens), _addr(draft_probs), ldd, _addr(row_start), n_seqs, n_rows, _addr(u_accept),
+            _addr(u_sample), _addr(n_accepted), _addr(tokens), max_out, _addr(workspace), workspace_bytes)
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,172 @@
+"""Operators between the mat-vecs, without a GPU: declared and exported, the
+host-only queries, and every refusal (arguments are checked before any device
+is touched)."""
+import ctypes
+
+import pytest
+
+from quantized_decode_gemv_quantize_amd import binding as B
+
+P, ODD = 1 << 20, (1 << 20) + 2     # never dereferenced
+
+
+@pytest.fixture(scope="module")
+def L():
+    return B.lib()
+
+
+def test_declared_symbols_are_exported_and_bound(L):
+    names = B.declared_symbols(B.DECODE_HEADER)
+    assert set(names) == {"mmvq_add_rms_norm", "mmvq_dequantize_q8_1", "mmvq_kv_page_bytes", "mmvq_kv_write",
+                          "mmvq_kv_read", "mmvq_attn_workspace", "mmvq_attn", "mmvq_verify_workspace",
+                          "mmvq_verify_draft"}
+    for n in names:
+        assert hasattr(L, n) and n in B._SIGS and hasattr(B, n), n
+
+
+@pytest.mark.parametrize("kind,bits", [(B.F16, 16), (B.Q8_0, 8.5), (B.Q4_0, 4.5)])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+def test_page_bytes(kind, bits, D):
+    assert B.mmvq_kv_page_bytes(kind, 16, 1, D) == 16 * D * bits / 8
+    assert B.mmvq_kv_page_bytes(kind, 1024, 1024, D) == 1024 * 1024 * D * bits / 8
+
+
+@pytest.mark.parametrize("args,code", [
+    ((B.Q4_K, 16, 1, 64), B.ERR_TYPE), ((0, 16, 1, 64), B.ERR_TYPE),
+    ((B.F16, 8, 1, 64), B.ERR_SHAPE), ((B.F16, 24, 1, 64), B.ERR_SHAPE), ((B.F16, 2048, 1, 64), B.ERR_SHAPE),
+    ((B.F16, 16, 0, 64), B.ERR_SHAPE), ((B.F16, 16, 1025, 64), B.ERR_SHAPE),
+    ((B.F16, 16, 1, 32), B.ERR_SHAPE), ((B.F16, 16, 1, 80), B.ERR_SHAPE), ((B.F16, 16, 1, 512), B.ERR_SHAPE),
+])
+def test_page_bytes_refusals(L, args, code):
+    with pytest.raises(B.MMVQError) as e:
+        B.mmvq_kv_page_bytes(*args)
+    assert e.value.code == code
+    assert L.mmvq_kv_page_bytes(B.F16, 16, 1, 64, None) == B.ERR_NULL
+
+
+def norm(L, x=P, K=64, n=2, ldx=64, res=P, ldr=64, w=P, s=P, lds=64, y=P, ldy=64, q=P):
+    return L.mmvq_add_rms_norm(x, K, n, ldx, res, ldr, w, 1e-5, s, lds, y, ldy, q, None)
+
+
+@pytest.mark.parametrize("kw,code", [
+    ({"x": None}, B.ERR_NULL), ({"y": None, "q": None}, B.ERR_NULL),
+    ({"K": 0}, B.ERR_SHAPE), ({"K": 48}, B.ERR_SHAPE), ({"K": (1 << 24) + 32, "ldx": 1 << 25}, B.ERR_SHAPE),
+    ({"n": -1}, B.ERR_SHAPE), ({"n": (1 << 34) + 1}, B.ERR_SHAPE),
+    ({"ldx": 63}, B.ERR_SHAPE), ({"ldr": 63}, B.ERR_SHAPE), ({"lds": 63}, B.ERR_SHAPE), ({"ldy": 63}, B.ERR_SHAPE),
+    ({"x": ODD}, B.ERR_ALIGN), ({"res": ODD}, B.ERR_ALIGN), ({"w": ODD}, B.ERR_ALIGN), ({"s": ODD}, B.ERR_ALIGN),
+    ({"y": ODD}, B.ERR_ALIGN), ({"q": P + 4}, B.ERR_ALIGN),
+    ({"n": 0}, 0), ({"n": 0, "res": None, "ldr": 0, "s": None, "lds": 0, "w": None, "y": None, "ldy": 0}, 0),
+])
+def test_norm_refusals(L, kw, code):
+    assert norm(L, **kw) == code
+
+
+@pytest.mark.parametrize("args,code", [
+    ((None, 64, 1, P, 64), B.ERR_NULL), ((P, 64, 1, None, 64), B.ERR_NULL), ((P, 48, 1, P, 64), B.ERR_SHAPE),
+    ((P, 64, 1, P, 63), B.ERR_SHAPE), ((P, 64, -1, P, 64), B.ERR_SHAPE), ((P + 4, 64, 1, P, 64), B.ERR_ALIGN),
+    ((P, 64, 1, ODD, 64), B.ERR_ALIGN), ((P, 64, 0, P, 64), 0),
+])
+def test_dequantize_refusals(L, args, code):
+    assert L.mmvq_dequantize_q8_1(*args, None) == code
+
+
+CACHE = dict(k=P, v=P, kv_type=B.Q8_0, n_pages=4, page_size=16, n_kv_heads=2, head_dim=64)
+BATCH = dict(token_start=P, seq_len=P, page_table=P, n_seqs=2, n_tokens=3, max_new=2, max_len=40, pages_per_seq=3)
+
+BAD_PAIR = [
+    ({"k": None}, {}, B.ERR_NULL), ({"v": None}, {}, B.ERR_NULL), ({"kv_type": B.Q6_K}, {}, B.ERR_TYPE),
+    ({"n_pages": 0}, {}, B.ERR_SHAPE), ({"page_size": 20}, {}, B.ERR_SHAPE), ({"head_dim": 48}, {}, B.ERR_SHAPE),
+    ({"k": P + 8}, {}, B.ERR_ALIGN), ({"v": P + 4}, {}, B.ERR_ALIGN),
+    ({}, {"token_start": None}, B.ERR_NULL), ({}, {"seq_len": None}, B.ERR_NULL), ({}, {"page_table": None}, B.ERR_NULL),
+    ({}, {"token_start": ODD}, B.ERR_ALIGN), ({}, {"seq_len": ODD}, B.ERR_ALIGN), ({}, {"page_table": ODD}, B.ERR_ALIGN),
+    ({}, {"n_seqs": -1}, B.ERR_SHAPE), ({}, {"n_seqs": (1 << 20) + 1}, B.ERR_SHAPE), ({}, {"n_tokens": -1}, B.ERR_SHAPE),
+    ({}, {"max_new": 0}, B.ERR_SHAPE), ({}, {"max_len": 0}, B.ERR_SHAPE), ({}, {"pages_per_seq": 0}, B.ERR_SHAPE),
+    ({}, {"table_stride": 2}, B.ERR_SHAPE), ({}, {"max_len": (1 << 30) + 1}, B.ERR_SHAPE),
+]
+
+
+def pair(c, b):
+    return B.kv_cache(**{**CACHE, **c}), B.kv_batch(**{**BATCH, **b})
+
+
+@pytest.mark.parametrize("c,b,code", BAD_PAIR)
+def test_cache_and_batch_refusals(L, c, b, code):
+    cache, batch = pair(c, b)
+    assert L.mmvq_kv_write(cache, batch, P, 128, P, 128, None) == code
+    assert L.mmvq_kv_read(cache, batch, P, 128, P, 128, None) == code
+    assert L.mmvq_attn(cache, batch, P, 256, 4, 0.125, 0, None, P, 256, P, 1 << 30, None) == code
+
+
+def test_cache_io_refusals(L):
+    cache, batch = pair({}, {})
+    assert L.mmvq_kv_write(None, batch, P, 128, P, 128, None) == B.ERR_NULL
+    assert L.mmvq_kv_write(cache, None, P, 128, P, 128, None) == B.ERR_NULL
+    assert L.mmvq_kv_write(cache, batch, None, 128, P, 128, None) == B.ERR_NULL
+    assert L.mmvq_kv_write(cache, batch, P, 128, None, 128, None) == B.ERR_NULL
+    assert L.mmvq_kv_read(cache, batch, None, 128, None, 128, None) == B.ERR_NULL
+    assert L.mmvq_kv_write(cache, batch, P, 127, P, 128, None) == B.ERR_SHAPE
+    assert L.mmvq_kv_read(cache, batch, P, 128, P, 127, None) == B.ERR_SHAPE
+    assert L.mmvq_kv_write(cache, batch, ODD, 128, P, 128, None) == B.ERR_ALIGN
+    assert L.mmvq_kv_read(cache, batch, P, 128, ODD, 128, None) == B.ERR_ALIGN
+    for empty in ({"n_seqs": 0}, {"n_tokens": 0}):
+        cache, batch = pair({}, empty)
+        assert L.mmvq_kv_write(cache, batch, P, 128, P, 128, None) == 0
+        assert L.mmvq_kv_read(cache, batch, P, 128, None, 0, None) == 0
+
+
+def test_attention_refusals(L):
+    cache, batch = pair({}, {})
+    ok = dict(q=P, ldq=256, heads=4, window=0, sinks=None, out=P, ldo=256, ws=P, size=1 << 30)
+
+    def attn(**kw):
+        a = {**ok, **kw}
+        return L.mmvq_attn(cache, batch, a["q"], a["ldq"], a["heads"], 0.1, a["window"], a["sinks"], a["out"], a["ldo"],
+                           a["ws"], a["size"], None)
+
+    for kw, code in [({"q": None}, B.ERR_NULL), ({"out": None}, B.ERR_NULL), ({"ldq": 255}, B.ERR_SHAPE),
+                     ({"ldo": 255}, B.ERR_SHAPE), ({"heads": 3}, B.ERR_SHAPE), ({"heads": 0}, B.ERR_SHAPE),
+                     ({"heads": 65536, "ldq": 1 << 30, "ldo": 1 << 30}, B.ERR_SHAPE), ({"window": -1}, B.ERR_SHAPE),
+                     ({"q": ODD}, B.ERR_ALIGN), ({"out": ODD}, B.ERR_ALIGN), ({"sinks": ODD}, B.ERR_ALIGN),
+                     ({"ws": P + 8}, B.ERR_ALIGN)]:
+        assert attn(**kw) == code, kw
+    # a long cache is cut into ranges, which need a workspace
+    cache, batch = pair({}, {"max_len": 4096})
+    need = B.mmvq_attn_workspace(cache, batch, 4)
+    assert need > 0
+    assert attn(ws=None, size=need) == B.ERR_NULL
+    assert attn(size=need - 1) == B.ERR_SHAPE
+    n = ctypes.c_int64()
+    assert L.mmvq_attn_workspace(cache, batch, 4, None) == B.ERR_NULL
+    assert L.mmvq_attn_workspace(cache, batch, 5, n) == B.ERR_SHAPE
+    assert L.mmvq_attn_workspace(None, batch, 4, n) == B.ERR_NULL
+    empty = B.kv_batch(**{**BATCH, "n_seqs": 0})
+    assert B.mmvq_attn_workspace(cache, empty, 4) == 0
+    assert L.mmvq_attn(cache, empty, P, 256, 4, 0.1, 0, None, P, 256, None, 0, None) == 0
+
+
+VERIFY = dict(target=P, ldt=100, vocab=100, kind=0, temp=None, tok=P, dp=P, ldd=100, start=P, n_seqs=2, n_rows=5, ua=P,
+              us=P, count=P, out=P, max_out=3, ws=P, size=1 << 20)
+
+
+@pytest.mark.parametrize("kw,code", [
+    *[({k: None}, B.ERR_NULL) for k in ("target", "tok", "start", "ua", "us", "count", "out", "ws")],
+    *[({k: ODD}, B.ERR_ALIGN) for k in ("target", "temp", "tok", "dp", "start", "ua", "us", "count", "out")],
+    ({"ws": P + 8}, B.ERR_ALIGN), ({"kind": 2}, B.ERR_TYPE), ({"kind": -1}, B.ERR_TYPE),
+    ({"vocab": 0}, B.ERR_SHAPE), ({"vocab": (1 << 24) + 1, "ldt": 1 << 25, "ldd": 1 << 25}, B.ERR_SHAPE),
+    ({"ldt": 99}, B.ERR_SHAPE), ({"ldd": 99}, B.ERR_SHAPE), ({"max_out": 0}, B.ERR_SHAPE), ({"n_seqs": -1}, B.ERR_SHAPE),
+    ({"n_rows": -1}, B.ERR_SHAPE), ({"n_rows": (1 << 20) + 1}, B.ERR_SHAPE), ({"size": 10}, B.ERR_SHAPE),
+    ({"n_seqs": 0}, 0), ({"n_seqs": 0, "dp": None, "ldd": 0}, 0),
+])
+def test_verify_refusals(L, kw, code):
+    a = {**VERIFY, **kw}
+    assert L.mmvq_verify_draft(*[a[k] for k in VERIFY], None) == code
+
+
+def test_verify_workspace(L):
+    assert B.mmvq_verify_workspace(0, 0, 10) >= 0
+    assert B.mmvq_verify_workspace(2, 5, 128256) < 1 << 20
+    assert L.mmvq_verify_workspace(1, 1, 1, None) == B.ERR_NULL
+    for bad in ((-1, 1, 1), (1, -1, 1), (1, 1, 0)):
+        with pytest.raises(B.MMVQError) as e:
+            B.mmvq_verify_workspace(*bad)
+        assert e.value.code == B.ERR_SHAPE
