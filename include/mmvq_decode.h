@@ -74,7 +74,8 @@ int mmvq_dequantize_q8_1(const void *y_q, int64_t K, int64_t n, float *x,
  *              roundf(x/d), 0 where d is 0; value fp16(d)*q) or MMVQ_Q4_0
  *              (d = m/-8 with m the value of largest magnitude, the first of
  *              equals; q = min(15, floor(x/d + 8.5)), 8 where d is 0; value
- *              fp16(d)*(q - 8)); the values to quantize must be finite;
+ *              fp16(d)*(q - 8)); a d beyond 65504 is stored as 65504; the
+ *              values to quantize must be finite;
  *   page_size  a power of two, 16..MMVQ_KV_MAX_PAGE;
  *   head_dim   64, 96, 128 or 256; n_kv_heads 1..1024.
  * Layout of a page: per head, page_size/16 units of 16 tokens, each in the
@@ -153,8 +154,8 @@ int mmvq_attn_workspace(const mmvq_kv_cache *cache, const mmvq_kv_batch *batch,
  * token that sees no key gets zeros. q and out: fp32, row t at + t*ld, head
  * h at h*head_dim; ld >= n_heads*head_dim, 4-byte aligned; q must be finite.
  * Keys and values enter at their stored precision; scores, softmax and sums
- * are fp32, with q carried as two fp16 parts and the probabilities as two
- * fp16 (F16 cache) or bf16 parts, 2^-16 or better of each.
+ * are fp32, with q carried as two fp16 parts (21 bits of the row's largest
+ * value) and each probability as two fp16 parts (20 bits).
  * workspace: 16-byte aligned, at least mmvq_attn_workspace bytes (fewer:
  * MMVQ_ERR_SHAPE). n_heads <= 65535 and n_tokens * n_heads <= 2^30; a launch
  * beyond 2^23 workgroups (sequences * key/value heads * tiles of 16 to 128

@@ -151,10 +151,17 @@ def _addr(x) -> int | None:
     return x.data_ptr()
 
 
+def _current_stream() -> int:
+    """Raw handle of torch's current stream on the current device."""
+    import torch
+    # without the Stream object that torch.cuda.current_stream() makes: 0.3 us against 2.9
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch.cuda.current_stream().cuda_stream if raw is None else raw(torch.cuda.current_device())
+
+
 def _stream(s) -> int | None:
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -277,12 +284,12 @@ def _launch(fn: str, where, stream, *args) -> None:
         _check(fn, f(*args, _stream(stream)))
         return
     import torch
-    index = where.device.index if isinstance(where, torch.Tensor) and where.is_cuda else None
-    if index is None or index == torch.cuda.current_device():
-        _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+    index = where.get_device() if isinstance(where, torch.Tensor) else -1
+    if index < 0 or index == torch.cuda.current_device():
+        _check(fn, f(*args, _current_stream()))
     else:
         with torch.cuda.device(index):
-            _check(fn, f(*args, torch.cuda.current_stream().cuda_stream))
+            _check(fn, f(*args, _current_stream()))
 
 
 def mmvq_add_rms_norm(x, K: int, n: int, ldx: int, residual, ldr: int, weight, eps: float, sum_out, lds: int,

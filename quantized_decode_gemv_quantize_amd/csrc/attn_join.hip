@@ -18,6 +18,7 @@ AttnShape attn_shape(int kind, int nb, int n_seqs, int n_kv_heads, int group, in
   AttnShape s;
   s.rows = rows > 64;
   s.mt = nb < 8 && rows > 16 ? 2 : 1;
+  if (nb == 2 && rows > 32 && rows <= 48) s.mt = 3;
   const int rt = 16 * s.mt * (s.rows ? 4 : 1);
   s.tiles = static_cast<int>((rows + rt - 1) / rt);
   const int64_t groups = static_cast<int64_t>(n_seqs) * n_kv_heads * s.tiles;
@@ -82,7 +83,7 @@ int launch_join_as(const AttnArgs& a, hipStream_t st) {
 }
 
 int launch_attn_join(const AttnArgs& a, bool f16, hipStream_t st) {
-  return f16 ? launch_join_as<static_cast<int>(kPShift)>(a, st) : launch_join_as<0>(a, st);
+  return f16 ? launch_join_as<static_cast<int>(weight_shift(kKvF16))>(a, st) : launch_join_as<static_cast<int>(weight_shift(kKvQ8))>(a, st);
 }
 
 }  // namespace qmv

@@ -5,31 +5,33 @@
 // The query heads that share a key/value head are rows of one product
 // (row = token * group + head of the group), so a cache byte is read once for
 // all of them. A wave owns MT tiles of 16 rows and walks the keys 32 at a
-// time with the running maximum m, sum l and unnormalised O of a softmax:
+// time with the running maximum M, sum l and unnormalised O of a softmax:
 //   S^T = K q^T     two 16x16 tiles of 16x16x32 fp16 products; a lane then
 //                   holds the scores of ONE row (lane % 16) for the 8 tokens
 //                   8g..8g+7 of the step (g = lane / 16)
 //   O^T += V^T P^T  whose right operand is exactly that: the probabilities
-//                   stay in their lanes, and m, l and the rescaling of O are
+//                   stay in their lanes, and M, l and the rescaling of O are
 //                   one value a lane
-// The cache is stored in operand order (kv_layout.hpp): operands go from
-// memory to registers in full 4 to 16-byte runs, without LDS. Quantized
-// codes are exact in fp16 (keys) and bf16 (values); a key's block scale is
-// applied to the block's partial score, a value's block scale to P.
+// The cache is stored in operand order (kv_layout.hpp). Quantized codes are
+// exact in fp16; a key's block scale is applied to the block's partial score,
+// a value's block scale d to the probability.
 //
-// Precision: fp32 q is carried as two fp16 parts of the row scaled by a
-// power of two (21 bits of the row's largest value); P as two fp16 parts
-// (F16 cache, P scaled by 2^14 so that small ones keep their bits; the scale
-// cancels in O / l) or, P times the value's scale, as two bf16 parts (2^-16;
-// bf16 for its range, since scales reach from 2^-24 to 65504). Scores, m, l
-// and O are fp32.
+// Precision: q (times scale * log2 e, in fp32) is carried as two fp16 parts
+// of the row scaled by a power of two, 21 bits of the row's largest value; a
+// probability (times d) as two fp16 parts, 20 bits. fp16 parts need their
+// factor in range: the reference M of a row is the maximum of s + e over the
+// keys, e the exponent field of the token's largest |d| (0 for F16), and the
+// weight w = 2^(s - M + K) enters l as it is and O as w d, which is at most
+// 2^15 whatever the scales are and keeps its bits 39 binary places below
+// that. The factor 2^(K - M) cancels in O / l. Scores, M, l and O are fp32.
 //
-// Two splits of the work over a workgroup's 4 waves: with few rows the waves
-// take every fourth step of the same rows and join O through LDS (ROWS =
-// false); with many each wave has rows of its own and the waves meet in the
-// cache only (ROWS = true). Either way the keys can be cut into a.splits
-// ranges whose partial (m, l, O) a second launch joins, so that few rows over
-// a long cache still fill the chip.
+// Two kernels: with few rows the four waves of a workgroup take every fourth
+// step of the same rows, read operands from memory straight into registers
+// (the cache is the traffic, nothing would be shared) and join O through
+// LDS; with many rows each wave has rows of its own, and the workgroup turns
+// each step's codes into operands once, in LDS, for all four. Either way the
+// keys can be cut into a.splits ranges whose partial (M, l, O) a second
+// launch joins, so that few rows over a long cache still fill the chip.
 #pragma once
 
 #include "decode_args.hpp"
@@ -39,20 +41,17 @@ namespace qmv {
 
 typedef _Float16 half8 __attribute__((ext_vector_type(8)));
 typedef _Float16 half2v __attribute__((ext_vector_type(2)));
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAttnThreads = 256;
 constexpr int kStep = 32;                       // keys a step
-constexpr float kPShift = 14.0f;                // P of an F16 cache is scaled by 2^14
+
+// K above: w d <= 2^(K - e) 2^(e - 14) for a quantized token, w <= 2^K (F16).
+__host__ __device__ constexpr float weight_shift(int kind) { return kind == kKvF16 ? 14.0f : 29.0f; }
 
 __device__ __forceinline__ f32x4 mfma_f16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
-}
-
 // Maximum and sum over the four lanes that share a row.
 __device__ __forceinline__ float row_max(float v) {
   auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
@@ -65,29 +64,25 @@ __device__ __forceinline__ float row_sum(float v) {
   return swap_pair_sum<16>(v, v);
 }
 
-__device__ __forceinline__ uint32_t pack_f16(float a, float b) {
-  const half2v h = {static_cast<_Float16>(a), static_cast<_Float16>(b)};
-  return __builtin_bit_cast(uint32_t, h);
-}
-// Two values as fp16 parts: hi toward zero, lo the nearest of the rest (together 21 bits).
+// Two values as fp16 parts: hi toward zero, lo the nearest of the rest
+// (together 21 bits).
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
   const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
   hi = __builtin_bit_cast(uint32_t, h);
-  lo = pack_f16(a - static_cast<float>(h[0]), b - static_cast<float>(h[1]));
+  const half2v r = {static_cast<_Float16>(a - static_cast<float>(h[0])), static_cast<_Float16>(b - static_cast<float>(h[1]))};
+  lo = __builtin_bit_cast(uint32_t, r);
 }
-__device__ __forceinline__ uint32_t pack_bf16(float a, float b) {   // nearest
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  const bf16x2 h = {static_cast<__bf16>(a), static_cast<__bf16>(b)};
-  return __builtin_bit_cast(uint32_t, h);
-}
-// Two values as bf16 parts, each the nearest: together within 2^-16. Cutting
-// toward zero would cost as much and lean every probability the same way.
-__device__ __forceinline__ void split_bf16(float a, float b, uint32_t& hi, uint32_t& lo) {
-  hi = pack_bf16(a, b);
-  lo = pack_bf16(a - __uint_as_float(hi << 16), b - __uint_as_float(hi & 0xFFFF0000u));
-}
-__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {   // values that are exact in bf16
-  return __builtin_amdgcn_perm(__float_as_uint(b), __float_as_uint(a), 0x07060302u);
+// The same of the products p0 d0 and p1 d1 (d: two fp16 scales). The fma
+// forms take the scales as they are (v_fma_mix), the second ones round the
+// rest of the exact product.
+__device__ __forceinline__ void split_scaled(float p0, float p1, uint32_t d, uint32_t& hi, uint32_t& lo) {
+  const half2v dd = __builtin_bit_cast(half2v, d);
+  const float d0 = static_cast<float>(dd[0]), d1 = static_cast<float>(dd[1]);
+  const auto h = __builtin_amdgcn_cvt_pkrtz(fmaf(p0, d0, 0.0f), fmaf(p1, d1, 0.0f));
+  hi = __builtin_bit_cast(uint32_t, h);
+  const half2v r = {static_cast<_Float16>(fmaf(p0, d0, -static_cast<float>(h[0]))),
+                    static_cast<_Float16>(fmaf(p1, d1, -static_cast<float>(h[1])))};
+  lo = __builtin_bit_cast(uint32_t, r);
 }
 
 // fp16 of four biased codes (bytes): 1024 + u by its bits, less the bias.
@@ -97,10 +92,31 @@ __device__ __forceinline__ void codes_f16(uint32_t w, float bias, uint32_t& lo, 
   lo = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, w, 0x04010400u)) + off);
   hi = __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, __builtin_amdgcn_perm(0x64646464u, w, 0x04030402u)) + off);
 }
-__device__ __forceinline__ void codes_bf16(uint32_t w, float bias, uint32_t& lo, uint32_t& hi) {
-  lo = bf16_pair(static_cast<float>(w & 0xFFu) - bias, static_cast<float>((w >> 8) & 0xFFu) - bias);
-  hi = bf16_pair(static_cast<float>((w >> 16) & 0xFFu) - bias, static_cast<float>(w >> 24) - bias);
+// Operand of 8 codes in two words (Q8_0), or in the low or high nibbles of them.
+__device__ __forceinline__ u32x4 operand_q8(uint32_t a, uint32_t b) {
+  uint32_t t[4];
+  codes_f16(a, 128.0f, t[0], t[1]);
+  codes_f16(b, 128.0f, t[2], t[3]);
+  return u32x4{t[0], t[1], t[2], t[3]};
 }
+__device__ __forceinline__ u32x4 operand_q4(uint32_t a, uint32_t b) {   // nibbles in bytes
+  uint32_t t[4];
+  codes_f16(a & 0x0F0F0F0Fu, 8.0f, t[0], t[1]);
+  codes_f16(b & 0x0F0F0F0Fu, 8.0f, t[2], t[3]);
+  return u32x4{t[0], t[1], t[2], t[3]};
+}
+
+__device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
+// Words of 8 fp16 whose elements c.. are cleared.
+__device__ __forceinline__ uint32_t keep_mask(int e, int c) {
+  return c >= 2 * e + 2 ? ~0u : c == 2 * e + 1 ? 0xFFFFu : 0u;
+}
+// Nonzero if one of the two fp16 is infinite or NaN.
+__device__ __forceinline__ uint32_t wild_bits(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u; }
 
 // Loads of a wave's 32-key step, as they lie in the cache.
 template <int KIND, int NB>
@@ -139,23 +155,13 @@ struct KeyRegs {
   // fp16 operand of block b, tile m
   __device__ __forceinline__ u32x4 operand(int m, int b) const {
     constexpr int LW = kv_lane_bytes(KIND, NB) / 4;
-    u32x4 r;
     if constexpr (KIND == kKvF16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = w[m * LW + 4 * b + e];
+      return u32x4{w[m * LW + 4 * b], w[m * LW + 4 * b + 1], w[m * LW + 4 * b + 2], w[m * LW + 4 * b + 3]};
     } else if constexpr (KIND == kKvQ8) {
-      uint32_t t[4];
-      codes_f16(w[m * LW + 2 * b], 128.0f, t[0], t[1]);
-      codes_f16(w[m * LW + 2 * b + 1], 128.0f, t[2], t[3]);
-      r = u32x4{t[0], t[1], t[2], t[3]};
+      return operand_q8(w[m * LW + 2 * b], w[m * LW + 2 * b + 1]);
     } else {
-      const uint32_t v = w[m * LW + b];
-      uint32_t t[4];
-      codes_f16(v & 0x0F0F0F0Fu, 8.0f, t[0], t[1]);
-      codes_f16((v >> 4) & 0x0F0F0F0Fu, 8.0f, t[2], t[3]);
-      r = u32x4{t[0], t[1], t[2], t[3]};
+      return operand_q4(w[m * LW + b], w[m * LW + b] >> 4);
     }
-    return r;
   }
   __device__ __forceinline__ float scale(int b, int j) const { return h2f(sc[b][j / 2] >> (16 * (j & 1))); }
 };
@@ -190,41 +196,48 @@ struct ValueRegs {
       if constexpr (KIND != kKvF16) sc[b] = ld_a16_x4(unit + kv_scale_at(KIND, NB, b, 8 * h8));
     }
   }
-  // operand of dims 32 b + 16 half ..: fp16 (F16) or bf16
+  // fp16 operand of dims 32 b + 16 half ..
   __device__ __forceinline__ u32x4 operand(int b, int half) const {
-    u32x4 r;
     if constexpr (KIND == kKvF16) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) r[e] = w[8 * b + 4 * half + e];
+      const uint32_t* p = w + 8 * b + 4 * half;
+      return u32x4{p[0], p[1], p[2], p[3]};
+    } else if constexpr (KIND == kKvQ8) {
+      return operand_q8(w[4 * b + 2 * half], w[4 * b + 2 * half + 1]);
     } else {
-      uint32_t t[4];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        uint32_t v;
-        if constexpr (KIND == kKvQ8) v = w[4 * b + 2 * half + e];
-        else v = (w[2 * b + e] >> (4 * half)) & 0x0F0F0F0Fu;
-        codes_bf16(v, KIND == kKvQ8 ? 128.0f : 8.0f, t[2 * e], t[2 * e + 1]);
-      }
-      r = u32x4{t[0], t[1], t[2], t[3]};
+      return operand_q4(w[2 * b] >> (4 * half), w[2 * b + 1] >> (4 * half));
     }
-    return r;
   }
-  __device__ __forceinline__ float scale(int b, int j) const { return h2f(sc[b][j / 2] >> (16 * (j & 1))); }
-
-  // F16: tokens c.. of this lane's 8 do not exist (what lies there is no value): zero.
+  // Exponent field of each token's largest scale.
+  __device__ __forceinline__ void exponents(float (&e5)[8]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      uint32_t top = sc[0][e] & 0x7FFF7FFFu;
+#pragma unroll
+      for (int b = 1; b < NB; ++b) top = max_u16x2(top, sc[b][e] & 0x7FFF7FFFu);
+      e5[2 * e] = static_cast<float>((top >> 10) & 31u);
+      e5[2 * e + 1] = static_cast<float>(top >> 26);
+    }
+  }
+  // Tokens c.. of this lane's 8 do not exist: what lies there is no value
+  // (F16) or scale, and 0 times it need not be 0.
   __device__ __forceinline__ void keep(int c) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint32_t mask = c >= 2 * e + 2 ? ~0u : c == 2 * e + 1 ? 0xFFFFu : 0u;
+      const uint32_t mask = keep_mask(e, c);
+      if constexpr (KIND == kKvF16) {
 #pragma unroll
-      for (int t = 0; t < 2 * NB; ++t) w[4 * t + e] &= mask;
+        for (int t = 0; t < 2 * NB; ++t) w[4 * t + e] &= mask;
+      } else {
+#pragma unroll
+        for (int b = 0; b < NB; ++b) sc[b][e] &= mask;
+      }
     }
   }
   // F16: whether any value is infinite or NaN
   __device__ __forceinline__ bool wild() const {
     uint32_t any = 0;
 #pragma unroll
-    for (int i = 0; i < NB * kPer; ++i) any |= ((w[i] & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u;
+    for (int i = 0; i < NB * kPer; ++i) any |= wild_bits(w[i]);
     return any != 0;
   }
 };
@@ -251,12 +264,14 @@ __device__ __forceinline__ StepPages step_pages(const AttnArgs& a, int s, int he
   return p;
 }
 
-// 1 / (sum of the row's probabilities), its sink among them; 0 for a row
-// that saw no key. m and l are in units of log2, l scaled by 2^shift.
+// Factor that turns a row's O into its result: 1 / l with the sink's share
+// in l; 0 for a row that saw no key. l and O are in units of 2^(m - shift).
 __device__ __forceinline__ float row_factor(const AttnArgs& a, int head, float m, float l, float shift) {
   if (m == -INFINITY) return 0.0f;
-  if (a.sinks) l += __builtin_amdgcn_exp2f(fmaf(a.sinks[head], 1.44269504088896340736f, shift - m));
-  return 1.0f / l;
+  if (!a.sinks) return 1.0f / l;
+  const float sink = a.sinks[head] * 1.44269504088896340736f, unit = m - shift, top = fmaxf(unit, sink);
+  const float f = __builtin_amdgcn_exp2f(unit - top);
+  return f / fmaf(l, f, __builtin_amdgcn_exp2f(sink - top));
 }
 
 // A finished row to out, or a split's share of it to the workspace. `write`
@@ -273,67 +288,64 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head
   }
 }
 
-template <int KIND, int NB, int MT, bool ROWS>
-__global__ void __launch_bounds__(kAttnThreads) attn_kernel(AttnArgs a) {
-  constexpr int D = 32 * NB, DT = 2 * NB;
-  constexpr int RW = 16 * MT;                   // rows a wave
-  constexpr int RT = ROWS ? 4 * RW : RW;        // rows a workgroup
-  constexpr float kShift = KIND == kKvF16 ? kPShift : 0.0f;
-  __shared__ float lds_o[ROWS ? 1 : 4 * RW * D];
-  __shared__ float lds_ml[ROWS ? 1 : 4 * RW * 2];
-
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), l = lane_id(), g = l >> 4, col = l & 15;
-  // Workgroups go to the 8 XCDs in turn: those that read the same keys (the
-  // tiles of one sequence, head and range) get the same XCD and its L2.
-  const int slot = blockIdx.x >> 3;
-  int group_id = (slot / a.tiles) * 8 + (blockIdx.x & 7);
-  const int tile0 = a.tiles - 1 - slot % a.tiles;   // the longest rows first
-  if (group_id >= a.b.n_seqs * a.splits * a.b.n_kv_heads) return;
-  const int head = group_id % a.b.n_kv_heads;
-  group_id /= a.b.n_kv_heads;
-  const int split = group_id % a.splits, s = group_id / a.splits;
-
-  int first, count;
-  a.b.rows(s, first, count);
-  const int len = a.b.seq_len[s] < 0 ? 0 : a.b.seq_len[s] > (1 << 30) ? (1 << 30) : a.b.seq_len[s];
-  const int64_t table_end = static_cast<int64_t>(a.b.pages_per_seq) << a.b.page_shift;
-  const int keys = len < table_end ? len : static_cast<int>(table_end);
-  const int rows = count * a.group;             // count <= 2^20, group <= 2^16: see the host check
-
-  for (int tile = tile0; tile * RT < rows; tile += a.tiles) {
-    const int row0 = tile * RT + (ROWS ? wave * RW : 0);
-    // positions of the workgroup's and the wave's rows
-    const int wg_last = (tile * RT + RT < rows ? tile * RT + RT : rows) - 1;
-    const int w_last = row0 + RW - 1 < rows ? row0 + RW - 1 : rows - 1;
-    const int base = len - count;               // position of new token 0
-    const int hi_wg = base + wg_last / a.group, lo_wg = base + tile * RT / a.group;
-    const int hi = base + w_last / a.group;
-    const int lo = base + (row0 < rows ? row0 : rows - 1) / a.group;
-    // the split's range of the keys that the workgroup sees, in steps
-    int k_end = hi_wg + 1 < keys ? hi_wg + 1 : keys;
-    const int k_beg = a.window > 0 && lo_wg - a.window + 1 > 0 ? (lo_wg - a.window + 1) & ~(kStep - 1) : 0;
+// What a workgroup works on: a tile of rows of one sequence and key/value
+// head, and a range of the keys.
+struct Place {
+  int head, split, s, tile0;
+  int first, count, len, keys, rows, base;      // base: position of new token 0
+  __device__ __forceinline__ bool find(const AttnArgs& a) {
+    // Workgroups go to the 8 XCDs in turn: those that read the same keys (the
+    // tiles of one sequence, head and range) get the same XCD and its L2.
+    const int slot = blockIdx.x >> 3;
+    int id = (slot / a.tiles) * 8 + (blockIdx.x & 7);
+    tile0 = a.tiles - 1 - slot % a.tiles;       // the longest rows first
+    if (id >= a.b.n_seqs * a.splits * a.b.n_kv_heads) return false;
+    head = id % a.b.n_kv_heads;
+    id /= a.b.n_kv_heads;
+    split = id % a.splits;
+    s = id / a.splits;
+    a.b.rows(s, first, count);
+    const int l = a.b.seq_len[s];
+    len = l < 0 ? 0 : l > (1 << 30) ? (1 << 30) : l;
+    const int64_t table_end = static_cast<int64_t>(a.b.pages_per_seq) << a.b.page_shift;
+    keys = len < table_end ? len : static_cast<int>(table_end);
+    rows = count * a.group;                     // n_tokens * n_heads <= 2^30
+    base = len - count;
+    return true;
+  }
+  // The split's range of the keys that rows r0..r1 see, in whole steps.
+  __device__ __forceinline__ void range(const AttnArgs& a, int r0, int r1, int& beg, int& end) const {
+    const int lo = base + r0 / a.group, hi = base + r1 / a.group;
+    const int k_end = hi + 1 < keys ? hi + 1 : keys;
+    const int k_beg = a.window > 0 && lo - a.window + 1 > 0 ? (lo - a.window + 1) & ~(kStep - 1) : 0;
     const int steps = k_end > k_beg ? (k_end - k_beg + kStep - 1) / kStep : 0;
     const int per = (steps + a.splits - 1) / a.splits;
-    int t_beg = k_beg + split * per * kStep;
-    int t_end = k_beg + (split + 1 < a.splits ? (split + 1) * per : steps) * kStep;
-    if (t_end > k_beg + steps * kStep) t_end = k_beg + steps * kStep;
-    if constexpr (ROWS) {                       // and of those the wave's own
-      if (row0 >= rows) t_end = t_beg;
-      else if (hi + 1 < t_end) t_end = hi + 1;
-      if (a.window > 0 && lo - a.window + 1 > t_beg) t_beg += (lo - a.window + 1 - t_beg) & ~(kStep - 1);
-    }
+    const int s0 = split * per < steps ? split * per : steps, s1 = s0 + per < steps ? s0 + per : steps;
+    beg = k_beg + s0 * kStep;
+    end = k_beg + s1 * kStep;
+  }
+};
 
-    // q as fp16 parts of its row scaled to 2^13..2^14
-    u32x4 qh[MT][NB], ql[MT][NB];
-    float to_log2[MT];
-    int qpos[MT];
+// A wave's rows: q as operands, and the running softmax.
+template <int KIND, int NB, int MT>
+struct Rows {
+  static constexpr int DT = 2 * NB;
+  static constexpr float kShift = weight_shift(KIND);
+  u32x4 qh[MT][NB], ql[MT][NB];
+  float to_log2[MT];                            // 2^-k of the row's scaling
+  int qpos[MT];                                 // position, -1: no row
+  float m[MT], l[MT];
+  f32x4 o[MT][DT];
+
+  __device__ __forceinline__ void init(const AttnArgs& a, const Place& w, int row0) {
+    const int lane = lane_id(), g = lane >> 4, col = lane & 15;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int row = row0 + 16 * t + col;
-      const bool live = row < rows;
-      const int tok = live ? row / a.group : 0, hd = head * a.group + (live ? row - tok * a.group : 0);
-      qpos[t] = live ? base + tok : -1;
-      const float* src = a.q + (first + tok) * a.ldq + static_cast<int64_t>(hd) * D;
+      const bool live = row < w.rows;
+      const int tok = live ? row / a.group : 0, hd = w.head * a.group + (live ? row - tok * a.group : 0);
+      qpos[t] = live ? w.base + tok : -1;
+      const float* src = a.q + (w.first + tok) * a.ldq + static_cast<int64_t>(hd) * (32 * NB);
       float v[NB][8], top = 0.0f;
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
@@ -342,8 +354,8 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(AttnArgs a) {
         const u32x4 y = ld_x4(reinterpret_cast<const uint8_t*>(src + d1));
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          v[b][e] = live ? __uint_as_float(x[e]) : 0.0f;
-          v[b][4 + e] = live ? __uint_as_float(y[e]) : 0.0f;
+          v[b][e] = live ? __uint_as_float(x[e]) * a.scale_log2 : 0.0f;
+          v[b][4 + e] = live ? __uint_as_float(y[e]) * a.scale_log2 : 0.0f;
         }
 #pragma unroll
         for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(v[b][e]));
@@ -351,259 +363,499 @@ __global__ void __launch_bounds__(kAttnThreads) attn_kernel(AttnArgs a) {
       top = row_max(top);
       int ex = static_cast<int>((__float_as_uint(top) >> 23) & 0xFFu) - 127;   // 2^ex <= top < 2^(ex+1)
       ex = top == 0.0f || ex == 128 ? 13 : ex < -100 ? -100 : ex;
-      const float up = __uint_as_float(static_cast<uint32_t>(13 - ex + 127) << 23);
-      to_log2[t] = a.scale_log2 * __uint_as_float(static_cast<uint32_t>(ex - 13 + 127) << 23);
+      const float up = __uint_as_float(static_cast<uint32_t>(13 - ex + 127) << 23);   // to 2^13..2^14
+      to_log2[t] = __uint_as_float(static_cast<uint32_t>(ex - 13 + 127) << 23);
 #pragma unroll
       for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t h, lo2;
-          split_f16(v[b][2 * e] * up, v[b][2 * e + 1] * up, h, lo2);
+          uint32_t h, lo;
+          split_f16(v[b][2 * e] * up, v[b][2 * e + 1] * up, h, lo);
           qh[t][b][e] = h;
-          ql[t][b][e] = lo2;
+          ql[t][b][e] = lo;
         }
-    }
-
-    float m[MT], lsum[MT];
-    f32x4 o[MT][DT];
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
       m[t] = -INFINITY;
-      lsum[t] = 0.0f;
+      l[t] = 0.0f;
 #pragma unroll
       for (int d = 0; d < DT; ++d) o[t][d] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
+  }
 
-    const int stride = ROWS ? kStep : 4 * kStep;
-    int t0 = t_beg + (ROWS ? 0 : wave * kStep);
+  // Adds block b of key tile mm to the scores; sc: the tokens' scales.
+  __device__ __forceinline__ void score(u32x4 kop, int b, int mm, u32x4 sc, f32x4 (&s)[MT][2]) const {
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      if constexpr (KIND == kKvF16) {
+        s[t][mm] = mfma_f16(kop, ql[t][b], s[t][mm]);
+        s[t][mm] = mfma_f16(kop, qh[t][b], s[t][mm]);
+      } else {
+        f32x4 acc = mfma_f16(kop, ql[t][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        acc = mfma_f16(kop, qh[t][b], acc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[t][mm][i] = fmaf(acc[i], h2f(sc[2 * mm + i / 2] >> (16 * (i & 1))), s[t][mm][i]);
+      }
+    }
+  }
+
+  // What tile t's row does not see of tokens k0..k0+7, of which `real` exist.
+  __device__ __forceinline__ void hide(const AttnArgs& a, int t, int k0, int real, f32x4 (&s)[MT][2]) const {
+    const int end = qpos[t] - k0 + 1 < real ? qpos[t] - k0 + 1 : real;
+    const int beg = a.window > 0 ? qpos[t] - a.window + 1 - k0 : -1;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[t][j / 4][j & 3] = j < end && j >= beg ? s[t][j / 4][j & 3] : -INFINITY;
+  }
+
+  // Scores to weights; M, l and O follow.
+  __device__ __forceinline__ void weigh(int t, const float (&e5)[8], f32x4 (&s)[MT][2]) {
+    float top;
+    if constexpr (KIND == kKvF16) {
+      top = s[t][0][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = fmaxf(top, s[t][j / 4][j & 3]);
+      top = row_max(top) * to_log2[t];
+    } else {
+      top = fmaf(s[t][0][0], to_log2[t], e5[0]);
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = fmaxf(top, fmaf(s[t][j / 4][j & 3], to_log2[t], e5[j]));
+      top = row_max(top);
+    }
+    if (__any(top > m[t])) {
+      top = fmaxf(m[t], top);
+      const float al = __builtin_amdgcn_exp2f(m[t] - (top == -INFINITY ? 0.0f : top));
+      l[t] *= al;
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][d][i] *= al;
+      m[t] = top;
+    }
+    const float off = kShift - (m[t] == -INFINITY ? 0.0f : m[t]);   // a row that has seen nothing yet: all weights 0
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      s[t][j / 4][j & 3] = __builtin_amdgcn_exp2f(fmaf(s[t][j / 4][j & 3], to_log2[t], off));
+      l[t] += s[t][j / 4][j & 3];
+    }
+  }
+
+  // Weights (times the scales d of the tokens, if any) as operand parts.
+  __device__ __forceinline__ void parts(int t, const f32x4 (&s)[MT][2], u32x4 d, u32x4& hi, u32x4& lo) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const float x = s[t][e / 2][2 * (e & 1)], y = s[t][e / 2][2 * (e & 1) + 1];
+      uint32_t h, r;
+      if constexpr (KIND == kKvF16) split_f16(x, y, h, r);
+      else split_scaled(x, y, d[e], h, r);
+      hi[e] = h;
+      lo[e] = r;
+    }
+  }
+
+  __device__ __forceinline__ void add(int t, int d, u32x4 vop, u32x4 hi, u32x4 lo) {
+    o[t][d] = mfma_f16(vop, lo, o[t][d]);
+    o[t][d] = mfma_f16(vop, hi, o[t][d]);
+  }
+
+  // F16, an infinity or NaN among the step's values: one token after the
+  // other, added only to the rows that see it (0 * inf is NaN).
+  template <class V>
+  __device__ __forceinline__ void add_wild(const AttnArgs& a, int t, int t0, u32x4 hi, u32x4 lo, V value) {
+    const int g = lane_id() >> 4;
+    for (int tok = 0; tok < kStep; ++tok) {
+      const bool mine = (tok >> 3) == g, see = t0 + tok <= qpos[t] && (a.window <= 0 || t0 + tok > qpos[t] - a.window);
+      u32x4 mask = {0u, 0u, 0u, 0u};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) mask[e] = mine && (tok & 7) >> 1 == e ? (tok & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+#pragma unroll
+      for (int d = 0; d < DT; ++d) {
+        const u32x4 vop = value(d) & mask;
+        f32x4 acc = mfma_f16(vop, lo & mask, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+        acc = mfma_f16(vop, hi & mask, acc);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) o[t][d][i] += see ? acc[i] : 0.0f;
+      }
+    }
+  }
+};
+
+// Few rows: the waves share the keys.
+template <int KIND, int NB, int MT>
+__global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_kernel(AttnArgs a) {
+  constexpr int D = 32 * NB, DT = 2 * NB, RW = 16 * MT;
+  __shared__ float lds_o[4 * RW * D];
+  __shared__ float lds_ml[4 * RW * 2];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
+  Place w;
+  if (!w.find(a)) return;
+  for (int tile = w.tile0; tile * RW < w.rows; tile += a.tiles) {
+    const int row0 = tile * RW, row1 = (row0 + RW < w.rows ? row0 + RW : w.rows) - 1;
+    int t_beg, t_end;
+    w.range(a, row0, row1, t_beg, t_end);
+    const int lo = w.base + row0 / a.group, hi = w.base + row1 / a.group;
+    Rows<KIND, NB, MT> r;
+    r.init(a, w, row0);
+    int t0 = t_beg + wave * kStep;
     KeyRegs<KIND, NB> kr;
     StepPages pg;
     const int kh = col >> 3, vh = g >> 1;       // halves of the step: of the lane's key row, of its tokens
     if (t0 < t_end) {
-      pg = step_pages<KIND, NB>(a, s, head, t0);
+      pg = step_pages<KIND, NB>(a, w.s, w.head, t0);
       kr.load(kh ? pg.k[1] : pg.k[0], vh ? pg.k[1] : pg.k[0]);
     }
-    for (; t0 < t_end; t0 += stride) {
+    for (; t0 < t_end; t0 += 4 * kStep) {
       ValueRegs<KIND, NB> vr;
       vr.load(vh ? pg.v[1] : pg.v[0]);
-      // scores
-      float p[MT][8];
+      f32x4 s[MT][2];
 #pragma unroll
-      for (int mm = 0; mm < 2; ++mm) {
-        f32x4 sc[MT];
+      for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-        for (int t = 0; t < MT; ++t) sc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      for (int mm = 0; mm < 2; ++mm)
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const u32x4 kop = kr.operand(mm, b);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            if constexpr (KIND == kKvF16) {
-              sc[t] = mfma_f16(kop, ql[t][b], sc[t]);
-              sc[t] = mfma_f16(kop, qh[t][b], sc[t]);
-            } else {
-              f32x4 acc = mfma_f16(kop, ql[t][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-              acc = mfma_f16(kop, qh[t][b], acc);
-#pragma unroll
-              for (int i = 0; i < 4; ++i) sc[t][i] = fmaf(acc[i], kr.scale(b, 4 * mm + i), sc[t][i]);
-            }
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) p[t][4 * mm + i] = sc[t][i] * to_log2[t];
-      }
+        for (int b = 0; b < NB; ++b) r.score(kr.operand(mm, b), b, mm, kr.sc[KIND == kKvF16 ? 0 : b], s);
       const bool ok0 = pg.ok[0], ok1 = pg.ok[1];
-      const int tn = t0 + stride;
-      if (tn < t_end) {
-        pg = step_pages<KIND, NB>(a, s, head, tn);
+      if (t0 + 4 * kStep < t_end) {
+        pg = step_pages<KIND, NB>(a, w.s, w.head, t0 + 4 * kStep);
         kr.load(kh ? pg.k[1] : pg.k[0], vh ? pg.k[1] : pg.k[0]);
       }
-      // what a row does not see; steps that every row sees whole skip this
-      const bool whole = ok0 && ok1 && t0 + kStep - 1 <= lo && t0 + kStep <= keys &&
-                         (a.window <= 0 || t0 > hi - a.window);
+      // steps that every row sees whole need no masks
+      const bool whole = ok0 && ok1 && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
       bool wild = false;
-      const int kpos = t0 + 8 * g;
       if (!whole) {
-        const bool ok = vh ? ok1 : ok0;
-        const int real = ok ? keys - kpos : 0;  // tokens of this lane that exist
+        const int real = (vh ? ok1 : ok0) ? w.keys - (t0 + 8 * g) : 0;   // tokens of this lane that exist
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int k = kpos + j;
-            const bool see = j < real && k <= qpos[t] && (a.window <= 0 || k > qpos[t] - a.window);
-            p[t][j] = see ? p[t][j] : -INFINITY;
-          }
-        if constexpr (KIND == kKvF16) {
-          vr.keep(real);
-          wild = __any(vr.wild());
-        }
+        for (int t = 0; t < MT; ++t) r.hide(a, t, t0 + 8 * g, real, s);
+        vr.keep(real);
+        if constexpr (KIND == kKvF16) wild = __any(vr.wild());
       }
-      // running maximum and sum
+      float e5[8];
+      if constexpr (KIND != kKvF16) vr.exponents(e5);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        float top = p[t][0];
-#pragma unroll
-        for (int j = 1; j < 8; ++j) top = fmaxf(top, p[t][j]);
-        top = fmaxf(m[t], row_max(top));
-        const float from = top == -INFINITY ? 0.0f : top;   // a row that has seen nothing yet
-        if (__any(top != m[t])) {
-          const float al = __builtin_amdgcn_exp2f(m[t] - from);
-          lsum[t] *= al;
-#pragma unroll
-          for (int d = 0; d < DT; ++d)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[t][d][i] *= al;
-          m[t] = top;
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          p[t][j] = __builtin_amdgcn_exp2f(p[t][j] - from + kShift);
-          lsum[t] += p[t][j];
-        }
-      }
-      // O
+      for (int t = 0; t < MT; ++t) r.weigh(t, e5, s);
       if constexpr (KIND == kKvF16) {
         u32x4 ph[MT], pl[MT];
 #pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t h, lo2;
-            split_f16(p[t][2 * e], p[t][2 * e + 1], h, lo2);
-            ph[t][e] = h;
-            pl[t][e] = lo2;
-          }
+        for (int t = 0; t < MT; ++t) r.parts(t, s, u32x4{}, ph[t], pl[t]);
         if (!wild) {
 #pragma unroll
-          for (int b = 0; b < NB; ++b)
+          for (int d = 0; d < DT; ++d) {
+            const u32x4 vop = vr.operand(d / 2, d & 1);
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const u32x4 vop = vr.operand(b, half);
-#pragma unroll
-              for (int t = 0; t < MT; ++t) {
-                o[t][2 * b + half] = mfma_f16(vop, pl[t], o[t][2 * b + half]);
-                o[t][2 * b + half] = mfma_f16(vop, ph[t], o[t][2 * b + half]);
-              }
-            }
-        } else {
-          // an infinity or NaN among the values: one token after the other,
-          // added only to the rows that see it (0 * inf is NaN)
-          for (int tok = 0; tok < kStep; ++tok) {
-            const bool mine = (tok >> 3) == g;
-            const int k = t0 + tok;
-            u32x4 mask = {0u, 0u, 0u, 0u};
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              mask[e] = mine && (tok & 7) >> 1 == e ? (tok & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
-#pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              const bool see = k <= qpos[t] && (a.window <= 0 || k > qpos[t] - a.window);
-#pragma unroll
-              for (int b = 0; b < NB; ++b)
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                  const u32x4 vop = vr.operand(b, half) & mask;
-                  f32x4 acc = mfma_f16(vop, pl[t] & mask, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-                  acc = mfma_f16(vop, ph[t] & mask, acc);
-#pragma unroll
-                  for (int i = 0; i < 4; ++i) o[t][2 * b + half][i] += see ? acc[i] : 0.0f;
-                }
-            }
+            for (int t = 0; t < MT; ++t) r.add(t, d, vop, ph[t], pl[t]);
           }
+        } else {
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+            r.add_wild(a, t, t0, ph[t], pl[t], [&](int d) QMV_INLINE { return vr.operand(d / 2, d & 1); });
         }
       } else {
 #pragma unroll
         for (int b = 0; b < NB; ++b) {
           u32x4 ph[MT], pl[MT];
 #pragma unroll
-          for (int t = 0; t < MT; ++t)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              float x = p[t][2 * e] * vr.scale(b, 2 * e), y = p[t][2 * e + 1] * vr.scale(b, 2 * e + 1);
-              if (!whole) {                     // an unseen token's scale may be anything
-                x = p[t][2 * e] == 0.0f ? 0.0f : x;
-                y = p[t][2 * e + 1] == 0.0f ? 0.0f : y;
-              }
-              uint32_t h, lo2;
-              split_bf16(x, y, h, lo2);
-              ph[t][e] = h;
-              pl[t][e] = lo2;
-            }
+          for (int t = 0; t < MT; ++t) r.parts(t, s, vr.sc[b], ph[t], pl[t]);
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             const u32x4 vop = vr.operand(b, half);
 #pragma unroll
-            for (int t = 0; t < MT; ++t) {
-              o[t][2 * b + half] = mfma_bf16(vop, pl[t], o[t][2 * b + half]);
-              o[t][2 * b + half] = mfma_bf16(vop, ph[t], o[t][2 * b + half]);
-            }
+            for (int t = 0; t < MT; ++t) r.add(t, 2 * b + half, vop, ph[t], pl[t]);
           }
         }
       }
     }
 
+    // the waves' shares joined: each scaled to the common maximum
+    __syncthreads();                            // the tile before is read out
 #pragma unroll
-    for (int t = 0; t < MT; ++t) lsum[t] = row_sum(lsum[t]);
-
-    if constexpr (ROWS) {
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        const int row = row0 + 16 * t + col;
-        if (row >= rows) continue;
-        const int tok = row / a.group, hd = head * a.group + row - tok * a.group;
-        store_row<D>(a, first + tok, hd, split, m[t], lsum[t], kShift, [&](float* dst, float f) QMV_INLINE {
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = f == 0.0f ? 0.0f : o[t][d][i] * f;
-            __builtin_memcpy(__builtin_assume_aligned(dst + 16 * d + 4 * g, 4), v, 16);
-          }
-        }, g == 0);
+    for (int t = 0; t < MT; ++t) {
+      const float l = row_sum(r.l[t]);
+      if (g == 0) {
+        lds_ml[(wave * RW + 16 * t + col) * 2] = r.m[t];
+        lds_ml[(wave * RW + 16 * t + col) * 2 + 1] = l;
       }
+#pragma unroll
+      for (int d = 0; d < DT; ++d)
+        *reinterpret_cast<f32x4*>(&lds_o[(wave * RW + 16 * t + col) * D + 16 * d + 4 * g]) = r.o[t][d];
+    }
+    __syncthreads();
+    for (int it = threadIdx.x; it < RW * (D / 4); it += kAttnThreads) {
+      const int rr = it / (D / 4), d = it % (D / 4) * 4, row = row0 + rr;
+      if (row >= w.rows) continue;
+      float mx = -INFINITY;
+#pragma unroll
+      for (int v = 0; v < 4; ++v) mx = fmaxf(mx, lds_ml[(v * RW + rr) * 2]);
+      const float from = mx == -INFINITY ? 0.0f : mx;
+      float ls = 0.0f;
+      f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int v = 0; v < 4; ++v) {
+        const float f = __builtin_amdgcn_exp2f(lds_ml[(v * RW + rr) * 2] - from);
+        ls = fmaf(lds_ml[(v * RW + rr) * 2 + 1], f, ls);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(&lds_o[(v * RW + rr) * D + d]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[i] = fmaf(x[i], f, acc[i]);
+      }
+      const int tok = row / a.group, hd = w.head * a.group + row - tok * a.group;
+      store_row<D>(a, w.first + tok, hd, w.split, mx, ls, weight_shift(KIND), [&](float* dst, float f) QMV_INLINE {
+        float v[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = f == 0.0f ? 0.0f : acc[i] * f;
+        __builtin_memcpy(__builtin_assume_aligned(dst + d, 4), v, 16);
+      }, d == 0);
+    }
+  }
+}
+
+// A 32-key step as operands, in LDS.
+template <int KIND, int NB>
+struct StepLds {
+  u32x4 k[2][NB][kWave];                        // key operands
+  u32x4 v[2 * NB][kWave];                       // value operands
+  uint32_t ksc[KIND == kKvF16 ? 1 : NB][16];    // scales of the 32 tokens, two a word
+  uint32_t vsc[KIND == kKvF16 ? 1 : NB][16];
+  float e5[kStep];                              // exponent fields
+  int wild[4];
+};
+
+// A lane's share of a step on its way to LDS: runs of block b of operand lane
+// `at`, NB * 64 of them over the workgroup.
+template <int KIND, int NB>
+struct StepRegs {
+  static constexpr int kItems = (NB * kWave + kAttnThreads - 1) / kAttnThreads;
+  static constexpr int kKeyWords = kv_run(KIND) / 4;
+  static constexpr int kValueWords = KIND == kKvF16 ? 8 : KIND == kKvQ8 ? 4 : 2;
+  uint32_t k[kItems][2][kKeyWords], v[kItems][kValueWords];
+  uint32_t ksc, vsc;                            // of lanes 0..16 NB-1 (word lane % 16 of block lane / 16)
+  uint16_t es[KIND == kKvF16 ? 1 : NB];         // lanes 0..31: the token's value scales
+  bool ok[2];
+
+  __device__ __forceinline__ void load(const AttnArgs& a, int s, int head, int t0) {
+    const StepPages pg = step_pages<KIND, NB>(a, s, head, t0);
+    ok[0] = pg.ok[0];
+    ok[1] = pg.ok[1];
+    const int tid = threadIdx.x;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int it = tid + i * kAttnThreads;
+      if (NB * kWave % kAttnThreads && it >= NB * kWave) break;
+      const int b = it >> 6, at = it & 63, g = at >> 4, row = at & 15;
+      const uint8_t* ku = row >> 3 ? pg.k[1] : pg.k[0];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        constexpr int PS = kv_piece(KIND, NB), NP = kv_lane_bytes(KIND, NB) / PS;
+        const int off = b * kv_run(KIND);
+        const uint8_t* src = ku + (((m * NP + off / PS) * 4 + g) * 8 + (row & 7)) * PS + off % PS;
+        if constexpr (KIND == kKvF16) {
+          const u32x4 r = ld_a16_x4(src);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) k[i][m][e] = r[e];
+        } else if constexpr (KIND == kKvQ8) {
+          const u32x2 r = ld_x2(src);
+          k[i][m][0] = r.x;
+          k[i][m][1] = r.y;
+        } else {
+          k[i][m][0] = ld_u32(src);
+        }
+      }
+      const uint8_t* vu = (g >> 1 ? pg.v[1] : pg.v[0]);
+      if constexpr (KIND == kKvF16) {
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          const u32x4 r = ld_a16_x4(vu + (((b * 2 + half) * 2 + (g & 1)) * 16 + row) * 16);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[i][4 * half + e] = r[e];
+        }
+      } else if constexpr (KIND == kKvQ8) {
+        const u32x4 r = ld_a16_x4(vu + ((b * 2 + (g & 1)) * 16 + row) * 16);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[i][e] = r[e];
+      } else {
+        const u32x2 r = ld_x2(vu + ((b * 2 + (g & 1)) * 16 + row) * 8);
+        v[i][0] = r.x;
+        v[i][1] = r.y;
+      }
+    }
+    if constexpr (KIND != kKvF16) {
+      if (tid < 16 * NB) {
+        const int b = tid >> 4, word = tid & 15, at = kv_scale_at(KIND, NB, b, 2 * (word & 7));
+        ksc = ld_u32((word >> 3 ? pg.k[1] : pg.k[0]) + at);
+        vsc = ld_u32((word >> 3 ? pg.v[1] : pg.v[0]) + at);
+      }
+      if (tid < kStep) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          es[b] = static_cast<uint16_t>(ld_u16((tid >> 4 ? pg.v[1] : pg.v[0]) + kv_scale_at(KIND, NB, b, tid & 15)));
+      }
+    }
+  }
+
+  __device__ __forceinline__ void store(StepLds<KIND, NB>& lds, int t0, int keys) {
+    const int tid = threadIdx.x;
+    const bool part = !ok[0] || !ok[1] || t0 + kStep > keys;   // slots without a token
+    uint32_t any = 0;
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int it = tid + i * kAttnThreads;
+      if (NB * kWave % kAttnThreads && it >= NB * kWave) break;
+      const int b = it >> 6, at = it & 63, g = at >> 4;
+#pragma unroll
+      for (int m = 0; m < 2; ++m) {
+        if constexpr (KIND == kKvF16) lds.k[m][b][at] = u32x4{k[i][m][0], k[i][m][1], k[i][m][2], k[i][m][3]};
+        else if constexpr (KIND == kKvQ8) lds.k[m][b][at] = operand_q8(k[i][m][0], k[i][m][1]);
+        else lds.k[m][b][at] = operand_q4(k[i][m][0], k[i][m][0] >> 4);
+      }
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        if constexpr (KIND == kKvF16) {
+          u32x4 x = {v[i][4 * half], v[i][4 * half + 1], v[i][4 * half + 2], v[i][4 * half + 3]};
+          if (part) {
+            const int real = (g >> 1 ? ok[1] : ok[0]) ? keys - (t0 + 8 * g) : 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) x[e] &= keep_mask(e, real);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) any |= wild_bits(x[e]);
+          lds.v[2 * b + half][at] = x;
+        } else if constexpr (KIND == kKvQ8) {
+          lds.v[2 * b + half][at] = operand_q8(v[i][2 * half], v[i][2 * half + 1]);
+        } else {
+          lds.v[2 * b + half][at] = operand_q4(v[i][0] >> (4 * half), v[i][1] >> (4 * half));
+        }
+      }
+    }
+    if constexpr (KIND == kKvF16) {
+      const bool w = __any(any != 0);
+      if (lane_id() == 0) lds.wild[tid >> 6] = w;
     } else {
-      // the waves' shares joined: each scaled to the common maximum
-      __syncthreads();                          // the tile before is read out
+      if (tid < 16 * NB) {
+        const int b = tid >> 4, word = tid & 15;
+        lds.ksc[b][word] = ksc;
+        if (part) {
+          const int real = (word >> 3 ? ok[1] : ok[0]) ? keys - (t0 + 2 * word) : 0;
+          vsc &= keep_mask(0, real);
+        }
+        lds.vsc[b][word] = vsc;
+      }
+      if (tid < kStep) {
+        uint32_t top = 0;
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
-        if (g == 0) {
-          lds_ml[(wave * RW + 16 * t + col) * 2] = m[t];
-          lds_ml[(wave * RW + 16 * t + col) * 2 + 1] = lsum[t];
+        for (int b = 0; b < NB; ++b) {
+          const uint32_t d = es[b] & 0x7FFFu;
+          top = top > d ? top : d;
+        }
+        lds.e5[tid] = static_cast<float>(top >> 10);
+      }
+    }
+  }
+};
+
+// Many rows: the waves have rows of their own and share each step's operands.
+template <int KIND, int NB, int MT>
+__global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel(AttnArgs a) {
+  constexpr int D = 32 * NB, DT = 2 * NB, RW = 16 * MT, RT = 4 * RW;
+  __shared__ StepLds<KIND, NB> lds[2];
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
+  Place w;
+  if (!w.find(a)) return;
+  for (int tile = w.tile0; tile * RT < w.rows; tile += a.tiles) {
+    const int row0 = tile * RT + wave * RW;
+    int t_beg, t_end;
+    w.range(a, tile * RT, (tile * RT + RT < w.rows ? tile * RT + RT : w.rows) - 1, t_beg, t_end);
+    // positions of the wave's first and last row; lo > hi where it has none
+    const int lo = row0 < w.rows ? w.base + row0 / a.group : 1;
+    const int hi = row0 < w.rows ? w.base + ((row0 + RW < w.rows ? row0 + RW : w.rows) - 1) / a.group : 0;
+    Rows<KIND, NB, MT> r;
+    r.init(a, w, row0);
+    StepRegs<KIND, NB> in;
+    __syncthreads();                            // the tile before is done with LDS
+    if (t_beg < t_end) {
+      in.load(a, w.s, w.head, t_beg);
+      in.store(lds[0], t_beg, w.keys);
+    }
+    __syncthreads();
+    int buf = 0;
+    for (int t0 = t_beg; t0 < t_end; t0 += kStep, buf ^= 1) {
+      const bool ok0 = in.ok[0], ok1 = in.ok[1], more = t0 + kStep < t_end;
+      if (more) in.load(a, w.s, w.head, t0 + kStep);
+      const StepLds<KIND, NB>& st = lds[buf];
+      if (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1)) {   // some row sees some of it
+        f32x4 s[MT][2];
+#pragma unroll
+        for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          u32x4 sc = {};
+          if constexpr (KIND != kKvF16) sc = *reinterpret_cast<const u32x4*>(&st.ksc[b][4 * g]);
+#pragma unroll
+          for (int mm = 0; mm < 2; ++mm) r.score(st.k[mm][b][lane], b, mm, sc, s);
+        }
+        const bool whole = ok0 && ok1 && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
+        bool wild = false;
+        if (!whole) {
+          const int real = (g >> 1 ? ok1 : ok0) ? w.keys - (t0 + 8 * g) : 0;
+#pragma unroll
+          for (int t = 0; t < MT; ++t) r.hide(a, t, t0 + 8 * g, real, s);
+          if constexpr (KIND == kKvF16) wild = st.wild[0] | st.wild[1] | st.wild[2] | st.wild[3];
+        }
+        float e5[8];
+        if constexpr (KIND != kKvF16) {
+#pragma unroll
+          for (int j = 0; j < 8; j += 4) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(&st.e5[8 * g + j]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) e5[j + i] = x[i];
+          }
         }
 #pragma unroll
-      for (int t = 0; t < MT; ++t)
+        for (int t = 0; t < MT; ++t) r.weigh(t, e5, s);
+        if constexpr (KIND == kKvF16) {
+          u32x4 ph[MT], pl[MT];
 #pragma unroll
-        for (int d = 0; d < DT; ++d)
-          *reinterpret_cast<f32x4*>(&lds_o[(wave * RW + 16 * t + col) * D + 16 * d + 4 * g]) = o[t][d];
+          for (int t = 0; t < MT; ++t) r.parts(t, s, u32x4{}, ph[t], pl[t]);
+          if (!wild) {
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+              const u32x4 vop = st.v[d][lane];
+#pragma unroll
+              for (int t = 0; t < MT; ++t) r.add(t, d, vop, ph[t], pl[t]);
+            }
+          } else {
+#pragma unroll
+            for (int t = 0; t < MT; ++t)
+              r.add_wild(a, t, t0, ph[t], pl[t], [&](int d) QMV_INLINE { return st.v[d][lane]; });
+          }
+        } else {
+#pragma unroll
+          for (int b = 0; b < NB; ++b) {
+            const u32x4 sc = *reinterpret_cast<const u32x4*>(&st.vsc[b][4 * g]);
+            u32x4 ph[MT], pl[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) r.parts(t, s, sc, ph[t], pl[t]);
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+              const u32x4 vop = st.v[2 * b + half][lane];
+#pragma unroll
+              for (int t = 0; t < MT; ++t) r.add(t, 2 * b + half, vop, ph[t], pl[t]);
+            }
+          }
+        }
+      }
+      if (more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
       __syncthreads();
-      for (int it = threadIdx.x; it < RW * (D / 4); it += kAttnThreads) {
-        const int r = it / (D / 4), d = it % (D / 4) * 4, row = row0 + r;
-        if (row >= rows) continue;
-        float mx = -INFINITY;
+    }
 #pragma unroll
-        for (int w = 0; w < 4; ++w) mx = fmaxf(mx, lds_ml[(w * RW + r) * 2]);
-        const float from = mx == -INFINITY ? 0.0f : mx;
-        float ls = 0.0f;
-        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int t = 0; t < MT; ++t) {
+      const float l = row_sum(r.l[t]);
+      const int row = row0 + 16 * t + col;
+      if (row >= w.rows) continue;
+      const int tok = row / a.group, hd = w.head * a.group + row - tok * a.group;
+      store_row<D>(a, w.first + tok, hd, w.split, r.m[t], l, weight_shift(KIND), [&](float* dst, float f) QMV_INLINE {
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float f = __builtin_amdgcn_exp2f(lds_ml[(w * RW + r) * 2] - from);
-          ls = fmaf(lds_ml[(w * RW + r) * 2 + 1], f, ls);
-          const f32x4 x = *reinterpret_cast<const f32x4*>(&lds_o[(w * RW + r) * D + d]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[i] = fmaf(x[i], f, acc[i]);
-        }
-        const int tok = row / a.group, hd = head * a.group + row - tok * a.group;
-        store_row<D>(a, first + tok, hd, split, mx, ls, kShift, [&](float* dst, float f) QMV_INLINE {
+        for (int d = 0; d < DT; ++d) {
           float v[4];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) v[i] = f == 0.0f ? 0.0f : acc[i] * f;
-          __builtin_memcpy(__builtin_assume_aligned(dst + d, 4), v, 16);
-        }, d == 0);
-      }
+          for (int i = 0; i < 4; ++i) v[i] = f == 0.0f ? 0.0f : r.o[t][d][i] * f;
+          __builtin_memcpy(__builtin_assume_aligned(dst + 16 * d + 4 * g, 4), v, 16);
+        }
+      }, g == 0);
     }
   }
 }
@@ -613,18 +865,20 @@ int launch_attn_as(const AttnArgs& a, hipStream_t st) {
   const int64_t groups = static_cast<int64_t>(a.b.n_seqs) * a.splits * a.b.n_kv_heads;
   const int64_t grid = (groups + 7) / 8 * 8 * a.tiles;
   if (grid > (1 << 23)) return MMVQ_ERR_SHAPE;   // 2^32 lanes in a launch
-  hipLaunchKernelGGL((attn_kernel<KIND, NB, MT, ROWS>), dim3(static_cast<unsigned>(grid)), dim3(kAttnThreads), 0, st, a);
+  const dim3 g(static_cast<unsigned>(grid)), b(kAttnThreads);
+  if constexpr (ROWS) hipLaunchKernelGGL((attn_rows_kernel<KIND, NB, MT>), g, b, 0, st, a);
+  else hipLaunchKernelGGL((attn_keys_kernel<KIND, NB, MT>), g, b, 0, st, a);
   return check_launch();
 }
 
 template <int KIND, int NB>
 int launch_attn_nb(const AttnShape& s, const AttnArgs& a, hipStream_t st) {
-  if constexpr (NB < 8) {
-    if (s.mt == 2) return s.rows ? launch_attn_as<KIND, NB, 2, true>(a, st) : launch_attn_as<KIND, NB, 2, false>(a, st);
-    return launch_attn_as<KIND, NB, 1, false>(a, st);
-  } else {
-    return s.rows ? launch_attn_as<KIND, NB, 1, true>(a, st) : launch_attn_as<KIND, NB, 1, false>(a, st);
-  }
+  if (s.rows) return launch_attn_as<KIND, NB, NB < 8 ? 2 : 1, true>(a, st);
+  if constexpr (NB < 8)
+    if (s.mt == 2) return launch_attn_as<KIND, NB, 2, false>(a, st);
+  if constexpr (NB == 2)
+    if (s.mt == 3) return launch_attn_as<KIND, NB, 3, false>(a, st);
+  return launch_attn_as<KIND, NB, 1, false>(a, st);
 }
 
 template <int KIND>

@@ -102,7 +102,7 @@ __device__ __forceinline__ void put_quad(uint8_t* img, int tt, int b, int sub, c
         for (int e = 0; e < 4; ++e) img[kv_value_at(KIND, tt, b, c + e)] = static_cast<uint8_t>(w >> (8 * e));
       }
     }
-    if (sub == 0) *reinterpret_cast<uint16_t*>(img + kv_scale_at(KIND, NB, b, tt)) = static_cast<uint16_t>(f2h_bits(d));
+    if (sub == 0) *reinterpret_cast<uint16_t*>(img + kv_scale_at(KIND, NB, b, tt)) = static_cast<uint16_t>(f2h_bits(fminf(fmaxf(d, -65504.0f), 65504.0f)));
   }
 }
 

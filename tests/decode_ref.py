@@ -148,19 +148,26 @@ def attention(q, k, v, scale, base, window=0, sinks=None, hidden=()):
     return out, mag, smax
 
 
-def attention_tolerance(out, mag, smax, keys, D, kind):
-    """|gpu - ref| for fp32 results. Per score: q in two fp16 parts is off by
-    2^-21 of the row's largest |q| (smax has max|q| sum|k|), the products sum
+def attention_tolerance(out, mag, smax, v, D):
+    """|gpu - ref| for fp32 results; v: the stored values [keys, H, D].
+    Per score: q in two fp16 parts is off by 2^-21 of the row's largest |q|
+    (smax has max|q| sum|k|), scaling it rounds once (2^-24), the products sum
     D terms in fp32 (D 2^-24 of sum|q k| <= smax), three more roundings of the
-    score: ds <= smax (2^-21 + (D + 3) 2^-24). A probability moves by
-    2 ds (its own and the sum's) + 2^-22 (exp2), its two parts are off by
-    2^-16 (bf16, both nearest: 2^-8 2^-8) or 2^-21 (fp16, the first toward
-    zero: 2^-10 2^-11), and the sums over the keys, 32 a step, round (keys/32 + 4 + 9) times: matrix
-    products add 8 terms a lane group, 4 groups, 2 parts, then the joins."""
-    ds = smax * (2.0 ** -21 + (D + 3) * 2.0 ** -24)
-    rel = 2 * np.expm1(ds) + 2.0 ** -22 + (2.0 ** -21 if kind == "f16" else 2.0 ** -16)
-    rel = rel + (keys / 32 * 2 + 48) * 2.0 ** -24
-    return mag * rel[..., None] + np.abs(out) * 2.0 ** -23 + 1e-30
+    score: ds <= smax (2^-21 + (D + 4) 2^-24). A probability moves by 2 ds
+    (its own and the sum's) + 2^-22 (exp2), its two parts are off by 2^-20 at
+    most (the first cut toward zero, 2^-10, the second to nearest of that,
+    2^-11, and the same again where a scale joins), and the sums over the
+    keys, 32 a step, round (keys/32 + 4 + 9) times: matrix products add 8
+    terms a lane group, 4 groups, 2 parts, then the joins. Below 2^-14 fp16
+    has steps of 2^-24: a weight is off by 2^-25 in units in which the
+    largest is at least 2^14 (times the largest scale, quantized), which
+    leaves 2^-39 of the largest value a key."""
+    keys = max(1, len(v))
+    ds = smax * (2.0 ** -21 + (D + 4) * 2.0 ** -24)
+    with np.errstate(over="ignore"):
+        rel = 2 * np.expm1(ds) + 2.0 ** -22 + 2.0 ** -20 + (keys / 32 * 2 + 48) * 2.0 ** -24
+    low = 2.0 ** -39 * keys * np.abs(v).max(initial=0.0)
+    return mag * rel[..., None] + np.abs(out) * 2.0 ** -23 + low + 1e-30
 
 
 # --- verification ------------------------------------------------------------------
