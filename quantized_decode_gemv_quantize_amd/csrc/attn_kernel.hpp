@@ -381,18 +381,55 @@ struct Rows {
     }
   }
 
-  // Adds block b of key tile mm to the scores; sc: the tokens' scales.
-  __device__ __forceinline__ void score(u32x4 kop, int b, int mm, u32x4 sc, f32x4 (&s)[MT][2]) const {
+  // Scores of the step. key(mm, b): operand of key tile mm, block b; scale(b):
+  // the 8 tokens' scales of the block. The products of one block are
+  // independent chains, and a block's partial scores are scaled while the
+  // next block's products run.
+  template <class K, class S>
+  __device__ __forceinline__ void scores(K key, S scale, f32x4 (&s)[MT][2]) const {
 #pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      if constexpr (KIND == kKvF16) {
-        s[t][mm] = mfma_f16(kop, ql[t][b], s[t][mm]);
-        s[t][mm] = mfma_f16(kop, qh[t][b], s[t][mm]);
-      } else {
-        f32x4 acc = mfma_f16(kop, ql[t][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-        acc = mfma_f16(kop, qh[t][b], acc);
+    for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    if constexpr (KIND == kKvF16) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s[t][mm][i] = fmaf(acc[i], h2f(sc[2 * mm + i / 2] >> (16 * (i & 1))), s[t][mm][i]);
+      for (int b = 0; b < NB; ++b) {
+        const u32x4 k0 = key(0, b), k1 = key(1, b);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          s[t][0] = mfma_f16(k0, ql[t][b], s[t][0]);
+          s[t][1] = mfma_f16(k1, ql[t][b], s[t][1]);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          s[t][0] = mfma_f16(k0, qh[t][b], s[t][0]);
+          s[t][1] = mfma_f16(k1, qh[t][b], s[t][1]);
+        }
+      }
+    } else {
+      f32x4 acc[2][MT][2];
+#pragma unroll
+      for (int b = 0; b <= NB; ++b) {
+        if (b < NB) {
+          const u32x4 k0 = key(0, b), k1 = key(1, b);
+          f32x4 (&c)[MT][2] = acc[b & 1];
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            c[t][0] = mfma_f16(k0, ql[t][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            c[t][1] = mfma_f16(k1, ql[t][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+          }
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            c[t][0] = mfma_f16(k0, qh[t][b], c[t][0]);
+            c[t][1] = mfma_f16(k1, qh[t][b], c[t][1]);
+          }
+        }
+        if (b > 0) {
+          const u32x4 sc = scale(b - 1);
+#pragma unroll
+          for (int t = 0; t < MT; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              s[t][j / 4][j & 3] = fmaf(acc[(b - 1) & 1][t][j / 4][j & 3], h2f(sc[j / 2] >> (16 * (j & 1))), s[t][j / 4][j & 3]);
+        }
       }
     }
   }
@@ -450,16 +487,42 @@ struct Rows {
     }
   }
 
-  __device__ __forceinline__ void add(int t, int d, u32x4 vop, u32x4 hi, u32x4 lo) {
-    o[t][d] = mfma_f16(vop, lo, o[t][d]);
-    o[t][d] = mfma_f16(vop, hi, o[t][d]);
+  // O of the step. value(d): operand of dims 16 d ..; scale(b): the 8 tokens'
+  // scales of block b. A quantized block's weights are formed while the
+  // products of the block before run.
+  template <class V, class S>
+  __device__ __forceinline__ void accumulate(V value, S scale, const f32x4 (&s)[MT][2]) {
+    u32x4 ph[2][MT], pl[2][MT];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) parts(t, s, scale(0), ph[0][t], pl[0][t]);
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      const int now = KIND == kKvF16 ? 0 : b & 1;
+      const u32x4 v0 = value(2 * b), v1 = value(2 * b + 1);
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        o[t][2 * b] = mfma_f16(v0, pl[now][t], o[t][2 * b]);
+        o[t][2 * b + 1] = mfma_f16(v1, pl[now][t], o[t][2 * b + 1]);
+      }
+      if (KIND != kKvF16 && b + 1 < NB) {
+#pragma unroll
+        for (int t = 0; t < MT; ++t) parts(t, s, scale(b + 1), ph[now ^ 1][t], pl[now ^ 1][t]);
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        o[t][2 * b] = mfma_f16(v0, ph[now][t], o[t][2 * b]);
+        o[t][2 * b + 1] = mfma_f16(v1, ph[now][t], o[t][2 * b + 1]);
+      }
+    }
   }
 
   // F16, an infinity or NaN among the step's values: one token after the
   // other, added only to the rows that see it (0 * inf is NaN).
   template <class V>
-  __device__ __forceinline__ void add_wild(const AttnArgs& a, int t, int t0, u32x4 hi, u32x4 lo, V value) {
+  __device__ __forceinline__ void accumulate_wild(const AttnArgs& a, int t, int t0, V value, const f32x4 (&s)[MT][2]) {
     const int g = lane_id() >> 4;
+    u32x4 hi, lo;
+    parts(t, s, u32x4{}, hi, lo);
     for (int tok = 0; tok < kStep; ++tok) {
       const bool mine = (tok >> 3) == g, see = t0 + tok <= qpos[t] && (a.window <= 0 || t0 + tok > qpos[t] - a.window);
       u32x4 mask = {0u, 0u, 0u, 0u};
@@ -505,12 +568,8 @@ __global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_k
       ValueRegs<KIND, NB> vr;
       vr.load(vh ? pg.v[1] : pg.v[0]);
       f32x4 s[MT][2];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-      for (int mm = 0; mm < 2; ++mm)
-#pragma unroll
-        for (int b = 0; b < NB; ++b) r.score(kr.operand(mm, b), b, mm, kr.sc[KIND == kKvF16 ? 0 : b], s);
+      r.scores([&](int mm, int b) QMV_INLINE { return kr.operand(mm, b); },
+               [&](int b) QMV_INLINE { return kr.sc[KIND == kKvF16 ? 0 : b]; }, s);
       const bool ok0 = pg.ok[0], ok1 = pg.ok[1];
       if (t0 + 4 * kStep < t_end) {
         pg = step_pages<KIND, NB>(a, w.s, w.head, t0 + 4 * kStep);
@@ -530,35 +589,12 @@ __global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_k
       if constexpr (KIND != kKvF16) vr.exponents(e5);
 #pragma unroll
       for (int t = 0; t < MT; ++t) r.weigh(t, e5, s);
-      if constexpr (KIND == kKvF16) {
-        u32x4 ph[MT], pl[MT];
+      const auto value = [&](int d) QMV_INLINE { return vr.operand(d / 2, d & 1); };
+      if (!wild) {
+        r.accumulate(value, [&](int b) QMV_INLINE { return vr.sc[KIND == kKvF16 ? 0 : b]; }, s);
+      } else if constexpr (KIND == kKvF16) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) r.parts(t, s, u32x4{}, ph[t], pl[t]);
-        if (!wild) {
-#pragma unroll
-          for (int d = 0; d < DT; ++d) {
-            const u32x4 vop = vr.operand(d / 2, d & 1);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) r.add(t, d, vop, ph[t], pl[t]);
-          }
-        } else {
-#pragma unroll
-          for (int t = 0; t < MT; ++t)
-            r.add_wild(a, t, t0, ph[t], pl[t], [&](int d) QMV_INLINE { return vr.operand(d / 2, d & 1); });
-        }
-      } else {
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          u32x4 ph[MT], pl[MT];
-#pragma unroll
-          for (int t = 0; t < MT; ++t) r.parts(t, s, vr.sc[b], ph[t], pl[t]);
-#pragma unroll
-          for (int half = 0; half < 2; ++half) {
-            const u32x4 vop = vr.operand(b, half);
-#pragma unroll
-            for (int t = 0; t < MT; ++t) r.add(t, 2 * b + half, vop, ph[t], pl[t]);
-          }
-        }
+        for (int t = 0; t < MT; ++t) r.accumulate_wild(a, t, t0, value, s);
       }
     }
 
@@ -778,15 +814,8 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
       const StepLds<KIND, NB>& st = lds[buf];
       if (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1)) {   // some row sees some of it
         f32x4 s[MT][2];
-#pragma unroll
-        for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          u32x4 sc = {};
-          if constexpr (KIND != kKvF16) sc = *reinterpret_cast<const u32x4*>(&st.ksc[b][4 * g]);
-#pragma unroll
-          for (int mm = 0; mm < 2; ++mm) r.score(st.k[mm][b][lane], b, mm, sc, s);
-        }
+        r.scores([&](int mm, int b) QMV_INLINE { return st.k[mm][b][lane]; },
+                 [&](int b) QMV_INLINE { return *reinterpret_cast<const u32x4*>(&st.ksc[KIND == kKvF16 ? 0 : b][4 * g]); }, s);
         const bool whole = ok0 && ok1 && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
         bool wild = false;
         if (!whole) {
@@ -806,36 +835,14 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) r.weigh(t, e5, s);
-        if constexpr (KIND == kKvF16) {
-          u32x4 ph[MT], pl[MT];
+        const auto value = [&](int d) QMV_INLINE { return st.v[d][lane]; };
+        if (!wild) {
+          r.accumulate(value, [&](int b) QMV_INLINE {
+            return *reinterpret_cast<const u32x4*>(&st.vsc[KIND == kKvF16 ? 0 : b][4 * g]);
+          }, s);
+        } else if constexpr (KIND == kKvF16) {
 #pragma unroll
-          for (int t = 0; t < MT; ++t) r.parts(t, s, u32x4{}, ph[t], pl[t]);
-          if (!wild) {
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-              const u32x4 vop = st.v[d][lane];
-#pragma unroll
-              for (int t = 0; t < MT; ++t) r.add(t, d, vop, ph[t], pl[t]);
-            }
-          } else {
-#pragma unroll
-            for (int t = 0; t < MT; ++t)
-              r.add_wild(a, t, t0, ph[t], pl[t], [&](int d) QMV_INLINE { return st.v[d][lane]; });
-          }
-        } else {
-#pragma unroll
-          for (int b = 0; b < NB; ++b) {
-            const u32x4 sc = *reinterpret_cast<const u32x4*>(&st.vsc[b][4 * g]);
-            u32x4 ph[MT], pl[MT];
-#pragma unroll
-            for (int t = 0; t < MT; ++t) r.parts(t, s, sc, ph[t], pl[t]);
-#pragma unroll
-            for (int half = 0; half < 2; ++half) {
-              const u32x4 vop = st.v[2 * b + half][lane];
-#pragma unroll
-              for (int t = 0; t < MT; ++t) r.add(t, 2 * b + half, vop, ph[t], pl[t]);
-            }
-          }
+          for (int t = 0; t < MT; ++t) r.accumulate_wild(a, t, t0, value, s);
         }
       }
       if (more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
