@@ -47,7 +47,10 @@ constexpr int kAttnThreads = 256;
 constexpr int kStep = 32;                       // keys a step
 
 // K above: w d <= 2^(K - e) 2^(e - 14) for a quantized token, w <= 2^K (F16).
-__host__ __device__ constexpr float weight_shift(int kind) { return kind == kKvF16 ? 14.0f : 29.0f; }
+// M may lag the true maximum by kLag, so that O is rescaled a few times a
+// walk instead of at every new maximum; K leaves room for it.
+constexpr float kLag = 4.0f;
+__host__ __device__ constexpr float weight_shift(int kind) { return (kind == kKvF16 ? 14.0f : 29.0f) - kLag; }
 
 __device__ __forceinline__ f32x4 mfma_f16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
@@ -298,7 +301,11 @@ struct Place {
     // tiles of one sequence, head and range) get the same XCD and its L2.
     const int slot = blockIdx.x >> 3;
     int id = (slot / a.tiles) * 8 + (blockIdx.x & 7);
-    tile0 = a.tiles - 1 - slot % a.tiles;       // the longest rows first
+    // Later rows see more keys. The longest first; where all workgroups of the
+    // launch run at once, two a compute unit, the second half from the
+    // shortest on, so that a long one has a short one beside it.
+    const int j = slot % a.tiles, back = a.tiles - a.tiles / 2;
+    tile0 = gridDim.x <= 512 && j >= back ? j - back : a.tiles - 1 - j;
     if (id >= a.b.n_seqs * a.splits * a.b.n_kv_heads) return false;
     head = id % a.b.n_kv_heads;
     id /= a.b.n_kv_heads;
@@ -456,7 +463,7 @@ struct Rows {
       for (int j = 1; j < 8; ++j) top = fmaxf(top, fmaf(s[t][j / 4][j & 3], to_log2[t], e5[j]));
       top = row_max(top);
     }
-    if (__any(top > m[t])) {
+    if (__any(top > m[t] + kLag)) {
       top = fmaxf(m[t], top);
       const float al = __builtin_amdgcn_exp2f(m[t] - (top == -INFINITY ? 0.0f : top));
       l[t] *= al;

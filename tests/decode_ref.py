@@ -160,13 +160,14 @@ def attention_tolerance(out, mag, smax, v, D):
     keys, 32 a step, round (keys/32 + 4 + 9) times: matrix products add 8
     terms a lane group, 4 groups, 2 parts, then the joins. Below 2^-14 fp16
     has steps of 2^-24: a weight is off by 2^-25 in units in which the
-    largest is at least 2^14 (times the largest scale, quantized), which
-    leaves 2^-39 of the largest value a key."""
+    largest is at least 2^10 (times the largest scale, quantized; the
+    reference of the exponents may lag the maximum by 2^4), which leaves
+    2^-35 of the largest value a key."""
     keys = max(1, len(v))
     ds = smax * (2.0 ** -21 + (D + 4) * 2.0 ** -24)
     with np.errstate(over="ignore"):
         rel = 2 * np.expm1(ds) + 2.0 ** -22 + 2.0 ** -20 + (keys / 32 * 2 + 48) * 2.0 ** -24
-    low = 2.0 ** -39 * keys * np.abs(v).max(initial=0.0)
+    low = 2.0 ** -35 * keys * np.abs(v).max(initial=0.0)
     return mag * rel[..., None] + np.abs(out) * 2.0 ** -23 + low + 1e-30
 
 
