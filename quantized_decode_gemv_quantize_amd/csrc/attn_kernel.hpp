@@ -821,8 +821,12 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
       const StepLds<KIND, NB>& st = lds[buf];
       if (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1)) {   // some row sees some of it
         f32x4 s[MT][2];
+        // products first: of the two waves of a SIMD, one multiplies while the
+        // other weighs (639 -> 608 us, 2048 tokens over 8192)
+        __builtin_amdgcn_s_setprio(1);
         r.scores([&](int mm, int b) QMV_INLINE { return st.k[mm][b][lane]; },
                  [&](int b) QMV_INLINE { return *reinterpret_cast<const u32x4*>(&st.ksc[KIND == kKvF16 ? 0 : b][4 * g]); }, s);
+        __builtin_amdgcn_s_setprio(0);
         const bool whole = ok0 && ok1 && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
         bool wild = false;
         if (!whole) {
