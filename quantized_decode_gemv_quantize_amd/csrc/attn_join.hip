@@ -4,7 +4,7 @@
 
 namespace qmv {
 
-constexpr int kMaxSplits = 128;
+constexpr int kMaxSplits = 128;                 // at most the lanes of a join's workgroup
 constexpr int kSplitKeys = 256;                 // fewest keys worth a workgroup of their own
 constexpr int kTargetGroups = 512;              // two workgroups for each of the 256 compute units
 
@@ -24,8 +24,10 @@ AttnShape attn_shape(int kind, int nb, int n_seqs, int n_kv_heads, int group, in
   const int64_t groups = static_cast<int64_t>(n_seqs) * n_kv_heads * s.tiles;
   const int64_t keys = window > 0 && window + static_cast<int64_t>(max_new) < max_len
                            ? window + static_cast<int64_t>(max_new) : max_len;
-  int64_t splits = (kTargetGroups + groups - 1) / groups;
-  const int64_t most = (keys + kSplitKeys - 1) / kSplitKeys;
+  const char* e1=getenv("ATG"); const char* e2=getenv("ASK");
+  const int tg=e1?atoi(e1):kTargetGroups, sk=e2?atoi(e2):kSplitKeys;
+  int64_t splits = (tg + groups - 1) / groups;
+  const int64_t most = (keys + sk - 1) / sk;
   if (splits > most) splits = most;
   if (splits > kMaxSplits) splits = kMaxSplits;
   s.splits = static_cast<int>(splits < 1 ? 1 : splits);
@@ -38,21 +40,21 @@ __global__ void __launch_bounds__(kAttnThreads) attn_join_kernel(AttnArgs a) {
   constexpr int L = D / 4, P = kAttnThreads / L;   // lanes a share, shares
   __shared__ float2 ml[kMaxSplits];
   __shared__ float acc_s[P * D];
-  const int tid = threadIdx.x, token = blockIdx.x, head = blockIdx.y;
-  int row0 = a.b.token_start[0], row1 = a.b.token_start[a.b.n_seqs];
-  if (token < row0 || token >= row1) return;
-  const int64_t at = (static_cast<int64_t>(token) * a.n_heads + head) * a.splits;
-  for (int i = tid; i < a.splits; i += kAttnThreads) ml[i] = a.part_ml[at + i];
+  const int tid = threadIdx.x, token = blockIdx.x, head = blockIdx.y, splits = static_cast<int>(a.splits.d);
+  const int64_t at = (static_cast<int64_t>(token) * a.n_heads + head) * splits;
+  const int row0 = a.b.token_start[0], row1 = a.b.token_start[a.b.n_seqs];
+  if (tid < splits) ml[tid] = a.part_ml[at + tid];   // (of a row outside, whatever is there)
   __syncthreads();
+  if (token < row0 || token >= row1) return;
   float m = -INFINITY;
-  for (int i = 0; i < a.splits; ++i) m = fmaxf(m, ml[i].x);
+  for (int i = 0; i < splits; ++i) m = fmaxf(m, ml[i].x);
   const float from = m == -INFINITY ? 0.0f : m;
   float l = 0.0f;
-  for (int i = 0; i < a.splits; ++i) l = fmaf(ml[i].y, __builtin_amdgcn_exp2f(ml[i].x - from), l);
+  for (int i = 0; i < splits; ++i) l = fmaf(ml[i].y, __builtin_amdgcn_exp2f(ml[i].x - from), l);
   const int d = 4 * (tid % L), share = tid / L;
   f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
   if (share < P)
-    for (int i = share; i < a.splits; i += P) {
+    for (int i = share; i < splits; i += P) {
       const float f = __builtin_amdgcn_exp2f(ml[i].x - from);
       const f32x4 x = *reinterpret_cast<const f32x4*>(a.part_o + (at + i) * D + d);
 #pragma unroll

@@ -30,7 +30,7 @@
 // (the cache is the traffic, nothing would be shared) and join O through
 // LDS; with many rows each wave has rows of its own, and the workgroup turns
 // each step's codes into operands once, in LDS, for all four. Either way the
-// keys can be cut into a.splits ranges whose partial (M, l, O) a second
+// keys can be cut into ranges whose partial (M, l, O) a second
 // launch joins, so that few rows over a long cache still fill the chip.
 #pragma once
 
@@ -245,24 +245,46 @@ struct ValueRegs {
   }
 };
 
-// Where the units of a 32-key step lie; 16-token halves may be holes.
+// Table entries of a 32-key step's two 16-token halves, read a step ahead of
+// its loads. They stay in vector registers as they come (`zero` keeps the
+// compiler from seeing that they are the same in all lanes): turned into
+// scalars at once they would make the wave wait for every load in flight.
+struct StepIds {
+  int id[2];
+};
+
+__device__ __forceinline__ int vector_zero() {
+  int z;
+  asm("v_mov_b32 %0, 0" : "=v"(z));
+  return z;
+}
+
+__device__ __forceinline__ StepIds step_ids(const AttnArgs& a, int s, int t0, int zero) {
+  const int32_t* row = a.b.page_table + static_cast<int64_t>(s) * a.b.table_stride;
+  const int last = a.b.pages_per_seq - 1, p0 = t0 >> a.b.page_shift, p1 = (t0 + 16) >> a.b.page_shift;
+  return StepIds{{row[(p0 < last ? p0 : last) + zero], row[(p1 < last ? p1 : last) + zero]}};
+}
+
+// Where the units of a step's halves lie, from the cache's start; a half may
+// be a hole.
 struct StepPages {
-  const uint8_t* k[2];
-  const uint8_t* v[2];
+  int64_t off[2];
   bool ok[2];
 };
 
 template <int KIND, int NB>
-__device__ __forceinline__ StepPages step_pages(const AttnArgs& a, int s, int head, int t0) {
+__device__ __forceinline__ StepPages step_pages(const AttnArgs& a, StepIds ids, int head, int t0) {
   constexpr int U = kv_unit_bytes(KIND, NB);
+  const int upp = 1 << (a.b.page_shift - 4);
+  const uint32_t page_bytes = static_cast<uint32_t>(a.b.n_kv_heads * upp) * U;   // 2^29 at most
   StepPages p;
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
-    const int pos = t0 + 16 * h, page = a.b.page(s, pos);
-    p.ok[h] = page >= 0;
-    const int64_t off = a.b.unit(page < 0 ? 0 : page, head, pos) * U;   // a hole's loads go to page 0 and are masked
-    p.k[h] = a.k + off;
-    p.v[h] = a.v + off;
+    const int pos = t0 + 16 * h;
+    p.ok[h] = (pos >> a.b.page_shift) < a.b.pages_per_seq && static_cast<uint32_t>(ids.id[h]) < static_cast<uint32_t>(a.b.n_pages);
+    const uint32_t page = p.ok[h] ? static_cast<uint32_t>(ids.id[h]) : 0u;   // a hole's loads go to page 0 and are masked
+    p.off[h] = static_cast<int64_t>(static_cast<uint64_t>(page) * page_bytes +
+                                    static_cast<uint32_t>(head * upp + ((pos >> 4) & (upp - 1))) * U);
   }
   return p;
 }
@@ -282,10 +304,10 @@ __device__ __forceinline__ float row_factor(const AttnArgs& a, int head, float m
 template <int D, class W>
 __device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head, int split, float m, float l,
                                           float shift, W write, bool lead) {
-  if (a.splits == 1) {
+  if (a.splits.d == 1) {
     write(a.out + token * a.ldo + static_cast<int64_t>(head) * D, row_factor(a, head, m, l, shift));
   } else {
-    const int64_t at = (static_cast<int64_t>(token) * a.n_heads + head) * a.splits + split;
+    const int64_t at = (static_cast<int64_t>(token) * a.n_heads + head) * static_cast<int>(a.splits.d) + split;
     write(a.part_o + at * D, 1.0f);
     if (lead) a.part_ml[at] = make_float2(m, l);
   }
@@ -300,33 +322,34 @@ struct Place {
     // Workgroups go to the 8 XCDs in turn: those that read the same keys (the
     // tiles of one sequence, head and range) get the same XCD and its L2.
     const int slot = blockIdx.x >> 3;
-    int id = (slot / a.tiles) * 8 + (blockIdx.x & 7);
+    const int slot_group = a.tiles.div(slot), tiles = static_cast<int>(a.tiles.d);
+    int id = slot_group * 8 + static_cast<int>(blockIdx.x & 7);
     // Later rows see more keys. The longest first; where all workgroups of the
     // launch run at once, two a compute unit, the second half from the
     // shortest on, so that a long one has a short one beside it.
-    const int j = slot % a.tiles, back = a.tiles - a.tiles / 2;
-    tile0 = gridDim.x <= 512 && j >= back ? j - back : a.tiles - 1 - j;
-    if (id >= a.b.n_seqs * a.splits * a.b.n_kv_heads) return false;
-    head = id % a.b.n_kv_heads;
-    id /= a.b.n_kv_heads;
-    split = id % a.splits;
-    s = id / a.splits;
-    a.b.rows(s, first, count);
-    const int l = a.b.seq_len[s];
+    const int j = slot - slot_group * tiles, back = tiles - tiles / 2;
+    tile0 = gridDim.x <= 512 && j >= back ? j - back : tiles - 1 - j;
+    const int per_head = a.heads.div(id);
+    head = id - per_head * static_cast<int>(a.heads.d);
+    s = a.splits.div(per_head);
+    split = per_head - s * static_cast<int>(a.splits.d);
+    if (s >= a.b.n_seqs) return false;
+    const int from = a.b.token_start[s], to = a.b.token_start[s + 1], l = a.b.seq_len[s];
+    a.b.clamp_rows(from, to, first, count);
     len = l < 0 ? 0 : l > (1 << 30) ? (1 << 30) : l;
     const int64_t table_end = static_cast<int64_t>(a.b.pages_per_seq) << a.b.page_shift;
     keys = len < table_end ? len : static_cast<int>(table_end);
-    rows = count * a.group;                     // n_tokens * n_heads <= 2^30
+    rows = count * static_cast<int>(a.group.d);   // n_tokens * n_heads <= 2^30
     base = len - count;
     return true;
   }
   // The split's range of the keys that rows r0..r1 see, in whole steps.
   __device__ __forceinline__ void range(const AttnArgs& a, int r0, int r1, int& beg, int& end) const {
-    const int lo = base + r0 / a.group, hi = base + r1 / a.group;
+    const int lo = base + a.group.div(r0), hi = base + a.group.div(r1);
     const int k_end = hi + 1 < keys ? hi + 1 : keys;
     const int k_beg = a.window > 0 && lo - a.window + 1 > 0 ? (lo - a.window + 1) & ~(kStep - 1) : 0;
     const int steps = k_end > k_beg ? (k_end - k_beg + kStep - 1) / kStep : 0;
-    const int per = (steps + a.splits - 1) / a.splits;
+    const int per = a.splits.div(steps + static_cast<int>(a.splits.d) - 1);
     const int s0 = split * per < steps ? split * per : steps, s1 = s0 + per < steps ? s0 + per : steps;
     beg = k_beg + s0 * kStep;
     end = k_beg + s1 * kStep;
@@ -350,7 +373,8 @@ struct Rows {
     for (int t = 0; t < MT; ++t) {
       const int row = row0 + 16 * t + col;
       const bool live = row < w.rows;
-      const int tok = live ? row / a.group : 0, hd = w.head * a.group + (live ? row - tok * a.group : 0);
+      const int group = static_cast<int>(a.group.d), tok = live ? a.group.div(row) : 0;
+      const int hd = w.head * group + (live ? row - tok * group : 0);
       qpos[t] = live ? w.base + tok : -1;
       const float* src = a.q + (w.first + tok) * a.ldq + static_cast<int64_t>(hd) * (32 * NB);
       float v[NB][8], top = 0.0f;
@@ -550,40 +574,45 @@ struct Rows {
 // Few rows: the waves share the keys.
 template <int KIND, int NB, int MT>
 __global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_kernel(AttnArgs a) {
-  constexpr int D = 32 * NB, DT = 2 * NB, RW = 16 * MT;
-  __shared__ float lds_o[4 * RW * D];
+  constexpr int D = 32 * NB, DT = 2 * NB, RW = 16 * MT, DP = D + 4;   // rows a bank apart
+  __shared__ __attribute__((aligned(16))) float lds_o[4 * RW * DP];
   __shared__ float lds_ml[4 * RW * 2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
   Place w;
   if (!w.find(a)) return;
-  for (int tile = w.tile0; tile * RW < w.rows; tile += a.tiles) {
+  for (int tile = w.tile0; tile * RW < w.rows; tile += static_cast<int>(a.tiles.d)) {
     const int row0 = tile * RW, row1 = (row0 + RW < w.rows ? row0 + RW : w.rows) - 1;
     int t_beg, t_end;
     w.range(a, row0, row1, t_beg, t_end);
-    const int lo = w.base + row0 / a.group, hi = w.base + row1 / a.group;
-    Rows<KIND, NB, MT> r;
-    r.init(a, w, row0);
+    const int lo = w.base + a.group.div(row0), hi = w.base + a.group.div(row1);
     int t0 = t_beg + wave * kStep;
     KeyRegs<KIND, NB> kr;
     StepPages pg;
+    StepIds next;
+    const int zero = vector_zero();
     const int kh = col >> 3, vh = g >> 1;       // halves of the step: of the lane's key row, of its tokens
     if (t0 < t_end) {
-      pg = step_pages<KIND, NB>(a, w.s, w.head, t0);
-      kr.load(kh ? pg.k[1] : pg.k[0], vh ? pg.k[1] : pg.k[0]);
+      const StepIds ids = step_ids(a, w.s, t0, zero);
+      next = step_ids(a, w.s, t0 + 4 * kStep, zero);
+      pg = step_pages<KIND, NB>(a, ids, w.head, t0);
+      kr.load(a.k + (kh ? pg.off[1] : pg.off[0]), a.k + (vh ? pg.off[1] : pg.off[0]));
     }
+    Rows<KIND, NB, MT> r;
+    r.init(a, w, row0);
     for (; t0 < t_end; t0 += 4 * kStep) {
       ValueRegs<KIND, NB> vr;
-      vr.load(vh ? pg.v[1] : pg.v[0]);
+      vr.load(a.v + (vh ? pg.off[1] : pg.off[0]));
       f32x4 s[MT][2];
       r.scores([&](int mm, int b) QMV_INLINE { return kr.operand(mm, b); },
                [&](int b) QMV_INLINE { return kr.sc[KIND == kKvF16 ? 0 : b]; }, s);
       const bool ok0 = pg.ok[0], ok1 = pg.ok[1];
       if (t0 + 4 * kStep < t_end) {
-        pg = step_pages<KIND, NB>(a, w.s, w.head, t0 + 4 * kStep);
-        kr.load(kh ? pg.k[1] : pg.k[0], vh ? pg.k[1] : pg.k[0]);
+        pg = step_pages<KIND, NB>(a, next, w.head, t0 + 4 * kStep);
+        kr.load(a.k + (kh ? pg.off[1] : pg.off[0]), a.k + (vh ? pg.off[1] : pg.off[0]));
+        next = step_ids(a, w.s, t0 + 8 * kStep, zero);
       }
       // steps that every row sees whole need no masks
-      const bool whole = ok0 && ok1 && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
+      const bool whole = __all(ok0 && ok1) && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
       bool wild = false;
       if (!whole) {
         const int real = (vh ? ok1 : ok0) ? w.keys - (t0 + 8 * g) : 0;   // tokens of this lane that exist
@@ -616,7 +645,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_k
       }
 #pragma unroll
       for (int d = 0; d < DT; ++d)
-        *reinterpret_cast<f32x4*>(&lds_o[(wave * RW + 16 * t + col) * D + 16 * d + 4 * g]) = r.o[t][d];
+        *reinterpret_cast<f32x4*>(&lds_o[(wave * RW + 16 * t + col) * DP + 16 * d + 4 * g]) = r.o[t][d];
     }
     __syncthreads();
     for (int it = threadIdx.x; it < RW * (D / 4); it += kAttnThreads) {
@@ -632,11 +661,11 @@ __global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_k
       for (int v = 0; v < 4; ++v) {
         const float f = __builtin_amdgcn_exp2f(lds_ml[(v * RW + rr) * 2] - from);
         ls = fmaf(lds_ml[(v * RW + rr) * 2 + 1], f, ls);
-        const f32x4 x = *reinterpret_cast<const f32x4*>(&lds_o[(v * RW + rr) * D + d]);
+        const f32x4 x = *reinterpret_cast<const f32x4*>(&lds_o[(v * RW + rr) * DP + d]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[i] = fmaf(x[i], f, acc[i]);
       }
-      const int tok = row / a.group, hd = w.head * a.group + row - tok * a.group;
+      const int tok = a.group.div(row), hd = (w.head - tok) * static_cast<int>(a.group.d) + row;
       store_row<D>(a, w.first + tok, hd, w.split, mx, ls, weight_shift(KIND), [&](float* dst, float f) QMV_INLINE {
         float v[4];
 #pragma unroll
@@ -670,8 +699,8 @@ struct StepRegs {
   uint16_t es[KIND == kKvF16 ? 1 : NB];         // lanes 0..31: the token's value scales
   bool ok[2];
 
-  __device__ __forceinline__ void load(const AttnArgs& a, int s, int head, int t0) {
-    const StepPages pg = step_pages<KIND, NB>(a, s, head, t0);
+  __device__ __forceinline__ void load(const AttnArgs& a, StepIds ids, int head, int t0) {
+    const StepPages pg = step_pages<KIND, NB>(a, ids, head, t0);
     ok[0] = pg.ok[0];
     ok[1] = pg.ok[1];
     const int tid = threadIdx.x;
@@ -680,7 +709,7 @@ struct StepRegs {
       const int it = tid + i * kAttnThreads;
       if (NB * kWave % kAttnThreads && it >= NB * kWave) break;
       const int b = it >> 6, at = it & 63, g = at >> 4, row = at & 15;
-      const uint8_t* ku = row >> 3 ? pg.k[1] : pg.k[0];
+      const uint8_t* ku = a.k + (row >> 3 ? pg.off[1] : pg.off[0]);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
         constexpr int PS = kv_piece(KIND, NB), NP = kv_lane_bytes(KIND, NB) / PS;
@@ -698,7 +727,7 @@ struct StepRegs {
           k[i][m][0] = ld_u32(src);
         }
       }
-      const uint8_t* vu = (g >> 1 ? pg.v[1] : pg.v[0]);
+      const uint8_t* vu = a.v + (g >> 1 ? pg.off[1] : pg.off[0]);
       if constexpr (KIND == kKvF16) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -719,20 +748,21 @@ struct StepRegs {
     if constexpr (KIND != kKvF16) {
       if (tid < 16 * NB) {
         const int b = tid >> 4, word = tid & 15, at = kv_scale_at(KIND, NB, b, 2 * (word & 7));
-        ksc = ld_u32((word >> 3 ? pg.k[1] : pg.k[0]) + at);
-        vsc = ld_u32((word >> 3 ? pg.v[1] : pg.v[0]) + at);
+        const int64_t off = (word >> 3 ? pg.off[1] : pg.off[0]) + at;
+        ksc = ld_u32(a.k + off);
+        vsc = ld_u32(a.v + off);
       }
       if (tid < kStep) {
 #pragma unroll
         for (int b = 0; b < NB; ++b)
-          es[b] = static_cast<uint16_t>(ld_u16((tid >> 4 ? pg.v[1] : pg.v[0]) + kv_scale_at(KIND, NB, b, tid & 15)));
+          es[b] = static_cast<uint16_t>(ld_u16(a.v + (tid >> 4 ? pg.off[1] : pg.off[0]) + kv_scale_at(KIND, NB, b, tid & 15)));
       }
     }
   }
 
   __device__ __forceinline__ void store(StepLds<KIND, NB>& lds, int t0, int keys) {
     const int tid = threadIdx.x;
-    const bool part = !ok[0] || !ok[1] || t0 + kStep > keys;   // slots without a token
+    const bool part = !__all(ok[0] && ok[1]) || t0 + kStep > keys;   // slots without a token
     uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < kItems; ++i) {
@@ -798,26 +828,33 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
   Place w;
   if (!w.find(a)) return;
-  for (int tile = w.tile0; tile * RT < w.rows; tile += a.tiles) {
+  for (int tile = w.tile0; tile * RT < w.rows; tile += static_cast<int>(a.tiles.d)) {
     const int row0 = tile * RT + wave * RW;
     int t_beg, t_end;
     w.range(a, tile * RT, (tile * RT + RT < w.rows ? tile * RT + RT : w.rows) - 1, t_beg, t_end);
     // positions of the wave's first and last row; lo > hi where it has none
-    const int lo = row0 < w.rows ? w.base + row0 / a.group : 1;
-    const int hi = row0 < w.rows ? w.base + ((row0 + RW < w.rows ? row0 + RW : w.rows) - 1) / a.group : 0;
+    const int lo = row0 < w.rows ? w.base + a.group.div(row0) : 1;
+    const int hi = row0 < w.rows ? w.base + a.group.div((row0 + RW < w.rows ? row0 + RW : w.rows) - 1) : 0;
+    StepRegs<KIND, NB> in;
+    StepIds next;
+    const int zero = vector_zero();
+    if (t_beg < t_end) {
+      const StepIds ids = step_ids(a, w.s, t_beg, zero);
+      next = step_ids(a, w.s, t_beg + kStep, zero);
+      in.load(a, ids, w.head, t_beg);
+    }
     Rows<KIND, NB, MT> r;
     r.init(a, w, row0);
-    StepRegs<KIND, NB> in;
     __syncthreads();                            // the tile before is done with LDS
-    if (t_beg < t_end) {
-      in.load(a, w.s, w.head, t_beg);
-      in.store(lds[0], t_beg, w.keys);
-    }
+    if (t_beg < t_end) in.store(lds[0], t_beg, w.keys);
     __syncthreads();
     int buf = 0;
     for (int t0 = t_beg; t0 < t_end; t0 += kStep, buf ^= 1) {
       const bool ok0 = in.ok[0], ok1 = in.ok[1], more = t0 + kStep < t_end;
-      if (more) in.load(a, w.s, w.head, t0 + kStep);
+      if (more) {
+        in.load(a, next, w.head, t0 + kStep);
+        next = step_ids(a, w.s, t0 + 2 * kStep, zero);
+      }
       const StepLds<KIND, NB>& st = lds[buf];
       if (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1)) {   // some row sees some of it
         f32x4 s[MT][2];
@@ -827,7 +864,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
         r.scores([&](int mm, int b) QMV_INLINE { return st.k[mm][b][lane]; },
                  [&](int b) QMV_INLINE { return *reinterpret_cast<const u32x4*>(&st.ksc[KIND == kKvF16 ? 0 : b][4 * g]); }, s);
         __builtin_amdgcn_s_setprio(0);
-        const bool whole = ok0 && ok1 && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
+        const bool whole = __all(ok0 && ok1) && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
         bool wild = false;
         if (!whole) {
           const int real = (g >> 1 ? ok1 : ok0) ? w.keys - (t0 + 8 * g) : 0;
@@ -864,7 +901,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
       const float l = row_sum(r.l[t]);
       const int row = row0 + 16 * t + col;
       if (row >= w.rows) continue;
-      const int tok = row / a.group, hd = w.head * a.group + row - tok * a.group;
+      const int tok = a.group.div(row), hd = (w.head - tok) * static_cast<int>(a.group.d) + row;
       store_row<D>(a, w.first + tok, hd, w.split, r.m[t], l, weight_shift(KIND), [&](float* dst, float f) QMV_INLINE {
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -880,8 +917,8 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
 
 template <int KIND, int NB, int MT, bool ROWS>
 int launch_attn_as(const AttnArgs& a, hipStream_t st) {
-  const int64_t groups = static_cast<int64_t>(a.b.n_seqs) * a.splits * a.b.n_kv_heads;
-  const int64_t grid = (groups + 7) / 8 * 8 * a.tiles;
+  const int64_t groups = static_cast<int64_t>(a.b.n_seqs) * a.splits.d * a.b.n_kv_heads;
+  const int64_t grid = (groups + 7) / 8 * 8 * a.tiles.d;
   if (grid > (1 << 23)) return MMVQ_ERR_SHAPE;   // 2^32 lanes in a launch
   const dim3 g(static_cast<unsigned>(grid)), b(kAttnThreads);
   if constexpr (ROWS) hipLaunchKernelGGL((attn_rows_kernel<KIND, NB, MT>), g, b, 0, st, a);

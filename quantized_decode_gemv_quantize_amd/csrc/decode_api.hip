@@ -201,10 +201,11 @@ int mmvq_attn(const mmvq_kv_cache* cache, const mmvq_kv_batch* batch, const floa
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * M_LOG2E);
   a.window = window;
   a.n_heads = n_heads;
-  a.group = n_heads / cache->n_kv_heads;
+  a.group = FastDiv(static_cast<uint32_t>(n_heads / cache->n_kv_heads));
+  a.heads = FastDiv(static_cast<uint32_t>(cache->n_kv_heads));
   a.head_dim = cache->head_dim;
-  a.tiles = s.tiles;
-  a.splits = s.splits;
+  a.tiles = FastDiv(static_cast<uint32_t>(s.tiles));
+  a.splits = FastDiv(static_cast<uint32_t>(s.splits));
   a.part_o = static_cast<float*>(workspace);
   a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(batch->n_tokens) * n_heads * s.splits * cache->head_dim);
   const hipStream_t st = static_cast<hipStream_t>(stream);

@@ -10,6 +10,24 @@
 
 namespace qmv {
 
+// Division of 0 <= n < 2^31 by a number that the host knows: the multiplier
+// is ceil(2^32 (2^s - d) / d) + ..., the usual round-up form. A 32-bit division
+// on the device is some forty dependent instructions, and a workgroup's place
+// takes a dozen of them before its first load.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  FastDiv() = default;
+  explicit FastDiv(uint32_t n) : d(n), mul(0), shift(0) {
+    while ((uint64_t(1) << shift) < n) ++shift;
+    mul = static_cast<uint32_t>((((uint64_t(1) << shift) - n) << 32) / n + 1);
+  }
+#ifndef QMV_HOST_MODEL
+  __device__ __forceinline__ int div(int n) const {
+    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
+  }
+#endif
+};
+
 // Ragged batch and page geometry on the device side; the checks of the
 // values that the host cannot see are here.
 struct BatchArgs {
@@ -23,7 +41,9 @@ struct BatchArgs {
 
   // First row and row count of sequence s, inside the activation buffers.
   __device__ __forceinline__ void rows(int s, int& first, int& count) const {
-    const int a = token_start[s], b = token_start[s + 1];
+    clamp_rows(token_start[s], token_start[s + 1], first, count);
+  }
+  __device__ __forceinline__ void clamp_rows(int a, int b, int& first, int& count) const {
     first = a < 0 ? 0 : a > n_tokens ? n_tokens : a;
     const int end = b > n_tokens ? n_tokens : b;
     count = end > first ? end - first : 0;
@@ -58,7 +78,8 @@ struct AttnArgs {
   const float* sinks;
   int64_t ldq, ldo;
   float scale_log2;        // scale * log2(e)
-  int window, n_heads, group, head_dim, tiles, splits;
+  int window, n_heads, head_dim;
+  FastDiv group, tiles, splits, heads;   // query heads a key/value head, ..., key/value heads
   float* part_o;           // [row][head][split][head_dim]
   float2* part_ml;         // [row][head][split]
 };
