@@ -1,18 +1,23 @@
 // verify.hip - verification of drafted tokens (speculative sampling).
 //
-// Three launches over the target's rows, cut into chunks of kChunk logits:
+// Launches over the target's rows, cut into chunks of kChunk logits:
 //   stats    per row and chunk: largest logit, its lowest index, and the sum
 //            of e_i = exp((l_i - largest) / T) (or of the weights);
-//   decide   per sequence: the rows' sums joined over the chunks, the drafts
-//            accepted one after the other, and per chunk the sums of the
-//            weights to draw from, max(e_i - q_i Z, 0) and e_i;
+//   decide   per sequence: the rows' sums joined over the chunks, and the
+//            drafts accepted one after the other;
 //   draw     per sequence: the chunk and then the index in which the running
-//            sum passes u * total.
+//            sum of the weights passes u * total.
+// Without draft probabilities decide and draw are one launch of a workgroup a
+// sequence: the weights to draw from are e_i but for the refused token, so
+// the chunks' sums are known but for one. With them, max(e_i - q_i Z, 0) has
+// to be summed over the row first: the decide launch has a workgroup a chunk,
+// each of which joins the sums for itself, and draw follows.
+//
 // Everything that a token depends on is in 64 bits: with 10^5 logits a
 // running sum in 32 bits moves a border by more than the probability of many
 // tokens. The stats launch reads every row once and is bound by that read
-// and by the 64-bit exponentials; the other two read one row a sequence
-// again, mostly from cache.
+// with the exponentials beside it (22 64-bit operations each, 2^f by its
+// Taylor polynomial); the others are short chains of latencies.
 #include "decode_args.hpp"
 #include "launch.hpp"
 
@@ -33,8 +38,7 @@ struct SeqSum {
 struct Decision {
   int row, taken, last, best;                  // row drawn from (-1: none)
   float top;
-  int pad;
-  double z, inv_t;                             // inv_t 0: greedy
+  double z;
 };
 
 __device__ __forceinline__ RowStat* row_stats(const VerifyArgs& a) { return reinterpret_cast<RowStat*>(a.ws); }
@@ -52,44 +56,99 @@ int64_t verify_bytes(int n_seqs, int n_rows, int vocab, int* chunks) {
          n_seqs * static_cast<int64_t>(sizeof(Decision));
 }
 
-// 1/T of a sequence; 0 for a greedy one.
-__device__ __forceinline__ double inv_temperature(const VerifyArgs& a, int s) {
-  if (!a.temperature) return 1.0;
+// A sequence's temperature: log2(e) / T, and whether it is greedy (T = +inf
+// gives a rate of 0, too: a softmax of equal weights, not a greedy row).
+struct Heat {
+  double rate;
+  bool greedy;
+};
+__device__ __forceinline__ Heat heat_of(const VerifyArgs& a, int s) {
+  constexpr double kLog2e = 1.4426950408889634073599246810019;
+  if (!a.temperature) return Heat{kLog2e, false};
   const float t = a.temperature[s];
-  return t > 0.0f ? 1.0 / static_cast<double>(t) : 0.0;
+  return Heat{t > 0.0f ? kLog2e / static_cast<double>(t) : 0.0, !(t > 0.0f)};
 }
-// T = +inf gives 1/T = 0, too: a softmax of equal weights, not a greedy row.
-__device__ __forceinline__ bool greedy(const VerifyArgs& a, int s) {
-  return a.kind == MMVQ_TARGET_LOGITS && a.temperature && !(a.temperature[s] > 0.0f);
+
+// 2^t for t <= 0: the integer part by rounding in the sum with 1.5 * 2^52, 2^f
+// of the rest, |f| <= 1/2, by the Taylor polynomial of degree 12 of
+// exp(f ln 2): its next term is below 2 10^-16.
+__device__ __forceinline__ double exp2_neg(double t) {
+  constexpr double kLn2 = 0.69314718055994530941723212145818;
+  constexpr double kRound = 6755399441055744.0;
+  t = fmax(t, -1080.0);                        // below the smallest double
+  const double k = t + kRound, f = t - (k - kRound);
+  double p = 0.0, c = 1.0, cs[13];
+#pragma unroll
+  for (int i = 0; i <= 12; ++i) {
+    cs[i] = c;
+    c = c * kLn2 / (i + 1);
+  }
+#pragma unroll
+  for (int i = 12; i >= 0; --i) p = fma(p, f, cs[i]);
+  return __builtin_ldexp(p, static_cast<int>(__double2loint(k)));
 }
 
 // Unnormalised weight of element i of a row whose largest logit is `top` (at
 // its lowest index `best`).
-__device__ __forceinline__ double weight(const VerifyArgs& a, float v, int i, float top, int best, double inv_t,
-                                         bool greedy_row) {
+__device__ __forceinline__ double weight(const VerifyArgs& a, float v, int i, float top, int best, Heat h) {
   if (a.kind == MMVQ_TARGET_WEIGHTS) return v > 0.0f && v < INFINITY ? static_cast<double>(v) : 0.0;
-  if (greedy_row) return i == best ? 1.0 : 0.0;
-  if (!(v > -INFINITY)) return 0.0;            // -inf, NaN
-  if (v == top) return 1.0;                    // +inf among them
-  if (top == INFINITY) return 0.0;
-  return exp((static_cast<double>(v) - static_cast<double>(top)) * inv_t);
+  if (h.greedy) return i == best ? 1.0 : 0.0;
+  // -inf and NaN have none; +inf ones share all of it
+  const bool none = !(v > -INFINITY) || (top == INFINITY && v != top);
+  const double d = v == top ? 0.0 : static_cast<double>(v) - static_cast<double>(top);
+  const double e = exp2_neg(d * h.rate);
+  return none ? 0.0 : e;
 }
 
 // A probability of the draft; what is not positive counts as 0.
 __device__ __forceinline__ double draft_weight(float q) { return q > 0.0f ? static_cast<double>(q) : 0.0; }
 
+template <int CTRL>
+__device__ __forceinline__ int dpp_i(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp_d(double v) {
+  return __hiloint2double(dpp_i<CTRL>(__double2hiint(v)), dpp_i<CTRL>(__double2loint(v)));
+}
+// Partner across lane bit 5 (MASK 32) or 4 (MASK 16).
+template <int MASK>
+__device__ __forceinline__ uint32_t swap_partner(uint32_t v) {
+  if constexpr (MASK == 32) {
+    const auto r = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return lane_id() & 32 ? r[0] : r[1];
+  } else {
+    const auto r = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    return lane_id() & 16 ? r[0] : r[1];
+  }
+}
+template <int MASK>
+__device__ __forceinline__ double swap_d(double v) {
+  return __hiloint2double(static_cast<int>(swap_partner<MASK>(static_cast<uint32_t>(__double2hiint(v)))),
+                          static_cast<int>(swap_partner<MASK>(static_cast<uint32_t>(__double2loint(v)))));
+}
+// Over the wave, the same in all lanes.
 __device__ __forceinline__ double wave_sum(double v) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+  v += dpp_d<kDppXor1>(v);
+  v += dpp_d<kDppXor2>(v);
+  v += dpp_d<kDppMirror8>(v);
+  v += dpp_d<kDppMirror16>(v);
+  v += swap_d<16>(v);
+  v += swap_d<32>(v);
   return v;
 }
+__device__ __forceinline__ void take_top(float& top, int& at, float t, int i) {
+  const bool take = t > top || (t == top && i < at);
+  top = take ? t : top;
+  at = take ? i : at;
+}
 __device__ __forceinline__ void wave_top(float& top, int& at) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) {
-    const float t = __shfl_xor(top, m);
-    const int i = __shfl_xor(at, m);
-    if (t > top || (t == top && i < at)) { top = t; at = i; }
-  }
+  take_top(top, at, dpp_f<kDppXor1>(top), dpp_i<kDppXor1>(at));
+  take_top(top, at, dpp_f<kDppXor2>(top), dpp_i<kDppXor2>(at));
+  take_top(top, at, dpp_f<kDppMirror8>(top), dpp_i<kDppMirror8>(at));
+  take_top(top, at, dpp_f<kDppMirror16>(top), dpp_i<kDppMirror16>(at));
+  take_top(top, at, __uint_as_float(swap_partner<16>(__float_as_uint(top))), static_cast<int>(swap_partner<16>(static_cast<uint32_t>(at))));
+  take_top(top, at, __uint_as_float(swap_partner<32>(__float_as_uint(top))), static_cast<int>(swap_partner<32>(static_cast<uint32_t>(at))));
 }
 
 // The sequence that row r belongs to, -1 for none: the last one that starts
@@ -162,11 +221,10 @@ __global__ void __launch_bounds__(kVThreads) verify_stats_kernel(VerifyArgs a) {
     } else {
       __syncthreads();
     }
-    const bool gr = greedy(a, s);
-    const double inv_t = inv_temperature(a, s);
-    if (!gr) {
+    const Heat h = heat_of(a, s);
+    if (!h.greedy) {
 #pragma unroll
-      for (int k = 0; k < kVPer; ++k) sum += weight(a, v[k], 0, top, 0, inv_t, false);
+      for (int k = 0; k < kVPer; ++k) sum += weight(a, v[k], 0, top, 0, h);
       sum = wave_sum(sum);
       if ((tid & 63) == 0) sums[wave] = sum;
     }
@@ -175,142 +233,132 @@ __global__ void __launch_bounds__(kVThreads) verify_stats_kernel(VerifyArgs a) {
       RowStat st;
       st.top = top;
       st.at = at;
-      st.sum = gr ? 0.0 : sums[0] + sums[1] + sums[2] + sums[3];
+      st.sum = h.greedy ? 0.0 : sums[0] + sums[1] + sums[2] + sums[3];
       row_stats(a)[static_cast<int64_t>(r) * a.chunks + c] = st;
     }
   }
 }
 
 // A row's chunks joined, by one wave: the same in all lanes.
-__device__ __forceinline__ void join_row(const VerifyArgs& a, int r, double inv_t, bool gr, float& top, int& at, double& z) {
+__device__ __forceinline__ double chunk_scale(const VerifyArgs& a, float chunk_top, float top, Heat h) {
+  if (a.kind == MMVQ_TARGET_WEIGHTS || chunk_top == top) return 1.0;
+  if (!(chunk_top > -INFINITY) || top == INFINITY) return 0.0;
+  return exp2_neg((static_cast<double>(chunk_top) - static_cast<double>(top)) * h.rate);
+}
+__device__ __forceinline__ void join_row(const VerifyArgs& a, int r, Heat h, float& top, int& at, double& z) {
   const RowStat* st = row_stats(a) + static_cast<int64_t>(r) * a.chunks;
   top = -INFINITY;
   at = 0x7fffffff;
   z = 0.0;
+  const RowStat none{-INFINITY, 0x7fffffff, 0.0}, own = lane_id() < a.chunks ? st[lane_id()] : none;
   if (a.kind == MMVQ_TARGET_LOGITS) {
-    for (int c = lane_id(); c < a.chunks; c += kWave)
-      if (st[c].top > top) { top = st[c].top; at = st[c].at; }
+    take_top(top, at, own.top, own.at);
+    for (int c = lane_id() + kWave; c < a.chunks; c += kWave) take_top(top, at, st[c].top, st[c].at);
     wave_top(top, at);
   }
-  if (gr) {
+  if (h.greedy) {
     z = top > -INFINITY ? 1.0 : 0.0;
     return;
   }
-  for (int c = lane_id(); c < a.chunks; c += kWave) {
-    if (a.kind == MMVQ_TARGET_WEIGHTS) z += st[c].sum;
-    else if (st[c].top > -INFINITY && (st[c].top == top || top < INFINITY))
-      z += st[c].top == top ? st[c].sum
-                            : st[c].sum * exp((static_cast<double>(st[c].top) - static_cast<double>(top)) * inv_t);
-  }
+  z = own.sum * chunk_scale(a, own.top, top, h);
+  for (int c = lane_id() + kWave; c < a.chunks; c += kWave) z += st[c].sum * chunk_scale(a, st[c].top, top, h);
   z = wave_sum(z);
 }
 
 // The weight to draw from and the plain one, of element i of the decided row.
-__device__ __forceinline__ void draw_weights(const VerifyArgs& a, const Decision& d, bool gr, int x, float v, float q,
-                                             int i, double& rest, double& all) {
-  all = weight(a, v, i, d.top, d.best, d.inv_t, gr);
-  const double off = a.draft_probs ? draft_weight(q) * d.z : i == x ? d.z : 0.0;
-  rest = all - off;
-  rest = rest > 0.0 ? rest : 0.0;
+__device__ __forceinline__ void draw_weights(const VerifyArgs& a, const Decision& d, Heat h, int x, float v, float q, int i,
+                                             double& rest, double& all) {
+  all = weight(a, v, i, d.top, d.best, h);
+  if (a.draft_probs) rest = fmax(all - draft_weight(q) * d.z, 0.0);
+  else rest = i == x ? 0.0 : all;              // q is 1 there, and e_i <= Z
 }
 
-__global__ void __launch_bounds__(kVThreads) verify_decide_kernel(VerifyArgs a) {
-  __shared__ Decision dec;
-  __shared__ int ok[4];
-  __shared__ float tops[4];
-  __shared__ int ats[4];
-  __shared__ double zs[4], sums[8];
-  const int tid = threadIdx.x, wave = tid >> 6, c = blockIdx.x;
-  for (int s = blockIdx.y; s < a.n_seqs; s += gridDim.y) {
-    int first, count;
-    seq_rows(a, s, first, count);
-    const bool gr = greedy(a, s);
-    const double inv_t = inv_temperature(a, s);
-    __syncthreads();
-    if (tid == 0) {
-      dec.row = -1;
-      dec.taken = 0;
-      dec.last = 0;
-      dec.inv_t = inv_t;
-    }
-    bool open = true;                          // uniform: every draft so far accepted
-    for (int i0 = 0; i0 < count && open; i0 += 4) {
-      const int i = i0 + wave, r = first + i;
-      if (i < count) {
-        float top;
-        int at;
-        double z;
-        join_row(a, r, inv_t, gr, top, at, z);
-        bool yes = false;
-        if (i + 1 < count) {
-          const int x = a.draft_tokens[r];
-          if (x >= 0 && x < a.vocab) {
-            const double e = weight(a, a.target[r * a.ldt + x], x, top, at, inv_t, gr);
-            const double q = a.draft_probs ? draft_weight(a.draft_probs[r * a.ldd + x]) : 1.0;
-            yes = static_cast<double>(a.u_accept[r]) * q * z < e;
-          }
-        }
-        if ((tid & 63) == 0) {
-          ok[wave] = yes && z > 0.0 && z < INFINITY;
-          tops[wave] = top;
-          ats[wave] = at;
-          zs[wave] = z;
-        }
+// Accepts the drafts of sequence s in order; the whole workgroup. Rows four
+// at a time, one a wave.
+struct DecideLds {
+  Decision dec;
+  int ok[4], ats[4];
+  float tops[4];
+  double zs[4];
+};
+__device__ __forceinline__ void decide(const VerifyArgs& a, int first, int count, Heat h, DecideLds& l) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  __syncthreads();                             // the sequence before is done with LDS
+  if (tid == 0) {
+    l.dec.row = -1;
+    l.dec.taken = 0;
+    l.dec.last = 0;
+  }
+  bool open = true;                            // uniform: every draft so far accepted
+  for (int i0 = 0; i0 < count && open; i0 += 4) {
+    const int i = i0 + wave, r = first + i;
+    if (i < count) {
+      // the draft's own values are on their way while the sums are joined
+      const bool drafted = i + 1 < count;
+      const int x = drafted ? a.draft_tokens[r] : -1;
+      const bool real = x >= 0 && x < a.vocab;
+      const float v = a.target[r * a.ldt + (real ? x : 0)];
+      const float q = a.draft_probs && real ? a.draft_probs[r * a.ldd + x] : 1.0f, u = drafted ? a.u_accept[r] : 0.0f;
+      float top;
+      int at;
+      double z;
+      join_row(a, r, h, top, at, z);
+      const bool yes = real && static_cast<double>(u) * draft_weight(q) * z < weight(a, v, x, top, at, h);
+      if ((tid & 63) == 0) {
+        l.ok[wave] = yes && z > 0.0 && z < INFINITY;
+        l.tops[wave] = top;
+        l.ats[wave] = at;
+        l.zs[wave] = z;
       }
-      __syncthreads();
-      if (tid == 0) {
-        for (int w = 0; w < 4 && i0 + w < count; ++w) {
-          if (ok[w]) {
-            ++dec.taken;
-            continue;
-          }
-          const bool valid = zs[w] > 0.0 && zs[w] < INFINITY;
-          dec.row = valid ? first + i0 + w : -2;
-          dec.last = i0 + w + 1 == count;
-          dec.top = tops[w];
-          dec.best = ats[w];
-          dec.z = zs[w];
-          break;
-        }
-      }
-      __syncthreads();
-      open = dec.row == -1;
-    }
-    __syncthreads();
-    const Decision d = dec;
-    if (c == 0 && tid == 0) decisions(a)[s] = d;
-    double rest = 0.0, all = 0.0;
-    if (d.row >= 0) {
-      const int x = d.last ? -1 : a.draft_tokens[d.row];
-#pragma unroll
-      for (int k = 0; k < kVPer / 4; ++k) {
-        const int i = c * kChunk + 4 * (k * kVThreads + tid);
-        float v[4], q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        load_quad(a.target + d.row * a.ldt, i, a.vocab, -INFINITY, v);
-        if (a.draft_probs && !d.last) load_quad(a.draft_probs + d.row * a.ldd, i, a.vocab, 0.0f, q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          double re, al;
-          draw_weights(a, d, gr, x, v[e], q[e], i + e, re, al);
-          rest += re;
-          all += al;
-        }
-      }
-    }
-    rest = wave_sum(rest);
-    all = wave_sum(all);
-    if ((tid & 63) == 0) {
-      sums[2 * wave] = rest;
-      sums[2 * wave + 1] = all;
     }
     __syncthreads();
     if (tid == 0) {
-      SeqSum ss;
-      ss.rest = sums[0] + sums[2] + sums[4] + sums[6];
-      ss.all = sums[1] + sums[3] + sums[5] + sums[7];
-      seq_sums(a)[static_cast<int64_t>(s) * a.chunks + c] = ss;
+      for (int w = 0; w < 4 && i0 + w < count; ++w) {
+        if (l.ok[w]) {
+          ++l.dec.taken;
+          continue;
+        }
+        const bool valid = l.zs[w] > 0.0 && l.zs[w] < INFINITY;
+        l.dec.row = valid ? first + i0 + w : -2;
+        l.dec.last = i0 + w + 1 == count;
+        l.dec.top = l.tops[w];
+        l.dec.best = l.ats[w];
+        l.dec.z = l.zs[w];
+        break;
+      }
+    }
+    __syncthreads();
+    open = l.dec.row == -1;
+  }
+  __syncthreads();
+}
+
+// Sums of a chunk's weights over the workgroup, in thread 0.
+__device__ __forceinline__ SeqSum chunk_sums(const VerifyArgs& a, const Decision& d, Heat h, int x, int c, double* lds) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  double rest = 0.0, all = 0.0;
+#pragma unroll
+  for (int k = 0; k < kVPer / 4; ++k) {
+    const int i = c * kChunk + 4 * (k * kVThreads + tid);
+    float v[4], q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    load_quad(a.target + d.row * a.ldt, i, a.vocab, -INFINITY, v);
+    if (a.draft_probs && !d.last) load_quad(a.draft_probs + d.row * a.ldd, i, a.vocab, 0.0f, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      double re, al;
+      draw_weights(a, d, h, x, v[e], q[e], i + e, re, al);
+      rest += re;
+      all += al;
     }
   }
+  rest = wave_sum(rest);
+  all = wave_sum(all);
+  if ((tid & 63) == 0) {
+    lds[2 * wave] = rest;
+    lds[2 * wave + 1] = all;
+  }
+  __syncthreads();
+  return SeqSum{lds[0] + lds[2] + lds[4] + lds[6], lds[1] + lds[3] + lds[5] + lds[7]};
 }
 
 __device__ __forceinline__ double wave_scan(double v) {   // inclusive
@@ -322,99 +370,160 @@ __device__ __forceinline__ double wave_scan(double v) {   // inclusive
   return v;
 }
 
-__global__ void __launch_bounds__(kVThreads) verify_draw_kernel(VerifyArgs a) {
-  __shared__ double wsum[4], before_s, goal_s;
-  __shared__ int chunk_s, rest_s, hit_s, last_s;
+struct DrawLds {
+  double wsum[4], before, goal;
+  int chunk, rest, hit, last;
+};
+// Draws from the decided row; sums(c): the chunks' sums. The whole workgroup.
+template <class S>
+__device__ __forceinline__ int draw(const VerifyArgs& a, const Decision& d, Heat h, int s, int x, S sums, DrawLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
-  for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
-    const Decision d = decisions(a)[s];
+  if (wave == 0) {
+    const SeqSum none{0.0, 0.0}, own = lane_id() < a.chunks ? sums(lane_id()) : none;
+    double rest = own.rest, all = own.all;
+    for (int c = lane_id() + kWave; c < a.chunks; c += kWave) {
+      const SeqSum o = sums(c);
+      rest += o.rest;
+      all += o.all;
+    }
+    rest = wave_sum(rest);
+    all = wave_sum(all);
+    const bool use = !d.last && rest > 0.0;
+    const double goal = static_cast<double>(a.u_sample[s]) * (use ? rest : all);
+    // first chunk in which the running sum passes the goal; behind the last
+    // border, the last chunk that has a weight
+    double run = 0.0, before = 0.0, last_before = 0.0;
+    int found = -1, last = 0;
+    for (int c0 = 0; c0 < a.chunks && found < 0; c0 += kWave) {
+      const int c = c0 + lane_id();
+      const SeqSum o = c0 == 0 ? own : c < a.chunks ? sums(c) : none;
+      const double w = use ? o.rest : o.all;
+      const double up = wave_scan(w) + run;
+      const uint64_t hit = __ballot(up > goal), some = __ballot(w > 0.0);
+      if (some) {
+        const int i = 63 - __builtin_clzll(some);
+        last = c0 + i;
+        last_before = __shfl(up - w, i);
+      }
+      if (hit) {
+        const int i = __builtin_ctzll(hit);
+        found = c0 + i;
+        before = __shfl(up - w, i);
+      }
+      run = __shfl(up, kWave - 1);
+    }
+    if (lane_id() == 0) {
+      l.chunk = found >= 0 ? found : last;
+      l.before = found >= 0 ? before : last_before;
+      l.goal = goal;
+      l.rest = use;
+      l.hit = 0x7fffffff;
+      l.last = -1;
+    }
+  }
+  __syncthreads();
+  // the chunk again, a run of consecutive elements a lane
+  const int base = l.chunk * kChunk + kVPer * tid;
+  double w[kVPer], own = 0.0;
+#pragma unroll
+  for (int k = 0; k < kVPer; k += 4) {
+    float v[4], q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    load_quad(a.target + d.row * a.ldt, base + k, a.vocab, -INFINITY, v);
+    if (a.draft_probs && !d.last) load_quad(a.draft_probs + d.row * a.ldd, base + k, a.vocab, 0.0f, q);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      double re, al;
+      draw_weights(a, d, h, x, v[e], q[e], base + k + e, re, al);
+      w[k + e] = l.rest ? re : al;
+      own += w[k + e];
+    }
+  }
+  const double up = wave_scan(own);
+  if ((tid & 63) == 63) l.wsum[wave] = up;
+  __syncthreads();
+  double run = l.before + (up - own);
+  for (int v = 0; v < wave; ++v) run += l.wsum[v];
+  int hit = 0x7fffffff, last = -1;
+#pragma unroll
+  for (int k = 0; k < kVPer; ++k) {
+    run += w[k];
+    if (w[k] > 0.0) {
+      last = base + k;
+      if (run > l.goal && hit == 0x7fffffff) hit = base + k;
+    }
+  }
+  if (hit != 0x7fffffff) atomicMin(&l.hit, hit);
+  if (last >= 0) atomicMax(&l.last, last);
+  __syncthreads();
+  return l.hit != 0x7fffffff ? l.hit : l.last;
+}
+
+__device__ __forceinline__ void put_tokens(const VerifyArgs& a, int s, int first, int taken, int token) {
+  for (int i = threadIdx.x; i < a.max_out; i += kVThreads)
+    a.tokens[static_cast<int64_t>(s) * a.max_out + i] = i < taken ? a.draft_tokens[first + i] : i == taken ? token : -1;
+  if (threadIdx.x == 0) a.n_accepted[s] = taken;
+}
+
+// With draft probabilities: the decision, and the sums to draw from.
+__global__ void __launch_bounds__(kVThreads) verify_decide_kernel(VerifyArgs a) {
+  __shared__ DecideLds l;
+  __shared__ double lds[8];
+  const int tid = threadIdx.x, c = blockIdx.x;
+  for (int s = blockIdx.y; s < a.n_seqs; s += gridDim.y) {
     int first, count;
     seq_rows(a, s, first, count);
-    const bool gr = greedy(a, s);
+    const Heat h = heat_of(a, s);
+    decide(a, first, count, h, l);
+    const Decision d = l.dec;
+    if (c == 0 && tid == 0) decisions(a)[s] = d;
+    if (d.row < 0) continue;                   // uniform
+    const SeqSum sum = chunk_sums(a, d, h, d.last ? -1 : a.draft_tokens[d.row], c, lds);
+    if (tid == 0) seq_sums(a)[static_cast<int64_t>(s) * a.chunks + c] = sum;
+  }
+}
+
+__global__ void __launch_bounds__(kVThreads) verify_draw_kernel(VerifyArgs a) {
+  __shared__ DrawLds l;
+  for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
+    const Decision d = decisions(a)[s];
+    int first, count, token = -1;
+    seq_rows(a, s, first, count);
     const SeqSum* cs = seq_sums(a) + static_cast<int64_t>(s) * a.chunks;
-    int token = -1;
+    __syncthreads();                           // the sequence before is done with LDS
+    if (d.row >= 0)                            // uniform
+      token = draw(a, d, heat_of(a, s), s, d.last ? -1 : a.draft_tokens[d.row],
+                   [&](int c) QMV_INLINE { return cs[c]; }, l);
+    put_tokens(a, s, first, d.taken, token);
+  }
+}
+
+// Without draft probabilities: decision and draw. Of the chunks' sums only
+// that of the refused token's changes; it is summed again without it, since
+// the difference of the two may be all that is left.
+__global__ void __launch_bounds__(kVThreads) verify_finish_kernel(VerifyArgs a) {
+  __shared__ DecideLds l;
+  __shared__ DrawLds dl;
+  __shared__ double lds[8];
+  for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
+    int first, count, token = -1;
+    seq_rows(a, s, first, count);
+    const Heat h = heat_of(a, s);
+    decide(a, first, count, h, l);
+    const Decision d = l.dec;
     if (d.row >= 0) {                          // uniform
-      __syncthreads();
-      if (wave == 0) {
-        double rest = 0.0, all = 0.0;
-        for (int c = lane_id(); c < a.chunks; c += kWave) {
-          rest += cs[c].rest;
-          all += cs[c].all;
-        }
-        rest = wave_sum(rest);
-        all = wave_sum(all);
-        const bool use = !d.last && rest > 0.0;
-        const double goal = static_cast<double>(a.u_sample[s]) * (use ? rest : all);
-        // first chunk in which the running sum passes the goal; behind the
-        // last border, the last chunk that has a weight
-        double run = 0.0, before = 0.0, last_before = 0.0;
-        int found = -1, last = 0;
-        for (int c0 = 0; c0 < a.chunks && found < 0; c0 += kWave) {
-          const int c = c0 + lane_id();
-          const double w = c < a.chunks ? (use ? cs[c].rest : cs[c].all) : 0.0;
-          const double up = wave_scan(w) + run;
-          const uint64_t hit = __ballot(up > goal), some = __ballot(w > 0.0);
-          if (some) {
-            const int l = 63 - __builtin_clzll(some);
-            last = c0 + l;
-            last_before = __shfl(up - w, l);
-          }
-          if (hit) {
-            const int l = __builtin_ctzll(hit);
-            found = c0 + l;
-            before = __shfl(up - w, l);
-          }
-          run = __shfl(up, kWave - 1);
-        }
-        if (lane_id() == 0) {
-          chunk_s = found >= 0 ? found : last;
-          before_s = found >= 0 ? before : last_before;
-          goal_s = goal;
-          rest_s = use;
-          hit_s = 0x7fffffff;
-          last_s = -1;
-        }
-      }
-      __syncthreads();
-      // the chunk again, a run of consecutive elements a lane
-      const int base = chunk_s * kChunk + kVPer * tid, x = d.last ? -1 : a.draft_tokens[d.row];
-      double w[kVPer], own = 0.0;
-#pragma unroll
-      for (int k = 0; k < kVPer; k += 4) {
-        float v[4], q[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        load_quad(a.target + d.row * a.ldt, base + k, a.vocab, -INFINITY, v);
-        if (a.draft_probs && !d.last) load_quad(a.draft_probs + d.row * a.ldd, base + k, a.vocab, 0.0f, q);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          double re, al;
-          draw_weights(a, d, gr, x, v[e], q[e], base + k + e, re, al);
-          w[k + e] = rest_s ? re : al;
-          own += w[k + e];
-        }
-      }
-      const double up = wave_scan(own);
-      if ((tid & 63) == 63) wsum[wave] = up;
-      __syncthreads();
-      double run = before_s + (up - own);
-      for (int v = 0; v < wave; ++v) run += wsum[v];
-      int hit = 0x7fffffff, last = -1;
-#pragma unroll
-      for (int k = 0; k < kVPer; ++k) {
-        run += w[k];
-        if (w[k] > 0.0) {
-          last = base + k;
-          if (run > goal_s && hit == 0x7fffffff) hit = base + k;
-        }
-      }
-      if (hit != 0x7fffffff) atomicMin(&hit_s, hit);
-      if (last >= 0) atomicMax(&last_s, last);
-      __syncthreads();
-      token = hit_s != 0x7fffffff ? hit_s : last_s;
+      const int x = d.last ? -1 : a.draft_tokens[d.row], cx = x >= 0 && x < a.vocab ? x / kChunk : -1;
+      double left = 0.0;
+      if (cx >= 0) left = chunk_sums(a, d, h, x, cx, lds).rest;
+      const RowStat* st = row_stats(a) + static_cast<int64_t>(d.row) * a.chunks;
+      const auto sums = [&](int c) QMV_INLINE {
+        double all;
+        if (h.greedy) all = d.best / kChunk == c ? 1.0 : 0.0;
+        else all = st[c].sum * chunk_scale(a, st[c].top, d.top, h);
+        return SeqSum{c == cx ? left : all, all};
+      };
+      token = draw(a, d, h, s, x, sums, dl);
     }
-    for (int i = tid; i < a.max_out; i += kVThreads)
-      a.tokens[static_cast<int64_t>(s) * a.max_out + i] =
-          i < d.taken ? a.draft_tokens[first + i] : i == d.taken ? token : -1;
-    if (tid == 0) a.n_accepted[s] = d.taken;
+    put_tokens(a, s, first, d.taken, token);
   }
 }
 
@@ -425,6 +534,10 @@ int launch_verify(const VerifyArgs& a, hipStream_t st) {
     hipLaunchKernelGGL(verify_stats_kernel, dim3(chunks, rows), dim3(kVThreads), 0, st, a);
     const int rc = check_launch();
     if (rc) return rc;
+  }
+  if (!a.draft_probs) {
+    hipLaunchKernelGGL(verify_finish_kernel, dim3(seqs), dim3(kVThreads), 0, st, a);
+    return check_launch();
   }
   hipLaunchKernelGGL(verify_decide_kernel, dim3(chunks, seqs), dim3(kVThreads), 0, st, a);
   const int rc = check_launch();
