@@ -16,16 +16,20 @@
 // Everything that a token depends on is in 64 bits: with 10^5 logits a
 // running sum in 32 bits moves a border by more than the probability of many
 // tokens. The stats launch reads every row once and is bound by that read
-// with the exponentials beside it (22 64-bit operations each, 2^f by its
+// with the exponentials beside it (21 64-bit operations each, 2^f by its
 // Taylor polynomial); the others are short chains of latencies.
 #include "decode_args.hpp"
 #include "launch.hpp"
 
 namespace qmv {
 
-constexpr int kVThreads = 256;
+constexpr int kVThreads = 512;
+constexpr int kVWaves = kVThreads / kWave;
 constexpr int kVPer = 8;                       // elements a lane
 constexpr int kChunk = kVThreads * kVPer;
+constexpr int kSThreads = 256;                 // the stats launch: fewer lanes with more elements each, as
+constexpr int kSPer = kChunk / kSThreads;      // its reductions cost a wave what 7 elements a lane do
+constexpr int kSWaves = kSThreads / kWave;
 
 struct RowStat {
   float top;                                   // largest logit of the chunk
@@ -71,33 +75,40 @@ __device__ __forceinline__ Heat heat_of(const VerifyArgs& a, int s) {
 
 // 2^t for t <= 0: the integer part by rounding in the sum with 1.5 * 2^52, 2^f
 // of the rest, |f| <= 1/2, by the Taylor polynomial of degree 12 of
-// exp(f ln 2): its next term is below 2 10^-16.
-__device__ __forceinline__ double exp2_neg(double t) {
-  constexpr double kLn2 = 0.69314718055994530941723212145818;
-  constexpr double kRound = 6755399441055744.0;
-  t = fmax(t, -1080.0);                        // below the smallest double
-  const double k = t + kRound, f = t - (k - kRound);
-  double p = 0.0, c = 1.0, cs[13];
+// exp(f ln 2): its next term is below 2 10^-16. NaN and -inf give 0.
+struct Exp2 {
+  double c[13];
+  // The coefficients in scalar registers: as literals each step of the
+  // polynomial would first move its own into a vector register.
+  __device__ __forceinline__ Exp2() {
+    double v = 1.0;
 #pragma unroll
-  for (int i = 0; i <= 12; ++i) {
-    cs[i] = c;
-    c = c * kLn2 / (i + 1);
+    for (int i = 0; i <= 12; ++i) {
+      c[i] = v;
+      v = v * 0.69314718055994530941723212145818 / (i + 1);
+    }
+#pragma unroll
+    for (int i = 0; i <= 12; ++i) asm("" : "+s"(c[i]));
   }
+  __device__ __forceinline__ double operator()(double t) const {
+    constexpr double kRound = 6755399441055744.0;
+    t = fmax(t, -1080.0);                      // below the smallest double
+    const double k = t + kRound, f = t - (k - kRound);
+    double p = c[12];
 #pragma unroll
-  for (int i = 12; i >= 0; --i) p = fma(p, f, cs[i]);
-  return __builtin_ldexp(p, static_cast<int>(__double2loint(k)));
-}
+    for (int i = 11; i >= 0; --i) p = fma(p, f, c[i]);
+    return __builtin_ldexp(p, static_cast<int>(__double2loint(k)));
+  }
+};
 
 // Unnormalised weight of element i of a row whose largest logit is `top` (at
 // its lowest index `best`).
-__device__ __forceinline__ double weight(const VerifyArgs& a, float v, int i, float top, int best, Heat h) {
+__device__ __forceinline__ double weight(const VerifyArgs& a, const Exp2& exp2, float v, int i, float top, int best, Heat h) {
   if (a.kind == MMVQ_TARGET_WEIGHTS) return v > 0.0f && v < INFINITY ? static_cast<double>(v) : 0.0;
   if (h.greedy) return i == best ? 1.0 : 0.0;
-  // -inf and NaN have none; +inf ones share all of it
-  const bool none = !(v > -INFINITY) || (top == INFINITY && v != top);
-  const double d = v == top ? 0.0 : static_cast<double>(v) - static_cast<double>(top);
-  const double e = exp2_neg(d * h.rate);
-  return none ? 0.0 : e;
+  if (top == -INFINITY) return 0.0;            // nothing but -inf and NaN
+  if (top == INFINITY) return v == top ? 1.0 : 0.0;
+  return exp2((static_cast<double>(v) - static_cast<double>(top)) * h.rate);
 }
 
 // A probability of the draft; what is not positive counts as 0.
@@ -176,76 +187,95 @@ __device__ __forceinline__ void seq_rows(const VerifyArgs& a, int s, int& first,
 
 // Four elements at i, `fill` behind the row's end.
 __device__ __forceinline__ void load_quad(const float* row, int i, int n, float fill, float (&v)[4]) {
-  if (i + 4 <= n) {
-    const u32x4 r = ld_x4(reinterpret_cast<const uint8_t*>(row + i));
+  if (n >= 4) {
+    const int at = i + 4 <= n ? i : n - 4;     // no branch, so that loads go out together
+    const u32x4 r = ld_x4(reinterpret_cast<const uint8_t*>(row + at));
 #pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = __uint_as_float(r[e]);
+    for (int e = 0; e < 4; ++e) {
+      const int from = i + e - at;             // 0..3 where the element exists
+      const uint32_t x = from <= 0 ? r[0] : from == 1 ? r[1] : from == 2 ? r[2] : r[3];
+      v[e] = i + e < n ? __uint_as_float(x) : fill;
+    }
   } else {
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = i + e < n ? row[i + e] : fill;
   }
 }
 
-__global__ void __launch_bounds__(kVThreads) verify_stats_kernel(VerifyArgs a) {
-  __shared__ float tops[4];
-  __shared__ int ats[4];
-  __shared__ double sums[4];
-  const int tid = threadIdx.x, wave = tid >> 6, c = blockIdx.x;
+// exp(chunk_top - top) of two largest logits, the factor between their sums.
+__device__ __forceinline__ double chunk_scale(const VerifyArgs& a, const Exp2& exp2, float chunk_top, float top, Heat h) {
+  if (a.kind == MMVQ_TARGET_WEIGHTS || chunk_top == top) return 1.0;
+  if (!(chunk_top > -INFINITY) || top == INFINITY) return 0.0;
+  return exp2((static_cast<double>(chunk_top) - static_cast<double>(top)) * h.rate);
+}
+
+// Each wave sums relative to its own largest logit; one wave joins the four.
+template <bool LOGITS>
+__global__ void __launch_bounds__(kSThreads) verify_stats_kernel(VerifyArgs a) {
+  __shared__ RowStat st[kSWaves];
+  const Exp2 exp2;
+  const int tid = threadIdx.x, wave = tid >> 6, c = blockIdx.x, i0 = c * kChunk + 4 * tid;
   for (int r = blockIdx.y; r < a.n_rows; r += gridDim.y) {
-    float v[kVPer];
+    const float* row = a.target + r * a.ldt;
+    float v[kSPer];
+    if ((c + 1) * kChunk <= a.vocab) {         // uniform: all loads at once
 #pragma unroll
-    for (int k = 0; k < kVPer / 4; ++k) {
-      float t[4];
-      load_quad(a.target + r * a.ldt, c * kChunk + 4 * (k * kVThreads + tid), a.vocab, -INFINITY, t);
+      for (int k = 0; k < kSPer; k += 4) {
+        const u32x4 x = ld_x4(reinterpret_cast<const uint8_t*>(row + i0 + k * kSThreads));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[4 * k + e] = t[e];
+        for (int e = 0; e < 4; ++e) v[k + e] = __uint_as_float(x[e]);
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < kSPer; ++k) {
+        const int i = i0 + (k / 4) * 4 * kSThreads + k % 4;
+        v[k] = row[i < a.vocab ? i : a.vocab - 1];
+        v[k] = i < a.vocab ? v[k] : -INFINITY;
+      }
     }
     const int s = sequence_of(a, r);
     if (s < 0) continue;                       // uniform: every wave finds the same
-    float top = -INFINITY;
-    int at = 0x7fffffff;
+    RowStat own{-INFINITY, 0x7fffffff, 0.0};
+    bool greedy = false;
+    Heat h{0.0, false};
+    if constexpr (LOGITS) {
+      h = heat_of(a, s);
+      greedy = h.greedy;
 #pragma unroll
-    for (int k = 0; k < kVPer; ++k) {
-      const int i = c * kChunk + 4 * ((k / 4) * kVThreads + tid) + k % 4;
-      if (v[k] > top) { top = v[k]; at = i; }
-    }
-    double sum = 0.0;
-    if (a.kind == MMVQ_TARGET_LOGITS) {
-      wave_top(top, at);
-      __syncthreads();                         // the row before is written
-      if ((tid & 63) == 0) { tops[wave] = top; ats[wave] = at; }
-      __syncthreads();
+      for (int k = 0; k < kSPer; ++k) own.top = fmaxf(own.top, v[k]);
 #pragma unroll
-      for (int w = 0; w < 4; ++w)
-        if (tops[w] > top || (tops[w] == top && ats[w] < at)) { top = tops[w]; at = ats[w]; }
+      for (int k = kSPer - 1; k >= 0; --k) own.at = v[k] == own.top && own.top > -INFINITY ? i0 + (k / 4) * 4 * kSThreads + k % 4 : own.at;
+      wave_top(own.top, own.at);
+      if (!greedy && own.top > -INFINITY) {
+        if (own.top < INFINITY) {
+          const double top = static_cast<double>(own.top);
+#pragma unroll
+          for (int k = 0; k < kSPer; ++k) own.sum += exp2((static_cast<double>(v[k]) - top) * h.rate);
+        } else {
+#pragma unroll
+          for (int k = 0; k < kSPer; ++k) own.sum += v[k] == own.top ? 1.0 : 0.0;
+        }
+      }
     } else {
-      __syncthreads();
-    }
-    const Heat h = heat_of(a, s);
-    if (!h.greedy) {
 #pragma unroll
-      for (int k = 0; k < kVPer; ++k) sum += weight(a, v[k], 0, top, 0, h);
-      sum = wave_sum(sum);
-      if ((tid & 63) == 0) sums[wave] = sum;
+      for (int k = 0; k < kSPer; ++k) own.sum += v[k] > 0.0f && v[k] < INFINITY ? static_cast<double>(v[k]) : 0.0;
     }
+    if (!greedy) own.sum = wave_sum(own.sum);
+    __syncthreads();                           // the row before is joined
+    if ((tid & 63) == 0) st[wave] = own;
     __syncthreads();
-    if (tid == 0) {
-      RowStat st;
-      st.top = top;
-      st.at = at;
-      st.sum = h.greedy ? 0.0 : sums[0] + sums[1] + sums[2] + sums[3];
-      row_stats(a)[static_cast<int64_t>(r) * a.chunks + c] = st;
+    if (wave == 0) {
+      const RowStat o = st[tid & (kSWaves - 1)];
+      RowStat all{o.top, o.at, 0.0};
+      if constexpr (LOGITS) wave_top(all.top, all.at);
+      all.sum = wave_sum(tid < kSWaves ? o.sum * chunk_scale(a, exp2, o.top, all.top, h) : 0.0);
+      if (tid == 0) row_stats(a)[static_cast<int64_t>(r) * a.chunks + c] = all;
     }
   }
 }
 
 // A row's chunks joined, by one wave: the same in all lanes.
-__device__ __forceinline__ double chunk_scale(const VerifyArgs& a, float chunk_top, float top, Heat h) {
-  if (a.kind == MMVQ_TARGET_WEIGHTS || chunk_top == top) return 1.0;
-  if (!(chunk_top > -INFINITY) || top == INFINITY) return 0.0;
-  return exp2_neg((static_cast<double>(chunk_top) - static_cast<double>(top)) * h.rate);
-}
-__device__ __forceinline__ void join_row(const VerifyArgs& a, int r, Heat h, float& top, int& at, double& z) {
+__device__ __forceinline__ void join_row(const VerifyArgs& a, const Exp2& exp2, int r, Heat h, float& top, int& at, double& z) {
   const RowStat* st = row_stats(a) + static_cast<int64_t>(r) * a.chunks;
   top = -INFINITY;
   at = 0x7fffffff;
@@ -260,28 +290,28 @@ __device__ __forceinline__ void join_row(const VerifyArgs& a, int r, Heat h, flo
     z = top > -INFINITY ? 1.0 : 0.0;
     return;
   }
-  z = own.sum * chunk_scale(a, own.top, top, h);
-  for (int c = lane_id() + kWave; c < a.chunks; c += kWave) z += st[c].sum * chunk_scale(a, st[c].top, top, h);
+  z = own.sum * chunk_scale(a, exp2, own.top, top, h);
+  for (int c = lane_id() + kWave; c < a.chunks; c += kWave) z += st[c].sum * chunk_scale(a, exp2, st[c].top, top, h);
   z = wave_sum(z);
 }
 
 // The weight to draw from and the plain one, of element i of the decided row.
-__device__ __forceinline__ void draw_weights(const VerifyArgs& a, const Decision& d, Heat h, int x, float v, float q, int i,
+__device__ __forceinline__ void draw_weights(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, int x, float v, float q, int i,
                                              double& rest, double& all) {
-  all = weight(a, v, i, d.top, d.best, h);
+  all = weight(a, exp2, v, i, d.top, d.best, h);
   if (a.draft_probs) rest = fmax(all - draft_weight(q) * d.z, 0.0);
   else rest = i == x ? 0.0 : all;              // q is 1 there, and e_i <= Z
 }
 
-// Accepts the drafts of sequence s in order; the whole workgroup. Rows four
+// Accepts the drafts of sequence s in order; the whole workgroup. Rows eight
 // at a time, one a wave.
 struct DecideLds {
   Decision dec;
-  int ok[4], ats[4];
-  float tops[4];
-  double zs[4];
+  int ok[kVWaves], ats[kVWaves];
+  float tops[kVWaves];
+  double zs[kVWaves];
 };
-__device__ __forceinline__ void decide(const VerifyArgs& a, int first, int count, Heat h, DecideLds& l) {
+__device__ __forceinline__ void decide(const VerifyArgs& a, const Exp2& exp2, int first, int count, Heat h, DecideLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
   __syncthreads();                             // the sequence before is done with LDS
   if (tid == 0) {
@@ -290,7 +320,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, int first, int count
     l.dec.last = 0;
   }
   bool open = true;                            // uniform: every draft so far accepted
-  for (int i0 = 0; i0 < count && open; i0 += 4) {
+  for (int i0 = 0; i0 < count && open; i0 += kVWaves) {
     const int i = i0 + wave, r = first + i;
     if (i < count) {
       // the draft's own values are on their way while the sums are joined
@@ -302,8 +332,8 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, int first, int count
       float top;
       int at;
       double z;
-      join_row(a, r, h, top, at, z);
-      const bool yes = real && static_cast<double>(u) * draft_weight(q) * z < weight(a, v, x, top, at, h);
+      join_row(a, exp2, r, h, top, at, z);
+      const bool yes = real && static_cast<double>(u) * draft_weight(q) * z < weight(a, exp2, v, x, top, at, h);
       if ((tid & 63) == 0) {
         l.ok[wave] = yes && z > 0.0 && z < INFINITY;
         l.tops[wave] = top;
@@ -313,7 +343,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, int first, int count
     }
     __syncthreads();
     if (tid == 0) {
-      for (int w = 0; w < 4 && i0 + w < count; ++w) {
+      for (int w = 0; w < kVWaves && i0 + w < count; ++w) {
         if (l.ok[w]) {
           ++l.dec.taken;
           continue;
@@ -333,8 +363,8 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, int first, int count
   __syncthreads();
 }
 
-// Sums of a chunk's weights over the workgroup, in thread 0.
-__device__ __forceinline__ SeqSum chunk_sums(const VerifyArgs& a, const Decision& d, Heat h, int x, int c, double* lds) {
+// Sums of a chunk's weights over the workgroup.
+__device__ __forceinline__ SeqSum chunk_sums(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, int x, int c, double* lds) {
   const int tid = threadIdx.x, wave = tid >> 6;
   double rest = 0.0, all = 0.0;
 #pragma unroll
@@ -346,7 +376,7 @@ __device__ __forceinline__ SeqSum chunk_sums(const VerifyArgs& a, const Decision
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       double re, al;
-      draw_weights(a, d, h, x, v[e], q[e], i + e, re, al);
+      draw_weights(a, exp2, d, h, x, v[e], q[e], i + e, re, al);
       rest += re;
       all += al;
     }
@@ -358,25 +388,40 @@ __device__ __forceinline__ SeqSum chunk_sums(const VerifyArgs& a, const Decision
     lds[2 * wave + 1] = all;
   }
   __syncthreads();
-  return SeqSum{lds[0] + lds[2] + lds[4] + lds[6], lds[1] + lds[3] + lds[5] + lds[7]};
+  SeqSum sum{0.0, 0.0};
+#pragma unroll
+  for (int w = 0; w < kVWaves; ++w) {
+    sum.rest += lds[2 * w];
+    sum.all += lds[2 * w + 1];
+  }
+  return sum;
 }
 
-__device__ __forceinline__ double wave_scan(double v) {   // inclusive
-#pragma unroll
-  for (int m = 1; m < kWave; m <<= 1) {
-    const double o = __shfl_up(v, m);
-    if (lane_id() >= m) v += o;
-  }
+// Value of the lane CTRL names, 0 where there is none or the row is masked out.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_zero_d(double v) {
+  return __hiloint2double(__builtin_amdgcn_update_dpp(0, __double2hiint(v), CTRL, ROWS, 0xF, false),
+                          __builtin_amdgcn_update_dpp(0, __double2loint(v), CTRL, ROWS, 0xF, false));
+}
+// Inclusive sums over the lanes: within rows of 16 by shifts, then the rows'
+// last lanes handed on.
+__device__ __forceinline__ double wave_scan(double v) {
+  v += dpp_zero_d<0x111, 0xF>(v);              // row_shr:1
+  v += dpp_zero_d<0x112, 0xF>(v);
+  v += dpp_zero_d<0x114, 0xF>(v);
+  v += dpp_zero_d<0x118, 0xF>(v);
+  v += dpp_zero_d<0x142, 0xA>(v);              // row_bcast:15 to rows 1 and 3
+  v += dpp_zero_d<0x143, 0xC>(v);              // row_bcast:31 to rows 2 and 3
   return v;
 }
 
 struct DrawLds {
-  double wsum[4], before, goal;
+  double wsum[kVWaves], before, goal;
   int chunk, rest, hit, last;
 };
 // Draws from the decided row; sums(c): the chunks' sums. The whole workgroup.
 template <class S>
-__device__ __forceinline__ int draw(const VerifyArgs& a, const Decision& d, Heat h, int s, int x, S sums, DrawLds& l) {
+__device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, int s, int x, S sums, DrawLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
   if (wave == 0) {
     const SeqSum none{0.0, 0.0}, own = lane_id() < a.chunks ? sums(lane_id()) : none;
@@ -433,7 +478,7 @@ __device__ __forceinline__ int draw(const VerifyArgs& a, const Decision& d, Heat
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       double re, al;
-      draw_weights(a, d, h, x, v[e], q[e], base + k + e, re, al);
+      draw_weights(a, exp2, d, h, x, v[e], q[e], base + k + e, re, al);
       w[k + e] = l.rest ? re : al;
       own += w[k + e];
     }
@@ -466,23 +511,25 @@ __device__ __forceinline__ void put_tokens(const VerifyArgs& a, int s, int first
 
 // With draft probabilities: the decision, and the sums to draw from.
 __global__ void __launch_bounds__(kVThreads) verify_decide_kernel(VerifyArgs a) {
+  const Exp2 exp2;
   __shared__ DecideLds l;
-  __shared__ double lds[8];
+  __shared__ double lds[2 * kVWaves];
   const int tid = threadIdx.x, c = blockIdx.x;
   for (int s = blockIdx.y; s < a.n_seqs; s += gridDim.y) {
     int first, count;
     seq_rows(a, s, first, count);
     const Heat h = heat_of(a, s);
-    decide(a, first, count, h, l);
+    decide(a, exp2, first, count, h, l);
     const Decision d = l.dec;
     if (c == 0 && tid == 0) decisions(a)[s] = d;
-    if (d.row < 0) continue;                   // uniform
-    const SeqSum sum = chunk_sums(a, d, h, d.last ? -1 : a.draft_tokens[d.row], c, lds);
+    if (d.row < 0) continue;                   // uniform; (decide waits for the sequence before)
+    const SeqSum sum = chunk_sums(a, exp2, d, h, d.last ? -1 : a.draft_tokens[d.row], c, lds);
     if (tid == 0) seq_sums(a)[static_cast<int64_t>(s) * a.chunks + c] = sum;
   }
 }
 
 __global__ void __launch_bounds__(kVThreads) verify_draw_kernel(VerifyArgs a) {
+  const Exp2 exp2;
   __shared__ DrawLds l;
   for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
     const Decision d = decisions(a)[s];
@@ -491,7 +538,7 @@ __global__ void __launch_bounds__(kVThreads) verify_draw_kernel(VerifyArgs a) {
     const SeqSum* cs = seq_sums(a) + static_cast<int64_t>(s) * a.chunks;
     __syncthreads();                           // the sequence before is done with LDS
     if (d.row >= 0)                            // uniform
-      token = draw(a, d, heat_of(a, s), s, d.last ? -1 : a.draft_tokens[d.row],
+      token = draw(a, exp2, d, heat_of(a, s), s, d.last ? -1 : a.draft_tokens[d.row],
                    [&](int c) QMV_INLINE { return cs[c]; }, l);
     put_tokens(a, s, first, d.taken, token);
   }
@@ -501,27 +548,28 @@ __global__ void __launch_bounds__(kVThreads) verify_draw_kernel(VerifyArgs a) {
 // that of the refused token's changes; it is summed again without it, since
 // the difference of the two may be all that is left.
 __global__ void __launch_bounds__(kVThreads) verify_finish_kernel(VerifyArgs a) {
+  const Exp2 exp2;
   __shared__ DecideLds l;
   __shared__ DrawLds dl;
-  __shared__ double lds[8];
+  __shared__ double lds[2 * kVWaves];
   for (int s = blockIdx.x; s < a.n_seqs; s += gridDim.x) {
     int first, count, token = -1;
     seq_rows(a, s, first, count);
     const Heat h = heat_of(a, s);
-    decide(a, first, count, h, l);
+    decide(a, exp2, first, count, h, l);
     const Decision d = l.dec;
     if (d.row >= 0) {                          // uniform
       const int x = d.last ? -1 : a.draft_tokens[d.row], cx = x >= 0 && x < a.vocab ? x / kChunk : -1;
       double left = 0.0;
-      if (cx >= 0) left = chunk_sums(a, d, h, x, cx, lds).rest;
+      if (cx >= 0) left = chunk_sums(a, exp2, d, h, x, cx, lds).rest;
       const RowStat* st = row_stats(a) + static_cast<int64_t>(d.row) * a.chunks;
       const auto sums = [&](int c) QMV_INLINE {
         double all;
         if (h.greedy) all = d.best / kChunk == c ? 1.0 : 0.0;
-        else all = st[c].sum * chunk_scale(a, st[c].top, d.top, h);
+        else all = st[c].sum * chunk_scale(a, exp2, st[c].top, d.top, h);
         return SeqSum{c == cx ? left : all, all};
       };
-      token = draw(a, d, h, s, x, sums, dl);
+      token = draw(a, exp2, d, h, s, x, sums, dl);
     }
     put_tokens(a, s, first, d.taken, token);
   }
@@ -531,7 +579,10 @@ int launch_verify(const VerifyArgs& a, hipStream_t st) {
   const unsigned chunks = static_cast<unsigned>(a.chunks);
   const unsigned rows = a.n_rows < 65535 ? a.n_rows : 65535, seqs = a.n_seqs < 65535 ? a.n_seqs : 65535;
   if (rows > 0) {
-    hipLaunchKernelGGL(verify_stats_kernel, dim3(chunks, rows), dim3(kVThreads), 0, st, a);
+    if (a.kind == MMVQ_TARGET_LOGITS)
+      hipLaunchKernelGGL((verify_stats_kernel<true>), dim3(chunks, rows), dim3(kSThreads), 0, st, a);
+    else
+      hipLaunchKernelGGL((verify_stats_kernel<false>), dim3(chunks, rows), dim3(kSThreads), 0, st, a);
     const int rc = check_launch();
     if (rc) return rc;
   }
