@@ -132,7 +132,7 @@ int mmvq_add_rms_norm(const float* x, int64_t K, int64_t n, int64_t ldx, const f
   const hipStream_t st = static_cast<hipStream_t>(stream);
   const OnStreamDevice on(st);
   return launch_norm(NormArgs{x, residual, weight, sum_out, y, static_cast<uint8_t*>(y_q), ldx, ldr, lds, ldy, n,
-                              static_cast<int>(K), static_cast<double>(eps)},
+                              static_cast<int>(K), static_cast<double>(eps), 1.0 / static_cast<double>(K)},
                      st);
 }
 

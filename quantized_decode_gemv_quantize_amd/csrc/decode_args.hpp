@@ -114,7 +114,7 @@ struct NormArgs {
   uint8_t* yq;
   int64_t ldx, ldr, lds, ldy, n;
   int K;
-  double eps;
+  double eps, inv_K;
 };
 
 int launch_norm(const NormArgs& a, hipStream_t st);

@@ -1,13 +1,14 @@
 // kv_cache.hip - new tokens' keys and values into the paged cache, and back.
 //
-// A workgroup owns one unit (16 tokens of one head, keys or values): it
-// quantizes the rows that fall into it (8 lanes a 32-value block, 4 values a
-// lane, reductions over the 8 lanes by DPP), arranges the unit in LDS and
-// copies out what belongs to the new tokens: 16-byte stores where the unit
-// is all new, the tokens' own bytes otherwise. The arrangement transposes
-// the values, which in memory would be stores of single bytes. Long prompts
-// are bound by memory bandwidth (4 bytes a value in, 0.56 to 2 out), single
-// tokens by latency.
+// Eight lanes hold a 32-value block, 4 values each, and reduce over it by
+// DPP. Keys: a workgroup owns one unit (16 tokens of one head), arranges it
+// in LDS and copies out what belongs to the new tokens. Values, which a unit
+// holds transposed: a lane takes 4 dims of 8 consecutive tokens, eight loads
+// at once, transposes them in registers and stores runs of 8 tokens; in LDS
+// the transposition costs 8-way bank conflicts. Whole units and runs go out
+// in 16-byte stores, parts of them as the new tokens' own bytes. Long
+// prompts are bound by memory bandwidth (4 bytes a value in, 0.56 to 2 out),
+// single tokens by latency.
 #include "decode_args.hpp"
 #include "launch.hpp"
 #include "q8.hpp"
@@ -57,52 +58,43 @@ struct UnitLds {
   alignas(16) uint8_t bytes[kv_unit_bytes(KIND, NB)];
 };
 
-// Quantizes value quad `sub` of block b of token tt into the unit image.
-template <int KIND, int NB, bool KEYS>
-__device__ __forceinline__ void put_quad(uint8_t* img, int tt, int b, int sub, const float (&x)[4]) {
-  const int c = 4 * sub;
-  if constexpr (KIND == kKvF16) {
-    uint16_t h[4];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) h[e] = static_cast<uint16_t>(f2h_bits(x[e]));
-    if constexpr (KEYS) {
-      *reinterpret_cast<u32x2*>(img + kv_key_at(KIND, NB, tt, b, c)) =
-          u32x2{h[0] | static_cast<uint32_t>(h[1]) << 16, h[2] | static_cast<uint32_t>(h[3]) << 16};
-    } else {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) *reinterpret_cast<uint16_t*>(img + kv_value_at(KIND, tt, b, c + e)) = h[e];
-    }
+__device__ __forceinline__ uint32_t scale_bits(float d) { return f2h_bits(fminf(fmaxf(d, -65504.0f), 65504.0f)); }
+
+// Codes of the lane's quad of a block, as a unit stores them (a byte each),
+// and the block's d.
+template <int KIND>
+__device__ __forceinline__ float quad_codes(const float (&x)[4], uint32_t& w) {
+  if constexpr (KIND == kKvQ8) {
+    const u32x4 raw[1] = {{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}};
+    float amax = absmax4(raw[0]);
+    amax = fmaxf(amax, dpp_f<kDppXor1>(amax));
+    amax = fmaxf(amax, dpp_f<kDppXor2>(amax));
+    amax = fmaxf(amax, dpp_f<kDppMirror8>(amax));
+    const float d = q8_scale(amax);
+    uint32_t packed[1];
+    int sum = 0;
+    q8_quant_block(raw, d, packed, sum);
+    w = packed[0] ^ 0x80808080u;                   // q + 128
+    return d;
   } else {
-    float d;
+    const float d = q4_most(x) / -8.0f;
+    w = q4_codes(x, d);
+    return d;
+  }
+}
+
+// Quantizes quad `sub` of block b of token tt into the image of a key unit.
+template <int KIND, int NB>
+__device__ __forceinline__ void put_keys(uint8_t* img, int tt, int b, int sub, const float (&x)[4]) {
+  uint8_t* to = img + kv_key_at(KIND, NB, tt, b, 4 * sub);
+  if constexpr (KIND == kKvF16) {
+    *reinterpret_cast<u32x2*>(to) = u32x2{f2h_bits(x[0]) | (f2h_bits(x[1]) << 16), f2h_bits(x[2]) | (f2h_bits(x[3]) << 16)};
+  } else {
     uint32_t w;
-    bool mine = true;
-    if constexpr (KIND == kKvQ8) {
-      const u32x4 raw[1] = {{__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3])}};
-      float amax = absmax4(raw[0]);
-      amax = fmaxf(amax, dpp_f<kDppXor1>(amax));
-      amax = fmaxf(amax, dpp_f<kDppXor2>(amax));
-      amax = fmaxf(amax, dpp_f<kDppMirror8>(amax));
-      d = q8_scale(amax);
-      uint32_t packed[1];
-      int sum = 0;
-      q8_quant_block(raw, d, packed, sum);
-      w = packed[0] ^ 0x80808080u;                 // q + 128
-    } else {
-      d = q4_most(x) / -8.0f;
-      w = q4_codes(x, d);
-      const uint32_t o = from_half(w);
-      w = w | (o << 4);                            // lower half of the lanes: its nibbles and those 16 dims on
-      mine = sub < 4;
-    }
-    if (mine) {
-      if constexpr (KEYS) {
-        *reinterpret_cast<uint32_t*>(img + kv_key_at(KIND, NB, tt, b, c)) = w;
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) img[kv_value_at(KIND, tt, b, c + e)] = static_cast<uint8_t>(w >> (8 * e));
-      }
-    }
-    if (sub == 0) *reinterpret_cast<uint16_t*>(img + kv_scale_at(KIND, NB, b, tt)) = static_cast<uint16_t>(f2h_bits(fminf(fmaxf(d, -65504.0f), 65504.0f)));
+    const float d = quad_codes<KIND>(x, w);
+    if constexpr (KIND == kKvQ4) w |= from_half(w) << 4;   // lower half of the lanes: its nibbles and those 16 dims on
+    if (KIND == kKvQ8 || sub < 4) *reinterpret_cast<uint32_t*>(to) = w;
+    if (sub == 0) *reinterpret_cast<uint16_t*>(img + kv_scale_at(KIND, NB, b, tt)) = static_cast<uint16_t>(scale_bits(d));
   }
 }
 
@@ -120,55 +112,58 @@ __device__ __forceinline__ void get_quad(const uint8_t* img, int tt, int b, int 
   }
 }
 
-template <int KIND, int NB, bool KEYS>
-__device__ __forceinline__ void write_units(const KvIoArgs& a, uint8_t* img) {
+// Units that a sequence's new tokens touch.
+struct Run {
+  int row0, count, len, p0;
+  __device__ __forceinline__ Run(const BatchArgs& b, int s) {
+    const int from = b.token_start[s], to = b.token_start[s + 1], l = b.seq_len[s];
+    b.clamp_rows(from, to, row0, count);
+    len = l < 0 ? 0 : l > (1 << 30) ? (1 << 30) : l;
+    p0 = len - count;
+  }
+};
+
+template <int KIND, int NB>
+__device__ __forceinline__ void write_keys(const KvIoArgs& a, uint8_t* img) {
   constexpr int U = kv_unit_bytes(KIND, NB), C = kv_code_bytes(KIND, NB);
+  constexpr int kItems = (16 * NB * 8 + 255) / 256;
   const int head = blockIdx.y >> 1, tid = threadIdx.x;
-  const float* act = a.act[KEYS ? 0 : 1];
-  const int64_t ld = a.ld[KEYS ? 0 : 1];
-  uint8_t* cache = a.cache[KEYS ? 0 : 1];
   for (int s = blockIdx.z; s < a.b.n_seqs; s += gridDim.z) {
-    int row0, count;
-    a.b.rows(s, row0, count);
-    const int len = a.b.seq_len[s] > 0 ? a.b.seq_len[s] : 0;
-    const int p0 = len - count;
-    for (int base = ((p0 >> 4) + static_cast<int>(blockIdx.x)) * 16; base < len; base += 16 * static_cast<int>(gridDim.x)) {
-      const int page = a.b.page(s, base);
-      if (count == 0 || page < 0) continue;
-      const int ta = p0 > base ? p0 - base : 0, tb = len - base < 16 ? len - base : 16;
-      __syncthreads();                             // the image of the unit before is copied out
-      for (int it = tid; it < (tb - ta) * NB * 8; it += 256) {
-        const int tt = ta + it / (NB * 8), b = it / 8 % NB, sub = it & 7;
-        const u32x4 r = ld_x4(reinterpret_cast<const uint8_t*>(
-            act + (row0 + (base + tt - p0)) * ld + head * (32 * NB) + 32 * b + 4 * sub));
-        float x[4];
+    const Run r(a.b, s);
+    for (int base = ((r.p0 >> 4) + static_cast<int>(blockIdx.x)) * 16; base < r.len; base += 16 * static_cast<int>(gridDim.x)) {
+      if (r.count == 0) continue;
+      const int ta = r.p0 > base ? r.p0 - base : 0, tb = r.len - base < 16 ? r.len - base : 16;
+      const int items = (tb - ta) * NB * 8;
+      u32x4 raw[kItems];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(r[e]);
-        put_quad<KIND, NB, KEYS>(img, tt, b, sub, x);
+      for (int k = 0; k < kItems; ++k) {
+        const int it = tid + 256 * k < items ? tid + 256 * k : 0;
+        const int tt = ta + it / (NB * 8), b = it / 8 % NB, sub = it & 7;
+        raw[k] = ld_x4(reinterpret_cast<const uint8_t*>(a.act[0] + (r.row0 + (base + tt - r.p0)) * a.ld[0] + head * (32 * NB) +
+                                                        32 * b + 4 * sub));
+      }
+      const int page = a.b.page(s, base);          // the rows are on their way
+      if (page < 0) continue;                      // uniform
+      __syncthreads();                             // the image of the unit before is copied out
+#pragma unroll
+      for (int k = 0; k < kItems; ++k) {
+        const int it = tid + 256 * k;
+        if (it < items) {
+          float x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(raw[k][e]);
+          put_keys<KIND, NB>(img, ta + it / (NB * 8), it / 8 % NB, it & 7, x);
+        }
       }
       __syncthreads();
-      uint8_t* dst = cache + a.b.unit(page, head, base) * U;
+      uint8_t* dst = a.cache[0] + a.b.unit(page, head, base) * U;
       if (ta == 0 && tb == 16) {
         for (int o = 16 * tid; o < U; o += 16 * 256)
           *reinterpret_cast<u32x4*>(dst + o) = *reinterpret_cast<const u32x4*>(img + o);
       } else {
-        if constexpr (KEYS) {
-          for (int w = tid; w < C / 4; w += 256) {
-            const int tt = kv_key_token(KIND, NB, w);
-            if (tt >= ta && tt < tb) reinterpret_cast<uint32_t*>(dst)[w] = reinterpret_cast<const uint32_t*>(img)[w];
-          }
-        } else {
-          // elements of 8 tokens lie together: element e is of token 8 h8 + e % 8
-          const int n = tb - ta;
-          for (int it = tid; it < n * (C / 16 / (KIND == kKvF16 ? 2 : 1)); it += 256) {
-            const int tt = ta + it % n, e = it / n;
-            const int run = KIND == kKvQ8 ? e / 32 * 4 + tt / 8 * 2 + 0 : e / 16 * 2 + tt / 8;
-            int at;
-            if constexpr (KIND == kKvQ8) at = ((run >> 1) * 32 + e % 32) * 8 + tt % 8;
-            else at = (run * 16 + e % 16) * 8 + tt % 8;
-            if constexpr (KIND == kKvF16) reinterpret_cast<uint16_t*>(dst)[at] = reinterpret_cast<const uint16_t*>(img)[at];
-            else dst[at] = img[at];
-          }
+        for (int w = tid; w < C / 4; w += 256) {
+          const int tt = kv_key_token(KIND, NB, w);
+          if (tt >= ta && tt < tb) reinterpret_cast<uint32_t*>(dst)[w] = reinterpret_cast<const uint32_t*>(img)[w];
         }
         if constexpr (KIND != kKvF16) {
           const int n = tb - ta;
@@ -176,6 +171,100 @@ __device__ __forceinline__ void write_units(const KvIoArgs& a, uint8_t* img) {
             const int o = kv_scale_at(KIND, NB, it / n, ta + it % n);
             *reinterpret_cast<uint16_t*>(dst + o) = *reinterpret_cast<const uint16_t*>(img + o);
           }
+        }
+      }
+    }
+  }
+}
+
+// 4x4 bytes: word e of the result holds byte e of the four words.
+__device__ __forceinline__ void transpose4(const uint32_t (&w)[4], uint32_t (&t)[4]) {
+  const uint32_t a = __builtin_amdgcn_perm(w[1], w[0], 0x05010400u), b = __builtin_amdgcn_perm(w[3], w[2], 0x05010400u);
+  const uint32_t c = __builtin_amdgcn_perm(w[1], w[0], 0x07030602u), d = __builtin_amdgcn_perm(w[3], w[2], 0x07030602u);
+  t[0] = __builtin_amdgcn_perm(b, a, 0x05040100u);
+  t[1] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+  t[2] = __builtin_amdgcn_perm(d, c, 0x05040100u);
+  t[3] = __builtin_amdgcn_perm(d, c, 0x07060302u);
+}
+
+template <int KIND, int NB>
+__device__ __forceinline__ void write_values(const KvIoArgs& a) {
+  constexpr int U = kv_unit_bytes(KIND, NB), L = 16 * NB, GROUPS = 256 / L;   // lanes a unit, units a workgroup
+  const int head = blockIdx.y >> 1, tid = threadIdx.x, grp = tid / L, lane = tid - grp * L;
+  const int h8 = lane / (8 * NB), b = lane / 8 % NB, sub = lane & 7;
+  if (grp >= GROUPS) return;
+  for (int s = blockIdx.z; s < a.b.n_seqs; s += gridDim.z) {
+    const Run r(a.b, s);
+    const int first = (r.p0 >> 4) + static_cast<int>(blockIdx.x) * GROUPS + grp;
+    for (int base = first * 16; base < r.len; base += 16 * GROUPS * static_cast<int>(gridDim.x)) {
+      const int ta = r.p0 - base - 8 * h8, tb = r.len - base - 8 * h8;   // tokens j of the lane's 8: ta <= j < tb
+      if (r.count == 0 || ta >= 8 || tb <= 0) continue;
+      u32x4 raw[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        raw[j] = u32x4{0u, 0u, 0u, 0u};
+        if (j >= ta && j < tb)
+          raw[j] = ld_x4(reinterpret_cast<const uint8_t*>(
+              a.act[1] + (r.row0 + (base + 8 * h8 + j - r.p0)) * a.ld[1] + head * (32 * NB) + 32 * b + 4 * sub));
+      }
+      const int page = a.b.page(s, base);          // the rows are on their way
+      if (page < 0) continue;
+      float x[8][4];
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[j][e] = __uint_as_float(raw[j][e]);
+      uint8_t* dst = a.cache[1] + a.b.unit(page, head, base) * U;
+      const bool full = ta <= 0 && tb >= 8;
+      if constexpr (KIND == kKvF16) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = f2h_bits(x[2 * j][e]) | (f2h_bits(x[2 * j + 1][e]) << 16);
+          uint8_t* to = dst + kv_value_at(KIND, 8 * h8, b, 4 * sub + e);
+          if (full) *reinterpret_cast<u32x4*>(to) = u32x4{w[0], w[1], w[2], w[3]};
+          else
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j >= ta && j < tb) reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+        }
+      } else {
+        uint32_t code[8], ds[4] = {0u, 0u, 0u, 0u};
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          code[j] = 0;
+          if (j >= ta && j < tb)                   // the same for the block's 8 lanes; one token's step does one
+            ds[j / 2] |= scale_bits(quad_codes<KIND>(x[j], code[j])) << (16 * (j & 1));
+        }
+        uint32_t lo[4], hi[4];
+        transpose4({code[0], code[1], code[2], code[3]}, lo);
+        transpose4({code[4], code[5], code[6], code[7]}, hi);
+        if constexpr (KIND == kKvQ4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            lo[e] |= from_half(lo[e]) << 4;
+            hi[e] |= from_half(hi[e]) << 4;
+          }
+        }
+        if (KIND == kKvQ8 || sub < 4) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            uint8_t* to = dst + kv_value_at(KIND, 8 * h8, b, 4 * sub + e);
+            if (full) *reinterpret_cast<u32x2*>(to) = u32x2{lo[e], hi[e]};
+            else
+#pragma unroll
+              for (int j = 0; j < 8; ++j)
+                if (j >= ta && j < tb) to[j] = static_cast<uint8_t>((j < 4 ? lo[e] : hi[e]) >> (8 * (j & 3)));
+          }
+        }
+        if (sub == 0) {
+          uint8_t* to = dst + kv_scale_at(KIND, NB, b, 8 * h8);
+          if (full) *reinterpret_cast<u32x4*>(to) = u32x4{ds[0], ds[1], ds[2], ds[3]};
+          else
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              if (j >= ta && j < tb) reinterpret_cast<uint16_t*>(to)[j] = static_cast<uint16_t>(ds[j / 2] >> (16 * (j & 1)));
         }
       }
     }
@@ -191,10 +280,8 @@ __device__ __forceinline__ void read_units(const KvIoArgs& a, uint8_t* img) {
   if (!act) return;
   const uint8_t* cache = a.cache[KEYS ? 0 : 1];
   for (int s = blockIdx.z; s < a.b.n_seqs; s += gridDim.z) {
-    int row0, count;
-    a.b.rows(s, row0, count);
-    const int len = a.b.seq_len[s] > 0 ? a.b.seq_len[s] : 0;
-    const int p0 = len - count;
+    const Run r(a.b, s);
+    const int row0 = r.row0, count = r.count, len = r.len, p0 = r.p0;
     for (int base = ((p0 >> 4) + static_cast<int>(blockIdx.x)) * 16; base < len; base += 16 * static_cast<int>(gridDim.x)) {
       if (count == 0) continue;
       const int page = a.b.page(s, base);
@@ -221,8 +308,8 @@ template <int KIND, int NB, bool WRITE>
 __global__ void __launch_bounds__(256) kv_io_kernel(KvIoArgs a) {
   __shared__ UnitLds<KIND, NB> img;
   if constexpr (WRITE) {
-    if (blockIdx.y & 1) write_units<KIND, NB, false>(a, img.bytes);
-    else write_units<KIND, NB, true>(a, img.bytes);
+    if (blockIdx.y & 1) write_values<KIND, NB>(a);
+    else write_keys<KIND, NB>(a, img.bytes);
   } else {
     if (blockIdx.y & 1) read_units<KIND, NB, false>(a, img.bytes);
     else read_units<KIND, NB, true>(a, img.bytes);

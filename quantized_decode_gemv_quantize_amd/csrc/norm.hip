@@ -16,6 +16,7 @@
 #include "decode_args.hpp"
 #include "launch.hpp"
 #include "q8.hpp"
+#include "reduce64.hpp"
 
 namespace qmv {
 
@@ -48,8 +49,7 @@ __device__ __forceinline__ void store4(float* row, int i, int K, const float (&v
 // Sum over the workgroup's T lanes, the same in every lane.
 template <int T>
 __device__ __forceinline__ double block_sum(double v, double* lds) {
-#pragma unroll
-  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m);
+  v = wave_sum(v);
   if (T > kWave) {
     if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
     __syncthreads();
@@ -58,6 +58,17 @@ __device__ __forceinline__ double block_sum(double v, double* lds) {
     for (int w = 0; w < T / kWave; ++w) v += lds[w];
   }
   return v;
+}
+
+// 1 / sqrt(a) by the hardware's estimate and two Newton steps (each doubles
+// its 26 bits): some 15 operations where the exact root and quotient take
+// 60 in a row, while every lane of the workgroup waits.
+__device__ __forceinline__ double rsqrt64(double a) {
+  double r = __builtin_amdgcn_rsq(a);
+  const double half = 0.5 * a;
+  r = r * fma(-half * r, r, 1.5);
+  r = r * fma(-half * r, r, 1.5);
+  return a < INFINITY ? r : a == INFINITY ? 0.0 : a;
 }
 
 // The q8_1 block of a group of 8 lanes that hold 4 values each.
@@ -79,9 +90,13 @@ __device__ __forceinline__ void store_q8_1(uint8_t* col, int i, const float (&y)
   if ((i & 31) == 0) *reinterpret_cast<uint32_t*>(yb) = f2h_bits(d) | (f2h_bits(q8_s(d, sq)) << 16);
 }
 
-__device__ __forceinline__ void scale4(const float (&h)[4], double r, const float* w, int i, int K, float (&y)[4]) {
-  float wv[4] = {1.0f, 1.0f, 1.0f, 1.0f};
-  if (w) load4(w, i, K, wv);
+__device__ __forceinline__ void weights4(const float* w, int i, int K, float (&v)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) v[e] = 1.0f;
+  if (w) load4(w, i, K, v);
+}
+
+__device__ __forceinline__ void scale4(const float (&h)[4], double r, const float (&wv)[4], float (&y)[4]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) y[e] = static_cast<float>(static_cast<double>(h[e]) * r * static_cast<double>(wv[e]));
 }
@@ -99,7 +114,7 @@ __global__ void __launch_bounds__(T) norm_kernel(NormArgs a) {
   for (int64_t j = blockIdx.x; j < a.n; j += gridDim.x, turn ^= 1) {
     const float* x = a.x + j * a.ldx;
     const float* res = a.res ? a.res + j * a.ldr : nullptr;
-    float h[V][4];
+    float h[V][4], w[V][4];
     double ss = 0.0;
 #pragma unroll
     for (int v = 0; v < V; ++v) load4(x, 4 * (v * T + static_cast<int>(threadIdx.x)), a.K, h[v]);
@@ -113,6 +128,8 @@ __global__ void __launch_bounds__(T) norm_kernel(NormArgs a) {
       }
     }
 #pragma unroll
+    for (int v = 0; v < V; ++v) weights4(a.w, 4 * (v * T + static_cast<int>(threadIdx.x)), a.K, w[v]);   // on their way meanwhile
+#pragma unroll
     for (int v = 0; v < V; ++v)
 #pragma unroll
       for (int e = 0; e < 4; ++e) ss = fma(static_cast<double>(h[v][e]), static_cast<double>(h[v][e]), ss);
@@ -123,13 +140,13 @@ __global__ void __launch_bounds__(T) norm_kernel(NormArgs a) {
         if (i < a.K) store4(a.sum + j * a.lds, i, a.K, h[v]);
       }
     }
-    const double r = 1.0 / sqrt(block_sum<T>(ss, lds[turn]) / a.K + a.eps);
+    const double r = rsqrt64(fma(block_sum<T>(ss, lds[turn]), a.inv_K, a.eps));
 #pragma unroll
     for (int v = 0; v < V; ++v) {
       const int i = 4 * (v * T + static_cast<int>(threadIdx.x));
       if (i < a.K) {
         float y[4];
-        scale4(h[v], r, a.w, i, a.K, y);
+        scale4(h[v], r, w[v], y);
         out4(a, j, i, y);
       }
     }
@@ -159,16 +176,17 @@ __global__ void __launch_bounds__(T) norm_long_kernel(NormArgs a) {
       for (int e = 0; e < 4; ++e) ss = fma(static_cast<double>(h[e]), static_cast<double>(h[e]), ss);
       if (sum) store4(sum, i, a.K, h);
     }
-    const double r = 1.0 / sqrt(block_sum<T>(ss, lds[turn]) / a.K + a.eps);
+    const double r = rsqrt64(fma(block_sum<T>(ss, lds[turn]), a.inv_K, a.eps));
     for (int i = 4 * static_cast<int>(threadIdx.x); i < a.K; i += 4 * T) {
-      float h[4], t[4], y[4];
+      float h[4], t[4], w[4], y[4];
+      weights4(a.w, i, a.K, w);
       load4(sum ? sum : x, i, a.K, h);
       if (res && !sum) {
         load4(res, i, a.K, t);
 #pragma unroll
         for (int e = 0; e < 4; ++e) h[e] += t[e];
       }
-      scale4(h, r, a.w, i, a.K, y);
+      scale4(h, r, w, y);
       out4(a, j, i, y);
     }
   }
