@@ -43,7 +43,7 @@ struct SeqSum {
 struct Decision {
   int row, taken, last, best;                  // row drawn from (-1: none)
   float top;
-  double z;
+  double z, refused;                           // sum of the row's weights, weight of the refused token
 };
 
 __device__ __forceinline__ RowStat* row_stats(const VerifyArgs& a) { return reinterpret_cast<RowStat*>(a.ws); }
@@ -276,7 +276,7 @@ struct DecideLds {
   Decision dec;
   int ok[kVWaves], ats[kVWaves];
   float tops[kVWaves];
-  double zs[kVWaves];
+  double zs[kVWaves], es[kVWaves];
 };
 __device__ __forceinline__ void decide(const VerifyArgs& a, const Exp2& exp2, int first, int count, Heat h, DecideLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
@@ -300,12 +300,14 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Exp2& exp2, in
       int at;
       double z;
       join_row(a, exp2, r, h, top, at, z);
-      const bool yes = real && static_cast<double>(u) * draft_weight(q) * z < weight(a, exp2, v, x, top, at, h);
+      const double e = real ? weight(a, exp2, v, x, top, at, h) : 0.0;
+      const bool yes = real && static_cast<double>(u) * draft_weight(q) * z < e;
       if ((tid & 63) == 0) {
         l.ok[wave] = yes && z > 0.0 && z < INFINITY;
         l.tops[wave] = top;
         l.ats[wave] = at;
         l.zs[wave] = z;
+        l.es[wave] = e;
       }
     }
     __syncthreads();
@@ -321,6 +323,7 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Exp2& exp2, in
         l.dec.top = l.tops[w];
         l.dec.best = l.ats[w];
         l.dec.z = l.zs[w];
+        l.dec.refused = l.es[w];
         break;
       }
     }
@@ -512,8 +515,8 @@ __global__ void __launch_bounds__(kVThreads) verify_draw_kernel(VerifyArgs a) {
 }
 
 // Without draft probabilities: decision and draw. Of the chunks' sums only
-// that of the refused token's changes; it is summed again without it, since
-// the difference of the two may be all that is left.
+// that of the refused token's changes. Its difference is off by 2^-53 of the
+// sum: where less than 2^-10 of the chunk is left, that is summed again.
 __global__ void __launch_bounds__(kVThreads) verify_finish_kernel(VerifyArgs a) {
   const Exp2 exp2;
   __shared__ DecideLds l;
@@ -527,16 +530,21 @@ __global__ void __launch_bounds__(kVThreads) verify_finish_kernel(VerifyArgs a) 
     const Decision d = l.dec;
     if (d.row >= 0) {                          // uniform
       const int x = d.last ? -1 : a.draft_tokens[d.row], cx = x >= 0 && x < a.vocab ? x / kChunk : -1;
-      double left = 0.0;
-      if (cx >= 0) left = chunk_sums(a, exp2, d, h, x, cx, lds).rest;
       const RowStat* st = row_stats(a) + static_cast<int64_t>(d.row) * a.chunks;
-      const auto sums = [&](int c) QMV_INLINE {
-        double all;
-        if (h.greedy) all = d.best / kChunk == c ? 1.0 : 0.0;
-        else all = st[c].sum * chunk_scale(a, exp2, st[c].top, d.top, h);
-        return SeqSum{c == cx ? left : all, all};
+      const auto sum_of = [&](int c) QMV_INLINE {
+        if (h.greedy) return d.best / kChunk == c ? 1.0 : 0.0;
+        return st[c].sum * chunk_scale(a, exp2, st[c].top, d.top, h);
       };
-      token = draw(a, exp2, d, h, s, x, sums, dl);
+      double left = 0.0;
+      if (cx >= 0) {
+        const double all = sum_of(cx);
+        left = all - d.refused;
+        if (left < 0x1p-10 * all) left = chunk_sums(a, exp2, d, h, x, cx, lds).rest;
+      }
+      token = draw(a, exp2, d, h, s, x, [&](int c) QMV_INLINE {
+        const double all = sum_of(c);
+        return SeqSum{c == cx ? left : all, all};
+      }, dl);
     }
     put_tokens(a, s, first, d.taken, token);
   }
