@@ -151,7 +151,8 @@ int mmvq_attn_workspace(const mmvq_kv_cache *cache, const mmvq_kv_batch *batch,
  * h / (n_heads / n_kv_heads)). A token at position p sees the keys at
  * positions 0..p, the last `window` of them where window > 0. sinks: NULL or
  * n_heads logits that join each head's softmax as a key without a value. A
- * token that sees no key gets zeros. q and out: fp32, row t at + t*ld, head
+ * token that sees no key gets zeros; an infinite cached value makes the
+ * results of the tokens that see it infinite or NaN, and no others. q and out: fp32, row t at + t*ld, head
  * h at h*head_dim; ld >= n_heads*head_dim, 4-byte aligned; q must be finite.
  * Keys and values enter at their stored precision; scores, softmax and sums
  * are fp32, with q carried as two fp16 parts (21 bits of the row's largest

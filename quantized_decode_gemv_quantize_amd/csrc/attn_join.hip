@@ -33,7 +33,7 @@ AttnShape attn_shape(int kind, int nb, int n_seqs, int n_kv_heads, int group, in
   const int64_t groups = static_cast<int64_t>(n_seqs) * n_kv_heads * s.tiles;
   const int64_t keys = window > 0 && window + static_cast<int64_t>(max_new) < max_len
                            ? window + static_cast<int64_t>(max_new) : max_len;
-  const bool heavy = !s.rows && nb * s.mt >= 8;
+  const bool heavy = !s.rows && nb == 8;
   const auto cut = [&](int64_t target, int64_t least) {
     const int64_t want = (target + groups - 1) / groups, most = (keys + least - 1) / least;
     return want < most ? want : most;

@@ -120,6 +120,8 @@ __device__ __forceinline__ uint32_t keep_mask(int e, int c) {
 }
 // Nonzero if one of the two fp16 is infinite or NaN.
 __device__ __forceinline__ uint32_t wild_bits(uint32_t w) { return ((w & 0x7FFF7FFFu) + 0x04000400u) & 0x80008000u; }
+// The two fp16, zero where infinite or NaN.
+__device__ __forceinline__ uint32_t tamed(uint32_t w) { return w & ~((wild_bits(w) >> 15) * 0xFFFFu); }
 
 // Loads of a wave's 32-key step, as they lie in the cache.
 template <int KIND, int NB>
@@ -236,12 +238,16 @@ struct ValueRegs {
       }
     }
   }
-  // F16: whether any value is infinite or NaN
+  // F16: whether any value is infinite or NaN; zeros in their place
   __device__ __forceinline__ bool wild() const {
     uint32_t any = 0;
 #pragma unroll
     for (int i = 0; i < NB * kPer; ++i) any |= wild_bits(w[i]);
     return any != 0;
+  }
+  __device__ __forceinline__ void tame() {
+#pragma unroll
+    for (int i = 0; i < NB * kPer; ++i) w[i] = tamed(w[i]);
   }
 };
 
@@ -356,19 +362,27 @@ struct Place {
   }
 };
 
-// A wave's rows: q as operands, and the running softmax.
-template <int KIND, int NB, int MT>
+// A wave's rows: q as operands, and the running softmax. QLDS: q in LDS, where
+// the four waves of the keys kernel share it, [tile][block][lo, hi][lane].
+template <int KIND, int NB, int MT, bool QLDS = false>
 struct Rows {
   static constexpr int DT = 2 * NB;
   static constexpr float kShift = weight_shift(KIND);
-  u32x4 qh[MT][NB], ql[MT][NB];
+  u32x4 qh[QLDS ? 1 : MT][QLDS ? 1 : NB], ql[QLDS ? 1 : MT][QLDS ? 1 : NB];
+  const u32x4* q_lds;
   float to_log2[MT];                            // 2^-k of the row's scaling
   int qpos[MT];                                 // position, -1: no row
   float m[MT], l[MT];
   f32x4 o[MT][DT];
 
-  __device__ __forceinline__ void init(const AttnArgs& a, const Place& w, int row0) {
+  __device__ __forceinline__ u32x4 q(int t, int b, int hi) const {
+    if constexpr (QLDS) return q_lds[((t * NB + b) * 2 + hi) * kWave + lane_id()];
+    else return hi ? qh[t][b] : ql[t][b];
+  }
+
+  __device__ __forceinline__ void init(const AttnArgs& a, const Place& w, int row0, u32x4* lds = nullptr) {
     const int lane = lane_id(), g = lane >> 4, col = lane & 15;
+    q_lds = lds;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const int row = row0 + 16 * t + col;
@@ -397,14 +411,25 @@ struct Rows {
       const float up = __uint_as_float(static_cast<uint32_t>(13 - ex + 127) << 23);   // to 2^13..2^14
       to_log2[t] = __uint_as_float(static_cast<uint32_t>(ex - 13 + 127) << 23);
 #pragma unroll
-      for (int b = 0; b < NB; ++b)
+      for (int b = 0; b < NB; ++b) {
+        u32x4 hi, lo;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          uint32_t h, lo;
-          split_f16(v[b][2 * e] * up, v[b][2 * e + 1] * up, h, lo);
-          qh[t][b][e] = h;
-          ql[t][b][e] = lo;
+          uint32_t h, r;
+          split_f16(v[b][2 * e] * up, v[b][2 * e + 1] * up, h, r);
+          hi[e] = h;
+          lo[e] = r;
         }
+        if constexpr (QLDS) {                   // all waves have the same rows: each stores its blocks
+          if ((b & 3) == static_cast<int>(threadIdx.x >> 6)) {
+            lds[((t * NB + b) * 2 + 0) * kWave + lane] = lo;
+            lds[((t * NB + b) * 2 + 1) * kWave + lane] = hi;
+          }
+        } else {
+          qh[t][b] = hi;
+          ql[t][b] = lo;
+        }
+      }
       m[t] = -INFINITY;
       l[t] = 0.0f;
 #pragma unroll
@@ -423,34 +448,36 @@ struct Rows {
     if constexpr (KIND == kKvF16) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
+        if constexpr (QLDS) __builtin_amdgcn_sched_barrier(0);   // a block after the other: registers
         const u32x4 k0 = key(0, b), k1 = key(1, b);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          s[t][0] = mfma_f16(k0, ql[t][b], s[t][0]);
-          s[t][1] = mfma_f16(k1, ql[t][b], s[t][1]);
+          s[t][0] = mfma_f16(k0, q(t, b, 0), s[t][0]);
+          s[t][1] = mfma_f16(k1, q(t, b, 0), s[t][1]);
         }
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
-          s[t][0] = mfma_f16(k0, qh[t][b], s[t][0]);
-          s[t][1] = mfma_f16(k1, qh[t][b], s[t][1]);
+          s[t][0] = mfma_f16(k0, q(t, b, 1), s[t][0]);
+          s[t][1] = mfma_f16(k1, q(t, b, 1), s[t][1]);
         }
       }
     } else {
       f32x4 acc[2][MT][2];
 #pragma unroll
       for (int b = 0; b <= NB; ++b) {
+        if constexpr (QLDS) __builtin_amdgcn_sched_barrier(0);   // a block after the other: registers
         if (b < NB) {
           const u32x4 k0 = key(0, b), k1 = key(1, b);
           f32x4 (&c)[MT][2] = acc[b & 1];
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            c[t][0] = mfma_f16(k0, ql[t][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-            c[t][1] = mfma_f16(k1, ql[t][b], f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            c[t][0] = mfma_f16(k0, q(t, b, 0), f32x4{0.0f, 0.0f, 0.0f, 0.0f});
+            c[t][1] = mfma_f16(k1, q(t, b, 0), f32x4{0.0f, 0.0f, 0.0f, 0.0f});
           }
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
-            c[t][0] = mfma_f16(k0, qh[t][b], c[t][0]);
-            c[t][1] = mfma_f16(k1, qh[t][b], c[t][1]);
+            c[t][0] = mfma_f16(k0, q(t, b, 1), c[t][0]);
+            c[t][1] = mfma_f16(k1, q(t, b, 1), c[t][1]);
           }
         }
         if (b > 0) {
@@ -528,6 +555,7 @@ struct Rows {
     for (int t = 0; t < MT; ++t) parts(t, s, scale(0), ph[0][t], pl[0][t]);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      if constexpr (QLDS) __builtin_amdgcn_sched_barrier(0);
       const int now = KIND == kKvF16 ? 0 : b & 1;
       const u32x4 v0 = value(2 * b), v1 = value(2 * b + 1);
 #pragma unroll
@@ -547,25 +575,30 @@ struct Rows {
     }
   }
 
-  // F16, an infinity or NaN among the step's values: one token after the
-  // other, added only to the rows that see it (0 * inf is NaN).
-  template <class V>
-  __device__ __forceinline__ void accumulate_wild(const AttnArgs& a, int t, int t0, V value, const f32x4 (&s)[MT][2]) {
-    const int g = lane_id() >> 4;
-    u32x4 hi, lo;
-    parts(t, s, u32x4{}, hi, lo);
+  // F16: the infinities and NaN among the step's values, which accumulate()
+  // meets as zeros, token by token and only into the rows that see them (a
+  // weight of 0 times one of them is NaN). Read from the cache again: rare,
+  // and few registers.
+  __device__ __forceinline__ void add_wild(const AttnArgs& a, const Place& w, int t, int t0, const f32x4 (&s)[MT][2]) {
+    const int lane = lane_id(), g = lane >> 4, col = lane & 15;
+#pragma unroll 1
     for (int tok = 0; tok < kStep; ++tok) {
-      const bool mine = (tok >> 3) == g, see = t0 + tok <= qpos[t] && (a.window <= 0 || t0 + tok > qpos[t] - a.window);
-      u32x4 mask = {0u, 0u, 0u, 0u};
+      const int pos = t0 + tok, page = a.b.page(w.s, pos);
+      if (pos >= w.keys || page < 0) continue;  // uniform
+      float own = s[t][0][0];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) mask[e] = mine && (tok & 7) >> 1 == e ? (tok & 1 ? 0xFFFF0000u : 0xFFFFu) : 0u;
+      for (int j = 1; j < 8; ++j) own = (tok & 7) == j ? s[t][j / 4][j & 3] : own;
+      const float weight = __shfl(own, (tok >> 3) * 16 + col);
+      const bool see = pos <= qpos[t] && (a.window <= 0 || pos > qpos[t] - a.window);
+      const uint8_t* unit = a.v + a.b.unit(page, w.head, pos) * kv_unit_bytes(KIND, NB);
 #pragma unroll
       for (int d = 0; d < DT; ++d) {
-        const u32x4 vop = value(d) & mask;
-        f32x4 acc = mfma_f16(vop, lo & mask, f32x4{0.0f, 0.0f, 0.0f, 0.0f});
-        acc = mfma_f16(vop, hi & mask, acc);
+        asm volatile("" ::: "memory");          // one tile's loads at a time: registers, not speed
 #pragma unroll
-        for (int i = 0; i < 4; ++i) o[t][d][i] += see ? acc[i] : 0.0f;
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t v = ld_u16(unit + kv_value_at(KIND, tok & 15, d / 2, 16 * (d & 1) + 4 * g + i));
+          if (see && (v & 0x7C00u) == 0x7C00u) o[t][d][i] = fmaf(weight, h2f(v), o[t][d][i]);
+        }
       }
     }
   }
@@ -573,8 +606,10 @@ struct Rows {
 
 // Few rows: the waves share the keys.
 template <int KIND, int NB, int MT>
-__global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_keys_kernel(AttnArgs a) {
+  constexpr bool QLDS = NB * MT >= 8;           // else its registers would leave one wave a SIMD
   constexpr int D = 32 * NB, DT = 2 * NB, RW = 16 * MT, DP = D + 4;   // rows a bank apart
+  // q, and after the walk the waves' O
   __shared__ __attribute__((aligned(16))) float lds_o[4 * RW * DP];
   __shared__ float lds_ml[4 * RW * 2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
@@ -597,9 +632,12 @@ __global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_k
       pg = step_pages<KIND, NB>(a, ids, w.head, t0);
       kr.load(a.k + (kh ? pg.off[1] : pg.off[0]), a.k + (vh ? pg.off[1] : pg.off[0]));
     }
-    Rows<KIND, NB, MT> r;
-    r.init(a, w, row0);
+    Rows<KIND, NB, MT, QLDS> r;
+    if (QLDS) __syncthreads();                  // the tile before is read out
+    r.init(a, w, row0, reinterpret_cast<u32x4*>(lds_o));
+    if (QLDS) __syncthreads();
     for (; t0 < t_end; t0 += 4 * kStep) {
+      if (QLDS) asm volatile("" ::: "memory");  // q is read each step, not kept
       ValueRegs<KIND, NB> vr;
       vr.load(a.v + (vh ? pg.off[1] : pg.off[0]));
       f32x4 s[MT][2];
@@ -619,23 +657,27 @@ __global__ void __launch_bounds__(kAttnThreads, NB * MT < 8 ? 2 : 1) attn_keys_k
 #pragma unroll
         for (int t = 0; t < MT; ++t) r.hide(a, t, t0 + 8 * g, real, s);
         vr.keep(real);
-        if constexpr (KIND == kKvF16) wild = __any(vr.wild());
+        if constexpr (KIND == kKvF16) {
+          wild = __any(vr.wild());              // (of a whole step every row sees them)
+          if (wild) vr.tame();
+        }
       }
       float e5[8];
       if constexpr (KIND != kKvF16) vr.exponents(e5);
 #pragma unroll
       for (int t = 0; t < MT; ++t) r.weigh(t, e5, s);
       const auto value = [&](int d) QMV_INLINE { return vr.operand(d / 2, d & 1); };
-      if (!wild) {
-        r.accumulate(value, [&](int b) QMV_INLINE { return vr.sc[KIND == kKvF16 ? 0 : b]; }, s);
-      } else if constexpr (KIND == kKvF16) {
+      if constexpr (KIND == kKvF16) {
+        if (wild) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) r.accumulate_wild(a, t, t0, value, s);
+          for (int t = 0; t < MT; ++t) r.add_wild(a, w, t, t0, s);
+        }
       }
+      r.accumulate(value, [&](int b) QMV_INLINE { return vr.sc[KIND == kKvF16 ? 0 : b]; }, s);
     }
 
     // the waves' shares joined: each scaled to the common maximum
-    __syncthreads();                            // the tile before is read out
+    __syncthreads();                            // q is not needed any more, the tile before is read out
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       const float l = row_sum(r.l[t]);
@@ -684,7 +726,7 @@ struct StepLds {
   uint32_t ksc[KIND == kKvF16 ? 1 : NB][16];    // scales of the 32 tokens, two a word
   uint32_t vsc[KIND == kKvF16 ? 1 : NB][16];
   float e5[kStep];                              // exponent fields
-  int wild[4];
+  int wild[4];                                  // F16, of each wave's share: an infinity or NaN was among the values
 };
 
 // A lane's share of a step on its way to LDS: runs of block b of operand lane
@@ -785,7 +827,10 @@ struct StepRegs {
             for (int e = 0; e < 4; ++e) x[e] &= keep_mask(e, real);
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) any |= wild_bits(x[e]);
+          for (int e = 0; e < 4; ++e) {
+            any |= wild_bits(x[e]);
+            x[e] = tamed(x[e]);
+          }
           lds.v[2 * b + half][at] = x;
         } else if constexpr (KIND == kKvQ8) {
           lds.v[2 * b + half][at] = operand_q8(v[i][2 * half], v[i][2 * half + 1]);
@@ -865,12 +910,10 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
                  [&](int b) QMV_INLINE { return *reinterpret_cast<const u32x4*>(&st.ksc[KIND == kKvF16 ? 0 : b][4 * g]); }, s);
         __builtin_amdgcn_s_setprio(0);
         const bool whole = __all(ok0 && ok1) && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
-        bool wild = false;
         if (!whole) {
           const int real = (g >> 1 ? ok1 : ok0) ? w.keys - (t0 + 8 * g) : 0;
 #pragma unroll
           for (int t = 0; t < MT; ++t) r.hide(a, t, t0 + 8 * g, real, s);
-          if constexpr (KIND == kKvF16) wild = st.wild[0] | st.wild[1] | st.wild[2] | st.wild[3];
         }
         float e5[8];
         if constexpr (KIND != kKvF16) {
@@ -884,14 +927,15 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel
 #pragma unroll
         for (int t = 0; t < MT; ++t) r.weigh(t, e5, s);
         const auto value = [&](int d) QMV_INLINE { return st.v[d][lane]; };
-        if (!wild) {
-          r.accumulate(value, [&](int b) QMV_INLINE {
-            return *reinterpret_cast<const u32x4*>(&st.vsc[KIND == kKvF16 ? 0 : b][4 * g]);
-          }, s);
-        } else if constexpr (KIND == kKvF16) {
+        if constexpr (KIND == kKvF16) {
+          if (st.wild[0] | st.wild[1] | st.wild[2] | st.wild[3]) {
 #pragma unroll
-          for (int t = 0; t < MT; ++t) r.accumulate_wild(a, t, t0, value, s);
+            for (int t = 0; t < MT; ++t) r.add_wild(a, w, t, t0, s);
+          }
         }
+        r.accumulate(value, [&](int b) QMV_INLINE {
+          return *reinterpret_cast<const u32x4*>(&st.vsc[KIND == kKvF16 ? 0 : b][4 * g]);
+        }, s);
       }
       if (more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
       __syncthreads();

@@ -286,12 +286,15 @@ def test_attention_holes_and_rows_without_keys(kind, new):
     assert (got[p.start[1]:p.start[2]] == 0).all() and (got[p.start[2]] == 0).all()
 
 
+@pytest.mark.parametrize("window,bad_at", [(0, -2), (60, 70), (0, 40)])
 @pytest.mark.parametrize("new", [4, 100])
-def test_attention_infinite_values_stay_hidden(new):
-    """F16: an infinite value of a later token, and of one behind the window,
-    reaches only the rows that see it."""
-    p = R.Paged("f16", 64, 1, 16, [new], [new + 60], seed=9)
-    bad = new + 60 - 2                                 # the last token but one
+def test_attention_infinite_values_stay_hidden(new, window, bad_at):
+    """F16: an infinite value of a later token, of one behind the window of
+    some rows, and of one that all rows see, reaches the rows that see it
+    (whose results are infinite or NaN) and no other."""
+    base = 60 if bad_at < 0 else 100                   # position of the first new token
+    p = R.Paged("f16", 64, 1, 16, [new], [new + base], seed=9)
+    bad = new + base + bad_at if bad_at < 0 else bad_at
 
     def change(p, k, v):
         rows = dev(np.full((1, 64), 1e6, np.float32))  # infinite in fp16
@@ -308,12 +311,16 @@ def test_attention_infinite_values_stay_hidden(new):
     out = nan(new, 128)
     batch = p.batch()
     size = B.mmvq_attn_workspace(p.cache, batch, 2)
-    B.mmvq_attn(p.cache, batch, dev(q), 128, 2, 0.125, 0, None, out, 128, torch.empty(size + 16, dtype=torch.uint8, device="cuda:0"), size)
+    B.mmvq_attn(p.cache, batch, dev(q), 128, 2, 0.125, window, None, out, 128,
+                torch.empty(size + 16, dtype=torch.uint8, device="cuda:0"), size)
     got = host(out).reshape(new, 2, 64)
-    ref, mag, smax = R.attention(q.reshape(new, 2, 64), k[0], v[0], 0.125, 60)
+    ref, mag, smax = R.attention(q.reshape(new, 2, 64), k[0], v[0], 0.125, base, window)
     tol = R.attention_tolerance(ref, mag, smax, v[0], 64)
-    assert (np.abs(got - ref) <= tol)[:new - 2].all()
-    assert np.isinf(got[new - 2:]).all()
+    pos = base + np.arange(new)
+    sees = (bad <= pos) & (bad > pos - window if window else True)
+    assert sees.any()
+    assert (np.abs(got - ref) <= tol)[~sees].all()
+    assert not np.isfinite(got[sees]).any()
 
 
 @pytest.mark.parametrize("kind", list(R.KINDS))
