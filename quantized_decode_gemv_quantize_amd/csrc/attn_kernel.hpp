@@ -607,7 +607,7 @@ struct Rows {
 // Few rows: the waves share the keys.
 template <int KIND, int NB, int MT>
 __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_keys_kernel(AttnArgs a) {
-  constexpr bool QLDS = NB * MT >= 8;           // else its registers would leave one wave a SIMD
+  constexpr bool QLDS = NB * MT >= 8 || (KIND == kKvF16 && NB == 4);   // else its registers would leave one wave a SIMD, or spill
   constexpr int D = 32 * NB, DT = 2 * NB, RW = 16 * MT, DP = D + 4;   // rows a bank apart
   // q, and after the walk the waves' O
   __shared__ __attribute__((aligned(16))) float lds_o[4 * RW * DP];
@@ -867,7 +867,7 @@ struct StepRegs {
 
 // Many rows: the waves have rows of their own and share each step's operands.
 template <int KIND, int NB, int MT>
-__global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_rows_kernel(AttnArgs a) {
+__global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) {
   constexpr int D = 32 * NB, DT = 2 * NB, RW = 16 * MT, RT = 4 * RW;
   __shared__ StepLds<KIND, NB> lds[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
