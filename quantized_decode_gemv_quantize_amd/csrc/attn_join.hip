@@ -1,52 +1,7 @@
-// attn_join.hip - the shape of an attention launch, and the join of the
-// ranges that a long cache is cut into.
+// attn_join.hip - the join of the ranges that a long cache is cut into.
 #include "attn_kernel.hpp"
 
 namespace qmv {
-
-constexpr int kMaxSplits = 128;                 // two a lane in the join
-constexpr int kSplitKeys = 256;                 // fewest keys worth a workgroup of their own
-constexpr int kLongKeys = 2048;                 // and where they are cut beyond one round of workgroups
-constexpr int kCus = 256;
-
-// Rows of one key/value head (new tokens times query heads that share it):
-// up to 16, 32 or (D = 64) 48 fit the tiles of one wave, and the four waves
-// share the keys; beyond 64 each wave takes rows of its own.
-//
-// The keys are cut until the chip is filled once: two workgroups a compute
-// unit, one where a wave needs more than half of the registers (D 16 MT >=
-// 256; 20 us with 256 workgroups against 29 with 512 for 3 tokens of 16 heads
-// of 256 over 20000). No range is shorter than kSplitKeys: at 8191 keys of
-// one user 11.0 us, 13.6 with ranges of 512 and 11.9 with 128. Several rows a
-// wave over quantized keys are bound by arithmetic, and there twice as many
-// ranges even out sequences of different lengths as long as they stay long
-// (16 users of 5300..16000 keys 70 -> 64 us; ranges of 250 keys 28 -> 39 us).
-AttnShape attn_shape(int kind, int nb, int n_seqs, int n_kv_heads, int group, int max_new, int max_len, int window) {
-  (void)kind;
-  const int64_t rows = static_cast<int64_t>(max_new) * group;
-  AttnShape s;
-  s.rows = rows > 64;
-  s.mt = nb < 8 && rows > 16 ? 2 : 1;
-  if (nb == 2 && rows > 32 && rows <= 48) s.mt = 3;
-  const int rt = 16 * s.mt * (s.rows ? 4 : 1);
-  s.tiles = static_cast<int>((rows + rt - 1) / rt);
-  const int64_t groups = static_cast<int64_t>(n_seqs) * n_kv_heads * s.tiles;
-  const int64_t keys = window > 0 && window + static_cast<int64_t>(max_new) < max_len
-                           ? window + static_cast<int64_t>(max_new) : max_len;
-  const bool heavy = !s.rows && nb == 8;
-  const auto cut = [&](int64_t target, int64_t least) {
-    const int64_t want = (target + groups - 1) / groups, most = (keys + least - 1) / least;
-    return want < most ? want : most;
-  };
-  int64_t splits = cut(heavy ? kCus : 2 * kCus, kSplitKeys);
-  if (!s.rows && s.mt > 1 && !heavy) {
-    const int64_t more = cut(4 * kCus, kLongKeys);
-    splits = more > splits ? more : splits;
-  }
-  if (splits > kMaxSplits) splits = kMaxSplits;
-  s.splits = static_cast<int>(splits < 1 ? 1 : splits);
-  return s;
-}
 
 __device__ __forceinline__ float wave_max(float v) {
   v = fmaxf(v, dpp_f<kDppXor1>(v));

@@ -44,7 +44,6 @@ typedef _Float16 half2v __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAttnThreads = 256;
-constexpr int kStep = 32;                       // keys a step
 
 // K above: w d <= 2^(K - e) 2^(e - 14) for a quantized token, w <= 2^K (F16).
 // M may lag the true maximum by kLag, so that O is rescaled a few times a
@@ -138,7 +137,7 @@ struct KeyRegs {
     for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
-        const uint8_t* src = unit + (((m * NP + p) * 4 + g) * 8 + (l & 7)) * PS;
+        const uint8_t* src = unit + kv_key_piece(KIND, NB, m, p, g, l & 7);
         uint32_t* dst = w + (m * NP + p) * PW;
         if constexpr (PS == 16) {
           const u32x4 r = ld_a16_x4(src);
@@ -185,16 +184,16 @@ struct ValueRegs {
       if constexpr (KIND == kKvF16) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const u32x4 v = ld_a16_x4(unit + (((b * 2 + half) * 2 + h8) * 16 + r) * 16);
+          const u32x4 v = ld_a16_x4(unit + kv_value_run(KIND, b, half, h8, r));
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[8 * b + 4 * half + e] = v[e];
         }
       } else if constexpr (KIND == kKvQ8) {
-        const u32x4 v = ld_a16_x4(unit + ((b * 2 + h8) * 16 + r) * 16);
+        const u32x4 v = ld_a16_x4(unit + kv_value_run(KIND, b, 0, h8, r));
 #pragma unroll
         for (int e = 0; e < 4; ++e) w[4 * b + e] = v[e];
       } else {
-        const u32x2 v = ld_x2(unit + ((b * 2 + h8) * 16 + r) * 8);
+        const u32x2 v = ld_x2(unit + kv_value_run(KIND, b, 0, h8, r));
         w[2 * b] = v.x;
         w[2 * b + 1] = v.y;
       }
@@ -354,11 +353,9 @@ struct Place {
     const int lo = base + a.group.div(r0), hi = base + a.group.div(r1);
     const int k_end = hi + 1 < keys ? hi + 1 : keys;
     const int k_beg = a.window > 0 && lo - a.window + 1 > 0 ? (lo - a.window + 1) & ~(kStep - 1) : 0;
-    const int steps = k_end > k_beg ? (k_end - k_beg + kStep - 1) / kStep : 0;
-    const int per = a.splits.div(steps + static_cast<int>(a.splits.d) - 1);
-    const int s0 = split * per < steps ? split * per : steps, s1 = s0 + per < steps ? s0 + per : steps;
-    beg = k_beg + s0 * kStep;
-    end = k_beg + s1 * kStep;
+    const KeyRange k = split_keys(k_beg, k_end, a.splits, split);
+    beg = k.beg;
+    end = k.end;
   }
 };
 
@@ -754,9 +751,9 @@ struct StepRegs {
       const uint8_t* ku = a.k + (row >> 3 ? pg.off[1] : pg.off[0]);
 #pragma unroll
       for (int m = 0; m < 2; ++m) {
-        constexpr int PS = kv_piece(KIND, NB), NP = kv_lane_bytes(KIND, NB) / PS;
+        constexpr int PS = kv_piece(KIND, NB);
         const int off = b * kv_run(KIND);
-        const uint8_t* src = ku + (((m * NP + off / PS) * 4 + g) * 8 + (row & 7)) * PS + off % PS;
+        const uint8_t* src = ku + kv_key_piece(KIND, NB, m, off / PS, g, row & 7) + off % PS;
         if constexpr (KIND == kKvF16) {
           const u32x4 r = ld_a16_x4(src);
 #pragma unroll
@@ -773,16 +770,16 @@ struct StepRegs {
       if constexpr (KIND == kKvF16) {
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
-          const u32x4 r = ld_a16_x4(vu + (((b * 2 + half) * 2 + (g & 1)) * 16 + row) * 16);
+          const u32x4 r = ld_a16_x4(vu + kv_value_run(KIND, b, half, g & 1, row));
 #pragma unroll
           for (int e = 0; e < 4; ++e) v[i][4 * half + e] = r[e];
         }
       } else if constexpr (KIND == kKvQ8) {
-        const u32x4 r = ld_a16_x4(vu + ((b * 2 + (g & 1)) * 16 + row) * 16);
+        const u32x4 r = ld_a16_x4(vu + kv_value_run(KIND, b, 0, g & 1, row));
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[i][e] = r[e];
       } else {
-        const u32x2 r = ld_x2(vu + ((b * 2 + (g & 1)) * 16 + row) * 8);
+        const u32x2 r = ld_x2(vu + kv_value_run(KIND, b, 0, g & 1, row));
         v[i][0] = r.x;
         v[i][1] = r.y;
       }

@@ -104,7 +104,7 @@ int check_attn(const mmvq_kv_cache* c, const mmvq_kv_batch* b, int n_heads) {
 
 AttnShape shape_of(const mmvq_kv_cache* c, const mmvq_kv_batch* b, int n_heads, int window) {
   const int most = b->max_new < b->n_tokens ? b->max_new : b->n_tokens;
-  return attn_shape(kv_kind(c->type), c->head_dim / 32, b->n_seqs, c->n_kv_heads, n_heads / c->n_kv_heads, most,
+  return attn_shape(c->head_dim / 32, b->n_seqs, c->n_kv_heads, n_heads / c->n_kv_heads, most,
                     b->max_len, window);
 }
 

@@ -6,27 +6,10 @@
 #include <stdint.h>
 
 #include "../../include/mmvq_decode.h"
+#include "decode_plan.hpp"
 #include "kv_layout.hpp"
 
 namespace qmv {
-
-// Division of 0 <= n < 2^31 by a number that the host knows: the multiplier
-// is ceil(2^32 (2^s - d) / d) + ..., the usual round-up form. A 32-bit division
-// on the device is some forty dependent instructions, and a workgroup's place
-// takes a dozen of them before its first load.
-struct FastDiv {
-  uint32_t d, mul, shift;
-  FastDiv() = default;
-  explicit FastDiv(uint32_t n) : d(n), mul(0), shift(0) {
-    while ((uint64_t(1) << shift) < n) ++shift;
-    mul = static_cast<uint32_t>((((uint64_t(1) << shift) - n) << 32) / n + 1);
-  }
-#ifndef QMV_HOST_MODEL
-  __device__ __forceinline__ int div(int n) const {
-    return static_cast<int>((__umulhi(static_cast<uint32_t>(n), mul) + static_cast<uint32_t>(n)) >> shift);
-  }
-#endif
-};
 
 // Ragged batch and page geometry on the device side; the checks of the
 // values that the host cannot see are here.
@@ -84,12 +67,6 @@ struct AttnArgs {
   float2* part_ml;         // [row][head][split]
 };
 
-struct AttnShape {
-  int mt;                  // 16-row tiles a wave
-  bool rows;               // waves own rows (else they share the keys)
-  int tiles, splits;
-};
-
 struct VerifyArgs {
   const float* target;
   const float* temperature;
@@ -121,7 +98,6 @@ int launch_norm(const NormArgs& a, hipStream_t st);
 int launch_dequantize_q8_1(const uint8_t* yq, int64_t K, int64_t n, float* x, int64_t ldx, hipStream_t st);
 int launch_kv_write(int kind, int nb, const KvIoArgs& a, int max_new, hipStream_t st);
 int launch_kv_read(int kind, int nb, const KvIoArgs& a, int max_new, hipStream_t st);
-AttnShape attn_shape(int kind, int nb, int n_seqs, int n_kv_heads, int group, int max_new, int max_len, int window);
 int launch_attn_f16(int nb, const AttnShape& s, const AttnArgs& a, hipStream_t st);
 int launch_attn_q8_0(int nb, const AttnShape& s, const AttnArgs& a, hipStream_t st);
 int launch_attn_q4_0(int nb, const AttnShape& s, const AttnArgs& a, hipStream_t st);

@@ -265,7 +265,7 @@ __global__ void __launch_bounds__(256) kv_io_kernel(KvIoArgs a) {
 
 template <int KIND, int NB, bool WRITE>
 int launch_io_as(const KvIoArgs& a, int max_new, hipStream_t st) {
-  const int units = (max_new + 14) / 16 + 1;       // a run of max_new tokens touches at most so many
+  const int units = units_of(max_new);
   constexpr int PER = WRITE ? 256 / (16 * NB) : 1; // units a workgroup
   // The writer has the heads side by side, so that the rows of one unit's
   // tokens are read together (31.7 -> 29.5 us for 8192 F16 tokens of 8 heads

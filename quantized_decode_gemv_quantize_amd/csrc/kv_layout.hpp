@@ -26,8 +26,10 @@
 #ifndef QMV_HOST_MODEL
 #include <hip/hip_runtime.h>
 #define KV_HD __host__ __device__ __forceinline__
+#define KV_DEV __device__ __forceinline__
 #else
 #define KV_HD inline
+#define KV_DEV inline
 #endif
 
 namespace qmv {
@@ -68,11 +70,17 @@ KV_HD constexpr int kv_value_at(int kind, int tt, int b, int c) {
          : kind == kKvQ8 ? (((b * 2 + h8) * 16 + r) * 2 + half) * 8 + j
                          : ((b * 2 + h8) * 16 + r) * 8 + j;
 }
-// Token of the unit to which the 4-byte word `w` of the key codes belongs.
-KV_HD constexpr int kv_key_token(int kind, int nb, int w) {
+// Byte of piece p of lane group g, row rr of key tile m; a lane's pieces in
+// turn are its runs of the blocks in turn.
+KV_HD constexpr int kv_key_piece(int kind, int nb, int m, int p, int g, int rr) {
   const int ps = kv_piece(kind, nb);
-  const int rr = w * 4 / ps % 8, m = w * 4 / (kv_code_bytes(kind, nb) / 2);
-  return rr / 4 * 8 + m * 4 + rr % 4;
+  return (((m * (kv_lane_bytes(kind, nb) / ps) + p) * 4 + g) * 8 + rr) * ps;
+}
+// Byte of a lane's values of block b (F16: of each 16-dim half) for tokens
+// 8 h8..: 8 tokens of dim r, of both halves for the quantized types.
+KV_HD constexpr int kv_value_run(int kind, int b, int half, int h8, int r) {
+  return kind == kKvF16 ? (((b * 2 + half) * 2 + h8) * 16 + r) * 16
+                        : ((b * 2 + h8) * 16 + r) * (kind == kKvQ8 ? 16 : 8);
 }
 
 }  // namespace qmv

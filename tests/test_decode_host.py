@@ -2,6 +2,9 @@
 host-only queries, and every refusal (arguments are checked before any device
 is touched)."""
 import ctypes
+import os
+import shutil
+import subprocess
 
 import pytest
 
@@ -170,3 +173,21 @@ def test_verify_workspace(L):
         with pytest.raises(B.MMVQError) as e:
             B.mmvq_verify_workspace(*bad)
         assert e.value.code == B.ERR_SHAPE
+
+
+def test_layout_and_launch_arithmetic(tmp_path):
+    """The kernels' own headers on the CPU: every byte of a cache unit is one
+    value's, operand loads find what the writer stores, ranges of keys cover
+    them once, divisions by multipliers are exact, launch shapes stay in their
+    limits."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    clang = next((c for c in ("/opt/rocm/llvm/bin/clang++", shutil.which("clang++")) if c and os.path.exists(c)), None)
+    if clang is None:
+        pytest.skip("clang++ (host) not available")
+    exe = tmp_path / "decode"
+    subprocess.check_call([clang, "-std=c++17", "-O2", "-Wall", "-DQMV_HOST_MODEL", "-I",
+                           os.path.join(root, "quantized_decode_gemv_quantize_amd", "csrc"), "-o", str(exe),
+                           os.path.join(root, "tests", "host_model", "decode.cpp")])
+    res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout[-4000:]
+    assert "0 failing check(s)" in res.stdout

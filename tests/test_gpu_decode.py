@@ -341,6 +341,42 @@ def test_attention_scales(kind, qscale, kscale):
     run_attention(p, 2, seed=5, qscale=qscale, kscale=kscale)
 
 
+def test_offsets_past_32_bits():
+    """A cache of more than 4 GiB: its last pages are written, read and attended."""
+    p = R.Paged("f16", 256, 8, 1024, [3], [1030], seed=17, spare=1100)
+    assert p.k.numel() > 1 << 32
+    p.table[0] = [p.n_pages - 1, p.n_pages - 2]
+    p.upload()
+    run_attention(p, 8, seed=6)
+    k, v = nan(3, 8 * 256), nan(3, 8 * 256)
+    B.mmvq_kv_read(p.cache, p.batch(), k, 8 * 256, v, 8 * 256)
+    assert np.isfinite(host(k)).all() and np.isfinite(host(v)).all()
+    assert (host(p.k[:1090]) == 0xA5).all()
+
+
+def test_rows_past_32_bits():
+    """Activation rows whose strides pass 2^31 floats."""
+    import torch
+    ld = (1 << 30) + 4
+    p = R.Paged("q8_0", 64, 1, 16, [3], [20], seed=18)
+    rng = np.random.default_rng(18)
+    k, v = p.fill(rng)
+    q = rng.standard_normal((3, 64)).astype(np.float32)
+    wide = torch.empty(2 * ld + 64, device="cuda:0")
+    out = torch.empty(2 * ld + 64, device="cuda:0")
+    for i in range(3):
+        wide[i * ld:i * ld + 64] = dev(q[i])
+    B.mmvq_attn(p.cache, p.batch(), wide, ld, 1, 0.125, 0, None, out, ld, None, 0)
+    got = np.stack([host(out[i * ld:i * ld + 64]) for i in range(3)])[:, None]
+    ref, mag, smax = R.attention(q[:, None], k[0], v[0], 0.125, 17)
+    assert (np.abs(got - ref) <= R.attention_tolerance(ref, mag, smax, v[0], 64)).all()
+    y = torch.empty(2 * ld + 64, device="cuda:0")
+    B.mmvq_add_rms_norm(wide, 64, 3, ld, None, 0, None, EPS, None, 0, y, ld, None)
+    _, e = R.rms_norm(q, None, None, EPS)
+    got = np.stack([host(y[i * ld:i * ld + 64]) for i in range(3)])
+    assert (np.abs(got - e) <= np.abs(e) * HALF32 * (1 + 1e-6)).all()
+
+
 # --- verification ------------------------------------------------------------------------
 
 def run_verify(target, kind, temp, tok, dp, start, ua, us, wide, ldt=None, ldd=None):
