@@ -48,8 +48,10 @@ enum { MMVQ_F16 = 1 };
  *   y[i] = fp32(h[i] * (1/sqrt(sum(h^2)/K + eps)) * weight[i]), the sum,
  *   the root and both products in 64 bits, rounded once (weight NULL: 1).
  * Outputs, each NULL if not wanted: sum_out (h), y (fp32), y_q (q8_1 columns
- * of y by the rule of mmvq_quantize_q8_1: n * K/32 blocks of 36 bytes, what
- * mmvq and its variants take). sum_out may be x or residual itself (same
+ * of y, n * K/32 blocks of 36 bytes, what mmvq and its variants take: q =
+ * roundf(y/d) and s = d*sum(q) as mmvq_quantize_q8_1 has them, with d =
+ * max|y| * fp32(1/127) in fp32, the product with the rounded reciprocal,
+ * within one unit in the last place of that function's quotient). sum_out may be x or residual itself (same
  * pointer and stride), and y may be x; otherwise the buffers do not overlap.
  * Requires 1 <= K <= 2^24, n >= 0 and n*K <= 2^40, every ld >= K, K % 32 == 0
  * with y_q, and at least one of y and y_q (MMVQ_ERR_NULL). fp32 buffers
@@ -70,8 +72,8 @@ int mmvq_dequantize_q8_1(const void *y_q, int64_t K, int64_t n, float *x,
  * mmvq_kv_page_bytes each (16-byte aligned); a page holds page_size
  * consecutive tokens of one sequence for every key/value head.
  *   type       MMVQ_F16 (nearest even; beyond 65504 infinite), MMVQ_Q8_0
- *              (per 32 values of a head: d = max|x|/127 in fp32, q =
- *              roundf(x/d), 0 where d is 0; value fp16(d)*q) or MMVQ_Q4_0
+ *              (per 32 values of a head: d = max|x| * fp32(1/127) in
+ *              fp32, q = roundf(x/d), 0 where d is 0; value fp16(d)*q) or MMVQ_Q4_0
  *              (d = m/-8 with m the value of largest magnitude, the first of
  *              equals; q = min(15, floor(x/d + 8.5)), 8 where d is 0; value
  *              fp16(d)*(q - 8)); a d beyond 65504 is stored as 65504; the

@@ -69,7 +69,7 @@ __device__ __forceinline__ float quad_codes(const float (&x)[4], uint32_t& w) {
     amax = fmaxf(amax, dpp_f<kDppXor1>(amax));
     amax = fmaxf(amax, dpp_f<kDppXor2>(amax));
     amax = fmaxf(amax, dpp_f<kDppMirror8>(amax));
-    const float d = q8_scale(amax);
+    const float d = q8_scale_product(amax);
     uint32_t packed[1];
     int sum = 0;
     q8_quant_block(raw, d, packed, sum);

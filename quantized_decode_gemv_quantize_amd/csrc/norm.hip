@@ -78,7 +78,7 @@ __device__ __forceinline__ void store_q8_1(uint8_t* col, int i, const float (&y)
   amax = fmaxf(amax, dpp_f<kDppXor1>(amax));
   amax = fmaxf(amax, dpp_f<kDppXor2>(amax));
   amax = fmaxf(amax, dpp_f<kDppMirror8>(amax));
-  const float d = q8_scale(amax);
+  const float d = q8_scale_product(amax);
   int sq = 0;
   uint32_t packed[1];
   q8_quant_block(raw, d, packed, sq);

@@ -18,10 +18,10 @@ def f32(x):
 
 def q8_codes(x):
     """Codes and fp16 scales of [..., 32] values by the q8 rule: scale and
-    quotient are fp32 (a 64-bit quotient of fp32 values rounded to fp32 is the
-    fp32 quotient), roundf goes away from zero."""
+    quotient are fp32 (the 64-bit product and quotient of fp32 values rounded
+    to fp32 are the fp32 ones), roundf goes away from zero."""
     x = np.asarray(x, dtype=np.float64)
-    d = f32(np.abs(x).max(-1, keepdims=True) / 127.0)
+    d = f32(np.abs(x).max(-1, keepdims=True) * float(np.float32(1.0) / np.float32(127.0)))
     safe = np.where(d == 0, 1.0, d)
     t = f32(x / safe)
     q = np.where(d == 0, 0.0, np.copysign(np.floor(np.abs(t) + 0.5), t))

@@ -19,6 +19,11 @@ def nan(*shape):
     return torch.full(shape, float("nan"), device="cuda:0")
 
 
+def d32(blk):
+    """fp32 scales of [..., 32] values, before they are stored as fp16."""
+    return R.f32(np.abs(blk.astype(np.float64)).max(-1, keepdims=True) * float(np.float32(1.0) / np.float32(127.0)))
+
+
 # --- norm -------------------------------------------------------------------------
 
 @pytest.mark.parametrize("n,K,ldx,off", [
@@ -41,16 +46,16 @@ def test_norm_q8_1(n, K, ldx, off):
     # one rounding to fp32 of a value that is off by some 2^-50
     assert (np.abs(gy[:, :K] - ey) <= np.abs(ey) * HALF32 * (1 + 1e-6)).all()
     assert np.isnan(gh[:, K:]).all() and np.isnan(gy[:, K:]).all()
-    want = torch.empty_like(yq)
-    for j in range(0, n, 256):                          # its column limit
-        B.mmvq_quantize_q8_1(y[j:], K, min(256, n - j), ldx, want[j:])
-    assert torch.equal(want, yq)
+    q, d = R.q8_codes(gy[:, :K].astype(np.float64).reshape(n, -1, 32))
+    with np.errstate(over="ignore"):
+        s = R.f32(d32(gy[:, :K].reshape(n, -1, 32)) * q.sum(-1, keepdims=True)).astype(np.float16)
+    want = np.concatenate([d.view(np.uint8), s.view(np.uint8), q.astype(np.int8).view(np.uint8)], -1).reshape(n, -1)
+    assert np.array_equal(host(yq), want)
     alone = torch.zeros_like(yq)                     # q8_1 only, no sum stored
     B.mmvq_add_rms_norm(xd, K, n, ldx, rd, ldx, dev(w), EPS, None, 0, None, 0, alone)
     assert torch.equal(alone, yq)
     back = nan(n, K + 3)
     B.mmvq_dequantize_q8_1(yq, K, n, back, K + 3)
-    q, d = R.q8_codes(gy[:, :K].astype(np.float64).reshape(n, -1, 32))
     assert np.array_equal(host(back)[:, :K], (q * d.astype(np.float64)).reshape(n, K).astype(np.float32))
     assert np.isnan(host(back)[:, K:]).all()
 
