@@ -51,8 +51,9 @@ enum { MMVQ_F16 = 1 };
  * of y, n * K/32 blocks of 36 bytes, what mmvq and its variants take: q =
  * roundf(y/d) and s = d*sum(q) as mmvq_quantize_q8_1 has them, with d =
  * max|y| * fp32(1/127) in fp32, the product with the rounded reciprocal,
- * within one unit in the last place of that function's quotient). sum_out may be x or residual itself (same
- * pointer and stride), and y may be x; otherwise the buffers do not overlap.
+ * within one unit in the last place of that function's quotient). sum_out may
+ * be x or residual itself (same pointer and stride), and y may be x where
+ * sum_out is not; otherwise the buffers do not overlap.
  * Requires 1 <= K <= 2^24, n >= 0 and n*K <= 2^40, every ld >= K, K % 32 == 0
  * with y_q, and at least one of y and y_q (MMVQ_ERR_NULL). fp32 buffers
  * 4-byte aligned, y_q 16-byte. With y_q the values must be finite, as for
@@ -72,8 +73,8 @@ int mmvq_dequantize_q8_1(const void *y_q, int64_t K, int64_t n, float *x,
  * mmvq_kv_page_bytes each (16-byte aligned); a page holds page_size
  * consecutive tokens of one sequence for every key/value head.
  *   type       MMVQ_F16 (nearest even; beyond 65504 infinite), MMVQ_Q8_0
- *              (per 32 values of a head: d = max|x| * fp32(1/127) in
- *              fp32, q = roundf(x/d), 0 where d is 0; value fp16(d)*q) or MMVQ_Q4_0
+ *              (per 32 values of a head: d = max|x| * fp32(1/127) in fp32,
+ *              q = roundf(x/d), 0 where d is 0; value fp16(d)*q) or MMVQ_Q4_0
  *              (d = m/-8 with m the value of largest magnitude, the first of
  *              equals; q = min(15, floor(x/d + 8.5)), 8 where d is 0; value
  *              fp16(d)*(q - 8)); a d beyond 65504 is stored as 65504; the
@@ -154,8 +155,9 @@ int mmvq_attn_workspace(const mmvq_kv_cache *cache, const mmvq_kv_batch *batch,
  * positions 0..p, the last `window` of them where window > 0. sinks: NULL or
  * n_heads logits that join each head's softmax as a key without a value. A
  * token that sees no key gets zeros; an infinite cached value makes the
- * results of the tokens that see it infinite or NaN, and no others. q and out: fp32, row t at + t*ld, head
- * h at h*head_dim; ld >= n_heads*head_dim, 4-byte aligned; q must be finite.
+ * results of the tokens that see it infinite or NaN, and no others. q and
+ * out: fp32, row t at + t*ld, head h at h*head_dim; ld >= n_heads*head_dim,
+ * 4-byte aligned, without overlap; q must be finite.
  * Keys and values enter at their stored precision; scores, softmax and sums
  * are fp32, with q carried as two fp16 parts (21 bits of the row's largest
  * value) and each probability as two fp16 parts (20 bits).
@@ -203,7 +205,7 @@ int mmvq_verify_workspace(int n_seqs, int n_rows, int vocab, int64_t *bytes);
  * n_rows floats, u_sample: n_seqs, in [0, 1).
  * Requires n_seqs and n_rows >= 0 (0 sequences: nothing is done), both <=
  * 2^20, 1 <= vocab <= 2^24, ldt and ldd >= vocab, max_out >= 1, row_start
- * rising within 0..n_rows (rows outside are not read); MMVQ_ERR_TYPE for an
+ * rising within 0..n_rows (other rows have no effect); MMVQ_ERR_TYPE for an
  * unknown target kind. All 4-byte aligned, workspace 16-byte and at least
  * mmvq_verify_workspace bytes (fewer: MMVQ_ERR_SHAPE). */
 int mmvq_verify_draft(const float *target, int64_t ldt, int vocab, int kind,

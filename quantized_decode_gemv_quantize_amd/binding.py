@@ -295,7 +295,7 @@ def _launch(fn: str, where, stream, *args) -> None:
     else:
         cuda = (_torch or _cuda()).cuda
         here = cuda.current_device()
-        index = here if where.__class__ is int else where.get_device()
+        index = here if where is None or where.__class__ is int else where.get_device()
         if index == here or index < 0:
             rc = f(*args, _raw_stream(here))
         else:

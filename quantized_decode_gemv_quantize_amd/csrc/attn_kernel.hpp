@@ -61,7 +61,7 @@ __device__ __forceinline__ float row_max(float v) {
   r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
 }
-__device__ __forceinline__ float row_sum(float v) { 
+__device__ __forceinline__ float row_sum(float v) {
   v = swap_pair_sum<32>(v, v);
   return swap_pair_sum<16>(v, v);
 }
@@ -167,7 +167,6 @@ struct KeyRegs {
       return operand_q4(w[m * LW + b], w[m * LW + b] >> 4);
     }
   }
-  __device__ __forceinline__ float scale(int b, int j) const { return h2f(sc[b][j / 2] >> (16 * (j & 1))); }
 };
 
 template <int KIND, int NB>
@@ -295,9 +294,10 @@ __device__ __forceinline__ StepPages step_pages(const AttnArgs& a, StepIds ids, 
 }
 
 // Factor that turns a row's O into its result: 1 / l with the sink's share
-// in l; 0 for a row that saw no key. l and O are in units of 2^(m - shift).
+// in l; 0 for a row that saw no key (l is NaN where all scores were). l and O
+// are in units of 2^(m - shift).
 __device__ __forceinline__ float row_factor(const AttnArgs& a, int head, float m, float l, float shift) {
-  if (m == -INFINITY) return 0.0f;
+  if (l == 0.0f) return 0.0f;
   if (!a.sinks) return 1.0f / l;
   const float sink = a.sinks[head] * 1.44269504088896340736f, unit = m - shift, top = fmaxf(unit, sink);
   const float f = __builtin_amdgcn_exp2f(unit - top);
@@ -368,7 +368,7 @@ struct Rows {
   u32x4 qh[QLDS ? 1 : MT][QLDS ? 1 : NB], ql[QLDS ? 1 : MT][QLDS ? 1 : NB];
   const u32x4* q_lds;
   float to_log2[MT];                            // 2^-k of the row's scaling
-  int qpos[MT];                                 // position, -1: no row
+  int qpos[MT];                                 // position; -1: no row, or one before position 0
   float m[MT], l[MT];
   f32x4 o[MT][DT];
 
@@ -386,7 +386,7 @@ struct Rows {
       const bool live = row < w.rows;
       const int group = static_cast<int>(a.group.d), tok = live ? a.group.div(row) : 0;
       const int hd = w.head * group + (live ? row - tok * group : 0);
-      qpos[t] = live ? w.base + tok : -1;
+      qpos[t] = live && w.base + tok >= 0 ? w.base + tok : -1;
       const float* src = a.q + (w.first + tok) * a.ldq + static_cast<int64_t>(hd) * (32 * NB);
       float v[NB][8], top = 0.0f;
 #pragma unroll

@@ -199,7 +199,7 @@ int mmvq_attn(const mmvq_kv_cache* cache, const mmvq_kv_batch* batch, const floa
   a.ldq = ldq;
   a.ldo = ldo;
   a.scale_log2 = static_cast<float>(static_cast<double>(scale) * M_LOG2E);
-  a.window = window;
+  a.window = window < (1 << 30) ? window : 0;   // positions are below 2^30: it hides nothing
   a.n_heads = n_heads;
   a.group = FastDiv(static_cast<uint32_t>(n_heads / cache->n_kv_heads));
   a.heads = FastDiv(static_cast<uint32_t>(cache->n_kv_heads));

@@ -22,10 +22,7 @@ struct BatchArgs {
   int page_shift;     // log2(page_size)
   int n_kv_heads;
 
-  // First row and row count of sequence s, inside the activation buffers.
-  __device__ __forceinline__ void rows(int s, int& first, int& count) const {
-    clamp_rows(token_start[s], token_start[s + 1], first, count);
-  }
+  // First row and row count of the sequence with rows a..b-1, inside the activation buffers.
   __device__ __forceinline__ void clamp_rows(int a, int b, int& first, int& count) const {
     first = a < 0 ? 0 : a > n_tokens ? n_tokens : a;
     const int end = b > n_tokens ? n_tokens : b;

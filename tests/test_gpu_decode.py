@@ -328,6 +328,42 @@ def test_attention_infinite_values_stay_hidden(new, window, bad_at):
     assert not np.isfinite(got[sees]).any()
 
 
+@pytest.mark.parametrize("length", [1, 40])
+@pytest.mark.parametrize("new", [1, 70])
+@pytest.mark.parametrize("sinks", [None, [0.5]])
+def test_attention_over_infinite_keys_alone(length, new, sinks):
+    """F16: rows whose every key is infinite have scores that are no numbers,
+    and are not taken for rows without keys."""
+    import torch
+    D = 64
+    p = R.Paged("f16", D, 1, 16, [new], [length + new - 1], seed=length)
+    p.fill(np.random.default_rng(0))
+    n = length + new - 1
+    rows = dev(np.tile(np.array([1e6, -1e6], np.float32), (n, D // 2)))
+    ones = dev(np.ones((n, D), np.float32))
+    whole = B.kv_batch(dev(np.array([0, n], np.int32)), dev(np.array([n], np.int32)), p.d[2], 1, n, n, n, p.wide)
+    B.mmvq_kv_write(p.cache, whole, rows, D, ones, D)
+    size = B.mmvq_attn_workspace(p.cache, p.batch(), 1)
+    out = torch.zeros(new, D, device="cuda:0")
+    B.mmvq_attn(p.cache, p.batch(), dev(np.ones((new, D), np.float32)), D, 1, 0.125, 0,
+                None if sinks is None else dev(np.array(sinks, np.float32)), out, D,
+                torch.empty(size + 16, dtype=torch.uint8, device="cuda:0"), size)
+    assert not np.isfinite(host(out)).any()
+
+
+@pytest.mark.parametrize("new", [5, 90])
+def test_attention_of_the_widest_window(new):
+    """A window of 2^31 - 1 hides nothing, also where rows lie before position 0."""
+    p = R.Paged("q8_0", 64, 2, 16, [new, new], [new + 20, new + 20], seed=21)
+
+    def change(p, k, v):
+        p.lens[1] = new - 3
+        k[1], v[1] = k[1][:new - 3], v[1][:new - 3]
+        p.upload()
+
+    run_attention(p, 2, window=0x7fffffff, seed=22, change=change)
+
+
 @pytest.mark.parametrize("kind", list(R.KINDS))
 def test_attention_of_stale_slots(kind):
     """Slots that no token was written to hold NaN patterns (0xFF): never seen."""
@@ -380,6 +416,13 @@ def test_rows_past_32_bits():
     _, e = R.rms_norm(q, None, None, EPS)
     got = np.stack([host(y[i * ld:i * ld + 64]) for i in range(3)])
     assert (np.abs(got - e) <= np.abs(e) * HALF32 * (1 + 1e-6)).all()
+
+
+def test_nothing_to_read_is_refused():
+    """Also without a tensor that would name the device."""
+    p = R.Paged("f16", 64, 1, 16, [1], [1], seed=1)
+    with pytest.raises(B.MMVQError):
+        B.mmvq_kv_read(p.cache, p.batch(), None, 64, None, 64)
 
 
 # --- verification ------------------------------------------------------------------------
