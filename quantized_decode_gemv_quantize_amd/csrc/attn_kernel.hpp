@@ -21,9 +21,10 @@
 // probability (times d) as two fp16 parts, 20 bits. fp16 parts need their
 // factor in range: the reference M of a row is the maximum of s + e over the
 // keys, e the exponent field of the token's largest |d| (0 for F16), and the
-// weight w = 2^(s - M + K) enters l as it is and O as w d, which is at most
-// 2^15 whatever the scales are and keeps its bits 39 binary places below
-// that. The factor 2^(K - M) cancels in O / l. Scores, M, l and O are fp32.
+// weight w = 2^(s + e - M + K) enters l times 2^(16 - e) and O times
+// d 2^(16 - e), which is below 4: all of it fp16 numbers, that keep their bits
+// 38 binary places below the largest whatever the scales are. The factor
+// 2^(K + 16 - M) cancels in O / l. Scores, M, l and O are fp32.
 //
 // Two kernels: with few rows the four waves of a workgroup take every fourth
 // step of the same rows, read operands from memory straight into registers
@@ -45,11 +46,12 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAttnThreads = 256;
 
-// K above: w d <= 2^(K - e) 2^(e - 14) for a quantized token, w <= 2^K (F16).
-// M may lag the true maximum by kLag, so that O is rescaled a few times a
-// walk instead of at every new maximum; K leaves room for it.
+// K above, with the 16 of a quantized token's factor: w <= 2^14 (F16), 2^13
+// where its product is below 4 times that. M may lag the true maximum by
+// kLag, so that O is rescaled a few times a walk instead of at every new
+// maximum; K leaves room for it.
 constexpr float kLag = 4.0f;
-__host__ __device__ constexpr float weight_shift(int kind) { return (kind == kKvF16 ? 14.0f : 29.0f) - kLag; }
+__host__ __device__ constexpr float weight_shift(int kind) { return (kind == kKvF16 ? 14.0f : 13.0f + 16.0f) - kLag; }
 
 __device__ __forceinline__ f32x4 mfma_f16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(half8, a), __builtin_bit_cast(half8, b), c, 0, 0, 0);
@@ -67,24 +69,25 @@ __device__ __forceinline__ float row_sum(float v) {
 }
 
 // Two values as fp16 parts: hi toward zero, lo the nearest of the rest
-// (together 21 bits).
+// (together 21 bits). The rest as a * 1 - hi: a fused multiply-add takes hi
+// as it is (v_fma_mix_f32), a difference would convert it first.
 __device__ __forceinline__ void split_f16(float a, float b, uint32_t& hi, uint32_t& lo) {
   const auto h = __builtin_amdgcn_cvt_pkrtz(a, b);
   hi = __builtin_bit_cast(uint32_t, h);
-  const half2v r = {static_cast<_Float16>(a - static_cast<float>(h[0])), static_cast<_Float16>(b - static_cast<float>(h[1]))};
+  float one = 1.0f;
+  asm("" : "+s"(one));
+  float ra = fmaf(a, one, -static_cast<float>(h[0])), rb = fmaf(b, one, -static_cast<float>(h[1]));
+  asm("" : "+v"(ra), "+v"(rb));                 // or fma and conversion in one, at half the rate
+  const half2v r = {static_cast<_Float16>(ra), static_cast<_Float16>(rb)};
   lo = __builtin_bit_cast(uint32_t, r);
 }
-// The same of the products p0 d0 and p1 d1 (d: two fp16 scales). The fma
-// forms take the scales as they are (v_fma_mix), the second ones round the
-// rest of the exact product.
-__device__ __forceinline__ void split_scaled(float p0, float p1, uint32_t d, uint32_t& hi, uint32_t& lo) {
-  const half2v dd = __builtin_bit_cast(half2v, d);
-  const float d0 = static_cast<float>(dd[0]), d1 = static_cast<float>(dd[1]);
-  const auto h = __builtin_amdgcn_cvt_pkrtz(fmaf(p0, d0, 0.0f), fmaf(p1, d1, 0.0f));
+// Parts of the products (ph + pl) d of two values: hi the nearest fp16 of
+// ph d, lo of its rest (exact in fp16) and pl d.
+__device__ __forceinline__ void scale_parts(uint32_t ph, uint32_t pl, uint32_t d, uint32_t& hi, uint32_t& lo) {
+  const half2v p = __builtin_bit_cast(half2v, ph), q = __builtin_bit_cast(half2v, pl), f = __builtin_bit_cast(half2v, d);
+  const half2v h = p * f;
   hi = __builtin_bit_cast(uint32_t, h);
-  const half2v r = {static_cast<_Float16>(fmaf(p0, d0, -static_cast<float>(h[0]))),
-                    static_cast<_Float16>(fmaf(p1, d1, -static_cast<float>(h[1])))};
-  lo = __builtin_bit_cast(uint32_t, r);
+  lo = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(q, f, __builtin_elementwise_fma(p, f, -h)));
 }
 
 // fp16 of four biased codes (bytes): 1024 + u by its bits, less the bias.
@@ -111,6 +114,18 @@ __device__ __forceinline__ u32x4 operand_q4(uint32_t a, uint32_t b) {   // nibbl
 __device__ __forceinline__ uint32_t max_u16x2(uint32_t a, uint32_t b) {
   typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
   return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+
+// Of two tokens' largest scales: fp16 factors 2^(16 - e), e the exponent
+// field, at least 1 (a subnormal's unit is that of the field 1), and e. A
+// scale of the token times its factor is below 4, without any rounding that
+// the largest would notice.
+__device__ __forceinline__ uint32_t token_factors(uint32_t top) { return 0x7C007C00u - max_u16x2(top & 0x7C007C00u, 0x04000400u); }
+__device__ __forceinline__ float factor_field(uint32_t word, int half) {   // e
+  return static_cast<float>(static_cast<int>(31u - ((word >> (16 * half + 10)) & 31u)));
+}
+__device__ __forceinline__ uint32_t pk_mul_f16(uint32_t a, uint32_t b) {
+  return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, a) * __builtin_bit_cast(half2v, b));
 }
 
 // Words of 8 fp16 whose elements c.. are cleared.
@@ -210,15 +225,18 @@ struct ValueRegs {
       return operand_q4(w[2 * b] >> (4 * half), w[2 * b + 1] >> (4 * half));
     }
   }
-  // Exponent field of each token's largest scale.
-  __device__ __forceinline__ void exponents(float (&e5)[8]) const {
+  // The tokens' factors and exponent fields; their scales times the factors.
+  __device__ __forceinline__ void normalise(u32x4& factor, float (&e5)[8]) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       uint32_t top = sc[0][e] & 0x7FFF7FFFu;
 #pragma unroll
       for (int b = 1; b < NB; ++b) top = max_u16x2(top, sc[b][e] & 0x7FFF7FFFu);
-      e5[2 * e] = static_cast<float>((top >> 10) & 31u);
-      e5[2 * e + 1] = static_cast<float>(top >> 26);
+      factor[e] = token_factors(top);
+      e5[2 * e] = factor_field(factor[e], 0);
+      e5[2 * e + 1] = factor_field(factor[e], 1);
+#pragma unroll
+      for (int b = 0; b < NB; ++b) sc[b][e] = pk_mul_f16(sc[b][e], factor[e]);
     }
   }
   // Tokens c.. of this lane's 8 do not exist: what lies there is no value
@@ -364,7 +382,7 @@ struct Place {
 template <int KIND, int NB, int MT, bool QLDS = false>
 struct Rows {
   static constexpr int DT = 2 * NB;
-  static constexpr float kShift = weight_shift(KIND);
+  static constexpr float kTop = KIND == kKvF16 ? weight_shift(KIND) : weight_shift(KIND) - 16.0f;   // the factors' 16
   u32x4 qh[QLDS ? 1 : MT][QLDS ? 1 : NB], ql[QLDS ? 1 : MT][QLDS ? 1 : NB];
   const u32x4* q_lds;
   float to_log2[MT];                            // 2^-k of the row's scaling
@@ -497,8 +515,8 @@ struct Rows {
     for (int j = 0; j < 8; ++j) s[t][j / 4][j & 3] = j < end && j >= beg ? s[t][j / 4][j & 3] : -INFINITY;
   }
 
-  // Scores to weights; M, l and O follow.
-  __device__ __forceinline__ void weigh(int t, const float (&e5)[8], f32x4 (&s)[MT][2]) {
+  // Scores to weights; M, l and O follow. factor, e5: of the 8 tokens (F16: not read).
+  __device__ __forceinline__ void weigh(int t, u32x4 factor, const float (&e5)[8], f32x4 (&s)[MT][2]) {
     float top;
     if constexpr (KIND == kKvF16) {
       top = s[t][0][0];
@@ -506,9 +524,11 @@ struct Rows {
       for (int j = 1; j < 8; ++j) top = fmaxf(top, s[t][j / 4][j & 3]);
       top = row_max(top) * to_log2[t];
     } else {
-      top = fmaf(s[t][0][0], to_log2[t], e5[0]);
 #pragma unroll
-      for (int j = 1; j < 8; ++j) top = fmaxf(top, fmaf(s[t][j / 4][j & 3], to_log2[t], e5[j]));
+      for (int j = 0; j < 8; ++j) s[t][j / 4][j & 3] = fmaf(s[t][j / 4][j & 3], to_log2[t], e5[j]);
+      top = s[t][0][0];
+#pragma unroll
+      for (int j = 1; j < 8; ++j) top = fmaxf(top, s[t][j / 4][j & 3]);
       top = row_max(top);
     }
     if (__any(top > m[t] + kLag)) {
@@ -521,35 +541,49 @@ struct Rows {
         for (int i = 0; i < 4; ++i) o[t][d][i] *= al;
       m[t] = top;
     }
-    const float off = kShift - (m[t] == -INFINITY ? 0.0f : m[t]);   // a row that has seen nothing yet: all weights 0
+    const float off = kTop - (m[t] == -INFINITY ? 0.0f : m[t]);   // a row that has seen nothing yet: all weights 0
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      s[t][j / 4][j & 3] = __builtin_amdgcn_exp2f(fmaf(s[t][j / 4][j & 3], to_log2[t], off));
-      l[t] += s[t][j / 4][j & 3];
+      const float x = s[t][j / 4][j & 3], w = __builtin_amdgcn_exp2f(KIND == kKvF16 ? fmaf(x, to_log2[t], off) : x + off);
+      s[t][j / 4][j & 3] = w;
+      if constexpr (KIND == kKvF16) l[t] += w;
+      else l[t] = fmaf(w, h2f(factor[j / 2] >> (16 * (j & 1))), l[t]);
     }
   }
 
-  // Weights (times the scales d of the tokens, if any) as operand parts.
-  __device__ __forceinline__ void parts(int t, const f32x4 (&s)[MT][2], u32x4 d, u32x4& hi, u32x4& lo) const {
+  // Parts of weights times scales.
+  static __device__ __forceinline__ void scaled(u32x4 wh, u32x4 wl, u32x4 d, u32x4& hi, u32x4& lo) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const float x = s[t][e / 2][2 * (e & 1)], y = s[t][e / 2][2 * (e & 1) + 1];
       uint32_t h, r;
-      if constexpr (KIND == kKvF16) split_f16(x, y, h, r);
-      else split_scaled(x, y, d[e], h, r);
+      scale_parts(wh[e], wl[e], d[e], h, r);
       hi[e] = h;
       lo[e] = r;
     }
   }
 
   // O of the step. value(d): operand of dims 16 d ..; scale(b): the 8 tokens'
-  // scales of block b. A quantized block's weights are formed while the
-  // products of the block before run.
+  // scales of block b, times the tokens' factors. A quantized block's weights
+  // are formed while the products of the block before run.
   template <class V, class S>
   __device__ __forceinline__ void accumulate(V value, S scale, const f32x4 (&s)[MT][2]) {
-    u32x4 ph[2][MT], pl[2][MT];
+    u32x4 wh[MT], wl[MT], ph[2][MT], pl[2][MT];
 #pragma unroll
-    for (int t = 0; t < MT; ++t) parts(t, s, scale(0), ph[0][t], pl[0][t]);
+    for (int t = 0; t < MT; ++t) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t h, r;
+        split_f16(s[t][e / 2][2 * (e & 1)], s[t][e / 2][2 * (e & 1) + 1], h, r);
+        wh[t][e] = h;
+        wl[t][e] = r;
+      }
+      if constexpr (KIND == kKvF16) {
+        ph[0][t] = wh[t];
+        pl[0][t] = wl[t];
+      } else {
+        scaled(wh[t], wl[t], scale(0), ph[0][t], pl[0][t]);
+      }
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if constexpr (QLDS) __builtin_amdgcn_sched_barrier(0);
@@ -562,7 +596,7 @@ struct Rows {
       }
       if (KIND != kKvF16 && b + 1 < NB) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) parts(t, s, scale(b + 1), ph[now ^ 1][t], pl[now ^ 1][t]);
+        for (int t = 0; t < MT; ++t) scaled(wh[t], wl[t], scale(b + 1), ph[now ^ 1][t], pl[now ^ 1][t]);
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
@@ -660,9 +694,10 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_keys_kernel
         }
       }
       float e5[8];
-      if constexpr (KIND != kKvF16) vr.exponents(e5);
+      u32x4 factor;
+      if constexpr (KIND != kKvF16) vr.normalise(factor, e5);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) r.weigh(t, e5, s);
+      for (int t = 0; t < MT; ++t) r.weigh(t, factor, e5, s);
       const auto value = [&](int d) QMV_INLINE { return vr.operand(d / 2, d & 1); };
       if constexpr (KIND == kKvF16) {
         if (wild) {
@@ -721,8 +756,9 @@ struct StepLds {
   u32x4 k[2][NB][kWave];                        // key operands
   u32x4 v[2 * NB][kWave];                       // value operands
   uint32_t ksc[KIND == kKvF16 ? 1 : NB][16];    // scales of the 32 tokens, two a word
-  uint32_t vsc[KIND == kKvF16 ? 1 : NB][16];
-  float e5[kStep];                              // exponent fields
+  uint32_t vsc[KIND == kKvF16 ? 1 : NB][16];    // times the tokens' factors
+  uint32_t factor[16];                          // the factors
+  float e5[kStep];                              // and their exponent fields
   int wild[4];                                  // F16, of each wave's share: an infinity or NaN was among the values
 };
 
@@ -734,8 +770,7 @@ struct StepRegs {
   static constexpr int kKeyWords = kv_run(KIND) / 4;
   static constexpr int kValueWords = KIND == kKvF16 ? 8 : KIND == kKvQ8 ? 4 : 2;
   uint32_t k[kItems][2][kKeyWords], v[kItems][kValueWords];
-  uint32_t ksc, vsc;                            // of lanes 0..16 NB-1 (word lane % 16 of block lane / 16)
-  uint16_t es[KIND == kKvF16 ? 1 : NB];         // lanes 0..31: the token's value scales
+  uint32_t ksc, vsc[KIND == kKvF16 ? 1 : NB];   // of lanes 0..16 NB-1: word lane % 16, of block lane / 16 and of all blocks
   bool ok[2];
 
   __device__ __forceinline__ void load(const AttnArgs& a, StepIds ids, int head, int t0) {
@@ -786,15 +821,11 @@ struct StepRegs {
     }
     if constexpr (KIND != kKvF16) {
       if (tid < 16 * NB) {
-        const int b = tid >> 4, word = tid & 15, at = kv_scale_at(KIND, NB, b, 2 * (word & 7));
-        const int64_t off = (word >> 3 ? pg.off[1] : pg.off[0]) + at;
-        ksc = ld_u32(a.k + off);
-        vsc = ld_u32(a.v + off);
-      }
-      if (tid < kStep) {
+        const int b = tid >> 4, word = tid & 15;
+        const int64_t off = word >> 3 ? pg.off[1] : pg.off[0];
+        ksc = ld_u32(a.k + off + kv_scale_at(KIND, NB, b, 2 * (word & 7)));
 #pragma unroll
-        for (int b = 0; b < NB; ++b)
-          es[b] = static_cast<uint16_t>(ld_u16(a.v + (tid >> 4 ? pg.off[1] : pg.off[0]) + kv_scale_at(KIND, NB, b, tid & 15)));
+        for (int i = 0; i < NB; ++i) vsc[i] = ld_u32(a.v + off + kv_scale_at(KIND, NB, i, 2 * (word & 7)));
       }
     }
   }
@@ -843,20 +874,21 @@ struct StepRegs {
       if (tid < 16 * NB) {
         const int b = tid >> 4, word = tid & 15;
         lds.ksc[b][word] = ksc;
-        if (part) {
-          const int real = (word >> 3 ? ok[1] : ok[0]) ? keys - (t0 + 2 * word) : 0;
-          vsc &= keep_mask(0, real);
-        }
-        lds.vsc[b][word] = vsc;
-      }
-      if (tid < kStep) {
-        uint32_t top = 0;
+        const uint32_t mask = part ? keep_mask(0, (word >> 3 ? ok[1] : ok[0]) ? keys - (t0 + 2 * word) : 0) : ~0u;
+        uint32_t own = 0, top = 0;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const uint32_t d = es[b] & 0x7FFFu;
-          top = top > d ? top : d;
+        for (int i = 0; i < NB; ++i) {
+          vsc[i] &= mask;
+          own = i == b ? vsc[i] : own;
+          top = max_u16x2(top, vsc[i] & 0x7FFF7FFFu);
         }
-        lds.e5[tid] = static_cast<float>(top >> 10);
+        const uint32_t f = token_factors(top);
+        lds.vsc[b][word] = pk_mul_f16(own, f);
+        if (b == 0) {
+          lds.factor[word] = f;
+          lds.e5[2 * word] = factor_field(f, 0);
+          lds.e5[2 * word + 1] = factor_field(f, 1);
+        }
       }
     }
   }
@@ -913,7 +945,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
           for (int t = 0; t < MT; ++t) r.hide(a, t, t0 + 8 * g, real, s);
         }
         float e5[8];
+        u32x4 factor;
         if constexpr (KIND != kKvF16) {
+          factor = *reinterpret_cast<const u32x4*>(&st.factor[4 * g]);
 #pragma unroll
           for (int j = 0; j < 8; j += 4) {
             const f32x4 x = *reinterpret_cast<const f32x4*>(&st.e5[8 * g + j]);
@@ -922,7 +956,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
           }
         }
 #pragma unroll
-        for (int t = 0; t < MT; ++t) r.weigh(t, e5, s);
+        for (int t = 0; t < MT; ++t) r.weigh(t, factor, e5, s);
         const auto value = [&](int d) QMV_INLINE { return st.v[d][lane]; };
         if constexpr (KIND == kKvF16) {
           if (st.wild[0] | st.wild[1] | st.wild[2] | st.wild[3]) {
