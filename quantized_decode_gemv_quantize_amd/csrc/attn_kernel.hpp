@@ -933,7 +933,9 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
       if (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1)) {   // some row sees some of it
         f32x4 s[MT][2];
         // products first: of the two waves of a SIMD, one multiplies while the
-        // other weighs (639 -> 608 us, 2048 tokens over 8192)
+        // other weighs (2048 tokens over 8192, Q4_0: 597 us without, 580 with
+        // the scores first, 544 with both products; 256 dims the other way:
+        // Q8_0 1745 us so, 1785 with both)
         __builtin_amdgcn_s_setprio(1);
         r.scores([&](int mm, int b) QMV_INLINE { return st.k[mm][b][lane]; },
                  [&](int b) QMV_INLINE { return *reinterpret_cast<const u32x4*>(&st.ksc[KIND == kKvF16 ? 0 : b][4 * g]); }, s);
@@ -964,9 +966,11 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
             for (int t = 0; t < MT; ++t) r.add_wild(a, w, t, t0, s);
           }
         }
+        if constexpr (NB < 8) __builtin_amdgcn_s_setprio(1);
         r.accumulate(value, [&](int b) QMV_INLINE {
           return *reinterpret_cast<const u32x4*>(&st.vsc[KIND == kKvF16 ? 0 : b][4 * g]);
         }, s);
+        if constexpr (NB < 8) __builtin_amdgcn_s_setprio(0);
       }
       if (more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
       __syncthreads();
