@@ -379,8 +379,16 @@ struct Place {
 
 // A wave's rows: q as operands, and the running softmax. QLDS: q in LDS, where
 // the four waves of the keys kernel share it, [tile][block][lo, hi][lane].
-template <int KIND, int NB, int MT, bool QLDS = false>
+// AHEAD: keys and values come from LDS, and a block's are read before the
+// products of the block before it: a wave waits for its own chain of reads and
+// products, two waves a SIMD do not cover it all (2048 tokens over 8192: F16
+// of 96 dims 418 -> 400 us, Q8_0 492 -> 469, of 256 1746 -> 1586). The keys of
+// quantized heads of 128 dims are read in place, for they have no registers
+// left to be read ahead to (Q8_0 577 us as it was, 538 with the values ahead,
+// 593 with both).
+template <int KIND, int NB, int MT, bool QLDS = false, bool AHEAD = false>
 struct Rows {
+  static constexpr bool kKeysAhead = AHEAD && (KIND == kKvF16 || NB != 4);
   static constexpr int DT = 2 * NB;
   static constexpr float kTop = KIND == kKvF16 ? weight_shift(KIND) : weight_shift(KIND) - 16.0f;   // the factors' 16
   u32x4 qh[QLDS ? 1 : MT][QLDS ? 1 : NB], ql[QLDS ? 1 : MT][QLDS ? 1 : NB];
@@ -460,11 +468,33 @@ struct Rows {
   __device__ __forceinline__ void scores(K key, S scale, f32x4 (&s)[MT][2]) const {
 #pragma unroll
     for (int t = 0; t < MT; ++t) s[t][0] = s[t][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    u32x4 n0, n1, ns;                           // the next block's, where they are read ahead
+    if constexpr (kKeysAhead) {
+      n0 = key(0, 0);
+      n1 = key(1, 0);
+      ns = scale(0);
+    }
+    const auto next = [&](int b, u32x4& k0, u32x4& k1) QMV_INLINE {
+      if constexpr (QLDS || kKeysAhead) __builtin_amdgcn_sched_barrier(0);   // a block after the other: registers
+      if constexpr (kKeysAhead) {
+        k0 = n0;
+        k1 = n1;
+        if (b + 1 < NB) {
+          n0 = key(0, b + 1);
+          n1 = key(1, b + 1);
+          if constexpr (KIND != kKvF16) ns = scale(b + 1);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        k0 = key(0, b);
+        k1 = key(1, b);
+      }
+    };
     if constexpr (KIND == kKvF16) {
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        if constexpr (QLDS) __builtin_amdgcn_sched_barrier(0);   // a block after the other: registers
-        const u32x4 k0 = key(0, b), k1 = key(1, b);
+        u32x4 k0, k1;
+        next(b, k0, k1);
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
           s[t][0] = mfma_f16(k0, q(t, b, 0), s[t][0]);
@@ -478,11 +508,13 @@ struct Rows {
       }
     } else {
       f32x4 acc[2][MT][2];
+      u32x4 sc_now, sc_done = {};               // of block b and of the one before it
 #pragma unroll
       for (int b = 0; b <= NB; ++b) {
-        if constexpr (QLDS) __builtin_amdgcn_sched_barrier(0);   // a block after the other: registers
+        sc_now = ns;
         if (b < NB) {
-          const u32x4 k0 = key(0, b), k1 = key(1, b);
+          u32x4 k0, k1;
+          next(b, k0, k1);
           f32x4 (&c)[MT][2] = acc[b & 1];
 #pragma unroll
           for (int t = 0; t < MT; ++t) {
@@ -496,13 +528,14 @@ struct Rows {
           }
         }
         if (b > 0) {
-          const u32x4 sc = scale(b - 1);
+          const u32x4 sc = kKeysAhead ? sc_done : scale(b - 1);
 #pragma unroll
           for (int t = 0; t < MT; ++t)
 #pragma unroll
             for (int j = 0; j < 8; ++j)
               s[t][j / 4][j & 3] = fmaf(acc[(b - 1) & 1][t][j / 4][j & 3], h2f(sc[j / 2] >> (16 * (j & 1))), s[t][j / 4][j & 3]);
         }
+        sc_done = sc_now;
       }
     }
   }
@@ -568,6 +601,12 @@ struct Rows {
   template <class V, class S>
   __device__ __forceinline__ void accumulate(V value, S scale, const f32x4 (&s)[MT][2]) {
     u32x4 wh[MT], wl[MT], ph[2][MT], pl[2][MT];
+    u32x4 n0, n1, ns;                           // the next block's values and the scales of its weights, read ahead
+    if constexpr (AHEAD) {
+      n0 = value(0);
+      n1 = value(1);
+      if constexpr (KIND != kKvF16) ns = scale(1);
+    }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
@@ -586,9 +625,24 @@ struct Rows {
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      if constexpr (QLDS) __builtin_amdgcn_sched_barrier(0);
+      if constexpr (QLDS || AHEAD) __builtin_amdgcn_sched_barrier(0);
       const int now = KIND == kKvF16 ? 0 : b & 1;
-      const u32x4 v0 = value(2 * b), v1 = value(2 * b + 1);
+      u32x4 v0, v1, vs;
+      if constexpr (AHEAD) {
+        v0 = n0;
+        v1 = n1;
+        vs = ns;
+        if (b + 1 < NB) {
+          n0 = value(2 * b + 2);
+          n1 = value(2 * b + 3);
+        }
+        if (KIND != kKvF16 && b + 2 < NB) ns = scale(b + 2);
+        __builtin_amdgcn_sched_barrier(0);
+      } else {
+        v0 = value(2 * b);
+        v1 = value(2 * b + 1);
+        if (KIND != kKvF16 && b + 1 < NB) vs = scale(b + 1);
+      }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
         o[t][2 * b] = mfma_f16(v0, pl[now][t], o[t][2 * b]);
@@ -596,7 +650,7 @@ struct Rows {
       }
       if (KIND != kKvF16 && b + 1 < NB) {
 #pragma unroll
-        for (int t = 0; t < MT; ++t) scaled(wh[t], wl[t], scale(b + 1), ph[now ^ 1][t], pl[now ^ 1][t]);
+        for (int t = 0; t < MT; ++t) scaled(wh[t], wl[t], vs, ph[now ^ 1][t], pl[now ^ 1][t]);
       }
 #pragma unroll
       for (int t = 0; t < MT; ++t) {
@@ -917,7 +971,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
       next = step_ids(a, w.s, t_beg + kStep, zero);
       in.load(a, ids, w.head, t_beg);
     }
-    Rows<KIND, NB, MT> r;
+    Rows<KIND, NB, MT, false, true> r;
     r.init(a, w, row0);
     __syncthreads();                            // the tile before is done with LDS
     if (t_beg < t_end) in.store(lds[0], t_beg, w.keys);
