@@ -952,6 +952,12 @@ struct StepRegs {
 template <int KIND, int NB, int MT>
 __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) {
   constexpr int D = 32 * NB, DT = 2 * NB, RW = 16 * MT, RT = 4 * RW;
+  // Quantized heads of 256 dims: the next step's operands go to LDS before
+  // the second product and free their registers for it, and no wave skips a
+  // step that none of its rows sees, for the compiler keeps O in memory
+  // across that branch (1586 -> 1119 us, 2048 tokens over 8192). Others lose
+  // by it, F16 of 256 dims 1238 -> 1664, half-filled tiles of 128 dims 86 -> 93.
+  constexpr bool kStraight = KIND != kKvF16 && NB == 8;
   __shared__ StepLds<KIND, NB> lds[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
   Place w;
@@ -984,12 +990,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
         next = step_ids(a, w.s, t0 + 2 * kStep, zero);
       }
       const StepLds<KIND, NB>& st = lds[buf];
-      if (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1)) {   // some row sees some of it
+      if (kStraight || (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1))) {   // some row sees some of it
         f32x4 s[MT][2];
         // products first: of the two waves of a SIMD, one multiplies while the
         // other weighs (2048 tokens over 8192, Q4_0: 597 us without, 580 with
-        // the scores first, 544 with both products; 256 dims the other way:
-        // Q8_0 1745 us so, 1785 with both)
+        // the scores first, 544 with both products; of 256 dims Q8_0 1745 us
+        // so, 1785 with both)
         __builtin_amdgcn_s_setprio(1);
         r.scores([&](int mm, int b) QMV_INLINE { return st.k[mm][b][lane]; },
                  [&](int b) QMV_INLINE { return *reinterpret_cast<const u32x4*>(&st.ksc[KIND == kKvF16 ? 0 : b][4 * g]); }, s);
@@ -1020,13 +1026,14 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
             for (int t = 0; t < MT; ++t) r.add_wild(a, w, t, t0, s);
           }
         }
+        if (kStraight && more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
         if constexpr (NB < 8) __builtin_amdgcn_s_setprio(1);
         r.accumulate(value, [&](int b) QMV_INLINE {
           return *reinterpret_cast<const u32x4*>(&st.vsc[KIND == kKvF16 ? 0 : b][4 * g]);
         }, s);
         if constexpr (NB < 8) __builtin_amdgcn_s_setprio(0);
       }
-      if (more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
+      if (!kStraight && more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
       __syncthreads();
     }
 #pragma unroll

@@ -266,6 +266,15 @@ def test_attention_window_and_sinks(kind, window, news, lens):
 
 
 @pytest.mark.parametrize("kind", list(R.KINDS))
+@pytest.mark.parametrize("D", [128, 256])
+def test_attention_window_of_wide_heads(kind, D):
+    """Many rows: steps that some waves' rows see and others' do not, and a
+    last tile with waves that have no rows."""
+    p = R.Paged(kind, D, 1, 32, [200, 70], [500, 70], seed=D)
+    run_attention(p, 1, window=40, seed=D)
+
+
+@pytest.mark.parametrize("kind", list(R.KINDS))
 @pytest.mark.parametrize("new", [3, 100])
 def test_attention_hints_are_hints(kind, new):
     p = R.Paged(kind, 64, 2, 32, [new, 1], [new + 200, 900], seed=new)
