@@ -341,6 +341,18 @@ __device__ __forceinline__ void store_row(const AttnArgs& a, int token, int head
 struct Place {
   int head, split, s, tile0;
   int first, count, len, keys, rows, base;      // base: position of new token 0
+  // The sequence with n longer ones (of equals the first is the longer). Up
+  // to 64 of them, a lane each.
+  static __device__ __forceinline__ int nth_longest(const AttnArgs& a, int n) {
+    const int lane = lane_id(), count = a.b.n_seqs, own = lane < count ? a.b.seq_len[lane] : 0;
+    int before = 0;
+    for (int j = 0; j < count; ++j) {
+      const int other = __builtin_amdgcn_readlane(own, j);
+      before += other > own || (other == own && j < lane);
+    }
+    return __builtin_ctzll(__ballot(lane < count && before == n));
+  }
+  template <bool ROWS>
   __device__ __forceinline__ bool find(const AttnArgs& a) {
     // Workgroups go to the 8 XCDs in turn: those that read the same keys (the
     // tiles of one sequence, head and range) get the same XCD and its L2.
@@ -357,6 +369,7 @@ struct Place {
     s = a.splits.div(per_head);
     split = per_head - s * static_cast<int>(a.splits.d);
     if (s >= a.b.n_seqs) return false;
+    if (ROWS && a.by_length) s = nth_longest(a, s);
     const int from = a.b.token_start[s], to = a.b.token_start[s + 1], l = a.b.seq_len[s];
     a.b.clamp_rows(from, to, first, count);
     len = l < 0 ? 0 : l > (1 << 30) ? (1 << 30) : l;
@@ -699,7 +712,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_keys_kernel
   __shared__ float lds_ml[4 * RW * 2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
   Place w;
-  if (!w.find(a)) return;
+  if (!w.find<false>(a)) return;
   for (int tile = w.tile0; tile * RW < w.rows; tile += static_cast<int>(a.tiles.d)) {
     const int row0 = tile * RW, row1 = (row0 + RW < w.rows ? row0 + RW : w.rows) - 1;
     int t_beg, t_end;
@@ -961,7 +974,7 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
   __shared__ StepLds<KIND, NB> lds[2];
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = lane_id(), g = lane >> 4, col = lane & 15;
   Place w;
-  if (!w.find(a)) return;
+  if (!w.find<true>(a)) return;
   for (int tile = w.tile0; tile * RT < w.rows; tile += static_cast<int>(a.tiles.d)) {
     const int row0 = tile * RT + wave * RW;
     int t_beg, t_end;
@@ -1061,8 +1074,18 @@ int launch_attn_as(const AttnArgs& a, hipStream_t st) {
   const int64_t grid = (groups + 7) / 8 * 8 * a.tiles.d;
   if (grid > (1 << 23)) return MMVQ_ERR_SHAPE;   // 2^32 lanes in a launch
   const dim3 g(static_cast<unsigned>(grid)), b(kAttnThreads);
-  if constexpr (ROWS) hipLaunchKernelGGL((attn_rows_kernel<KIND, NB, MT>), g, b, 0, st, a);
-  else hipLaunchKernelGGL((attn_keys_kernel<KIND, NB, MT>), g, b, 0, st, a);
+  if constexpr (ROWS) {
+    // More workgroups than run at once: those of the longest sequences first,
+    // so that none of them is what the chip waits for in the end (12 of 200
+    // new tokens over 1300..4000: 327 -> 271 us). Few rows gain nothing by it
+    // (16 of 5 over 5300..16000: 63.2 and 64.5 us), and short ones lose the
+    // time that the order takes (30 of 2 over 700: 20.4 and 23.3).
+    AttnArgs args = a;
+    args.by_length = a.b.n_seqs > 1 && a.b.n_seqs <= kWave && grid > 2 * kCus;
+    hipLaunchKernelGGL((attn_rows_kernel<KIND, NB, MT>), g, b, 0, st, args);
+  } else {
+    hipLaunchKernelGGL((attn_keys_kernel<KIND, NB, MT>), g, b, 0, st, a);
+  }
   return check_launch();
 }
 

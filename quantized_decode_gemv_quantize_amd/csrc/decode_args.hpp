@@ -59,6 +59,7 @@ struct AttnArgs {
   int64_t ldq, ldo;
   float scale_log2;        // scale * log2(e)
   int window, n_heads, head_dim;
+  bool by_length;          // workgroups of the longest sequences first
   FastDiv group, tiles, splits, heads;   // query heads a key/value head, ..., key/value heads
   float* part_o;           // [row][head][split][head_dim]
   float2* part_ml;         // [row][head][split]

@@ -274,6 +274,18 @@ def test_attention_window_of_wide_heads(kind, D):
     run_attention(p, 1, window=40, seed=D)
 
 
+@pytest.mark.parametrize("n_seqs", [2, 63, 64, 65])
+def test_attention_of_many_prompts(n_seqs):
+    """More workgroups than run at once, of sequences of all lengths, equal
+    ones and empty ones among them."""
+    rng = np.random.default_rng(n_seqs)
+    news = [int(x) for x in rng.integers(70, 100, n_seqs)] if n_seqs > 2 else [1000, 70]
+    news[n_seqs // 2] = 0
+    lens = [new + int(x) for new, x in zip(news, rng.integers(0, 90, n_seqs) // 30 * 30)]
+    p = R.Paged("q8_0", 64, 8 if n_seqs > 2 else 32, 16, news, lens, seed=n_seqs)
+    run_attention(p, 8 if n_seqs > 2 else 32, seed=n_seqs)
+
+
 @pytest.mark.parametrize("kind", list(R.KINDS))
 @pytest.mark.parametrize("new", [3, 100])
 def test_attention_hints_are_hints(kind, new):
