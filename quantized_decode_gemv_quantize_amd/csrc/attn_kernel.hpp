@@ -22,9 +22,9 @@
 // factor in range: the reference M of a row is the maximum of s + e over the
 // keys, e the exponent field of the token's largest |d| (0 for F16), and the
 // weight w = 2^(s + e - M + K) enters l times 2^(16 - e) and O times
-// d 2^(16 - e), which is below 4: all of it fp16 numbers, that keep their bits
-// 38 binary places below the largest whatever the scales are. The factor
-// 2^(K + 16 - M) cancels in O / l. Scores, M, l and O are fp32.
+// d 2^(16 - e), which is below 4: fp16 numbers, off by 2^-32 of the largest at
+// most however small they are, whatever the scales. The factor 2^(K + 16 - M)
+// cancels in O / l. Scores, M, l and O are fp32.
 //
 // Two kernels: with few rows the four waves of a workgroup take every fourth
 // step of the same rows, read operands from memory straight into registers
@@ -33,6 +33,14 @@
 // each step's codes into operands once, in LDS, for all four. Either way the
 // keys can be cut into ranges whose partial (M, l, O) a second
 // launch joins, so that few rows over a long cache still fill the chip.
+//
+// Measured: F16, 64 sequences of one token over 1500..4500 keys of 8 heads of
+// 128, 155 us, 5.3 TB/s, bound by memory; Q4_0, 16 of 5 tokens and 64 query
+// heads of 64 over 5300..16000, 64 us, bound by vector issue (79 %); Q8_0, 2048
+// tokens of 32 heads of 128 over 8192, 540 us, 445 TFLOP/s of the formula's
+// operations (the parts double them), vector issue 70 % and the chain of one
+// wave's own reads and products: a compute unit with one workgroup instead of
+// two takes as long for it.
 #pragma once
 
 #include "decode_args.hpp"

@@ -11,8 +11,9 @@
 //
 // One workgroup owns a column and keeps it in registers between the sum and
 // the products, so each input is read once and each output written once. It
-// is bound by memory bandwidth from about a hundred columns and by the
-// latency of one column's load, reduction and store below.
+// is bound by memory bandwidth from about a hundred columns (256 of 14336
+// with all outputs but y: 12.4 us, 3.9 TB/s) and by the latency of one
+// column's load, reduction and store below (one of 4096: 3.4 us).
 #include "decode_args.hpp"
 #include "launch.hpp"
 #include "q8.hpp"

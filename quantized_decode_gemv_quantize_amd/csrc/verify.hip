@@ -17,7 +17,9 @@
 // running sum in 32 bits moves a border by more than the probability of many
 // tokens. The stats launch reads every row once and is bound by that read
 // with the exponentials beside it (21 64-bit operations each, 2^f by its
-// Taylor polynomial); the others are short chains of latencies.
+// Taylor polynomial): 141 rows of 128256 take 23 us, 3.1 TB/s, of which 16 are
+// vector issue. The others are short chains of latencies (finish 13.5 us for
+// 32 sequences, decide and draw 7.6 and 6.4 for one).
 #include "decode_args.hpp"
 #include "launch.hpp"
 #include "reduce64.hpp"

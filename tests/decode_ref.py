@@ -155,19 +155,26 @@ def attention_tolerance(out, mag, smax, v, D):
     D terms in fp32 (D 2^-24 of sum|q k| <= smax), three more roundings of the
     score: ds <= smax (2^-21 + (D + 4) 2^-24). A probability moves by 2 ds
     (its own and the sum's) + 2^-22 (exp2), its two parts are off by 2^-20 at
-    most (the first cut toward zero, 2^-10, the second to nearest of that,
-    2^-11, and the same again where a scale joins), and the sums over the
-    keys, 32 a step, round (keys/32 + 4 + 9) times: matrix products add 8
-    terms a lane group, 4 groups, 2 parts, then the joins. Below 2^-14 fp16
-    has steps of 2^-24: a weight is off by 2^-25 in units in which the
-    largest is at least 2^10 (times the largest scale, quantized; the
-    reference of the exponents may lag the maximum by 2^4), which leaves
-    2^-35 of the largest value a key."""
+    most, and the sums over the keys, 32 a step, round (keys/32 + 4 + 9)
+    times: matrix products add 8 terms a lane group, 4 groups, 2 parts, then
+    the joins.
+    The two parts of p = 2^e m: the first, cut toward zero, leaves less than
+    2^(e-10), which the second rounds by 2^(e-22). Of p d = 2^E M, where a
+    scale joins, the first is off by 2^(E-11), the second holds that and less
+    than p d 2^-10 / m of the rest: below 2^(E-9) its rounding is 2^(E-21);
+    from there on, M >= 1.5 and it is 2^(E-20): 2^-20 / 1.5 of p d at most,
+    together 0.92 2^-20.
+    Below 2^-14 fp16 has steps of 2^-24. F16: a weight is off by 2^-25 where
+    the largest is 2^10 at least. Quantized: by 2^-25 times a normalised scale
+    below 4, and its product by 2^-25 twice more, 1.5 2^-23 together, where
+    the largest weight is at least 2^9 and its scale 2: 1.5 2^-33 of the
+    largest value a key, the code with the largest magnitude being in every
+    block."""
     keys = max(1, len(v))
     ds = smax * (2.0 ** -21 + (D + 4) * 2.0 ** -24)
     with np.errstate(over="ignore"):
         rel = 2 * np.expm1(ds) + 2.0 ** -22 + 2.0 ** -20 + (keys / 32 * 2 + 48) * 2.0 ** -24
-    low = 2.0 ** -35 * keys * np.abs(v).max(initial=0.0)
+    low = 1.5 * 2.0 ** -33 * keys * np.abs(v).max(initial=0.0)
     return mag * rel[..., None] + np.abs(out) * 2.0 ** -23 + low + 1e-30
 
 

@@ -396,7 +396,7 @@ def test_attention_of_stale_slots(kind):
 @pytest.mark.parametrize("qscale,kscale", [(1e-30, 1.0), (1e12, 1e-12), (20.0, 1.0), (1.0, 1e-3), (0.01, 300.0)])
 def test_attention_scales(kind, qscale, kscale):
     """Query and cache values of any size: the parts of q are scaled by its
-    row's exponent, block scales enter in fp32 and bf16."""
+    row's exponent, block scales of values by their token's."""
     p = R.Paged(kind, 64, 1, 32, [2, 60], [500, 60], seed=13)
     if kind == "f16" and kscale < 1e-3:                # below fp16's range
         qscale, kscale = qscale * kscale / 1e-3, 1e-3
