@@ -18,8 +18,8 @@
 // tokens. The stats launch reads every row once and is bound by that read
 // with the exponentials beside it (21 64-bit operations each, 2^f by its
 // Taylor polynomial): 141 rows of 128256 take 23 us, 3.1 TB/s, of which 16 are
-// vector issue. The others are short chains of latencies (finish 13.5 us for
-// 32 sequences, decide and draw 7.6 and 6.4 for one).
+// vector issue. The others are short chains of latencies (finish 12.3 us for
+// 32 sequences, decide and draw 7.1 and 6.2 for one).
 #include "decode_args.hpp"
 #include "launch.hpp"
 #include "reduce64.hpp"
@@ -45,6 +45,7 @@ struct SeqSum {
 struct Decision {
   int row, taken, last, best;                  // row drawn from (-1: none)
   float top;
+  int token;                                   // refused there, -1 in a sequence's last row
   double z, refused;                           // sum of the row's weights, weight of the refused token
 };
 
@@ -243,8 +244,10 @@ __global__ void __launch_bounds__(kSThreads) verify_stats_kernel(VerifyArgs a) {
   }
 }
 
-// A row's chunks joined, by one wave: the same in all lanes.
-__device__ __forceinline__ void join_row(const VerifyArgs& a, const Exp2& exp2, int r, Heat h, float& top, int& at, double& z) {
+// A row's chunks joined, by one wave: the same in all lanes; `mine` is the
+// lane's chunk's part of z (not for a greedy row).
+__device__ __forceinline__ void join_row(const VerifyArgs& a, const Exp2& exp2, int r, Heat h, float& top, int& at, double& z,
+                                         double& mine) {
   const RowStat* st = row_stats(a) + static_cast<int64_t>(r) * a.chunks;
   top = -INFINITY;
   at = 0x7fffffff;
@@ -255,11 +258,12 @@ __device__ __forceinline__ void join_row(const VerifyArgs& a, const Exp2& exp2, 
     for (int c = lane_id() + kWave; c < a.chunks; c += kWave) take_top(top, at, st[c].top, st[c].at);
     wave_top(top, at);
   }
+  mine = 0.0;
   if (h.greedy) {
     z = top > -INFINITY ? 1.0 : 0.0;
     return;
   }
-  z = own.sum * chunk_scale(a, exp2, own.top, top, h);
+  z = mine = own.sum * chunk_scale(a, exp2, own.top, top, h);
   for (int c = lane_id() + kWave; c < a.chunks; c += kWave) z += st[c].sum * chunk_scale(a, exp2, st[c].top, top, h);
   z = wave_sum(z);
 }
@@ -276,9 +280,10 @@ __device__ __forceinline__ void draw_weights(const VerifyArgs& a, const Exp2& ex
 // at a time, one a wave.
 struct DecideLds {
   Decision dec;
-  int ok[kVWaves], ats[kVWaves];
+  int ok[kVWaves], ats[kVWaves], tokens[kVWaves], slot;   // slot: wave that had the decided row
   float tops[kVWaves];
   double zs[kVWaves], es[kVWaves];
+  double sums[kVWaves][kWave];                 // parts of z of each wave's row, of its first 64 chunks
 };
 __device__ __forceinline__ void decide(const VerifyArgs& a, const Exp2& exp2, int first, int count, Heat h, DecideLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
@@ -300,14 +305,16 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Exp2& exp2, in
       const float q = a.draft_probs && real ? a.draft_probs[r * a.ldd + x] : 1.0f, u = drafted ? a.u_accept[r] : 0.0f;
       float top;
       int at;
-      double z;
-      join_row(a, exp2, r, h, top, at, z);
+      double z, mine;
+      join_row(a, exp2, r, h, top, at, z, mine);
+      l.sums[wave][tid & 63] = mine;
       const double e = real ? weight(a, exp2, v, x, top, at, h) : 0.0;
       const bool yes = real && static_cast<double>(u) * draft_weight(q) * z < e;
       if ((tid & 63) == 0) {
         l.ok[wave] = yes && z > 0.0 && z < INFINITY;
         l.tops[wave] = top;
         l.ats[wave] = at;
+        l.tokens[wave] = x;
         l.zs[wave] = z;
         l.es[wave] = e;
       }
@@ -324,6 +331,8 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Exp2& exp2, in
         l.dec.last = i0 + w + 1 == count;
         l.dec.top = l.tops[w];
         l.dec.best = l.ats[w];
+        l.dec.token = l.tokens[w];
+        l.slot = w;
         l.dec.z = l.zs[w];
         l.dec.refused = l.es[w];
         break;
@@ -391,9 +400,10 @@ struct DrawLds {
   double wsum[kVWaves], before, goal;
   int chunk, rest, hit, last;
 };
-// Draws from the decided row; sums(c): the chunks' sums. The whole workgroup.
+// Draws from the decided row with the number u; sums(c): the chunks' sums.
+// The whole workgroup.
 template <class S>
-__device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, int s, int x, S sums, DrawLds& l) {
+__device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, float u, int x, S sums, DrawLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
   if (wave == 0) {
     const SeqSum none{0.0, 0.0}, own = lane_id() < a.chunks ? sums(lane_id()) : none;
@@ -406,7 +416,7 @@ __device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const
     rest = wave_sum(rest);
     all = wave_sum(all);
     const bool use = !d.last && rest > 0.0;
-    const double goal = static_cast<double>(a.u_sample[s]) * (use ? rest : all);
+    const double goal = static_cast<double>(u) * (use ? rest : all);
     // first chunk in which the running sum passes the goal; behind the last
     // border, the last chunk that has a weight
     double run = 0.0, before = 0.0, last_before = 0.0;
@@ -475,9 +485,15 @@ __device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const
   return l.hit != 0x7fffffff ? l.hit : l.last;
 }
 
-__device__ __forceinline__ void put_tokens(const VerifyArgs& a, int s, int first, int taken, int token) {
+// The drafted token that this lane will put out, if it is accepted.
+__device__ __forceinline__ int own_draft(const VerifyArgs& a, int first, int count) {
+  const int tid = threadIdx.x;
+  return tid + 1 < count ? a.draft_tokens[first + tid] : -1;   // (the last row has none)
+}
+__device__ __forceinline__ void put_tokens(const VerifyArgs& a, int s, int first, int taken, int token, int own) {
   for (int i = threadIdx.x; i < a.max_out; i += kVThreads)
-    a.tokens[static_cast<int64_t>(s) * a.max_out + i] = i < taken ? a.draft_tokens[first + i] : i == taken ? token : -1;
+    a.tokens[static_cast<int64_t>(s) * a.max_out + i] =
+        i < taken ? (i < kVThreads ? own : a.draft_tokens[first + i]) : i == taken ? token : -1;
   if (threadIdx.x == 0) a.n_accepted[s] = taken;
 }
 
@@ -495,7 +511,7 @@ __global__ void __launch_bounds__(kVThreads) verify_decide_kernel(VerifyArgs a) 
     const Decision d = l.dec;
     if (c == 0 && tid == 0) decisions(a)[s] = d;
     if (d.row < 0) continue;                   // uniform; (decide waits for the sequence before)
-    const SeqSum sum = chunk_sums(a, exp2, d, h, d.last ? -1 : a.draft_tokens[d.row], c, lds);
+    const SeqSum sum = chunk_sums(a, exp2, d, h, d.token, c, lds);
     if (tid == 0) seq_sums(a)[static_cast<int64_t>(s) * a.chunks + c] = sum;
   }
 }
@@ -508,11 +524,13 @@ __global__ void __launch_bounds__(kVThreads) verify_draw_kernel(VerifyArgs a) {
     int first, count, token = -1;
     seq_rows(a, s, first, count);
     const SeqSum* cs = seq_sums(a) + static_cast<int64_t>(s) * a.chunks;
+    const Heat h = heat_of(a, s);
+    const float u = a.u_sample[s];
+    const int own = own_draft(a, first, count);
     __syncthreads();                           // the sequence before is done with LDS
     if (d.row >= 0)                            // uniform
-      token = draw(a, exp2, d, heat_of(a, s), s, d.last ? -1 : a.draft_tokens[d.row],
-                   [&](int c) QMV_INLINE { return cs[c]; }, l);
-    put_tokens(a, s, first, d.taken, token);
+      token = draw(a, exp2, d, h, u, d.token, [&](int c) QMV_INLINE { return cs[c]; }, l);
+    put_tokens(a, s, first, d.taken, token, own);
   }
 }
 
@@ -528,13 +546,17 @@ __global__ void __launch_bounds__(kVThreads) verify_finish_kernel(VerifyArgs a) 
     int first, count, token = -1;
     seq_rows(a, s, first, count);
     const Heat h = heat_of(a, s);
+    const float u = a.u_sample[s];
+    const int own = own_draft(a, first, count);
     decide(a, exp2, first, count, h, l);
     const Decision d = l.dec;
     if (d.row >= 0) {                          // uniform
-      const int x = d.last ? -1 : a.draft_tokens[d.row], cx = x >= 0 && x < a.vocab ? x / kChunk : -1;
+      const int x = d.token, cx = x >= 0 && x < a.vocab ? x / kChunk : -1;
+      const double* parts = l.sums[l.slot];
       const RowStat* st = row_stats(a) + static_cast<int64_t>(d.row) * a.chunks;
       const auto sum_of = [&](int c) QMV_INLINE {
         if (h.greedy) return d.best / kChunk == c ? 1.0 : 0.0;
+        if (a.chunks <= kWave) return parts[c];
         return st[c].sum * chunk_scale(a, exp2, st[c].top, d.top, h);
       };
       double left = 0.0;
@@ -543,12 +565,12 @@ __global__ void __launch_bounds__(kVThreads) verify_finish_kernel(VerifyArgs a) 
         left = all - d.refused;
         if (left < 0x1p-10 * all) left = chunk_sums(a, exp2, d, h, x, cx, lds).rest;
       }
-      token = draw(a, exp2, d, h, s, x, [&](int c) QMV_INLINE {
+      token = draw(a, exp2, d, h, u, x, [&](int c) QMV_INLINE {
         const double all = sum_of(c);
         return SeqSum{c == cx ? left : all, all};
       }, dl);
     }
-    put_tokens(a, s, first, d.taken, token);
+    put_tokens(a, s, first, d.taken, token, own);
   }
 }
 

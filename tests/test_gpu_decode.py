@@ -513,6 +513,37 @@ def test_verify_many_sequences():
     run_verify(logits, B.TARGET_LOGITS, temp, tok, q, start, rng.random(rows, np.float32), rng.random(333, np.float32), 2)
 
 
+@pytest.mark.parametrize("drafted", [True, False])
+def test_verify_large_vocabulary(drafted):
+    """More chunks of a row than a wave has lanes."""
+    V, start = 300007, np.array([0, 3, 5])
+    rng = np.random.default_rng(9)
+    logits = (rng.standard_normal((5, V)) * 2).astype(np.float32)
+    q = softmax(logits + 0.3 * rng.standard_normal((5, V)))
+    tok = np.array([rng.choice(V, p=r / r.sum()) for r in q.astype(np.float64)])
+    seen = set()
+    for t in range(4):
+        ua = rng.random(5, np.float32) * (1 if drafted else np.float32(1e-5))
+        count, _ = run_verify(logits, B.TARGET_LOGITS, np.array([1.0, 0.5], np.float32), tok, q if drafted else None, start, ua,
+                              rng.random(2, np.float32), 4)
+        seen.update(count.tolist())
+    assert len(seen) > 1
+
+
+@pytest.mark.parametrize("refused", [0, 7, 8, 512, 513, 599, 600])
+def test_verify_long_drafts(refused):
+    """More drafted tokens than a workgroup has lanes; the first refused one anywhere."""
+    V, rows = 50, 601
+    rng = np.random.default_rng(refused)
+    logits = rng.standard_normal((rows, V)).astype(np.float32)
+    tok = logits.argmax(1)
+    if refused < 600:
+        tok[refused] = (tok[refused] + 1) % V
+    count, out = run_verify(logits, B.TARGET_LOGITS, np.zeros(1, np.float32), tok, None, [0, rows], rng.random(rows, np.float32),
+                            rng.random(1, np.float32), 700)
+    assert count[0] == refused and out[0, refused] == logits[refused].argmax() and (out[0, refused + 1:] == -1).all()
+
+
 def test_verify_edges():
     """Ties, masked and missing logits, tokens outside, numbers at the ends."""
     V, start = 5000, np.arange(0, 25, 2)                # one draft each
