@@ -160,7 +160,9 @@ int mmvq_attn_workspace(const mmvq_kv_cache *cache, const mmvq_kv_batch *batch,
  * 4-byte aligned, without overlap; q must be finite.
  * Keys and values enter at their stored precision; scores, softmax and sums
  * are fp32, with q carried as two fp16 parts (21 bits of the row's largest
- * value) and each probability as two fp16 parts (20 bits).
+ * value) and each probability as two fp16 parts (20 bits; a key's share of the
+ * result is good to 2^-32 of the largest value that the row sees, where that
+ * is more).
  * workspace: 16-byte aligned, at least mmvq_attn_workspace bytes (fewer:
  * MMVQ_ERR_SHAPE). n_heads <= 65535 and n_tokens * n_heads <= 2^30; a launch
  * beyond 2^23 workgroups (sequences * key/value heads * tiles of 16 to 128

@@ -54,27 +54,31 @@ _EP = ctypes.POINTER(Epilogue)
 
 
 class KVCache(ctypes.Structure):
-    """``mmvq_kv_cache`` (made by ``kv_cache()``; holds addresses, not tensors)."""
+    """``mmvq_kv_cache``: addresses; made by ``kv_cache()`` it keeps the tensors, too."""
     _fields_ = [("k", _p), ("v", _p), ("type", _int), ("n_pages", _int), ("page_size", _int),
                 ("n_kv_heads", _int), ("head_dim", _int)]
 
 
 class KVBatch(ctypes.Structure):
-    """``mmvq_kv_batch`` (made by ``kv_batch()``; holds addresses, not tensors)."""
+    """``mmvq_kv_batch``: addresses; made by ``kv_batch()`` it keeps the tensors, too."""
     _fields_ = [("token_start", _p), ("seq_len", _p), ("page_table", _p), ("table_stride", _i64),
                 ("n_seqs", _int), ("n_tokens", _int), ("pages_per_seq", _int), ("max_new", _int),
                 ("max_len", _int)]
 
 
 def kv_cache(k, v, kv_type: int, n_pages: int, page_size: int, n_kv_heads: int, head_dim: int) -> KVCache:
-    return KVCache(_addr(k), _addr(v), kv_type, n_pages, page_size, n_kv_heads, head_dim)
+    c = KVCache(_addr(k), _addr(v), kv_type, n_pages, page_size, n_kv_heads, head_dim)
+    c.tensors = k, v
+    return c
 
 
 def kv_batch(token_start, seq_len, page_table, n_seqs: int, n_tokens: int, max_new: int, max_len: int,
              pages_per_seq: int, table_stride: int | None = None) -> KVBatch:
-    return KVBatch(_addr(token_start), _addr(seq_len), _addr(page_table),
-                   pages_per_seq if table_stride is None else table_stride, n_seqs, n_tokens, pages_per_seq,
-                   max_new, max_len)
+    b = KVBatch(_addr(token_start), _addr(seq_len), _addr(page_table),
+                pages_per_seq if table_stride is None else table_stride, n_seqs, n_tokens, pages_per_seq,
+                max_new, max_len)
+    b.tensors = token_start, seq_len, page_table
+    return b
 
 
 _KC, _KB = ctypes.POINTER(KVCache), ctypes.POINTER(KVBatch)

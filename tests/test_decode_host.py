@@ -191,3 +191,20 @@ def test_layout_and_launch_arithmetic(tmp_path):
     res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
     assert res.returncode == 0, res.stdout[-4000:]
     assert "0 failing check(s)" in res.stdout
+
+
+def test_descriptors_keep_their_tensors():
+    """A batch made of temporaries stays valid as long as it is itself there."""
+    import gc
+    import weakref
+    import torch
+    parts = [torch.zeros(4, dtype=torch.int32) for _ in range(3)]
+    refs = [weakref.ref(x) for x in parts]
+    b = B.kv_batch(*parts, 1, 1, 1, 1, 1)
+    c = B.kv_cache(torch.zeros(64), torch.zeros(64), B.F16, 1, 16, 1, 64)
+    del parts
+    gc.collect()
+    assert all(r() is not None for r in refs) and c.tensors[0].data_ptr() == c.k
+    del b
+    gc.collect()
+    assert all(r() is None for r in refs)

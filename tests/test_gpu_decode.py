@@ -362,8 +362,7 @@ def test_attention_over_infinite_keys_alone(length, new, sinks):
     n = length + new - 1
     rows = dev(np.tile(np.array([1e6, -1e6], np.float32), (n, D // 2)))
     ones = dev(np.ones((n, D), np.float32))
-    whole = B.kv_batch(dev(np.array([0, n], np.int32)), dev(np.array([n], np.int32)), p.d[2], 1, n, n, n, p.wide)
-    B.mmvq_kv_write(p.cache, whole, rows, D, ones, D)
+    B.mmvq_kv_write(p.cache, p.batch(whole=True), rows, D, ones, D)
     size = B.mmvq_attn_workspace(p.cache, p.batch(), 1)
     out = torch.zeros(new, D, device="cuda:0")
     B.mmvq_attn(p.cache, p.batch(), dev(np.ones((new, D), np.float32)), D, 1, 0.125, 0,
@@ -401,6 +400,35 @@ def test_attention_scales(kind, qscale, kscale):
     if kind == "f16" and kscale < 1e-3:                # below fp16's range
         qscale, kscale = qscale * kscale / 1e-3, 1e-3
     run_attention(p, 2, seed=5, qscale=qscale, kscale=kscale)
+
+
+@pytest.mark.parametrize("kind", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("new", [4, 100])
+def test_attention_of_uneven_scales(kind, new):
+    """Value blocks whose scales differ by 2^28 between tokens and between the
+    blocks of a token, subnormal and zero ones among them."""
+    D, H = 128, 2
+    p = R.Paged(kind, D, H, 32, [new], [new + 300], seed=31)
+    rng = np.random.default_rng(31)
+    n = new + 300
+    raw = rng.standard_normal((n, H, D)) * np.repeat(2.0 ** rng.integers(-18, 11, (n, H, D // 32)), 32, axis=2)
+    raw[5] = 0
+    raw[6, :, 32:] = 0
+    raw[7] *= 1e-12                                    # scales below fp16's range are 0
+    raw = raw.astype(np.float32)
+    kk = rng.standard_normal((n, H, D)).astype(np.float32)
+    B.mmvq_kv_write(p.cache, p.batch(whole=True), dev(kk.reshape(n, -1)), H * D, dev(raw.reshape(n, -1)), H * D)
+
+    k, v = R.stored(kk, kind), R.stored(raw, kind)
+    q = (rng.standard_normal((new, 2 * H, D)) * 2).astype(np.float32)
+    size = B.mmvq_attn_workspace(p.cache, p.batch(), 2 * H)
+    import torch
+    out = nan(new, 2 * H * D)
+    B.mmvq_attn(p.cache, p.batch(), dev(q.reshape(new, -1)), 2 * H * D, 2 * H, D ** -0.5, 0, None, out, 2 * H * D,
+                torch.empty(size + 16, dtype=torch.uint8, device="cuda:0"), size)
+    ref, mag, smax = R.attention(q, k, v, float(np.float32(D ** -0.5)), 300)
+    tol = R.attention_tolerance(ref, mag, smax, v, D)
+    assert (np.abs(host(out).reshape(ref.shape) - ref) <= tol).all()
 
 
 def test_offsets_past_32_bits():
