@@ -23,8 +23,9 @@
 // keys, e the exponent field of the token's largest |d| (0 for F16), and the
 // weight w = 2^(s + e - M + K) enters l times 2^(16 - e) and O times
 // d 2^(16 - e), which is below 4: fp16 numbers, off by 2^-32 of the largest at
-// most however small they are, whatever the scales. The factor 2^(K + 16 - M)
-// cancels in O / l. Scores, M, l and O are fp32.
+// most however small they are. The factor 2^(K + 16 - M) cancels in O / l. A
+// token's scales that lie so far below its largest that the factor takes bits
+// from them have these added apart (lost_f16). Scores, M, l and O are fp32.
 //
 // Two kernels: with few rows the four waves of a workgroup take every fourth
 // step of the same rows, read operands from memory straight into registers
@@ -134,6 +135,26 @@ __device__ __forceinline__ float factor_field(uint32_t word, int half) {   // e
 }
 __device__ __forceinline__ uint32_t pk_mul_f16(uint32_t a, uint32_t b) {
   return __builtin_bit_cast(uint32_t, __builtin_bit_cast(half2v, a) * __builtin_bit_cast(half2v, b));
+}
+
+// A factor below 1 (a largest scale of 4 and more) takes the token's scales
+// that are 2^-15 of the largest and less under fp16's 2^-14, where they lose
+// up to 2^-25 of a product that is 2 and more for the largest. What they lose
+// is exact in fp32, and times 2^kLost in fp16; with the first part of the
+// weight times 2^-kLost it is one more product, below 2^-12 and so off by
+// 2^-25 itself. Rare; either kernel takes it where it costs its walk least.
+constexpr int kLost = 14;
+__device__ __forceinline__ uint32_t min_u16x2(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_min(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
+__device__ __forceinline__ bool below_one(uint32_t factors) { return (factors & 0xFFFFu) < 0x3C00u || (factors >> 16) < 0x3C00u; }
+__device__ __forceinline__ uint32_t lost_f16(uint32_t d, uint32_t factor) {
+  constexpr float up = static_cast<float>(1 << kLost);
+  const uint32_t kept = pk_mul_f16(d, factor);
+  const half2v r = {static_cast<_Float16>(up * fmaf(h2f(d), h2f(factor), -h2f(kept))),
+                    static_cast<_Float16>(up * fmaf(h2f(d >> 16), h2f(factor >> 16), -h2f(kept >> 16)))};
+  return __builtin_bit_cast(uint32_t, r);
 }
 
 // Words of 8 fp16 whose elements c.. are cleared.
@@ -570,7 +591,8 @@ struct Rows {
   }
 
   // Scores to weights; M, l and O follow. factor, e5: of the 8 tokens (F16: not read).
-  __device__ __forceinline__ void weigh(int t, u32x4 factor, const float (&e5)[8], f32x4 (&s)[MT][2]) {
+  // shift: kTop, less kLost in a walk for what scales lost.
+  __device__ __forceinline__ void weigh(int t, u32x4 factor, const float (&e5)[8], float shift, f32x4 (&s)[MT][2]) {
     float top;
     if constexpr (KIND == kKvF16) {
       top = s[t][0][0];
@@ -595,7 +617,7 @@ struct Rows {
         for (int i = 0; i < 4; ++i) o[t][d][i] *= al;
       m[t] = top;
     }
-    const float off = kTop - (m[t] == -INFINITY ? 0.0f : m[t]);   // a row that has seen nothing yet: all weights 0
+    const float off = shift - (m[t] == -INFINITY ? 0.0f : m[t]);   // a row that has seen nothing yet: all weights 0
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = s[t][j / 4][j & 3], w = __builtin_amdgcn_exp2f(KIND == kKvF16 ? fmaf(x, to_log2[t], off) : x + off);
@@ -617,11 +639,12 @@ struct Rows {
   }
 
   // O of the step. value(d): operand of dims 16 d ..; scale(b): the 8 tokens'
-  // scales of block b, times the tokens' factors. A quantized block's weights
-  // are formed while the products of the block before run.
+  // scales of block b, times the tokens' factors; wh: the weights' first
+  // parts. A quantized block's weights are formed while the products of the
+  // block before run.
   template <class V, class S>
-  __device__ __forceinline__ void accumulate(V value, S scale, const f32x4 (&s)[MT][2]) {
-    u32x4 wh[MT], wl[MT], ph[2][MT], pl[2][MT];
+  __device__ __forceinline__ void accumulate(V value, S scale, const f32x4 (&s)[MT][2], u32x4 (&wh)[MT]) {
+    u32x4 wl[MT], ph[2][MT], pl[2][MT];
     u32x4 n0, n1, ns;                           // the next block's values and the scales of its weights, read ahead
     if constexpr (AHEAD) {
       n0 = value(0);
@@ -708,6 +731,31 @@ struct Rows {
       }
     }
   }
+
+  // Quantized: what the step's scales lost by their factors. Read from the
+  // cache again: few registers.
+  template <class V>
+  __device__ __forceinline__ void add_lost(const AttnArgs& a, const Place& w, int t0, V value, u32x4 factor, const u32x4 (&wh)[MT]) {
+    const int g = lane_id() >> 4, pos = t0 + 8 * g, page = a.b.page(w.s, pos), real = page < 0 ? 0 : w.keys - pos;
+    const uint8_t* unit = a.v + a.b.unit(page < 0 ? 0 : page, w.head, pos) * kv_unit_bytes(KIND, NB);   // a hole's is masked
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      asm volatile("" ::: "memory");            // one block's loads at a time
+      u32x4 rest = ld_a16_x4(unit + kv_scale_at(KIND, NB, b, 8 * (g & 1)));
+#pragma unroll
+      for (int e = 0; e < 4; ++e) rest[e] = lost_f16(rest[e] & keep_mask(e, real), factor[e]);
+      if (!__any((rest[0] | rest[1] | rest[2] | rest[3]) != 0)) continue;
+      constexpr uint32_t down = ((15u - kLost) << 10) * 0x10001u;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        u32x4 p;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) p[e] = pk_mul_f16(pk_mul_f16(wh[t][e], down), rest[e]);
+        o[t][2 * b] = mfma_f16(value(2 * b), p, o[t][2 * b]);
+        o[t][2 * b + 1] = mfma_f16(value(2 * b + 1), p, o[t][2 * b + 1]);
+      }
+    }
+  }
 };
 
 // Few rows: the waves share the keys.
@@ -772,7 +820,7 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_keys_kernel
       u32x4 factor;
       if constexpr (KIND != kKvF16) vr.normalise(factor, e5);
 #pragma unroll
-      for (int t = 0; t < MT; ++t) r.weigh(t, factor, e5, s);
+      for (int t = 0; t < MT; ++t) r.weigh(t, factor, e5, r.kTop, s);
       const auto value = [&](int d) QMV_INLINE { return vr.operand(d / 2, d & 1); };
       if constexpr (KIND == kKvF16) {
         if (wild) {
@@ -780,7 +828,12 @@ __global__ void __launch_bounds__(kAttnThreads, NB < 8 ? 2 : 1) attn_keys_kernel
           for (int t = 0; t < MT; ++t) r.add_wild(a, w, t, t0, s);
         }
       }
-      r.accumulate(value, [&](int b) QMV_INLINE { return vr.sc[KIND == kKvF16 ? 0 : b]; }, s);
+      u32x4 wh[MT];
+      r.accumulate(value, [&](int b) QMV_INLINE { return vr.sc[KIND == kKvF16 ? 0 : b]; }, s, wh);
+      if constexpr (KIND != kKvF16) {
+        const uint32_t low = min_u16x2(min_u16x2(factor[0], factor[1]), min_u16x2(factor[2], factor[3]));
+        if (__builtin_expect(__any(below_one(low)), 0)) r.add_lost(a, w, t0, value, factor, wh);
+      }
     }
 
     // the waves' shares joined: each scaled to the common maximum
@@ -835,6 +888,7 @@ struct StepLds {
   uint32_t factor[16];                          // the factors
   float e5[kStep];                              // and their exponent fields
   int wild[4];                                  // F16, of each wave's share: an infinity or NaN was among the values
+  int low;                                      // quantized: a factor of the walk was below 1
 };
 
 // A lane's share of a step on its way to LDS: runs of block b of operand lane
@@ -846,6 +900,7 @@ struct StepRegs {
   static constexpr int kValueWords = KIND == kKvF16 ? 8 : KIND == kKvQ8 ? 4 : 2;
   uint32_t k[kItems][2][kKeyWords], v[kItems][kValueWords];
   uint32_t ksc, vsc[KIND == kKvF16 ? 1 : NB];   // of lanes 0..16 NB-1: word lane % 16, of block lane / 16 and of all blocks
+  uint32_t low = ~0u;                           // of lanes 0..15: smallest factors stored
   bool ok[2];
 
   __device__ __forceinline__ void load(const AttnArgs& a, StepIds ids, int head, int t0) {
@@ -905,7 +960,8 @@ struct StepRegs {
     }
   }
 
-  __device__ __forceinline__ void store(StepLds<KIND, NB>& lds, int t0, int keys) {
+  // lost: what the value scales lose by their factors, in their place
+  __device__ __forceinline__ void store(StepLds<KIND, NB>& lds, int t0, int keys, bool lost) {
     const int tid = threadIdx.x;
     const bool part = !__all(ok[0] && ok[1]) || t0 + kStep > keys;   // slots without a token
     uint32_t any = 0;
@@ -958,8 +1014,9 @@ struct StepRegs {
           top = max_u16x2(top, vsc[i] & 0x7FFF7FFFu);
         }
         const uint32_t f = token_factors(top);
-        lds.vsc[b][word] = pk_mul_f16(own, f);
+        lds.vsc[b][word] = __builtin_expect(lost, 0) ? lost_f16(own, f) : pk_mul_f16(own, f);
         if (b == 0) {
+          low = min_u16x2(low, f);
           lds.factor[word] = f;
           lds.e5[2 * word] = factor_field(f, 0);
           lds.e5[2 * word + 1] = factor_field(f, 1);
@@ -993,69 +1050,96 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
     StepRegs<KIND, NB> in;
     StepIds next;
     const int zero = vector_zero();
-    if (t_beg < t_end) {
+    const auto begin = [&]() QMV_INLINE {       // the first step's loads
+      if (t_beg >= t_end) return;
       const StepIds ids = step_ids(a, w.s, t_beg, zero);
       next = step_ids(a, w.s, t_beg + kStep, zero);
       in.load(a, ids, w.head, t_beg);
-    }
+    };
+    begin();
     Rows<KIND, NB, MT, false, true> r;
     r.init(a, w, row0);
-    __syncthreads();                            // the tile before is done with LDS
-    if (t_beg < t_end) in.store(lds[0], t_beg, w.keys);
-    __syncthreads();
-    int buf = 0;
-    for (int t0 = t_beg; t0 < t_end; t0 += kStep, buf ^= 1) {
-      const bool ok0 = in.ok[0], ok1 = in.ok[1], more = t0 + kStep < t_end;
-      if (more) {
-        in.load(a, next, w.head, t0 + kStep);
-        next = step_ids(a, w.s, t0 + 2 * kStep, zero);
-      }
-      const StepLds<KIND, NB>& st = lds[buf];
-      if (kStraight || (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1))) {   // some row sees some of it
-        f32x4 s[MT][2];
-        // products first: of the two waves of a SIMD, one multiplies while the
-        // other weighs (2048 tokens over 8192, Q4_0: 597 us without, 580 with
-        // the scores first, 544 with both products; of 256 dims Q8_0 1745 us
-        // so, 1785 with both)
-        __builtin_amdgcn_s_setprio(1);
-        r.scores([&](int mm, int b) QMV_INLINE { return st.k[mm][b][lane]; },
-                 [&](int b) QMV_INLINE { return *reinterpret_cast<const u32x4*>(&st.ksc[KIND == kKvF16 ? 0 : b][4 * g]); }, s);
-        __builtin_amdgcn_s_setprio(0);
-        const bool whole = __all(ok0 && ok1) && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
-        if (!whole) {
-          const int real = (g >> 1 ? ok1 : ok0) ? w.keys - (t0 + 8 * g) : 0;
-#pragma unroll
-          for (int t = 0; t < MT; ++t) r.hide(a, t, t0 + 8 * g, real, s);
-        }
-        float e5[8];
-        u32x4 factor;
-        if constexpr (KIND != kKvF16) {
-          factor = *reinterpret_cast<const u32x4*>(&st.factor[4 * g]);
-#pragma unroll
-          for (int j = 0; j < 8; j += 4) {
-            const f32x4 x = *reinterpret_cast<const f32x4*>(&st.e5[8 * g + j]);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) e5[j + i] = x[i];
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < MT; ++t) r.weigh(t, factor, e5, s);
-        const auto value = [&](int d) QMV_INLINE { return st.v[d][lane]; };
-        if constexpr (KIND == kKvF16) {
-          if (st.wild[0] | st.wild[1] | st.wild[2] | st.wild[3]) {
-#pragma unroll
-            for (int t = 0; t < MT; ++t) r.add_wild(a, w, t, t0, s);
-          }
-        }
-        if (kStraight && more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
-        if constexpr (NB < 8) __builtin_amdgcn_s_setprio(1);
-        r.accumulate(value, [&](int b) QMV_INLINE {
-          return *reinterpret_cast<const u32x4*>(&st.vsc[KIND == kKvF16 ? 0 : b][4 * g]);
-        }, s);
-        if constexpr (NB < 8) __builtin_amdgcn_s_setprio(0);
-      }
-      if (!kStraight && more) in.store(lds[buf ^ 1], t0 + kStep, w.keys);
+    // What scales lost is added by a second walk: a branch for it in the first
+    // costs every step (Q8_0, 2048 tokens over 8192: 128 dims 543 -> 686 us
+    // behind the second product and 554 before it, 256 dims 1150 -> 1213). Its
+    // weights are those of the first, whose M stands; l is the first one's.
+    bool lost = false;
+    float shift = r.kTop, l_first[MT];
+    while (true) {
+      __syncthreads();                          // the tile or walk before is done with LDS
+      if (t_beg < t_end) in.store(lds[0], t_beg, w.keys, lost);
       __syncthreads();
+      int buf = 0;
+      for (int t0 = t_beg; t0 < t_end; t0 += kStep, buf ^= 1) {
+        const bool ok0 = in.ok[0], ok1 = in.ok[1], more = t0 + kStep < t_end;
+        if (more) {
+          in.load(a, next, w.head, t0 + kStep);
+          next = step_ids(a, w.s, t0 + 2 * kStep, zero);
+        }
+        const StepLds<KIND, NB>& st = lds[buf];
+        if (kStraight || (lo <= hi && t0 <= hi && (a.window <= 0 || t0 + kStep > lo - a.window + 1))) {   // some row sees some of it
+          f32x4 s[MT][2];
+          // products first: of the two waves of a SIMD, one multiplies while the
+          // other weighs (2048 tokens over 8192, Q4_0: 597 us without, 580 with
+          // the scores first, 544 with both products; of 256 dims Q8_0 1745 us
+          // so, 1785 with both)
+          __builtin_amdgcn_s_setprio(1);
+          r.scores([&](int mm, int b) QMV_INLINE { return st.k[mm][b][lane]; },
+                   [&](int b) QMV_INLINE { return *reinterpret_cast<const u32x4*>(&st.ksc[KIND == kKvF16 ? 0 : b][4 * g]); }, s);
+          __builtin_amdgcn_s_setprio(0);
+          const bool whole = __all(ok0 && ok1) && t0 + kStep - 1 <= lo && t0 + kStep <= w.keys && (a.window <= 0 || t0 > hi - a.window);
+          if (!whole) {
+            const int real = (g >> 1 ? ok1 : ok0) ? w.keys - (t0 + 8 * g) : 0;
+#pragma unroll
+            for (int t = 0; t < MT; ++t) r.hide(a, t, t0 + 8 * g, real, s);
+          }
+          float e5[8];
+          u32x4 factor;
+          if constexpr (KIND != kKvF16) {
+            factor = *reinterpret_cast<const u32x4*>(&st.factor[4 * g]);
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) {
+              const f32x4 x = *reinterpret_cast<const f32x4*>(&st.e5[8 * g + j]);
+#pragma unroll
+              for (int i = 0; i < 4; ++i) e5[j + i] = x[i];
+            }
+          }
+#pragma unroll
+          for (int t = 0; t < MT; ++t) r.weigh(t, factor, e5, shift, s);
+          const auto value = [&](int d) QMV_INLINE { return st.v[d][lane]; };
+          if constexpr (KIND == kKvF16) {
+            if (st.wild[0] | st.wild[1] | st.wild[2] | st.wild[3]) {
+#pragma unroll
+              for (int t = 0; t < MT; ++t) r.add_wild(a, w, t, t0, s);
+            }
+          }
+          if (kStraight && more) in.store(lds[buf ^ 1], t0 + kStep, w.keys, lost);
+          if constexpr (NB < 8) __builtin_amdgcn_s_setprio(1);
+          u32x4 wh[MT];
+          r.accumulate(value, [&](int b) QMV_INLINE {
+            return *reinterpret_cast<const u32x4*>(&st.vsc[KIND == kKvF16 ? 0 : b][4 * g]);
+          }, s, wh);
+          if constexpr (NB < 8) __builtin_amdgcn_s_setprio(0);
+        }
+        if (!kStraight && more) in.store(lds[buf ^ 1], t0 + kStep, w.keys, lost);
+        __syncthreads();
+      }
+      if (KIND == kKvF16 || lost) break;
+      if (wave == 0) {
+        const bool low = __any(below_one(in.low));
+        if (lane == 0) lds[0].low = low;
+      }
+      __syncthreads();
+      if (!__builtin_amdgcn_readfirstlane(lds[0].low)) break;
+      lost = true;
+      shift = r.kTop - kLost;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) l_first[t] = r.l[t];
+      begin();
+    }
+    if (lost) {
+#pragma unroll
+      for (int t = 0; t < MT; ++t) r.l[t] = l_first[t];
     }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {

@@ -1,0 +1,73 @@
+"""Attention over the cache: the precision that include/mmvq_decode.h states,
+held key by key and block by block."""
+import numpy as np
+import pytest
+
+import decode_ref as R
+from gpu_helpers import announce, dev, host
+from quantized_decode_gemv_quantize_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+def attend(p, q, heads, window=0, scale=None, sinks=None):
+    """The operator on rows q [n, heads, D]."""
+    import torch
+    n, D = len(q), p.D
+    out = torch.full((n, heads * D), float("nan"), device="cuda:0")
+    batch = p.batch()
+    size = B.mmvq_attn_workspace(p.cache, batch, heads)
+    ws = torch.empty(size + 16, dtype=torch.uint8, device="cuda:0")
+    B.mmvq_attn(p.cache, batch, dev(q.reshape(n, -1)), heads * D, heads, float(np.float32(D ** -0.5)) if scale is None else scale,
+                window, None if sinks is None else dev(sinks), out, heads * D, ws, size)
+    return host(out).reshape(n, heads, D).astype(np.float64)
+
+
+def write(p, k, v):
+    """k, v [tokens, H, D] into the cache, from position 0; what is stored of them."""
+    n = len(k)
+    B.mmvq_kv_write(p.cache, p.batch(whole=True), dev(k.reshape(n, -1)), p.H * p.D, dev(v.reshape(n, -1)), p.H * p.D)
+    return R.stored(k, p.kind), R.stored(v, p.kind)
+
+
+@pytest.mark.parametrize("kind", ["q8_0", "q4_0"])
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("new,window", [(1, 1), (20, 1), (20, 3), (100, 1), (300, 3)])
+def test_small_blocks_beside_large_ones(kind, D, new, window):
+    """Tokens whose largest value scale is 4 to 2^10 and whose other blocks'
+    are 2^14 to 2^26 below it (fp16 has no more), seen one key at a time or
+    three: every value within the stated part of its own size, and of the
+    largest value that the row sees in its head.
+
+    A lone key's probability is 1. Its parts are off by 2^-20, the sum, the
+    factor and the product round a few times (2^-24 each). Of three keys the
+    exponent that joins each score (below 32) rounds by 2^-20 in units of
+    log2, 2 ln 2 2^-20 between two keys, exp2 by 2^-23 twice; scores below
+    2^-5, of sums of at most 256 terms, are off by 2^-21: 2^-18 covers it."""
+    announce(f"small blocks {kind} D={D} new={new} window={window}")
+    H, n, NB = 2, new, D // 32
+    rng = np.random.default_rng(D + new + window)
+    p = R.Paged(kind, D, H, 32, [new], [n], seed=D)
+    e = rng.integers(-16, -5, (n, H, NB))
+    top = rng.integers(0, NB, (n, H))
+    np.put_along_axis(e, top[..., None], rng.integers(2, 11, (n, H))[..., None], -1)
+    if n > 1:
+        e[n // 2, :, 0] = -30                           # a block that is stored as zeros
+    full = 127 if kind == "q8_0" else 8                 # a scale is the block's largest value by this
+    raw = rng.uniform(-1, 1, (n, H, NB, 32))
+    raw[..., 7] = rng.choice([-1.0, 1.0], (n, H, NB))
+    v = (raw * full * 1.3 * 2.0 ** e[..., None]).reshape(n, H, D).astype(np.float32)
+    k = rng.standard_normal((n, H, D)).astype(np.float32)
+    k, v = write(p, k, v)
+    q = (rng.standard_normal((new, 2 * H, D)) * 2.0 ** -13).astype(np.float32)
+    got = attend(p, q, 2 * H, window=window)
+    ref, mag, smax = R.attention(q, k, v, float(np.float32(D ** -0.5)), 0, window)
+    assert smax.max() < 2.0 ** -5
+    keys = np.arange(n)
+    for i in range(new):
+        seen = (keys <= i) & (keys > i - window)
+        big = np.abs(v[seen]).max((0, 2)).repeat(2)     # of each query head
+        rel = (2.0 ** -20 + 2.0 ** -21) if seen.sum() == 1 else 2.0 ** -18
+        tol = rel * mag[i] + seen.sum() * 2.0 ** -32 * big[:, None]
+        err = np.abs(got[i] - ref[i])
+        assert (err <= tol).all(), f"row {i}: {(~(err <= tol)).sum()} off, worst err/tol {(err / tol).max()}"
