@@ -3,6 +3,7 @@ held key by key and block by block."""
 import numpy as np
 import pytest
 
+import decode_pins as P
 import decode_ref as R
 from gpu_helpers import announce, dev, host
 from quantized_decode_gemv_quantize_amd import binding as B
@@ -71,3 +72,21 @@ def test_small_blocks_beside_large_ones(kind, D, new, window):
         tol = rel * mag[i] + seen.sum() * 2.0 ** -32 * big[:, None]
         err = np.abs(got[i] - ref[i])
         assert (err <= tol).all(), f"row {i}: {(~(err <= tol)).sum()} off, worst err/tol {(err / tol).max()}"
+
+
+@pytest.mark.parametrize("kind", list(R.KINDS))
+@pytest.mark.parametrize("D", [64, 96, 128, 256])
+@pytest.mark.parametrize("new", [3, 8, 12, 40])
+@pytest.mark.parametrize("part", ["q", "weights"])
+def test_parts_of_scores_and_weights(kind, D, new, part):
+    """The query's and the probabilities' second parts, at bounds that forms
+    of five bits fewer do not keep (tests/test_decode_pins.py), for every
+    shape of a workgroup: 12, 32, 48 and 160 rows."""
+    announce(f"parts {kind} D={D} new={new} {part}")
+    k, v, q = P.inputs(kind, D, part, new)
+    p = R.Paged(kind, D, k.shape[1], 16, [new], [len(k)], seed=new)
+    k, v = write(p, k, v)
+    ref, mag = P.reference(q, k, v, float(np.float32(D ** -0.5)))
+    err = np.abs(attend(p, q, q.shape[1], window=P.WINDOW) - ref)
+    tol = P.tolerance(mag, part, v)
+    assert (err <= tol).all(), f"worst err/tol {(err / tol).max()}"
