@@ -90,3 +90,25 @@ def test_parts_of_scores_and_weights(kind, D, new, part):
     err = np.abs(attend(p, q, q.shape[1], window=P.WINDOW) - ref)
     tol = P.tolerance(mag, part, v)
     assert (err <= tol).all(), f"worst err/tol {(err / tol).max()}"
+
+
+@pytest.mark.parametrize("kind", list(R.KINDS))
+@pytest.mark.parametrize("qscale,kscale", [(1e5, 1e-5), (1e3, 1e-3), (1e-3, 1e3)])
+@pytest.mark.parametrize("new", [2, 60])
+def test_large_queries_of_small_keys(kind, qscale, kscale, new):
+    """Ordinary scores and values from queries and keys of any size that the
+    cache's types hold (at 1e-5 block scales are 4 to 60 of fp16's smallest
+    steps): the row's exponent of the query is taken in and out again."""
+    announce(f"scales {kind} q {qscale} k {kscale} new={new}")
+    D, n = 64, new + 440
+    rng = np.random.default_rng(23)
+    p = R.Paged(kind, D, 1, 32, [new], [n], seed=23)
+    k, v = write(p, (rng.standard_normal((n, 1, D)) * kscale).astype(np.float32), rng.standard_normal((n, 1, D)).astype(np.float32))
+    assert (np.abs(k).max((1, 2)) > 0).all() and (np.abs(v).max((1, 2)) > 0).all()
+    q = (rng.standard_normal((new, 2, D)) * qscale).astype(np.float32)
+    scale = float(np.float32(D ** -0.5))
+    ref, mag, smax = R.attention(q, k, v, scale, n - new)
+    z = scale * np.abs(np.einsum("nhd,kd->nhk", q.astype(np.float64), k[:, 0]))
+    assert z.max() > 1 and np.abs(ref).max() > 0.1
+    err, tol = np.abs(attend(p, q, 2) - ref), R.attention_tolerance(ref, mag, smax, v, D)
+    assert (err <= tol).all(), f"worst err/tol {(err / tol).max()}"
