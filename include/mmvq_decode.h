@@ -51,7 +51,10 @@ enum { MMVQ_F16 = 1 };
  * of y, n * K/32 blocks of 36 bytes, what mmvq and its variants take: q =
  * roundf(y/d) and s = d*sum(q) as mmvq_quantize_q8_1 has them, with d =
  * max|y| * fp32(1/127) in fp32, the product with the rounded reciprocal,
- * within one unit in the last place of that function's quotient). sum_out may
+ * which is what torch computes for amax / 127.0 on this GPU). That function's
+ * d is a quotient: stored scales differ by at most one fp16 step and codes by
+ * at most 1, where y/d lies within 2^-14 of a border (some 10^-7 of them).
+ * Where its bits matter, take y and call it. sum_out may
  * be x or residual itself (same pointer and stride), and y may be x where
  * sum_out is not; otherwise the buffers do not overlap.
  * Requires 1 <= K <= 2^24, n >= 0 and n*K <= 2^40, every ld >= K, K % 32 == 0

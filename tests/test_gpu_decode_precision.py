@@ -112,3 +112,46 @@ def test_large_queries_of_small_keys(kind, qscale, kscale, new):
     assert z.max() > 1 and np.abs(ref).max() > 0.1
     err, tol = np.abs(attend(p, q, 2) - ref), R.attention_tolerance(ref, mag, smax, v, D)
     assert (err <= tol).all(), f"worst err/tol {(err / tol).max()}"
+
+
+@pytest.mark.parametrize("n,K", [(3, 4096), (40, 14336), (2, 40000), (1, 32)])
+def test_norm_columns_beside_the_quantizer(n, K):
+    """The norm's q8_1 columns and mmvq_quantize_q8_1 on its fp32 output.
+
+    Their scales, a product with fp32(1/127) and a quotient, are off from
+    amax/127 by 2^-23 (two roundings) and 2^-24 of it: fp16(d) is the same or
+    the next. Quotients x/d round once more each, 5 2^-24 of at most 127 in
+    all: below 2^-14, so that codes differ by 1 at most, and only where x/d
+    lies within that of a half."""
+    import torch
+    rng = np.random.default_rng(K)
+    x = rng.choice([-1.0, 1.0], (n, K)).astype(np.float32)     # of mean square 1: the norm is the weight
+    w = (rng.standard_normal(K) * np.exp(rng.standard_normal(K))).astype(np.float32)
+    at = np.arange(0, K, 32)[: K // 64 + 1]
+    half = rng.integers(0, 127, len(at)) + 0.5                  # codes on borders, of scales that are not
+    top = rng.uniform(1, 2000, len(at)).astype(np.float32)
+    top[0], half[0] = 18.0, 63.5                                # 9 of 18
+    for i, b in enumerate(at):
+        w[b:b + 32] *= 0.1 * top[i] / max(1.0, np.abs(w[b:b + 32]).max())
+        w[b] = top[i]
+        w[b + 1:b + 4] = np.float32(half[i] * (float(top[i]) / 127.0))
+    y = torch.full((n, K), float("nan"), device="cuda:0")
+    got = torch.zeros((n, K // 32 * 36), dtype=torch.uint8, device="cuda:0")
+    want = torch.zeros_like(got)
+    B.mmvq_add_rms_norm(dev(x), K, n, K, None, 0, dev(w), 0.0, None, 0, y, K, got)
+    assert np.array_equal(host(y), x * w)
+    B.mmvq_quantize_q8_1(y, K, n, K, want)
+    got, want = (host(t).reshape(n, -1, 36) for t in (got, want))
+    d, s = (lambda a: a[..., :2].copy().view(np.float16), lambda a: a[..., 2:4].copy().view(np.float16))
+    q = lambda a: a[..., 4:].copy().view(np.int8).astype(np.int64)  # noqa: E731
+    steps = np.abs(d(got).view(np.int16).astype(int) - d(want).view(np.int16))
+    assert steps.max() <= 1
+    off = q(got) - q(want)
+    blk = (x * w).astype(np.float64).reshape(n, -1, 32)
+    t = np.abs(blk) / (np.abs(blk).max(-1, keepdims=True) / 127.0)
+    border = np.abs(t - np.floor(t) - 0.5) < 2.0 ** -14
+    assert np.abs(off).max() <= 1 and not off[~border].any()
+    assert border.any()
+    same = ~off.any(-1)                                        # where the codes are the same, s moves with d
+    a, b = (s(v)[..., 0].view(np.int16).astype(int)[same] for v in (got, want))
+    assert np.abs(a - b).max(initial=0) <= 1
