@@ -148,7 +148,7 @@ def declared_symbols(header: str = HEADER) -> list[str]:
 
 
 def _addr(x) -> int | None:
-    if x is None or x.__class__ is int:
+    if x is None or x.__class__ is int or isinstance(x, int):   # the exact test is the quicker one
         return x
     return x.data_ptr()
 
@@ -298,7 +298,7 @@ def _launch(fn: str, where, stream, *args) -> None:
     else:
         torch = _torch or _cuda()
         here = _current_device()
-        index = here if where is None or where.__class__ is int else where.get_device()
+        index = here if where is None or isinstance(where, int) else where.get_device()
         if index == here or index < 0:
             rc = f(*args, _raw_stream(here))
         else:

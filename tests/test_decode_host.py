@@ -208,3 +208,28 @@ def test_descriptors_keep_their_tensors():
     del b
     gc.collect()
     assert all(r() is None for r in refs)
+
+
+class Address(int):
+    """An address of a type of its own, as allocators hand them out."""
+
+
+def test_addresses_of_int_subclasses(L):
+    assert B._addr(Address(P)) == P and B._addr(True) == 1
+    cache = B.kv_cache(Address(P), Address(P), B.Q8_0, 4, 16, 2, 64)
+    assert cache.k == P
+    # refused for its shape, after the address was taken
+    with pytest.raises(B.MMVQError) as e:
+        B.mmvq_add_rms_norm(Address(P), 0, 1, 64, None, 0, None, 1e-5, None, 0, Address(P), 64, None, stream=0)
+    assert e.value.code == B.ERR_SHAPE
+
+
+def test_launch_beside_an_address_of_an_int_subclass(monkeypatch):
+    """Without a stream, the current one of the current device."""
+    calls = []
+    monkeypatch.setattr(B, "_lib", type("Lib", (), {"f": staticmethod(lambda *a: calls.append(a) and 0)}))
+    monkeypatch.setattr(B, "_torch", object())
+    monkeypatch.setattr(B, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(B, "_raw_stream", lambda i: 100 + i, raising=False)
+    B._launch("f", Address(P), None, 7)
+    assert calls == [(7, 100)]
