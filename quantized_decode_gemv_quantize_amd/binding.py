@@ -294,7 +294,12 @@ def _launch(fn: str, where, stream, *args) -> None:
     need not be the current device."""
     f = getattr(_lib or lib(), fn)
     if stream is not None:
-        rc = f(*args, _stream(stream))
+        handle = _stream(stream)
+        if handle or isinstance(stream, int):
+            rc = f(*args, handle)
+        else:                               # a device's default stream: the handle does not say of which
+            with (_torch or _cuda()).cuda.device(stream.device_index):
+                rc = f(*args, handle)
     else:
         torch = _torch or _cuda()
         here = _current_device()

@@ -233,3 +233,28 @@ def test_launch_beside_an_address_of_an_int_subclass(monkeypatch):
     monkeypatch.setattr(B, "_raw_stream", lambda i: 100 + i, raising=False)
     B._launch("f", Address(P), None, 7)
     assert calls == [(7, 100)]
+
+
+@pytest.mark.parametrize("handle,index,device", [(0, 1, 1), (0, 0, 0), (77, 1, 0)])
+def test_launch_on_a_stream_of_another_device(monkeypatch, handle, index, device):
+    """The default stream of a device has no handle that names it: its device
+    is made current for the call. (The library finds that of other streams.)"""
+    current, calls = [0], []
+
+    class Device:
+        def __init__(self, i):
+            self.i = i
+
+        def __enter__(self):
+            self.back, current[0] = current[0], self.i
+
+        def __exit__(self, *_):
+            current[0] = self.back
+
+    stream = type("Stream", (), {"cuda_stream": handle, "device_index": index})()
+    torch = type("Torch", (), {"cuda": type("Cuda", (), {"device": Device})})
+    monkeypatch.setattr(B, "_lib", type("Lib", (), {"f": staticmethod(lambda *a: calls.append((a, current[0])) and 0)}))
+    monkeypatch.setattr(B, "_torch", torch)
+    monkeypatch.setattr(B, "_current_device", lambda: current[0], raising=False)
+    B._launch("f", P, stream, 7)
+    assert calls == [((7, handle), device)] and current == [0]
