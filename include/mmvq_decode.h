@@ -17,7 +17,8 @@
  * call; everything is enqueued on `stream` and nothing synchronizes; the
  * library keeps no allocation and no state; return values are MMVQ_OK or
  * MMVQ_ERR_*, arguments are validated on the host before anything is
- * enqueued, and an invalid call enqueues nothing. The kernels run on the
+ * enqueued, and an invalid call enqueues nothing. Buffers that hold nothing
+ * (no column, row, token or sequence) may be NULL. The kernels run on the
  * stream's device (NULL: the current device). Calls can be captured into HIP
  * graphs. A workspace belongs to one call until the stream has passed it;
  * calls that may run at the same time (two streams, two graphs) need one

@@ -61,10 +61,13 @@ int check_shapes(const mmvq_kv_cache* c, const mmvq_kv_batch* b) {
   return MMVQ_OK;
 }
 
+// Nothing to do: buffers that have no element then may have no address.
+bool empty(const mmvq_kv_batch* b) { return b->n_seqs == 0 || b->n_tokens == 0; }
+
 int check_kv(const mmvq_kv_cache* c, const mmvq_kv_batch* b, BatchArgs* out) {
   const int rc = check_shapes(c, b);
   if (rc) return rc;
-  if (!c->k || !c->v || !b->token_start || !b->seq_len || !b->page_table) return MMVQ_ERR_NULL;
+  if (!c->k || !c->v || !b->token_start || (b->n_seqs > 0 && (!b->seq_len || !b->page_table))) return MMVQ_ERR_NULL;
   if (!aligned(c->k, 16) || !aligned(c->v, 16)) return MMVQ_ERR_ALIGN;
   if (!aligned(b->token_start, 4) || !aligned(b->seq_len, 4) || !aligned(b->page_table, 4)) return MMVQ_ERR_ALIGN;
   *out = BatchArgs{b->token_start, b->seq_len, b->page_table, b->table_stride, b->n_seqs, b->n_tokens,
@@ -77,11 +80,11 @@ int kv_io(const mmvq_kv_cache* c, const mmvq_kv_batch* b, float* k, int64_t ldk,
   KvIoArgs a{};
   const int rc = check_kv(c, b, &a.b);
   if (rc) return rc;
-  if (write ? !k || !v : !k && !v) return MMVQ_ERR_NULL;
+  if (!empty(b) && (write ? !k || !v : !k && !v)) return MMVQ_ERR_NULL;
   const int64_t width = static_cast<int64_t>(c->n_kv_heads) * c->head_dim;
-  if ((k && (ldk < width || ldk > kMaxElems)) || (v && (ldv < width || ldv > kMaxElems))) return MMVQ_ERR_SHAPE;
+  if (((k || write) && (ldk < width || ldk > kMaxElems)) || ((v || write) && (ldv < width || ldv > kMaxElems))) return MMVQ_ERR_SHAPE;
   if (!aligned(k, 4) || !aligned(v, 4)) return MMVQ_ERR_ALIGN;
-  if (b->n_seqs == 0 || b->n_tokens == 0) return MMVQ_OK;
+  if (empty(b)) return MMVQ_OK;
   a.cache[0] = static_cast<uint8_t*>(c->k);
   a.cache[1] = static_cast<uint8_t*>(c->v);
   a.act[0] = k;
@@ -120,7 +123,7 @@ extern "C" {
 int mmvq_add_rms_norm(const float* x, int64_t K, int64_t n, int64_t ldx, const float* residual, int64_t ldr,
                       const float* weight, float eps, float* sum_out, int64_t lds, float* y, int64_t ldy, void* y_q,
                       void* stream) {
-  if (!x || (!y && !y_q)) return MMVQ_ERR_NULL;
+  if (n != 0 && (!x || (!y && !y_q))) return MMVQ_ERR_NULL;
   if (K < 1 || K > kMaxRow || n < 0 || n > kMaxElems / K || (y_q && K % 32)) return MMVQ_ERR_SHAPE;
   if (ldx < K || ldx > kMaxElems || (residual && (ldr < K || ldr > kMaxElems)) ||
       (sum_out && (lds < K || lds > kMaxElems)) || (y && (ldy < K || ldy > kMaxElems)))
@@ -137,7 +140,7 @@ int mmvq_add_rms_norm(const float* x, int64_t K, int64_t n, int64_t ldx, const f
 }
 
 int mmvq_dequantize_q8_1(const void* y_q, int64_t K, int64_t n, float* x, int64_t ldx, void* stream) {
-  if (!y_q || !x) return MMVQ_ERR_NULL;
+  if (n != 0 && (!y_q || !x)) return MMVQ_ERR_NULL;
   if (K < 1 || K > kMaxRow || K % 32 || n < 0 || n > kMaxElems / K || ldx < K || ldx > kMaxElems) return MMVQ_ERR_SHAPE;
   if (!aligned(y_q, 16) || !aligned(x, 4)) return MMVQ_ERR_ALIGN;
   if (n == 0) return MMVQ_OK;
@@ -169,7 +172,7 @@ int mmvq_attn_workspace(const mmvq_kv_cache* cache, const mmvq_kv_batch* batch, 
   const int rc = check_attn(cache, batch, n_heads);
   if (rc) return rc;
   // without a window the keys are most, and so are the ranges they are cut into
-  *bytes = batch->n_seqs == 0 || batch->n_tokens == 0
+  *bytes = empty(batch)
                ? 0 : attn_bytes(cache, batch, n_heads, shape_of(cache, batch, n_heads, 0).splits);
   return MMVQ_OK;
 }
@@ -182,11 +185,11 @@ int mmvq_attn(const mmvq_kv_cache* cache, const mmvq_kv_batch* batch, const floa
   if (rc) return rc;
   rc = check_kv(cache, batch, &a.b);
   if (rc) return rc;
-  if (!q || !out) return MMVQ_ERR_NULL;
+  if (!empty(batch) && (!q || !out)) return MMVQ_ERR_NULL;
   const int64_t width = static_cast<int64_t>(n_heads) * cache->head_dim;
   if (ldq < width || ldq > kMaxElems || ldo < width || ldo > kMaxElems || window < 0) return MMVQ_ERR_SHAPE;
   if (!aligned(q, 4) || !aligned(out, 4) || !aligned(sinks, 4) || !aligned(workspace, 16)) return MMVQ_ERR_ALIGN;
-  if (batch->n_seqs == 0 || batch->n_tokens == 0) return MMVQ_OK;
+  if (empty(batch)) return MMVQ_OK;
   const AttnShape s = shape_of(cache, batch, n_heads, window);
   const int64_t need = attn_bytes(cache, batch, n_heads, s.splits);
   if (need > 0 && !workspace) return MMVQ_ERR_NULL;
@@ -230,7 +233,8 @@ int mmvq_verify_draft(const float* target, int64_t ldt, int vocab, int kind, con
                       const int32_t* draft_tokens, const float* draft_probs, int64_t ldd, const int32_t* row_start,
                       int n_seqs, int n_rows, const float* u_accept, const float* u_sample, int32_t* n_accepted,
                       int32_t* tokens, int max_out, void* workspace, int64_t workspace_bytes, void* stream) {
-  if (!target || !draft_tokens || !row_start || !u_accept || !u_sample || !n_accepted || !tokens || !workspace)
+  if ((n_seqs != 0 && (!row_start || !u_sample || !n_accepted || !tokens || !workspace)) ||
+      (n_seqs != 0 && n_rows != 0 && (!target || !draft_tokens || !u_accept)))
     return MMVQ_ERR_NULL;
   if (kind != MMVQ_TARGET_LOGITS && kind != MMVQ_TARGET_WEIGHTS) return MMVQ_ERR_TYPE;
   int64_t need = 0;

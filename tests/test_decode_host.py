@@ -258,3 +258,31 @@ def test_launch_on_a_stream_of_another_device(monkeypatch, handle, index, device
     monkeypatch.setattr(B, "_current_device", lambda: current[0], raising=False)
     B._launch("f", P, stream, 7)
     assert calls == [((7, handle), device)] and current == [0]
+
+
+def test_nothing_to_do_needs_no_buffers(L):
+    """Buffers without an element have no address (an empty torch tensor's is
+    NULL): where the header says that nothing is done, they are not asked for."""
+    assert norm(L, n=0, x=None, res=None, w=None, s=None, y=None, q=None) == 0
+    assert norm(L, n=0, x=None, y=None, q=None, K=0) == B.ERR_SHAPE
+    assert norm(L, n=0, x=ODD) == B.ERR_ALIGN
+    assert L.mmvq_dequantize_q8_1(None, 64, 0, None, 64, None) == 0
+    for empty in ({"n_seqs": 0, "seq_len": None, "page_table": None}, {"n_tokens": 0}, {"n_seqs": 0, "n_tokens": 0}):
+        cache, batch = pair({}, empty)
+        assert L.mmvq_kv_write(cache, batch, None, 128, None, 128, None) == 0
+        assert L.mmvq_kv_read(cache, batch, None, 128, None, 128, None) == 0
+        assert L.mmvq_attn(cache, batch, None, 256, 4, 0.1, 0, None, None, 256, None, 0, None) == 0
+        assert L.mmvq_kv_write(cache, batch, None, 127, None, 128, None) == B.ERR_SHAPE
+        assert L.mmvq_attn(cache, batch, None, 255, 4, 0.1, 0, None, None, 256, None, 0, None) == B.ERR_SHAPE
+    # one of the two with work to do: they are
+    for some in ({"n_seqs": 2, "seq_len": None}, {"n_seqs": 2, "page_table": None}):
+        cache, batch = pair({}, some)
+        assert L.mmvq_kv_write(cache, batch, P, 128, P, 128, None) == B.ERR_NULL
+    none = {k: None for k in ("target", "tok", "start", "ua", "us", "count", "out", "ws", "dp", "temp")}
+    a = {**VERIFY, **none, "n_seqs": 0, "n_rows": 0, "size": 0}
+    assert L.mmvq_verify_draft(*[a[k] for k in VERIFY], None) == 0
+    assert L.mmvq_verify_draft(*[{**a, "ldt": 99}[k] for k in VERIFY], None) == B.ERR_SHAPE
+    # sequences without rows have outputs, and a row_start
+    a = {**VERIFY, "n_rows": 0, "target": None, "tok": None, "ua": None}
+    for name in ("start", "us", "count", "out", "ws"):
+        assert L.mmvq_verify_draft(*[{**a, name: None}[k] for k in VERIFY], None) == B.ERR_NULL
