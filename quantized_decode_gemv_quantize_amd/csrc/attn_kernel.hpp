@@ -44,6 +44,8 @@
 // two takes as long for it.
 #pragma once
 
+#include <float.h>
+
 #include "decode_args.hpp"
 #include "launch.hpp"
 
@@ -346,7 +348,9 @@ __device__ __forceinline__ StepPages step_pages(const AttnArgs& a, StepIds ids, 
 __device__ __forceinline__ float row_factor(const AttnArgs& a, int head, float m, float l, float shift) {
   if (l == 0.0f) return 0.0f;
   if (!a.sinks) return 1.0f / l;
-  const float sink = a.sinks[head] * 1.44269504088896340736f, unit = m - shift, top = fmaxf(unit, sink);
+  float sink = a.sinks[head] * 1.44269504088896340736f;
+  sink = sink > FLT_MAX ? FLT_MAX : sink;       // as much above every score, and a difference to them
+  const float unit = m - shift, top = fmaxf(unit, sink);
   const float f = __builtin_amdgcn_exp2f(unit - top);
   return f / fmaf(l, f, __builtin_amdgcn_exp2f(sink - top));
 }

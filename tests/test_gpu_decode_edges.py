@@ -63,3 +63,27 @@ def test_on_the_default_stream_as_an_object():
     x, y = dev(np.ones((2, 64), np.float32)), floats(2, 64)
     B.mmvq_add_rms_norm(x, 64, 2, 64, None, 0, None, 0.0, None, 0, y, 64, None, stream=torch.cuda.default_stream())
     assert (host(y) == 1).all()
+
+
+# --- sinks of any size ------------------------------------------------------------------
+
+@pytest.mark.parametrize("kind", list(R.KINDS))
+@pytest.mark.parametrize("new,length", [(1, 40), (1, 3000), (90, 130)])
+def test_sinks_to_the_ends_of_fp32(kind, new, length):
+    """A sink far above all scores leaves nothing for the keys, one far below
+    them takes nothing; in one launch, with a join, and of many rows."""
+    announce(f"sinks {kind} new={new} len={length}")
+    top = float(np.finfo(np.float32).max)
+    sinks = np.array([top, 3e38, 2e38, 1.0, -2e38, -3e38, -top, -np.inf], np.float32)
+    p = R.Paged(kind, 64, 1, 32, [new], [length], seed=3)
+    rng = np.random.default_rng(length)
+    k, v = p.fill(rng)
+    q = rng.standard_normal((new, 8, 64)).astype(np.float32)
+    batch = p.batch()
+    size = B.mmvq_attn_workspace(p.cache, batch, 8)
+    out = floats(new, 512)
+    B.mmvq_attn(p.cache, batch, dev(q.reshape(new, 512)), 512, 8, 0.125, 0, dev(sinks), out, 512, space(size + 16), size)
+    got = host(out).reshape(new, 8, 64)
+    ref, mag, smax = R.attention(q, k[0], v[0], 0.125, length - new, 0, sinks.astype(np.float64))
+    assert (np.abs(got - ref) <= R.attention_tolerance(ref, mag, smax, v[0], 64)).all()
+    assert (got[:, :3] == 0).all() and np.abs(got[:, 3:]).max() > 0.01
