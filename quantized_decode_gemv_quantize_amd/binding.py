@@ -12,6 +12,7 @@ There is no fallback: if the library has not been built, loading raises.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 import re
 
@@ -125,6 +126,20 @@ class MMVQError(RuntimeError):
         self.code = code
 
 
+def _load_hip() -> None:
+    """torch's own HIP runtime, where torch is installed and no runtime is loaded yet: the library would bind
+    to the system's, and torch bring its own beside it, on whose streams the library's launches fail."""
+    with open("/proc/self/maps") as maps:
+        if "libamdhip64" in maps.read():
+            return
+    spec = importlib.util.find_spec("torch")
+    for where in (spec and spec.submodule_search_locations) or ():
+        hip = os.path.join(where, "lib", "libamdhip64.so")
+        if os.path.exists(hip):
+            ctypes.CDLL(hip)
+            return
+
+
 def lib() -> ctypes.CDLL:
     """The loaded HIP library; raises if it has not been built."""
     global _lib
@@ -132,6 +147,7 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB):
             raise RuntimeError(f"{LIB} is missing: build it with "
                                "`python -m quantized_decode_gemv_quantize_amd.build`")
+        _load_hip()
         L = ctypes.CDLL(LIB)
         for name, (res, args) in _SIGS.items():
             f = getattr(L, name)

@@ -286,3 +286,24 @@ def test_nothing_to_do_needs_no_buffers(L):
     a = {**VERIFY, "n_rows": 0, "target": None, "tok": None, "ua": None}
     for name in ("start", "us", "count", "out", "ws"):
         assert L.mmvq_verify_draft(*[{**a, name: None}[k] for k in VERIFY], None) == B.ERR_NULL
+
+
+@pytest.mark.parametrize("first", ["import torch; B.mmvq_kv_page_bytes(B.F16, 16, 1, 64)", "B.mmvq_kv_page_bytes(B.F16, 16, 1, 64); import torch"])
+def test_one_hip_runtime(first):
+    """A query that touches no device, made before torch is there, must not
+    bring a HIP runtime beside torch's: launches on torch's streams fail then."""
+    import sys
+    code = ("from quantized_decode_gemv_quantize_amd import binding as B; " + first +
+            "; print(len({l.split()[-1] for l in open('/proc/self/maps') if 'libamdhip64' in l}))")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300, check=True).stdout
+    assert out.split()[-1] == "1"
+
+
+def test_a_query_does_not_import_torch():
+    import sys
+    code = ("import sys; from quantized_decode_gemv_quantize_amd import binding as B; "
+            "B.mmvq_kv_page_bytes(B.F16, 16, 1, 64); print('torch' in sys.modules)")
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    out = subprocess.run([sys.executable, "-c", code], cwd=root, capture_output=True, text=True, timeout=300, check=True).stdout
+    assert out.split()[-1] == "False"
