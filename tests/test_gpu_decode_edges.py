@@ -87,3 +87,50 @@ def test_sinks_to_the_ends_of_fp32(kind, new, length):
     ref, mag, smax = R.attention(q, k[0], v[0], 0.125, length - new, 0, sinks.astype(np.float64))
     assert (np.abs(got - ref) <= R.attention_tolerance(ref, mag, smax, v[0], 64)).all()
     assert (got[:, :3] == 0).all() and np.abs(got[:, 3:]).max() > 0.01
+
+
+# --- little left beside a refused token ---------------------------------------------------
+
+def verify(target, kind, temp, tok, start, ua, us, wide):
+    V, n, rows = target.shape[1], len(start) - 1, len(target)
+    size = B.mmvq_verify_workspace(n, rows, V)
+    count, out = ints(n), ints(n, wide)
+    B.mmvq_verify_draft(dev(target), V, V, kind, None if temp is None else dev(temp), dev(tok.astype(np.int32)), None, V,
+                        dev(np.asarray(start, np.int32)), n, rows, dev(ua), dev(us), count, out, wide, space(size), size)
+    ec, eo = R.verify(target, kind, temp, tok, None, start, ua, us, wide)
+    gc, go = host(count), host(out)
+    assert np.array_equal(gc, ec) and np.array_equal(go, eo), (gc, ec, go, eo)
+    return gc, go
+
+
+@pytest.mark.parametrize("kind", [B.TARGET_LOGITS, B.TARGET_WEIGHTS])
+@pytest.mark.parametrize("V", [1000, 9001, 300007])
+@pytest.mark.parametrize("x", [0, 3, 400, 999])
+def test_refused_token_with_nearly_all_of_its_chunk(kind, V, x):
+    """Without draft probabilities: what is left of the refused token's chunk
+    is a millionth of it, or 10^-20 beside weights in other chunks, where the
+    chunk's sum less the token's weight would be nothing or noise. Numbers of 0
+    draw the lowest index that has a weight."""
+    announce(f"refused kind={kind} V={V} x={x}")
+    rng = np.random.default_rng(V + x)
+    us = np.array([0.0, 0.0, 0.25, 0.5, 0.999, 0.0, 0.6], np.float32)
+    n = len(us)
+    w = rng.random((2 * n, V)) + 0.5                    # weights of each sequence's two rows
+    for s in range(n):
+        row = w[2 * s]
+        first = slice(0, 1000)                          # inside the first chunk, where x is
+        if s % 2 == 0 or V == 1000:
+            row *= 3e-6 / row.sum()                     # all the rest: a few millionths
+        else:
+            row[first] *= 1e-20
+            row[1000:5000] *= 1e-20                     # to the chunk's end and a little further
+            row[5000:] *= 0.02 / row[5000:].sum()
+        row[x] = 1.0
+    ua = np.full(2 * n, np.float32(1 - 2.0 ** -24))
+    tok = np.full(2 * n, x)
+    with np.errstate(divide="ignore"):
+        target = (np.log(w) if kind == B.TARGET_LOGITS else w).astype(np.float32)
+    count, out = verify(target, kind, None, tok, np.arange(0, 2 * n + 1, 2), ua, us, 2)
+    assert (count == 0).all() and (out[:, 0] != x).all()
+    low = 1 if x == 0 else 0
+    assert (out[us == 0, 0] == low).all()
