@@ -167,6 +167,11 @@ int mmvq_attn_workspace(const mmvq_kv_cache *cache, const mmvq_kv_batch *batch,
  * value) and each probability as two fp16 parts (20 bits; a key's share of the
  * result is good to 2^-32 of the largest value that the row sees, where that
  * is more).
+ * The launch is shaped by max_new and max_len, for all sequences alike: one
+ * chunk of a prompt among single tokens, or one long sequence among many short
+ * ones, makes the others wait. A descriptor holds any consecutive sequences
+ * (token_start + a, seq_len + a, page_table + a * table_stride, with their own
+ * maxima), so such batches are better given in two calls over the same rows.
  * workspace: 16-byte aligned, at least mmvq_attn_workspace bytes (fewer:
  * MMVQ_ERR_SHAPE). n_heads <= 65535 and n_tokens * n_heads <= 2^30; a launch
  * beyond 2^23 workgroups (sequences * key/value heads * tiles of 16 to 128

@@ -134,3 +134,52 @@ def test_refused_token_with_nearly_all_of_its_chunk(kind, V, x):
     assert (count == 0).all() and (out[:, 0] != x).all()
     low = 1 if x == 0 else 0
     assert (out[us == 0, 0] == low).all()
+
+
+# --- batches of unlike sequences ----------------------------------------------------------
+
+@pytest.mark.parametrize("kind", list(R.KINDS))
+@pytest.mark.parametrize("D,H,G,news,lens", [
+    (128, 2, 4, [200] + [1] * 7, [260, 700, 33, 1, 512, 90, 301, 16]),      # a prompt's chunk beside single tokens
+    (64, 1, 8, [1] * 5 + [7, 2, 1, 3], [2600, 40, 1, 17, 300, 7, 90, 64, 3]),   # a long sequence among short ones, drafts beside
+    (256, 2, 2, [1, 90, 5, 0], [900, 90, 40, 55]),
+])
+@pytest.mark.parametrize("window", [0, 50])
+def test_attention_of_unlike_sequences(kind, D, H, G, news, lens, window):
+    """Every form of a launch works on all sequences; one call, and the same
+    sequences in two calls, the long chunks apart from the rest."""
+    announce(f"unlike {kind} D={D} new={news} len={lens} window={window}")
+    p = R.Paged(kind, D, H, 32, news, lens, seed=D)
+    rng = np.random.default_rng(D + window)
+    k, v = p.fill(rng)
+    heads, n = H * G, p.n_tokens
+    q = rng.standard_normal((n, heads, D)).astype(np.float32)
+    qd, scale = dev(q.reshape(n, -1)), float(np.float32(D ** -0.5))
+
+    def run(batch, out):
+        size = B.mmvq_attn_workspace(p.cache, batch, heads)
+        B.mmvq_attn(p.cache, batch, qd, heads * D, heads, scale, window, None, out, heads * D, space(size + 16), size)
+
+    def check(out, seqs):
+        got = host(out).reshape(n, heads, D)
+        for s in range(len(news)):
+            rows = slice(p.start[s], p.start[s] + news[s])
+            if s not in seqs:
+                assert np.isnan(got[rows]).all()
+            elif news[s]:
+                ref, mag, smax = R.attention(q[rows], k[s], v[s], scale, lens[s] - news[s], window)
+                tol = R.attention_tolerance(ref, mag, smax, v[s], D)
+                assert (np.abs(got[rows] - ref) <= tol).all(), s
+
+    whole = floats(n, heads * D)
+    run(p.batch(), whole)
+    check(whole, range(len(news)))
+    # parts of the batch by descriptors of their own: sequences a .. b-1
+    long = int(np.argmax(news))
+    for a, b in ((long, long + 1), (long + 1, len(news)), (0, long)):
+        if a == b or max(news[a:b]) == 0:
+            continue
+        part = B.kv_batch(p.d[0][a:b + 1], p.d[1][a:b], p.d[2][a:b], b - a, n, max(news[a:b]), max(lens[a:b]), p.wide, p.wide)
+        out = floats(n, heads * D)
+        run(part, out)
+        check(out, range(a, b))
