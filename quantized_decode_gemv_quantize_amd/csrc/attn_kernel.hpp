@@ -44,8 +44,6 @@
 // two takes as long for it.
 #pragma once
 
-#include <float.h>
-
 #include "decode_args.hpp"
 #include "launch.hpp"
 
@@ -344,15 +342,12 @@ __device__ __forceinline__ StepPages step_pages(const AttnArgs& a, StepIds ids, 
 
 // Factor that turns a row's O into its result: 1 / l with the sink's share
 // in l; 0 for a row that saw no key (l is NaN where all scores were). l and O
-// are in units of 2^(m - shift).
+// are in units of 2^(m - shift), in which a sink 2^128 above is infinite: it
+// leaves the keys nothing.
 __device__ __forceinline__ float row_factor(const AttnArgs& a, int head, float m, float l, float shift) {
   if (l == 0.0f) return 0.0f;
   if (!a.sinks) return 1.0f / l;
-  float sink = a.sinks[head] * 1.44269504088896340736f;
-  sink = sink > FLT_MAX ? FLT_MAX : sink;       // as much above every score, and a difference to them
-  const float unit = m - shift, top = fmaxf(unit, sink);
-  const float f = __builtin_amdgcn_exp2f(unit - top);
-  return f / fmaf(l, f, __builtin_amdgcn_exp2f(sink - top));
+  return 1.0f / (l + __builtin_amdgcn_exp2f(fmaf(a.sinks[head], 1.44269504088896340736f, shift - m)));
 }
 
 // A finished row to out, or a split's share of it to the workspace. `write`
@@ -643,12 +638,12 @@ struct Rows {
   }
 
   // O of the step. value(d): operand of dims 16 d ..; scale(b): the 8 tokens'
-  // scales of block b, times the tokens' factors; wh: the weights' first
-  // parts. A quantized block's weights are formed while the products of the
-  // block before run.
+  // scales of block b, times the tokens' factors; first: where to leave the
+  // weights' first parts. A quantized block's weights are formed while the
+  // products of the block before run.
   template <class V, class S>
-  __device__ __forceinline__ void accumulate(V value, S scale, const f32x4 (&s)[MT][2], u32x4 (&wh)[MT]) {
-    u32x4 wl[MT], ph[2][MT], pl[2][MT];
+  __device__ __forceinline__ void accumulate(V value, S scale, const f32x4 (&s)[MT][2], u32x4* first = nullptr) {
+    u32x4 wh[MT], wl[MT], ph[2][MT], pl[2][MT];
     u32x4 n0, n1, ns;                           // the next block's values and the scales of its weights, read ahead
     if constexpr (AHEAD) {
       n0 = value(0);
@@ -664,6 +659,7 @@ struct Rows {
         wh[t][e] = h;
         wl[t][e] = r;
       }
+      if (first) first[t] = wh[t];
       if constexpr (KIND == kKvF16) {
         ph[0][t] = wh[t];
         pl[0][t] = wl[t];
@@ -892,7 +888,7 @@ struct StepLds {
   uint32_t factor[16];                          // the factors
   float e5[kStep];                              // and their exponent fields
   int wild[4];                                  // F16, of each wave's share: an infinity or NaN was among the values
-  int low;                                      // quantized: a factor of the walk was below 1
+                                                // quantized, [0]: a factor of the walk was below 1
 };
 
 // A lane's share of a step on its way to LDS: runs of block b of operand lane
@@ -1067,9 +1063,12 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
     // costs every step (Q8_0, 2048 tokens over 8192: 128 dims 543 -> 686 us
     // behind the second product and 554 before it, 256 dims 1150 -> 1213). Its
     // weights are those of the first, whose M stands; l is the first one's.
-    bool lost = false;
-    float shift = r.kTop, l_first[MT];
+    constexpr bool kTwice = KIND != kKvF16;
+    bool again = false;
+    float l_first[MT];
     while (true) {
+      const bool lost = kTwice && again;
+      const float shift = lost ? r.kTop - kLost : r.kTop;
       __syncthreads();                          // the tile or walk before is done with LDS
       if (t_beg < t_end) in.store(lds[0], t_beg, w.keys, lost);
       __syncthreads();
@@ -1119,29 +1118,27 @@ __global__ void __launch_bounds__(kAttnThreads, 2) attn_rows_kernel(AttnArgs a) 
           }
           if (kStraight && more) in.store(lds[buf ^ 1], t0 + kStep, w.keys, lost);
           if constexpr (NB < 8) __builtin_amdgcn_s_setprio(1);
-          u32x4 wh[MT];
           r.accumulate(value, [&](int b) QMV_INLINE {
             return *reinterpret_cast<const u32x4*>(&st.vsc[KIND == kKvF16 ? 0 : b][4 * g]);
-          }, s, wh);
+          }, s);
           if constexpr (NB < 8) __builtin_amdgcn_s_setprio(0);
         }
         if (!kStraight && more) in.store(lds[buf ^ 1], t0 + kStep, w.keys, lost);
         __syncthreads();
       }
-      if (KIND == kKvF16 || lost) break;
+      if (!kTwice || again) break;
       if (wave == 0) {
         const bool low = __any(below_one(in.low));
-        if (lane == 0) lds[0].low = low;
+        if (lane == 0) lds[0].wild[0] = low;
       }
       __syncthreads();
-      if (!__builtin_amdgcn_readfirstlane(lds[0].low)) break;
-      lost = true;
-      shift = r.kTop - kLost;
+      if (!__builtin_amdgcn_readfirstlane(lds[0].wild[0])) break;
+      again = true;
 #pragma unroll
       for (int t = 0; t < MT; ++t) l_first[t] = r.l[t];
       begin();
     }
-    if (lost) {
+    if (again) {
 #pragma unroll
       for (int t = 0; t < MT; ++t) r.l[t] = l_first[t];
     }
