@@ -82,7 +82,8 @@ int kv_io(const mmvq_kv_cache* c, const mmvq_kv_batch* b, float* k, int64_t ldk,
   if (rc) return rc;
   if (!empty(b) && (write ? !k || !v : !k && !v)) return MMVQ_ERR_NULL;
   const int64_t width = static_cast<int64_t>(c->n_kv_heads) * c->head_dim;
-  if (((k || write) && (ldk < width || ldk > kMaxElems)) || ((v || write) && (ldv < width || ldv > kMaxElems))) return MMVQ_ERR_SHAPE;
+  if (((k || write) && (ldk < width || ldk > kMaxElems)) || ((v || write) && (ldv < width || ldv > kMaxElems)))
+    return MMVQ_ERR_SHAPE;
   if (!aligned(k, 4) || !aligned(v, 4)) return MMVQ_ERR_ALIGN;
   if (empty(b)) return MMVQ_OK;
   a.cache[0] = static_cast<uint8_t*>(c->k);

@@ -178,32 +178,33 @@ __device__ __forceinline__ void write_units(const KvIoArgs& a) {
 #pragma unroll
           for (int j = 0; j < 8; ++j)
             if (j >= ta && j < tb) {
-              if constexpr (KIND == kKvQ4) code[j] |= from_half(code[j]) << 4;   // lower half of the lanes: its nibbles and those 16 dims on
+              // the lower half of the lanes: its nibbles and those 16 dims on
+              if constexpr (KIND == kKvQ4) code[j] |= from_half(code[j]) << 4;
               if (KIND == kKvQ8 || sub < 4)
                 *reinterpret_cast<uint32_t*>(dst + kv_key_at(KIND, NB, 8 * h8 + j, b, 4 * sub)) = code[j];
             }
         } else {
-        uint32_t lo[4], hi[4];
-        transpose4({code[0], code[1], code[2], code[3]}, lo);
-        transpose4({code[4], code[5], code[6], code[7]}, hi);
-        if constexpr (KIND == kKvQ4) {
+          uint32_t lo[4], hi[4];
+          transpose4({code[0], code[1], code[2], code[3]}, lo);
+          transpose4({code[4], code[5], code[6], code[7]}, hi);
+          if constexpr (KIND == kKvQ4) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            lo[e] |= from_half(lo[e]) << 4;
-            hi[e] |= from_half(hi[e]) << 4;
+            for (int e = 0; e < 4; ++e) {
+              lo[e] |= from_half(lo[e]) << 4;
+              hi[e] |= from_half(hi[e]) << 4;
+            }
           }
-        }
-        if (KIND == kKvQ8 || sub < 4) {
+          if (KIND == kKvQ8 || sub < 4) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint8_t* to = dst + kv_value_at(KIND, 8 * h8, b, 4 * sub + e);
-            if (full) *reinterpret_cast<u32x2*>(to) = u32x2{lo[e], hi[e]};
-            else
+            for (int e = 0; e < 4; ++e) {
+              uint8_t* to = dst + kv_value_at(KIND, 8 * h8, b, 4 * sub + e);
+              if (full) *reinterpret_cast<u32x2*>(to) = u32x2{lo[e], hi[e]};
+              else
 #pragma unroll
-              for (int j = 0; j < 8; ++j)
-                if (j >= ta && j < tb) to[j] = static_cast<uint8_t>((j < 4 ? lo[e] : hi[e]) >> (8 * (j & 3)));
+                for (int j = 0; j < 8; ++j)
+                  if (j >= ta && j < tb) to[j] = static_cast<uint8_t>((j < 4 ? lo[e] : hi[e]) >> (8 * (j & 3)));
+            }
           }
-        }
         }
         if (sub == 0) {
           uint8_t* to = dst + kv_scale_at(KIND, NB, b, 8 * h8);

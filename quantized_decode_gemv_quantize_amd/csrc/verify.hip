@@ -128,8 +128,10 @@ __device__ __forceinline__ void wave_top(float& top, int& at) {
   take_top(top, at, dpp_f<kDppXor2>(top), dpp_i<kDppXor2>(at));
   take_top(top, at, dpp_f<kDppMirror8>(top), dpp_i<kDppMirror8>(at));
   take_top(top, at, dpp_f<kDppMirror16>(top), dpp_i<kDppMirror16>(at));
-  take_top(top, at, __uint_as_float(swap_partner<16>(__float_as_uint(top))), static_cast<int>(swap_partner<16>(static_cast<uint32_t>(at))));
-  take_top(top, at, __uint_as_float(swap_partner<32>(__float_as_uint(top))), static_cast<int>(swap_partner<32>(static_cast<uint32_t>(at))));
+  take_top(top, at, __uint_as_float(swap_partner<16>(__float_as_uint(top))),
+           static_cast<int>(swap_partner<16>(static_cast<uint32_t>(at))));
+  take_top(top, at, __uint_as_float(swap_partner<32>(__float_as_uint(top))),
+           static_cast<int>(swap_partner<32>(static_cast<uint32_t>(at))));
 }
 
 // The sequence that row r belongs to, -1 for none: the last one that starts
@@ -214,7 +216,8 @@ __global__ void __launch_bounds__(kSThreads) verify_stats_kernel(VerifyArgs a) {
 #pragma unroll
       for (int k = 0; k < kSPer; ++k) own.top = fmaxf(own.top, v[k]);
 #pragma unroll
-      for (int k = kSPer - 1; k >= 0; --k) own.at = v[k] == own.top && own.top > -INFINITY ? i0 + (k / 4) * 4 * kSThreads + k % 4 : own.at;
+      for (int k = kSPer - 1; k >= 0; --k)
+        own.at = v[k] == own.top && own.top > -INFINITY ? i0 + (k / 4) * 4 * kSThreads + k % 4 : own.at;
       wave_top(own.top, own.at);
       if (!greedy && own.top > -INFINITY) {
         if (own.top < INFINITY) {
@@ -269,8 +272,8 @@ __device__ __forceinline__ void join_row(const VerifyArgs& a, const Exp2& exp2, 
 }
 
 // The weight to draw from and the plain one, of element i of the decided row.
-__device__ __forceinline__ void draw_weights(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, int x, float v, float q, int i,
-                                             double& rest, double& all) {
+__device__ __forceinline__ void draw_weights(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, int x, float v,
+                                             float q, int i, double& rest, double& all) {
   all = weight(a, exp2, v, i, d.top, d.best, h);
   if (a.draft_probs) rest = fmax(all - draft_weight(q) * d.z, 0.0);
   else rest = i == x ? 0.0 : all;              // q is 1 there, and e_i <= Z
@@ -345,7 +348,8 @@ __device__ __forceinline__ void decide(const VerifyArgs& a, const Exp2& exp2, in
 }
 
 // Sums of a chunk's weights over the workgroup.
-__device__ __forceinline__ SeqSum chunk_sums(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, int x, int c, double* lds) {
+__device__ __forceinline__ SeqSum chunk_sums(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, int x, int c,
+                                             double* lds) {
   const int tid = threadIdx.x, wave = tid >> 6;
   double rest = 0.0, all = 0.0;
 #pragma unroll
@@ -403,7 +407,8 @@ struct DrawLds {
 // Draws from the decided row with the number u; sums(c): the chunks' sums.
 // The whole workgroup.
 template <class S>
-__device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, float u, int x, S sums, DrawLds& l) {
+__device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const Decision& d, Heat h, float u, int x, S sums,
+                                    DrawLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
   if (wave == 0) {
     const SeqSum none{0.0, 0.0}, own = lane_id() < a.chunks ? sums(lane_id()) : none;
