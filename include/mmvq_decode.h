@@ -10,7 +10,9 @@
  *   mmvq_attn           attention of the new tokens over that cache;
  *   mmvq_verify_draft   after the LM head: which drafted tokens stand, and
  *                       the token that follows them.
- * mmvq_kv_read and mmvq_dequantize_q8_1 read the stored forms back.
+ * mmvq_kv_read and mmvq_dequantize_q8_1 read the stored forms back. What else
+ * a model puts between these (a rotary embedding of queries and keys, biases,
+ * norms of its heads) is the caller's: q, k and v are fp32 rows in memory.
  *
  * Conventions are those of mmvq.h: data pointers are DEVICE pointers owned by
  * the caller; the struct arguments themselves are read on the host during the
