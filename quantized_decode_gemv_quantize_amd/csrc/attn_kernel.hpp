@@ -36,9 +36,10 @@
 // launch joins, so that few rows over a long cache still fill the chip.
 //
 // Measured: F16, 64 sequences of one token over 1500..4500 keys of 8 heads of
-// 128, 155 us, 5.3 TB/s, bound by memory; Q4_0, 16 of 5 tokens and 64 query
-// heads of 64 over 5300..16000, 64 us, bound by vector issue (79 %); Q8_0, 2048
-// tokens of 32 heads of 128 over 8192, 540 us, 445 TFLOP/s of the formula's
+// 128, 154 us, 5.3 TB/s, bound by memory (Q8_0 95, Q4_0 88); Q4_0, 16 of 2 to 5
+// tokens and 64 query heads of 64 over 5300..16000, 64 us, bound by vector issue
+// (79 %, a third of it for rows that a sequence does not have); Q8_0, 2048
+// tokens of 32 heads of 128 over 8192, 543 us, 442 TFLOP/s of the formula's
 // operations (the parts double them), vector issue 70 % and the chain of one
 // wave's own reads and products: a compute unit with one workgroup instead of
 // two takes as long for it.
