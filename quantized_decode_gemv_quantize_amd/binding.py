@@ -164,9 +164,14 @@ def declared_symbols(header: str = HEADER) -> list[str]:
 
 
 def _addr(x) -> int | None:
-    if x is None or x.__class__ is int or isinstance(x, int):   # the exact test is the quicker one
+    if x is None or x.__class__ is int:
         return x
-    return x.data_ptr()
+    try:
+        return x.data_ptr()
+    except AttributeError:
+        if isinstance(x, int):              # of a class of its own: rare, and the test costs every tensor
+            return x
+        raise
 
 
 _torch = _current_device = _raw_stream = None
@@ -311,10 +316,11 @@ def _launch(fn: str, where, stream, *args) -> None:
     f = getattr(_lib or lib(), fn)
     if stream is not None:
         handle = _stream(stream)
-        if handle or isinstance(stream, int):
+        index = None if handle else getattr(stream, "device_index", None)
+        if index is None:
             rc = f(*args, handle)
         else:                               # a device's default stream: the handle does not say of which
-            with (_torch or _cuda()).cuda.device(stream.device_index):
+            with (_torch or _cuda()).cuda.device(index):
                 rc = f(*args, handle)
     else:
         torch = _torch or _cuda()

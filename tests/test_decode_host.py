@@ -215,7 +215,9 @@ class Address(int):
 
 
 def test_addresses_of_int_subclasses(L):
-    assert B._addr(Address(P)) == P and B._addr(True) == 1
+    assert B._addr(Address(P)) == P and B._addr(True) == 1 and B._addr(None) is None
+    with pytest.raises(AttributeError):
+        B._addr("an address")
     cache = B.kv_cache(Address(P), Address(P), B.Q8_0, 4, 16, 2, 64)
     assert cache.k == P
     # refused for its shape, after the address was taken
@@ -258,6 +260,9 @@ def test_launch_on_a_stream_of_another_device(monkeypatch, handle, index, device
     monkeypatch.setattr(B, "_current_device", lambda: current[0], raising=False)
     B._launch("f", P, stream, 7)
     assert calls == [((7, handle), device)] and current == [0]
+    B._launch("f", P, handle, 7)                        # as a number: the current device's
+    B._launch("f", P, type("Stream", (), {"cuda_stream": handle})(), 7)   # of a type that names no device
+    assert calls[1:] == [((7, handle), 0)] * 2
 
 
 def test_nothing_to_do_needs_no_buffers(L):
