@@ -57,9 +57,9 @@ enum { MMVQ_F16 = 1 };
  * which is what torch computes for amax / 127.0 on this GPU). That function's
  * d is a quotient: stored scales differ by at most one fp16 step and codes by
  * at most 1, where y/d lies within 2^-14 of a border (some 10^-7 of them).
- * Where its bits matter, take y and call it. sum_out may
- * be x or residual itself (same pointer and stride), and y may be x where
- * sum_out is not; otherwise the buffers do not overlap.
+ * Where its bits matter, take y and call it. sum_out may be x or residual
+ * itself (same pointer and stride), and y may be x where sum_out is not;
+ * otherwise the buffers do not overlap.
  * Requires 1 <= K <= 2^24, n >= 0 and n*K <= 2^40, every ld >= K, K % 32 == 0
  * with y_q, and at least one of y and y_q (MMVQ_ERR_NULL). fp32 buffers
  * 4-byte aligned, y_q 16-byte. With y_q the values must be finite, as for
