@@ -1,5 +1,6 @@
-"""Python binding of ``libmmvq.so`` (C ABI in ``include/mmvq.h`` and, for the
-operators between the mat-vecs, ``include/mmvq_decode.h``).
+"""Python binding of ``libmmvq.so`` (C ABI in ``include/mmvq.h``, for the
+operators between the mat-vecs ``include/mmvq_decode.h`` and for those of a step
+over many requests ``include/mmvq_serve.h``).
 
 Argument marshalling only: every step of the computation runs in the HIP
 library. Functions keep the C names; device buffers may be given as torch
@@ -20,10 +21,11 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB = os.path.join(HERE, "libmmvq.so")
 HEADER = os.path.join(os.path.dirname(HERE), "include", "mmvq.h")
 DECODE_HEADER = os.path.join(os.path.dirname(HERE), "include", "mmvq_decode.h")
+SERVE_HEADER = os.path.join(os.path.dirname(HERE), "include", "mmvq_serve.h")
 
 Q4_0, Q8_0, Q8_1, Q4_K, Q6_K = 2, 8, 9, 12, 14
 Q4_1, Q5_0, Q5_1, Q5_K = 3, 6, 7, 13
-F16 = 1
+F32, F16, BF16 = 0, 1, 30
 TARGET_LOGITS, TARGET_WEIGHTS = 0, 1
 GLU_PLAIN, GLU_SWIGLU, GLU_GEGLU, GLU_SWIGLU_OAI, GLU_SWIGLU_CLAMP = 0, 1, 2, 3, 4
 MAX_COLS = 8
@@ -82,7 +84,47 @@ def kv_batch(token_start, seq_len, page_table, n_seqs: int, n_tokens: int, max_n
     return b
 
 
-_KC, _KB = ctypes.POINTER(KVCache), ctypes.POINTER(KVBatch)
+class KVPool(ctypes.Structure):
+    """``mmvq_kv_pool``: addresses; made by ``kv_pool()`` it keeps the tensors, too."""
+    _fields_ = [("page_table", _p), ("table_stride", _i64), ("pages_held", _p), ("free_pages", _p), ("n_free", _p),
+                ("pages_per_seq", _int), ("n_pages", _int), ("page_size", _int)]
+
+
+class LoraSet(ctypes.Structure):
+    """``mmvq_lora_set``: addresses; made by ``lora_set()`` it keeps the tensors, too."""
+    _fields_ = [("A", _p), ("B", _p), ("rank", _p), ("scale", _p), ("stride_a", _i64), ("stride_b", _i64), ("K", _i64),
+                ("M", _i64), ("type", _int), ("n_adapters", _int), ("max_rank", _int)]
+
+
+class Sampling(ctypes.Structure):
+    """``mmvq_sampling``: addresses; made by ``sampling()`` it keeps the tensors, too."""
+    _fields_ = [("temperature", _p), ("top_k", _p), ("top_p", _p), ("min_p", _p)]
+
+
+def kv_pool(page_table, pages_held, free_pages, n_free, pages_per_seq: int, n_pages: int, page_size: int,
+            table_stride: int | None = None) -> KVPool:
+    p = KVPool(_addr(page_table), pages_per_seq if table_stride is None else table_stride, _addr(pages_held),
+               _addr(free_pages), _addr(n_free), pages_per_seq, n_pages, page_size)
+    p.tensors = page_table, pages_held, free_pages, n_free
+    return p
+
+
+def lora_set(A, B, wtype: int, n_adapters: int, K: int, M: int, max_rank: int, rank=None, scale=None,
+             stride_a: int | None = None, stride_b: int | None = None) -> LoraSet:
+    s = LoraSet(_addr(A), _addr(B), _addr(rank), _addr(scale), max_rank * K if stride_a is None else stride_a,
+                M * max_rank if stride_b is None else stride_b, K, M, wtype, n_adapters, max_rank)
+    s.tensors = A, B, rank, scale
+    return s
+
+
+def sampling(temperature=None, top_k=None, top_p=None, min_p=None) -> Sampling:
+    s = Sampling(_addr(temperature), _addr(top_k), _addr(top_p), _addr(min_p))
+    s.tensors = temperature, top_k, top_p, min_p
+    return s
+
+
+_KC, _KB, _KP = ctypes.POINTER(KVCache), ctypes.POINTER(KVBatch), ctypes.POINTER(KVPool)
+_LS, _SA = ctypes.POINTER(LoraSet), ctypes.POINTER(Sampling)
 _pi64 = ctypes.POINTER(_i64)
 _f32 = ctypes.c_float
 
@@ -115,6 +157,14 @@ _SIGS = {
     "mmvq_verify_workspace": (_int, [_int, _int, _int, _pi64]),
     "mmvq_verify_draft": (_int, [_p, _i64, _int, _int, _p, _p, _p, _i64, _p, _int, _int, _p, _p, _p, _p, _int,
                                  _p, _i64, _p]),
+    "mmvq_embed": (_int, [_p, _int, _i64, _i64, _p, _i64, _f32, _p, _i64, _p]),
+    "mmvq_kv_release": (_int, [_KP, _int, _p, _p, _p]),
+    "mmvq_kv_plan_workspace": (_int, [_int, _pi64]),
+    "mmvq_kv_plan": (_int, [_KP, _p, _p, _int, _int, _p, _p, _p, _p, _p, _p, _p, _i64, _p]),
+    "mmvq_lora_workspace": (_int, [_LS, _i64, _pi64]),
+    "mmvq_lora": (_int, [_LS, _p, _i64, _i64, _p, _p, _int, _p, _i64, _p, _i64, _p, _i64, _p]),
+    "mmvq_sample_workspace": (_int, [_int, _int, _pi64]),
+    "mmvq_sample": (_int, [_p, _i64, _int, _int, _SA, _p, _int, _p, _p, _p, _p, _i64, _p, _i64, _p]),
 }
 
 _lib = None
@@ -383,6 +433,55 @@ def mmvq_verify_draft(target, ldt: int, vocab: int, kind: int, temperature, draf
     _launch("mmvq_verify_draft", target, stream, _addr(target), ldt, vocab, kind, _addr(temperature),
             _addr(draft_tokens), _addr(draft_probs), ldd, _addr(row_start), n_seqs, n_rows, _addr(u_accept),
             _addr(u_sample), _addr(n_accepted), _addr(tokens), max_out, _addr(workspace), workspace_bytes)
+
+
+# ---------------------------------------------------------------------------
+# Operators of a step over many requests (include/mmvq_serve.h)
+# ---------------------------------------------------------------------------
+
+def mmvq_embed(table, wtype: int, vocab: int, K: int, ids, n: int, scale: float, out, ldo: int, stream=None) -> None:
+    _launch("mmvq_embed", out, stream, _addr(table), wtype, vocab, K, _addr(ids), n, scale, _addr(out), ldo)
+
+
+def mmvq_kv_release(pool: KVPool, n_seqs: int, keep, shared=None, stream=None) -> None:
+    _launch("mmvq_kv_release", keep, stream, pool, n_seqs, _addr(keep), _addr(shared))
+
+
+def mmvq_kv_plan_workspace(n_seqs: int) -> int:
+    n = _i64()
+    _check("mmvq_kv_plan_workspace", lib().mmvq_kv_plan_workspace(n_seqs, n))
+    return n.value
+
+
+def mmvq_kv_plan(pool: KVPool, cached, n_new, n_seqs: int, n_rows: int, token_start, seq_len, row_seq, row_pos,
+                 row_slot, n_missing, workspace, workspace_bytes: int, stream=None) -> None:
+    _launch("mmvq_kv_plan", token_start, stream, pool, _addr(cached), _addr(n_new), n_seqs, n_rows,
+            _addr(token_start), _addr(seq_len), _addr(row_seq), _addr(row_pos), _addr(row_slot), _addr(n_missing),
+            _addr(workspace), workspace_bytes)
+
+
+def mmvq_lora_workspace(adapters: LoraSet, n: int) -> int:
+    b = _i64()
+    _check("mmvq_lora_workspace", lib().mmvq_lora_workspace(adapters, n, b))
+    return b.value
+
+
+def mmvq_lora(adapters: LoraSet, x, ldx: int, n: int, row_seq, adapter, n_seqs: int, base, ldb: int, out, ldo: int,
+              workspace, workspace_bytes: int, stream=None) -> None:
+    _launch("mmvq_lora", x, stream, adapters, _addr(x), ldx, n, _addr(row_seq), _addr(adapter), n_seqs, _addr(base),
+            ldb, _addr(out), ldo, _addr(workspace), workspace_bytes)
+
+
+def mmvq_sample_workspace(n_rows: int, vocab: int) -> int:
+    n = _i64()
+    _check("mmvq_sample_workspace", lib().mmvq_sample_workspace(n_rows, vocab, n))
+    return n.value
+
+
+def mmvq_sample(logits, ldl: int, vocab: int, n_rows: int, params: Sampling | None, row_seq, n_seqs: int, u, tokens,
+                chosen, probs, ldp: int, workspace, workspace_bytes: int, stream=None) -> None:
+    _launch("mmvq_sample", logits, stream, _addr(logits), ldl, vocab, n_rows, params, _addr(row_seq), n_seqs,
+            _addr(u), _addr(tokens), _addr(chosen), _addr(probs), ldp, _addr(workspace), workspace_bytes)
 
 
 # ---------------------------------------------------------------------------

@@ -26,7 +26,8 @@ SOURCES = ["kernels_q4_k_f32.hip", "kernels_q4_k_f32_id.hip", "kernels_q4_k.hip"
            "kernels_q4_1_f32.hip", "kernels_q5_0_f32.hip", "kernels_q5_1_f32.hip", "kernels_q4_1.hip",
            "kernels_q5_0.hip", "kernels_q5_1.hip", "kernels_mmq.hip", "kernels_mmq_f32.hip", "attn_f16.hip",
            "attn_q8_0.hip", "attn_q4_0.hip", "attn_join.hip", "api.hip", "quantize.hip", "probe.hip",
-           "decode_api.hip", "norm.hip", "kv_cache.hip", "verify.hip"]
+           "decode_api.hip", "norm.hip", "kv_cache.hip", "verify.hip",
+           "serve_api.hip", "sample.hip", "lora.hip", "pages.hip", "embed.hip"]
 
 # Packed fp32 VALU instructions stay disabled (hipcc forms them from plain
 # float code otherwise); fp32 division is correctly rounded and fp32

@@ -4,38 +4,13 @@
 // nothing when they are invalid; it never synchronizes and never aborts.
 #include <math.h>
 
+#include "call.hpp"
 #include "decode_args.hpp"
 #include "launch.hpp"
 
 using namespace qmv;
 
 namespace {
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-constexpr int64_t kMaxElems = int64_t(1) << 40;
-constexpr int64_t kMaxRow = int64_t(1) << 24;
-
-// The stream's device current for the launch, as the kernels and their
-// arguments belong to it.
-class OnStreamDevice {
- public:
-  explicit OnStreamDevice(hipStream_t st) {
-    hipDevice_t dev;
-    if (!st || hipStreamGetDevice(st, &dev) != hipSuccess) return;
-    int now = 0;
-    if (hipGetDevice(&now) != hipSuccess || now == dev) return;
-    if (hipSetDevice(dev) == hipSuccess) back_ = now;
-  }
-  ~OnStreamDevice() {
-    if (back_ >= 0) (void)hipSetDevice(back_);
-  }
-  OnStreamDevice(const OnStreamDevice&) = delete;
-  OnStreamDevice& operator=(const OnStreamDevice&) = delete;
-
- private:
-  int back_ = -1;
-};
 
 int kv_kind(int type) {
   return type == MMVQ_F16 ? kKvF16 : type == MMVQ_Q8_0 ? kKvQ8 : type == MMVQ_Q4_0 ? kKvQ4 : -1;
