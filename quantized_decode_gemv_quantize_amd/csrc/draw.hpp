@@ -68,6 +68,19 @@ __device__ __forceinline__ double wave_scan(double v) {
   return v;
 }
 
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_zero_i(int v) {
+  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+  v += dpp_zero_i<0x111, 0xF>(v);
+  v += dpp_zero_i<0x112, 0xF>(v);
+  v += dpp_zero_i<0x114, 0xF>(v);
+  v += dpp_zero_i<0x118, 0xF>(v);
+  v += dpp_zero_i<0x142, 0xA>(v);
+  v += dpp_zero_i<0x143, 0xC>(v);
+  return v;
+}
 // Four elements at i, `fill` behind the row's end.
 __device__ __forceinline__ void load_quad(const float* row, int i, int n, float fill, float (&v)[4]) {
   if (n >= 4) {

@@ -21,20 +21,6 @@ constexpr int kPWaves = kPThreads / kWave;
 constexpr int kPlanRows = 4096;                // rows that one workgroup maps beside the sums
 constexpr int kFThreads = 256;
 
-template <int CTRL, int ROWS>
-__device__ __forceinline__ int dpp_zero_i(int v) {
-  return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);
-}
-__device__ __forceinline__ int wave_scan(int v) {
-  v += dpp_zero_i<0x111, 0xF>(v);
-  v += dpp_zero_i<0x112, 0xF>(v);
-  v += dpp_zero_i<0x114, 0xF>(v);
-  v += dpp_zero_i<0x118, 0xF>(v);
-  v += dpp_zero_i<0x142, 0xA>(v);
-  v += dpp_zero_i<0x143, 0xC>(v);
-  return v;
-}
-
 // Sum of the values of the lanes before this one over the workgroup (they and
 // their sum below 2^31), and the sum of all. lds: kPWaves numbers that no
 // other scan uses before the next barrier.

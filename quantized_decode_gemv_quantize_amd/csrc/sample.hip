@@ -9,14 +9,18 @@
 // Nothing is sorted but the few tokens about that border. Launches:
 //   stats   per row and chunk of kChunk logits: largest logit, sum of the
 //           weights, and for filtered rows a histogram of their number and
-//           sum over bins of a quarter octave of the weight;
-//   pick    a workgroup a row: the chunks joined, the bin in which the border
-//           lies, its tokens sorted, the kept weights summed, the token drawn;
+//           sum over bins of a quarter octave of the weight, and the chunk's
+//           tokens in its first bins (at most kTops);
+//   pick    a workgroup a row: the chunks' histograms joined, and the bin in
+//           which the border lies. Where no more than kList tokens come up to
+//           its end, they are sorted, cut and drawn from in LDS; else the
+//           bin is narrowed until as few are left of it, and the row is
+//           summed again;
 //   probs   the distribution written out, if wanted.
-// A bin's sums are 64-bit whole numbers in units of 2^-51 of its weights (sums
-// in LDS in any order give the same bits), everything else is in 64-bit
-// floating point: with 10^5 logits a running sum in 32 bits moves a border by
-// more than many tokens' probability.
+// A chunk's bin is one 64-bit whole number: the count, and the sum in units of
+// 2^-38 of its weights (adding in LDS in any order gives the same bits).
+// Everything else is in 64-bit floating point: with 10^5 logits a running sum
+// in 32 bits moves a border by more than many tokens' probability.
 #include "draw.hpp"
 #include "launch.hpp"
 #include "serve_args.hpp"
@@ -31,11 +35,17 @@ constexpr int kBins = 256;                     // the last one: everything below
 constexpr int kDThreads = 1024;
 constexpr int kDWaves = kDThreads / kWave;
 constexpr int kList = 2048;                    // tokens that are sorted in LDS
+constexpr int kTops = 256;                     // tokens that a chunk lists
+constexpr int kUnit = 38;                      // a bin's sum is in units of 2^-kUnit
+constexpr int kSumBits = 51;                   // and behind them its count
+constexpr uint64_t kSumMask = (uint64_t(1) << kSumBits) - 1;
 
 struct ChunkStat {
   float top;                                   // largest logit of the chunk
   int at;                                      // its lowest index
   double sum;                                  // of the weights relative to top, in pick: of the kept ones to the row's
+  int listed;                                  // tokens in its list: all those of its bins
+  int cut;                                     // up to this one
 };
 struct Pick {
   uint64_t border;                             // last kept place (below)
@@ -49,15 +59,15 @@ __device__ __forceinline__ ChunkStat* chunk_stats(const SampleArgs& a) { return 
 __device__ __forceinline__ Pick* picks(const SampleArgs& a) {
   return reinterpret_cast<Pick*>(chunk_stats(a) + static_cast<int64_t>(a.n_rows) * a.chunks);
 }
-__device__ __forceinline__ uint64_t* bin_sums(const SampleArgs& a) { return reinterpret_cast<uint64_t*>(picks(a) + a.n_rows); }
-__device__ __forceinline__ uint32_t* bin_counts(const SampleArgs& a) {
-  return reinterpret_cast<uint32_t*>(bin_sums(a) + static_cast<int64_t>(a.n_rows) * a.chunks * kBins);
+__device__ __forceinline__ uint64_t* chunk_bins(const SampleArgs& a) { return reinterpret_cast<uint64_t*>(picks(a) + a.n_rows); }
+__device__ __forceinline__ uint64_t* chunk_tops(const SampleArgs& a) {
+  return chunk_bins(a) + static_cast<int64_t>(a.n_rows) * a.chunks * kBins;
 }
 
 int64_t sample_bytes(int n_rows, int vocab, int* chunks) {
   const int64_t c = (vocab + kChunk - 1) / kChunk;
   if (chunks) *chunks = static_cast<int>(c);
-  return n_rows * (c * (static_cast<int64_t>(sizeof(ChunkStat)) + kBins * 12) + static_cast<int64_t>(sizeof(Pick)));
+  return n_rows * (c * static_cast<int64_t>(sizeof(ChunkStat) + (kBins + kTops) * sizeof(uint64_t)) + static_cast<int64_t>(sizeof(Pick)));
 }
 
 // Settings of a row: log2(e) / T, and its filters (k = 0, p = 1, m = 0: off).
@@ -115,95 +125,185 @@ __device__ __forceinline__ double weight(const Exp2& exp2, float v, float top, d
   return exp2((static_cast<double>(v) - static_cast<double>(top)) * rate);
 }
 // A quarter octave that a logit's weight lies in, on a grid that all chunks
-// share: whole numbers that never fall with the logit.
-__device__ __forceinline__ double quarter(float v, double rate) {
-  constexpr double kMost = 1125899906842624.0;   // 2^50: differences stay exact
-  if (!(v < INFINITY)) return kMost;
-  return fmin(fmax(floor(static_cast<double>(v) * (4.0 * rate)), -kMost), kMost);
-}
+// share: whole numbers that never fall with the logit. They and their
+// differences are exact up to 2^53, and unlike logits that far up are more
+// than kBins apart (2^-24 of their size).
+__device__ __forceinline__ double quarter(float v, double rate4) { return floor(static_cast<double>(v) * rate4); }
+// Bins between two quarters, the first one not below the other.
+__device__ __forceinline__ int bins_between(double above, double below, int most) { return static_cast<int>(fmin(above - below, static_cast<double>(most))); }
 // Bin of a logit below a largest one, kBins for none.
-__device__ __forceinline__ int bin_of(float v, double rate, float top, double top_quarter) {
+__device__ __forceinline__ int bin_of(float v, double rate4, float top, double top_quarter) {
   if (!(v > -INFINITY)) return kBins;
   if (top == INFINITY) return v == top ? 0 : kBins;
-  return static_cast<int>(fmin(top_quarter - quarter(v, rate), kBins - 1.0));
+  return bins_between(top_quarter, quarter(v, rate4), kBins - 1);
 }
 
-template <int WAVES>
-__device__ __forceinline__ double join_waves(const double* lds) {
-  double sum = 0.0;
-#pragma unroll
-  for (int w = 0; w < WAVES; ++w) sum += lds[w];
-  return sum;
+// 2^(-b / 4): what a bin's weights are relative to.
+__device__ __forceinline__ double bin_scale(int b) {
+  const double lower = b & 1 ? 0.84089641525371454303112547623321 : 1.0, half = b & 2 ? 0.70710678118654752440084436210485 : 1.0;
+  return __builtin_ldexp(lower * half, -(b >> 2));
 }
+// A bin's sum, from its units.
+__device__ __forceinline__ double bin_sum_of(uint64_t bin, int b) {
+  return __builtin_ldexp(static_cast<double>(bin & kSumMask), -kUnit) * bin_scale(b);
+}
+
+// 2^(38 + x / 4) as a whole number, -1 <= x <= 1, in the low 52 bits of the
+// result: the Taylor polynomial of degree 10 of exp(x ln 2 / 4), whose next
+// term is below 2 10^-16, in units of 2^-kUnit, added to 2^52.
+struct Units {
+  double c[11];
+  __device__ __forceinline__ Units() {
+    double v = 0x1p38;
+#pragma unroll
+    for (int i = 0; i <= 10; ++i) {
+      c[i] = v + (i == 0 ? 0x1p52 : 0.0);
+      v = v * (0.69314718055994530941723212145818 / 4) / (i + 1);
+    }
+#pragma unroll
+    for (int i = 0; i <= 10; ++i) asm("" : "+s"(c[i]));
+  }
+  __device__ __forceinline__ long long operator()(double x) const {
+    double p = c[10];
+#pragma unroll
+    for (int i = 9; i >= 0; --i) p = fma(p, x, c[i]);
+    return __double_as_longlong(p);
+  }
+};
+static_assert(kUnit == 38);
+
+// The row of a workgroup of a grid of chunks by rows. (Rows in a loop would
+// have the compiler keep addresses and masks of every branch across it.)
+constexpr int kGridRows = 1 << 15;
+__device__ __forceinline__ int row_of_grid() { return static_cast<int>(blockIdx.z) * kGridRows + static_cast<int>(blockIdx.y); }
+
+// Histogram of a chunk. Lanes add to one of kCopies copies, so that those of
+// one bin meet less often (one copy 106 us, NN for four, for 256 rows of 151669).
+constexpr int kCopies = 4;
 
 __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
   __shared__ float tops[kSWaves];
-  __shared__ int ats[kSWaves];
+  __shared__ int ats[kSWaves], scans[kSWaves], listed, cut;
   __shared__ double sums[kSWaves];
-  __shared__ uint64_t bin_sum[kBins];
-  __shared__ uint32_t bin_count[kBins];
-  const Exp2 exp2;
+  __shared__ unsigned long long bins[kBins * kCopies];
   const int tid = threadIdx.x, wave = tid >> 6, c = blockIdx.x, i0 = c * kChunk + 4 * tid;
-  for (int r = blockIdx.y; r < a.n_rows; r += gridDim.y) {
-    const Settings s = settings_of(a, r);
-    if (s.none) continue;                      // uniform
-    const float* row = a.logits + r * a.ldl;
-    float v[kSPer];
+  const int r = row_of_grid();
+  if (r >= a.n_rows) return;
+  const Settings s = settings_of(a, r);
+  if (s.none) return;                          // uniform
+  const float* row = a.logits + r * a.ldl;
+  float v[kSPer];
+  if ((c + 1) * kChunk <= a.vocab) {         // uniform: all loads at once
 #pragma unroll
     for (int k = 0; k < kSPer; k += 4) {
-      float four[4];
-      load_quad(row, i0 + k * kSThreads, a.vocab, -INFINITY, four);
+      const u32x4 x = ld_x4(reinterpret_cast<const uint8_t*>(row + i0 + k * kSThreads));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[k + e] = taken(four[e]);
+      for (int e = 0; e < 4; ++e) v[k + e] = taken(__uint_as_float(x[e]));
     }
-    float top = -INFINITY;
-    int at = 0x7fffffff;
+  } else {
 #pragma unroll
-    for (int k = 0; k < kSPer; ++k) top = fmaxf(top, v[k]);
+    for (int k = 0; k < kSPer; ++k) {
+      const int i = i0 + (k / 4) * 4 * kSThreads + k % 4;
+      v[k] = row[i < a.vocab ? i : a.vocab - 1];
+      v[k] = i < a.vocab ? taken(v[k]) : -INFINITY;
+    }
+  }
+  float top = -INFINITY;
+  int at = 0x7fffffff;
+#pragma unroll
+  for (int k = 0; k < kSPer; ++k) top = fmaxf(top, v[k]);
+  if (s.greedy) {                            // uniform; the others do without the index
 #pragma unroll
     for (int k = kSPer - 1; k >= 0; --k)
       at = v[k] == top && top > -INFINITY ? i0 + (k / 4) * 4 * kSThreads + k % 4 : at;
-    wave_top(top, at);
-    const bool bins = s.filtered();
-    __syncthreads();                           // the row before is done with LDS
-    if ((tid & 63) == 0) {
-      tops[wave] = top;
-      ats[wave] = at;
-    }
-    if (bins) {
-      bin_sum[tid] = 0;
-      bin_count[tid] = 0;
-    }
-    __syncthreads();
+  }
+  wave_top(top, at);
+  const bool filtered = s.filtered();
+  if ((tid & 63) == 0) {
+    tops[wave] = top;
+    ats[wave] = at;
+  }
+  if (filtered) {
 #pragma unroll
-    for (int w = 0; w < kSWaves; ++w) take_top(top, at, tops[w], ats[w]);
-    double sum = 0.0;
-    if (!s.greedy && top > -INFINITY) {
-      const double top_quarter = quarter(top, s.rate);
+    for (int k = 0; k < kCopies; ++k) bins[k * kSThreads + tid] = 0;
+    if (tid == 0) {
+      listed = 0;
+      cut = -1;
+    }
+  }
+  __syncthreads();
 #pragma unroll
-      for (int k = 0; k < kSPer; ++k) {
-        const double w = weight(exp2, v[k], top, s.rate);
-        sum += w;
-        if (bins) {
-          const int b = bin_of(v[k], s.rate, top, top_quarter);
-          if (b < kBins) {
-            // w 2^(b / 4) is below 2^1.25: 4096 of them in units of 2^-50 stay below 2^64
-            atomicAdd(reinterpret_cast<unsigned long long*>(&bin_sum[b]),
-                      static_cast<unsigned long long>(__builtin_ldexp(w, 50 + b / 4) + 0.5));
-            atomicAdd(&bin_count[b], 1u);
-          }
-        }
-      }
+  for (int w = 0; w < kSWaves; ++w) take_top(top, at, tops[w], ats[w]);
+  const bool any = !s.greedy && top > -INFINITY;
+  double sum = 0.0;
+  int bin[kSPer];
+  float x[kSPer];
+#pragma unroll
+  for (int k = 0; k < kSPer; ++k) x[k] = v[k];
+  if (top == INFINITY) {                     // uniform: the infinite ones share all
+#pragma unroll
+    for (int k = 0; k < kSPer; ++k) x[k] = v[k] == top ? 0.0f : -INFINITY;
+  }
+  const double dtop = top < INFINITY ? static_cast<double>(top) : 0.0;
+  if (any && !filtered) {
+    const Exp2 exp2;                         // (in scalar registers that the other branch has no use for)
+#pragma unroll
+    for (int k = 0; k < kSPer; ++k) sum += exp2((static_cast<double>(x[k]) - dtop) * s.rate);
+  } else if (any) {
+    const Units units;
+    unsigned long long* mine = bins + (tid & (kCopies - 1));
+    constexpr long long kOne = (1ll << kSumBits) - (0x433ll << 52);   // a count, without the exponent of 2^52
+    const double rate4 = 4.0 * s.rate, top_quarter = floor(dtop * rate4);
+#pragma unroll
+    for (int k = 0; k < kSPer; ++k) {
+      const double d = static_cast<double>(x[k]);
+      const int b = bins_between(top_quarter, floor(d * rate4), kBins - 1);
+      // 4 log2(w) + b is within +-1 but for the last bin, whose tokens count
+      // as 2^-64 of the largest at least: 2^-52 of the sum for all of them
+      const double f = fmax(fma(d - dtop, rate4, static_cast<double>(b)), -1.0);
+      const unsigned long long add = static_cast<unsigned long long>(units(f) + kOne);
+      if (x[k] > -INFINITY) atomicAdd(mine + b * kCopies, add);
+      bin[k] = x[k] > -INFINITY ? b : kBins;
     }
-    sum = wave_sum(sum);
-    if ((tid & 63) == 0) sums[wave] = sum;
+  }
+  const int64_t place = static_cast<int64_t>(r) * a.chunks + c;
+  __syncthreads();
+  if (filtered) {
+    // the bins of at most kTops tokens together, and these tokens
+    unsigned long long all = 0;
+#pragma unroll
+    for (int k = 0; k < kCopies; ++k) all += bins[tid * kCopies + k];
+    chunk_bins(a)[place * kBins + tid] = all;
+    sum = bin_sum_of(all, tid);
+    int up = wave_scan(static_cast<int>(all >> kSumBits));
+    if (lane_id() == kWave - 1) scans[wave] = up;
     __syncthreads();
-    const int64_t place = static_cast<int64_t>(r) * a.chunks + c;
-    if (tid == 0) chunk_stats(a)[place] = ChunkStat{top, at, join_waves<kSWaves>(sums)};
-    if (bins) {
-      bin_sums(a)[place * kBins + tid] = bin_sum[tid];
-      bin_counts(a)[place * kBins + tid] = bin_count[tid];
+    for (int w = 0; w < wave; ++w) up += scans[w];
+    const uint64_t fits = __ballot(up <= kTops);
+    if (lane_id() == 0 && fits) atomicMax(&cut, 64 * wave + 63 - __builtin_clzll(fits));
+    __syncthreads();
+    int hits = 0;
+#pragma unroll
+    for (int k = 0; k < kSPer; ++k) hits += any && bin[k] <= cut;
+    int to = wave_scan(hits);
+    int first = 0;
+    if (lane_id() == kWave - 1 && to) first = atomicAdd(&listed, to);
+    to += __builtin_amdgcn_readlane(first, kWave - 1) - hits;
+    if (hits) {
+      uint64_t* list = chunk_tops(a) + place * kTops;
+#pragma unroll
+      for (int k = 0; k < kSPer; ++k)
+        if (bin[k] <= cut) list[to++] = place_of(v[k], i0 + (k / 4) * 4 * kSThreads + k % 4);
     }
+  }
+  sum = wave_sum(sum);
+  if ((tid & 63) == 0) sums[wave] = sum;
+  __syncthreads();
+  if (tid == 0) {
+    double all = 0.0;
+#pragma unroll
+    for (int w = 0; w < kSWaves; ++w) all += sums[w];
+    chunk_stats(a)[place] = ChunkStat{top, at, all, filtered ? listed : 0, filtered ? cut : -1};
   }
 }
 
@@ -214,18 +314,23 @@ __device__ __forceinline__ double chunk_factor(const Exp2& exp2, float chunk_top
 }
 
 struct PickLds {
-  double sum[4][kBins];                        // of bins, by quarter of the chunks
-  int count[4][kBins];
-  double bin_sum[kBins];
+  double part_sum[4][kBins];                   // of bins, by quarter of the chunks
+  int part_count[4][kBins];
+  double bin_sum[kBins];                       // of the row's bins, then running sums up to their ends
   int bin_count[kBins];
   uint64_t list[kList];
+  double weights[kList];
   double waves[kDWaves];
-  int iwaves[kDWaves];
   unsigned long long cell_sum[kBins];
   uint32_t cell_count[kBins];
-  uint64_t border;
-  double d0, d1;
+  int64_t ahead;
+  double d0, d1, d2;
   int i0, i1, i2;
+};
+struct ChunkShift {                            // of each chunk, in dynamic LDS
+  double factor;                               // from its weights to the row's; below 0: it has none
+  int shift;                                   // from its bins to the row's
+  int pad;
 };
 
 // Sum over the workgroup's lanes before this one, and of all.
@@ -245,18 +350,23 @@ __device__ __forceinline__ double block_scan_d(double v, double* lds, double& to
   return before + (up - v);
 }
 
-// Elements of the row whose place is in lo..hi: f(place, value), by all lanes.
+// Elements of the row whose place is in lo..hi: f(place, value), by all lanes,
+// with eight loads on their way.
 template <class Fn>
 __device__ __forceinline__ void each_between(const SampleArgs& a, const float* row, uint64_t lo, uint64_t hi, Fn f) {
-  for (int i0 = 4 * static_cast<int>(threadIdx.x); i0 < a.vocab; i0 += 4 * kDThreads) {
-    float v[4];
-    load_quad(row, i0, a.vocab, -INFINITY, v);
+  constexpr int kAhead = 8;
+  for (int i0 = 4 * static_cast<int>(threadIdx.x); i0 < a.vocab; i0 += 4 * kDThreads * kAhead) {
+    float v[kAhead][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const float x = taken(v[e]);
-      const uint64_t at = place_of(x, i0 + e);
-      if (x > -INFINITY && at >= lo && at <= hi) f(at, x);
-    }
+    for (int q = 0; q < kAhead; ++q) load_quad(row, i0 + 4 * kDThreads * q, a.vocab, -INFINITY, v[q]);
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float x = taken(v[q][e]);
+        const uint64_t at = place_of(x, i0 + 4 * kDThreads * q + e);
+        if (x > -INFINITY && at >= lo && at <= hi) f(at, x);
+      }
   }
 }
 
@@ -317,14 +427,14 @@ __device__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const flo
       }
       l.i0 = cell;
       l.d0 = passed;
-      l.list[0] = static_cast<uint64_t>(ahead);
+      l.ahead = ahead;
     }
     __syncthreads();
     const uint64_t from = lo + (static_cast<uint64_t>(l.i0) << shift), to = from + ((uint64_t(1) << shift) - 1);
     lo = from;
     hi = to < hi ? to : hi;
     count = l.cell_count[l.i0];
-    ahead = static_cast<int64_t>(l.list[0]);
+    ahead = l.ahead;
     passed = l.d0;
     __syncthreads();
   }
@@ -382,274 +492,428 @@ __device__ __forceinline__ uint32_t first_key(uint32_t most, Fn passes) {
   return static_cast<uint32_t>(lo);
 }
 
-// The row's border by all filters.
-__device__ uint64_t border_of(const SampleArgs& a, const Exp2& exp2, const float* row, int r, const Settings& s, float top, PickLds& l) {
-  const int tid = threadIdx.x;
-  const ChunkStat* st = chunk_stats(a) + static_cast<int64_t>(r) * a.chunks;
-  const uint64_t* hs = bin_sums(a) + static_cast<int64_t>(r) * a.chunks * kBins;
-  const uint32_t* hc = bin_counts(a) + static_cast<int64_t>(r) * a.chunks * kBins;
-  const double top_quarter = quarter(top, s.rate);
-  // a fourth of the threads takes a fourth of the chunks
-  const int part = tid / kBins, bin = tid % kBins;
-  double bin_sum = 0.0;
-  int bin_count = 0;
+// Running sums of the row's bins: of the chunks', each moved to the row's
+// grid. A fourth of the threads takes a fourth of the chunks; chunk bins that
+// the row's last bin takes in are summed by the threads they belong to.
+__device__ __forceinline__ void join_bins(const SampleArgs& a, int r, const ChunkShift* chunk, PickLds& l) {
+  const int tid = threadIdx.x, part = tid / kBins, bin = tid % kBins;
+  const uint64_t* bins = chunk_bins(a) + static_cast<int64_t>(r) * a.chunks * kBins;
+  double sum = 0.0, far_sum = 0.0;
+  int count = 0, far_count = 0;
+#pragma unroll 4
   for (int c = part; c < a.chunks; c += kDThreads / kBins) {
-    const float ct = st[c].top;
-    if (!(ct > -INFINITY) || (top == INFINITY && ct != top)) continue;
-    const double shift = top == INFINITY ? 0.0 : top_quarter - quarter(ct, s.rate);
-    const double factor = chunk_factor(exp2, ct, top, s.rate);
-    // bins of the chunk that fall into this one: the last takes all behind it
-    int from = static_cast<int>(fmax(bin - shift, -1.0)), to = from;
-    if (bin == kBins - 1) {
-      from = from < 0 ? 0 : from;
-      to = kBins - 1;
-    }
-    for (int b = from; b <= to; ++b) {
-      if (b < 0) continue;
-      bin_sum += __builtin_ldexp(static_cast<double>(hs[c * kBins + b]), -(50 + b / 4)) * factor;
-      bin_count += static_cast<int>(hc[c * kBins + b]);
-    }
+    const ChunkShift h = chunk[c];
+    if (h.factor < 0.0) continue;              // uniform in a wave
+    const int from = bin - h.shift;
+    const bool near = from >= 0 && bin < kBins - 1, far = bin + h.shift >= kBins - 1;
+    const uint64_t x = near ? bins[static_cast<int64_t>(c) * kBins + from] : 0, y = far ? bins[static_cast<int64_t>(c) * kBins + bin] : 0;
+    sum += bin_sum_of(x, near ? from : 0) * h.factor;
+    count += static_cast<int>(x >> kSumBits);
+    far_sum += bin_sum_of(y, bin) * h.factor;
+    far_count += static_cast<int>(y >> kSumBits);
   }
+  // the last bin
+  const double far_wave = wave_sum(far_sum);
+  const int far_wave_count = __builtin_amdgcn_readlane(wave_scan(far_count), kWave - 1);
   __syncthreads();                             // the row before is done with LDS
-  l.sum[part][bin] = bin_sum;
-  l.count[part][bin] = bin_count;
+  l.part_sum[part][bin] = sum;
+  l.part_count[part][bin] = count;
+  if (tid < kDWaves) l.cell_count[tid] = 0;
+  __syncthreads();
+  if (lane_id() == 0) {
+    l.waves[tid >> 6] = far_wave;
+    l.cell_count[tid >> 6] = far_wave_count;
+  }
+  __syncthreads();
+  double own = 0.0;
+  int own_count = 0;
+  if (tid < kBins) {
+    own = (l.part_sum[0][tid] + l.part_sum[1][tid]) + (l.part_sum[2][tid] + l.part_sum[3][tid]);
+    own_count = l.part_count[0][tid] + l.part_count[1][tid] + l.part_count[2][tid] + l.part_count[3][tid];
+    if (tid == kBins - 1)
+      for (int w = 0; w < kDWaves; ++w) {
+        own += l.waves[w];
+        own_count += static_cast<int>(l.cell_count[w]);
+      }
+  }
+  double up = wave_scan(own);
+  int up_count = wave_scan(own_count);
+  __syncthreads();
+  if (lane_id() == kWave - 1) {
+    l.waves[tid >> 6] = up;
+    l.cell_count[tid >> 6] = up_count;
+  }
   __syncthreads();
   if (tid < kBins) {
-    l.bin_sum[tid] = (l.sum[0][tid] + l.sum[1][tid]) + (l.sum[2][tid] + l.sum[3][tid]);
-    l.bin_count[tid] = l.count[0][tid] + l.count[1][tid] + l.count[2][tid] + l.count[3][tid];
-  }
-  // min-p: the smallest logit that is kept
-  __syncthreads();
-  if (tid < kWave && s.m > 0.0) {
-    const uint32_t least = first_key(key_of(top), [&](float v) QMV_INLINE { return weight(exp2, v, top, s.rate) >= s.m; });
-    if (tid == 0) l.border = last_place(least);
+    for (int w = 0; w < (tid >> 6); ++w) {
+      up += l.waves[w];
+      up_count += static_cast<int>(l.cell_count[w]);
+    }
+    l.bin_sum[tid] = up;
+    l.bin_count[tid] = up_count;
   }
   __syncthreads();
-  uint64_t border = s.m > 0.0 ? l.border : ~uint64_t(0);
-  double total = 0.0;
+}
+
+// First bin whose running count (k > 0) or sum reaches k or the goal; the
+// last one that has tokens where none does.
+__device__ __forceinline__ int crossing(const PickLds& l, int k, double goal, int* slot) {
+  const int tid = threadIdx.x;
+  if (tid == 0) *slot = kBins;
+  __syncthreads();
+  if (tid < kBins) {
+    const int count = l.bin_count[tid], all = l.bin_count[kBins - 1];
+    const bool hit = (k > 0 ? count >= k : l.bin_sum[tid] >= goal) || count == all;
+    const uint64_t hits = __ballot(hit && count > 0);
+    if (lane_id() == 0 && hits) atomicMin(slot, (tid & ~63) + __builtin_ctzll(hits));
+  }
+  __syncthreads();
+  return *slot;
+}
+
+// Where a row's draw stands.
+struct Drawn {
+  uint64_t border;
+  double total, chosen;
+  int token;
+};
+
+// All `count` tokens up to the border's bin, in LDS: sorted, cut by all
+// filters, and drawn from. all: the sum of the row's weights.
+__device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Settings& s, float top, int count, double all, float u, PickLds& l) {
+  const int tid = threadIdx.x;
+  int n = 2;
+  while (n < count) n <<= 1;
+  for (int i = count + tid; i < n; i += kDThreads) l.list[i] = ~uint64_t(0);
+  sort_list(l.list, n);
+  double w[2], total;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) w[e] = 2 * tid + e < count ? weight(exp2, value_at(l.list[2 * tid + e]), top, s.rate) : 0.0;
+  const int k = s.k > 0 && s.k < count ? s.k : count;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) w[e] = 2 * tid + e < k ? w[e] : 0.0;
+  const double before = block_scan_d(w[0] + w[1], l.waves, total);
+  const double goal = s.p * (s.k > 0 ? total : all);
+  if (tid == 0) l.i0 = 0;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * tid + e;
+    const bool in = i < k && (s.p >= 1.0 || before + (e ? w[0] : 0.0) < goal) && w[e] >= s.m;
+    const uint64_t ins = __ballot(in);
+    if (ins && lane_id() == 63 - __builtin_clzll(ins)) atomicMax(&l.i0, i);
+  }
+  __syncthreads();
+  const int last = l.i0;                       // the first token is kept in any case
+  Drawn d;
+  d.border = l.list[last];
+  // the kept ones by their indices
+  n = 2;
+  while (n < last + 1) n <<= 1;
+  __syncthreads();
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * tid + e;
+    if (i < n) {
+      l.weights[i] = w[e];
+      l.list[i] = i <= last ? (l.list[i] & kLowIndex) << 12 | static_cast<uint64_t>(i) : ~uint64_t(0);
+    }
+  }
+  sort_list(l.list, n);
+  int index[2] = {-1, -1};
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = 2 * tid + e;
+    w[e] = 0.0;
+    if (i <= last) {
+      const uint64_t x = l.list[i];
+      w[e] = l.weights[x & 4095];
+      index[e] = static_cast<int>(x >> 12);
+    }
+  }
+  const double up = block_scan_d(w[0] + w[1], l.waves, d.total);
+  if (tid == 0) {
+    l.i0 = 0x7fffffff;
+    l.i1 = -1;
+  }
+  __syncthreads();
+  const double drawn = static_cast<double>(u) * d.total;
+  const bool hit0 = w[0] > 0.0 && up + w[0] > drawn, hit1 = w[1] > 0.0 && up + w[0] + w[1] > drawn;
+  const uint64_t hits = __ballot(hit0 || hit1), some = __ballot(w[0] > 0.0 || w[1] > 0.0);
+  if (hits && lane_id() == __builtin_ctzll(hits)) atomicMin(&l.i0, 2 * tid + (hit0 ? 0 : 1));
+  if (some && lane_id() == 63 - __builtin_clzll(some)) atomicMax(&l.i1, 2 * tid + (w[1] > 0.0 ? 1 : 0));
+  __syncthreads();
+  const int take = l.i0 != 0x7fffffff ? l.i0 : l.i1;
+  const uint64_t x = l.list[take];
+  d.token = static_cast<int>(x >> 12);
+  d.chosen = l.weights[x & 4095] / d.total;
+  return d;
+}
+
+// The border by all filters, of a row with more tokens up to it than fit LDS.
+__device__ uint64_t far_border(const SampleArgs& a, const Exp2& exp2, const float* row, const Settings& s, float top, PickLds& l) {
+  const int tid = threadIdx.x;
+  const double top_quarter = quarter(top, 4.0 * s.rate);
+  const uint32_t most = key_of(top);
+  uint64_t border = ~uint64_t(0);
+  if (s.m > 0.0)                               // every wave for itself
+    border = last_place(first_key(most, [&](float v) QMV_INLINE { return weight(exp2, v, top, s.rate) >= s.m; }));
+  double total = l.bin_sum[kBins - 1];
   for (int turn = 0; turn < 2; ++turn) {       // top-k, then top-p
-    if (turn == 0 ? s.k == 0 : s.p >= 1.0) continue;
+    if (turn == 0 ? s.k == 0 || s.k >= l.bin_count[kBins - 1] : s.p >= 1.0) continue;   // uniform
+    const int k = turn == 0 ? s.k : 0;
     const double goal = s.p * total;
-    __syncthreads();
-    if (tid == 0) {
-      int b = 0, last = -1;
-      int64_t ahead = 0, ahead_last = 0;
-      double passed = 0.0, passed_last = 0.0, all = 0.0;
-      if (turn == 1 && s.k == 0)
-        for (int i = 0; i < kBins; ++i) all += l.bin_sum[i];
-      l.d1 = all;
-      const double want = s.k == 0 ? s.p * all : goal;
-      for (; b < kBins; ++b) {
-        if (l.bin_count[b] == 0) continue;
-        last = b;
-        ahead_last = ahead;
-        passed_last = passed;
-        if (turn == 0 ? ahead + l.bin_count[b] >= s.k : passed + l.bin_sum[b] >= want) break;
-        ahead += l.bin_count[b];
-        passed += l.bin_sum[b];
-      }
-      l.i0 = last;
-      l.i1 = static_cast<int>(ahead_last);
-      l.i2 = b == kBins;                       // nothing is cut off
-      l.d0 = passed_last;
-    }
-    __syncthreads();
-    const int b = l.i0, ahead = l.i1, open = l.i2;
-    const double passed = l.d0, all = l.d1;
-    if (turn == 1 && s.k == 0) total = all;
-    __syncthreads();
-    if (turn == 0 && open) {                   // fewer than k tokens have a weight
-      if (tid == 0) {
-        double sum = 0.0;
-        for (int i = 0; i < kBins; ++i) sum += l.bin_sum[i];
-        l.d0 = sum;
-      }
-      __syncthreads();
-      total = l.d0;
-      continue;
-    }
-    // keys of the bin
-    if (tid < kWave) {
-      const uint32_t most = key_of(top);
-      const uint32_t low = first_key(most, [&](float v) QMV_INLINE { return bin_of(v, s.rate, top, top_quarter) <= b; });
-      const uint32_t high = b == 0 ? most : first_key(most, [&](float v) QMV_INLINE { return bin_of(v, s.rate, top, top_quarter) < b; }) - 1;
-      if (tid == 0) {
-        l.list[0] = first_place(high);
-        l.list[1] = last_place(low);
-      }
-    }
-    __syncthreads();
-    const uint64_t lo = l.list[0], hi = l.list[1];
-    __syncthreads();
+    const int b = crossing(l, k, goal, &l.i2);
+    const int ahead = b > 0 ? l.bin_count[b - 1] : 0, count = l.bin_count[b] - ahead;
+    const double passed = b > 0 ? l.bin_sum[b - 1] : 0.0;
+    const uint32_t low = first_key(most, [&](float v) QMV_INLINE { return bin_of(v, 4.0 * s.rate, top, top_quarter) <= b; });
+    const uint32_t high = b == 0 ? most : first_key(most, [&](float v) QMV_INLINE { return bin_of(v, 4.0 * s.rate, top, top_quarter) < b; }) - 1;
     double kept;
-    const uint64_t found = find_border(a, exp2, row, top, s.rate, lo, hi, l.bin_count[b], ahead, passed, turn == 0 ? s.k : 0,
-                                       s.p * total, l, kept);
+    const uint64_t found = find_border(a, exp2, row, top, s.rate, first_place(high), last_place(low), count, ahead, passed, k, goal, l, kept);
     if (turn == 0) total = kept;
     border = found < border ? found : border;
     __syncthreads();
   }
+  (void)tid;
   return border;
+}
+
+// The kept weights of each chunk, and a draw by them: the chunk in which the
+// running sum passes the goal, then its element.
+__device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2, const float* row, ChunkStat* st, const Settings& s, float top,
+                                           uint64_t border, float u, PickLds& l) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  Drawn d{border, 0.0, 0.0, -1};
+  __syncthreads();
+  if (border != ~uint64_t(0)) {
+    for (int c = wave; c < a.chunks; c += kDWaves) {
+      double sum = 0.0;
+#pragma unroll 4
+      for (int j = 0; j < kChunk / (4 * kWave); ++j) {
+        const int i = c * kChunk + 4 * (j * kWave + lane_id());
+        float v[4];
+        load_quad(row, i, a.vocab, -INFINITY, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float x = taken(v[e]);
+          if (place_of(x, i + e) <= border) sum += weight(exp2, x, top, s.rate);
+        }
+      }
+      sum = wave_sum(sum);
+      if (lane_id() == 0) st[c].sum = sum;
+    }
+  } else {
+    for (int c = tid; c < a.chunks; c += kDThreads) st[c].sum *= chunk_factor(exp2, st[c].top, top, s.rate);
+  }
+  __syncthreads();
+  double sum = 0.0;
+  for (int c = lane_id(); c < a.chunks; c += kWave) sum += st[c].sum;
+  d.total = wave_sum(sum);
+  if (!a.tokens && !a.chosen) return d;
+  const double goal = static_cast<double>(u) * d.total;
+  double run = 0.0, before = 0.0, last_before = 0.0;
+  int found = -1, last = 0;
+  for (int c0 = 0; c0 < a.chunks && found < 0; c0 += kWave) {
+    const int c = c0 + lane_id();
+    const double w = c < a.chunks ? st[c].sum : 0.0, up = wave_scan(w) + run;
+    const uint64_t hit = __ballot(up > goal), some = __ballot(w > 0.0);
+    if (some) {
+      const int i = 63 - __builtin_clzll(some);
+      last = c0 + i;
+      last_before = __shfl(up - w, i);
+    }
+    if (hit) {
+      const int i = __builtin_ctzll(hit);
+      found = c0 + i;
+      before = __shfl(up - w, i);
+    }
+    run = __shfl(up, kWave - 1);
+  }
+  const int c = found >= 0 ? found : last;
+  if (found < 0) before = last_before;
+  // its elements, a run of four a lane
+  const int i0 = c * kChunk + 4 * tid;
+  float v[4];
+  double w[4], own = 0.0;
+  load_quad(row, i0, a.vocab, -INFINITY, v);
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const float x = taken(v[e]);
+    w[e] = place_of(x, i0 + e) <= border ? weight(exp2, x, top, s.rate) : 0.0;
+    own += w[e];
+  }
+  double all;
+  double up = before + block_scan_d(own, l.waves, all);
+  if (tid == 0) {
+    l.i0 = 0x7fffffff;
+    l.i1 = -1;
+  }
+  __syncthreads();
+  int hit = 0x7fffffff, last_hit = -1;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    up += w[e];
+    if (w[e] > 0.0) {
+      last_hit = i0 + e;
+      if (up > goal && hit == 0x7fffffff) hit = i0 + e;
+    }
+  }
+  if (hit != 0x7fffffff) atomicMin(&l.i0, hit);
+  if (last_hit >= 0) atomicMax(&l.i1, last_hit);
+  __syncthreads();
+  d.token = l.i0 != 0x7fffffff ? l.i0 : l.i1;
+  if (d.token >= 0) d.chosen = weight(exp2, taken(row[d.token]), top, s.rate) / d.total;
+  return d;
+}
+
+// The tokens of bins 0..b in l.list: from the chunks' lists, or from the row
+// where a chunk lists fewer. Returns their number.
+__device__ __forceinline__ int gather(const SampleArgs& a, const float* row, int r, const Settings& s, float top, int b, const ChunkShift* chunk,
+                                      PickLds& l) {
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const ChunkStat* st = chunk_stats(a) + static_cast<int64_t>(r) * a.chunks;
+  const double top_quarter = quarter(top, 4.0 * s.rate);
+  bool covered = true;
+  for (int c = tid; c < a.chunks; c += kDThreads)
+    if (chunk[c].factor >= 0.0 && st[c].cut < kBins - 1 && (b == kBins - 1 || st[c].cut + chunk[c].shift < b)) covered = false;
+  if (tid == 0) l.i0 = 0;
+  if (__syncthreads_and(covered)) {
+    for (int c = wave; c < a.chunks; c += kDWaves) {
+      if (chunk[c].factor < 0.0 || chunk[c].shift > b) continue;
+      const uint64_t* list = chunk_tops(a) + (static_cast<int64_t>(r) * a.chunks + c) * kTops;
+      const int listed = st[c].listed;
+#pragma unroll
+      for (int j = 0; j < kTops / kWave; ++j) {
+        const int i = j * kWave + lane_id();
+        const uint64_t x = i < listed ? list[i] : 0;
+        const bool in = i < listed && bin_of(value_at(x), 4.0 * s.rate, top, top_quarter) <= b;
+        const uint64_t ins = __ballot(in);
+        if (ins == 0) continue;
+        int first = 0;
+        if (lane_id() == 0) first = atomicAdd(&l.i0, __builtin_popcountll(ins));
+        first = __builtin_amdgcn_readfirstlane(first);
+        const int at = first + __builtin_popcountll(ins & ((uint64_t(1) << lane_id()) - 1));
+        if (in && at < kList) l.list[at] = x;
+      }
+    }
+  } else {
+    const uint32_t low = first_key(key_of(top), [&](float v) QMV_INLINE { return bin_of(v, 4.0 * s.rate, top, top_quarter) <= b; });
+    each_between(a, row, 0, last_place(low), [&](uint64_t at, float) QMV_INLINE {
+      const int to = atomicAdd(&l.i0, 1);
+      if (to < kList) l.list[to] = at;
+    });
+  }
+  __syncthreads();
+  const int n = l.i0 < kList ? l.i0 : kList;
+  __syncthreads();
+  return n;
 }
 
 __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
   __shared__ PickLds l;
+  extern __shared__ __align__(16) uint8_t dynamic[];
+  ChunkShift* chunk = reinterpret_cast<ChunkShift*>(dynamic);
   const Exp2 exp2;
-  const int tid = threadIdx.x, wave = tid >> 6;
-  for (int r = blockIdx.x; r < a.n_rows; r += gridDim.x) {
-    const Settings s = settings_of(a, r);
-    const float* row = a.logits + r * a.ldl;
-    ChunkStat* st = chunk_stats(a) + static_cast<int64_t>(r) * a.chunks;
-    float top = -INFINITY;
-    int at = 0x7fffffff;
-    if (!s.none) {
-      for (int c = lane_id(); c < a.chunks; c += kWave) take_top(top, at, st[c].top, st[c].at);
-      wave_top(top, at);
+  const int tid = threadIdx.x;
+  const int r = blockIdx.x;
+  const Settings s = settings_of(a, r);
+  const float* row = a.logits + r * a.ldl;
+  const float u = a.u ? a.u[r] : 0.0f;
+  ChunkStat* st = chunk_stats(a) + static_cast<int64_t>(r) * a.chunks;
+  float top = -INFINITY;
+  int at = 0x7fffffff;
+  if (!s.none) {
+    for (int c = lane_id(); c < a.chunks; c += kWave) take_top(top, at, st[c].top, st[c].at);
+    wave_top(top, at);
+  }
+  Drawn d{0, 0.0, 0.0, -1};
+  if (top == -INFINITY) {                    // uniform
+  } else if (s.greedy) {
+    d = Drawn{place_of(top, at), 1.0, 1.0, at};
+  } else if (!s.filtered()) {
+    d = draw_long(a, exp2, row, st, s, top, ~uint64_t(0), u, l);
+  } else {
+    const double top_quarter = quarter(top, 4.0 * s.rate);
+    for (int c = tid; c < a.chunks; c += kDThreads) {
+      const float ct = st[c].top;
+      const bool has = ct > -INFINITY && (top < INFINITY || ct == top);
+      const int shift = has && top < INFINITY ? bins_between(top_quarter, quarter(ct, 4.0 * s.rate), kBins) : 0;
+      chunk[c] = ChunkShift{has ? chunk_factor(exp2, ct, top, s.rate) : -1.0, shift, 0};
     }
-    Pick pick{0, 0.0, s.rate, top, 0};
-    int token = -1;
-    double chosen = 0.0;
-    if (top == -INFINITY) {                    // uniform
-    } else if (s.greedy) {
-      pick.border = place_of(top, at);
-      pick.total = chosen = 1.0;
-      token = at;
+    __syncthreads();
+    join_bins(a, r, chunk, l);
+    // the last bin that can hold the border
+    const double all = l.bin_sum[kBins - 1];
+    int b = kBins - 1;
+    if (s.k > 0) b = crossing(l, s.k, 0.0, &l.i2);
+    else if (s.p < 1.0) b = crossing(l, 0, s.p * all, &l.i2);
+    if (s.m > 0.0 && (s.k == 0 || s.p >= 1.0)) {   // (top-p needs the sum of all k)
+      // w >= m ends in the bin of 4 log2(m), to one by rounding, behind the top's
+      const double end = 4.0 * -log2(s.m) + 2.0;
+      if (end < b) b = static_cast<int>(end);
+    }
+    __syncthreads();
+    if (l.bin_count[b] <= kList) {
+      const int n = gather(a, row, r, s, top, b, chunk, l);
+      d = draw_short(exp2, s, top, n, all, u, l);
     } else {
-      pick.border = s.filtered() ? border_of(a, exp2, row, r, s, top, l) : ~uint64_t(0);
-      // the chunks' kept weights, relative to the row's top
-      __syncthreads();
-      if (s.filtered()) {
-        for (int c = wave; c < a.chunks; c += kDWaves) {
-          double sum = 0.0;
-          for (int i = c * kChunk + 4 * lane_id(); i < (c + 1) * kChunk && i < a.vocab; i += 4 * kWave) {
-            float v[4];
-            load_quad(row, i, a.vocab, -INFINITY, v);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float x = taken(v[e]);
-              if (place_of(x, i + e) <= pick.border) sum += weight(exp2, x, top, s.rate);
-            }
-          }
-          sum = wave_sum(sum);
-          if (lane_id() == 0) st[c].sum = sum;
-        }
-      } else {
-        for (int c = tid; c < a.chunks; c += kDThreads) st[c].sum *= chunk_factor(exp2, st[c].top, top, s.rate);
-      }
-      __syncthreads();
-      // the chunk in which the running sum passes the goal
-      double sum = 0.0;
-      for (int c = lane_id(); c < a.chunks; c += kWave) sum += st[c].sum;
-      pick.total = wave_sum(sum);
-      if (a.tokens || a.chosen) {
-        const double goal = static_cast<double>(a.u[r]) * pick.total;
-        double run = 0.0, before = 0.0, last_before = 0.0;
-        int found = -1, last = 0;
-        for (int c0 = 0; c0 < a.chunks && found < 0; c0 += kWave) {
-          const int c = c0 + lane_id();
-          const double w = c < a.chunks ? st[c].sum : 0.0, up = wave_scan(w) + run;
-          const uint64_t hit = __ballot(up > goal), some = __ballot(w > 0.0);
-          if (some) {
-            const int i = 63 - __builtin_clzll(some);
-            last = c0 + i;
-            last_before = __shfl(up - w, i);
-          }
-          if (hit) {
-            const int i = __builtin_ctzll(hit);
-            found = c0 + i;
-            before = __shfl(up - w, i);
-          }
-          run = __shfl(up, kWave - 1);
-        }
-        const int c = found >= 0 ? found : last;
-        if (found < 0) before = last_before;
-        // its elements, a run of four a lane
-        const int i0 = c * kChunk + 4 * tid;
-        float v[4];
-        double w[4], own = 0.0;
-        load_quad(row, i0, a.vocab, -INFINITY, v);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = taken(v[e]);
-          w[e] = place_of(x, i0 + e) <= pick.border ? weight(exp2, x, top, s.rate) : 0.0;
-          own += w[e];
-        }
-        double all;
-        double up = before + block_scan_d(own, l.waves, all);
-        if (tid == 0) {
-          l.i0 = 0x7fffffff;
-          l.i1 = -1;
-        }
-        __syncthreads();
-        int hit = 0x7fffffff, last_hit = -1;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          up += w[e];
-          if (w[e] > 0.0) {
-            last_hit = i0 + e;
-            if (up > goal && hit == 0x7fffffff) hit = i0 + e;
-          }
-        }
-        if (hit != 0x7fffffff) atomicMin(&l.i0, hit);
-        if (last_hit >= 0) atomicMax(&l.i1, last_hit);
-        __syncthreads();
-        token = l.i0 != 0x7fffffff ? l.i0 : l.i1;
-        if (token >= 0) chosen = weight(exp2, taken(row[token]), top, s.rate) / pick.total;
-      }
+      const uint64_t border = far_border(a, exp2, row, s, top, l);
+      d = draw_long(a, exp2, row, st, s, top, border, u, l);
     }
-    if (tid == 0) {
-      if (a.tokens) a.tokens[r] = token;
-      if (a.chosen) a.chosen[r] = static_cast<float>(chosen);
-      if (a.probs) picks(a)[r] = pick;
-    }
-    __syncthreads();                           // the row is done with LDS
+  }
+  if (tid == 0) {
+    if (a.tokens) a.tokens[r] = d.token;
+    if (a.chosen) a.chosen[r] = static_cast<float>(d.chosen);
+    if (a.probs) picks(a)[r] = Pick{d.border, d.total, s.rate, top, 0};
   }
 }
 
 __global__ void __launch_bounds__(kSThreads) sample_probs_kernel(SampleArgs a) {
   const Exp2 exp2;
-  for (int r = blockIdx.y; r < a.n_rows; r += gridDim.y) {
-    const Pick pick = picks(a)[r];
-    const float* row = a.logits + r * a.ldl;
-    float* out = a.probs + r * a.ldp;
-    float v[kSPer];
-    const int i0 = blockIdx.x * kChunk + 4 * static_cast<int>(threadIdx.x);
+  const int r = row_of_grid();
+  if (r >= a.n_rows) return;
+  const Pick pick = picks(a)[r];
+  const float* row = a.logits + r * a.ldl;
+  float* out = a.probs + r * a.ldp;
+  float v[kSPer];
+  const int i0 = blockIdx.x * kChunk + 4 * static_cast<int>(threadIdx.x);
 #pragma unroll
-    for (int k = 0; k < kSPer; k += 4) {
+  for (int k = 0; k < kSPer; k += 4) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int i = i0 + k * kSThreads + e;
-        v[k + e] = i < a.vocab ? taken(row[i]) : -INFINITY;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + k * kSThreads + e;
+      v[k + e] = i < a.vocab ? taken(row[i]) : -INFINITY;
     }
+  }
 #pragma unroll
-    for (int k = 0; k < kSPer; k += 4) {
-      const int i = i0 + k * kSThreads;
-      float p[4];
+  for (int k = 0; k < kSPer; k += 4) {
+    const int i = i0 + k * kSThreads;
+    float p[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const bool in = pick.total > 0.0 && place_of(v[k + e], i + e) <= pick.border;
-        p[e] = in ? static_cast<float>(weight(exp2, v[k + e], pick.top, pick.rate) / pick.total) : 0.0f;
-      }
-      if (i + 4 <= a.vocab) {
-        __builtin_memcpy(__builtin_assume_aligned(out + i, 4), p, 16);
-      } else {
+    for (int e = 0; e < 4; ++e) {
+      const bool in = pick.total > 0.0 && place_of(v[k + e], i + e) <= pick.border;
+      p[e] = in ? static_cast<float>(weight(exp2, v[k + e], pick.top, pick.rate) / pick.total) : 0.0f;
+    }
+    if (i + 4 <= a.vocab) {
+      __builtin_memcpy(__builtin_assume_aligned(out + i, 4), p, 16);
+    } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (i + e < a.vocab) out[i + e] = p[e];
-      }
+      for (int e = 0; e < 4; ++e)
+        if (i + e < a.vocab) out[i + e] = p[e];
     }
   }
 }
 
 int launch_sample(const SampleArgs& a, hipStream_t st) {
-  const unsigned chunks = static_cast<unsigned>(a.chunks), rows = a.n_rows < 65535 ? a.n_rows : 65535;
-  hipLaunchKernelGGL(sample_stats_kernel, dim3(chunks, rows), dim3(kSThreads), 0, st, a);
+  const unsigned chunks = static_cast<unsigned>(a.chunks), rows = static_cast<unsigned>(a.n_rows);
+  const dim3 grid(chunks, rows < kGridRows ? rows : kGridRows, (rows + kGridRows - 1) / kGridRows);
+  hipLaunchKernelGGL(sample_stats_kernel, grid, dim3(kSThreads), 0, st, a);
   int rc = check_launch();
   if (rc) return rc;
-  hipLaunchKernelGGL(sample_pick_kernel, dim3(rows), dim3(kDThreads), 0, st, a);
+  hipLaunchKernelGGL(sample_pick_kernel, dim3(rows), dim3(kDThreads), chunks * sizeof(ChunkShift), st, a);
   rc = check_launch();
   if (rc || !a.probs) return rc;
-  hipLaunchKernelGGL(sample_probs_kernel, dim3(chunks, rows), dim3(kSThreads), 0, st, a);
+  hipLaunchKernelGGL(sample_probs_kernel, grid, dim3(kSThreads), 0, st, a);
   return check_launch();
 }
 
