@@ -32,9 +32,11 @@ constexpr int kSPer = 16;                      // logits a lane
 constexpr int kSWaves = kSThreads / kWave;
 constexpr int kChunk = kSThreads * kSPer;
 constexpr int kBins = 256;                     // the last one: everything below
-constexpr int kDThreads = 1024;
+constexpr int kDThreads = 512;
 constexpr int kDWaves = kDThreads / kWave;
-constexpr int kList = 2048;                    // tokens that are sorted in LDS
+constexpr int kRank = 256;                     // tokens that are sorted by counting those before each
+constexpr int kList = 2048;                    // tokens that are sorted, cut and drawn from in LDS
+constexpr int kArena = 3 * kList;              // tokens of one bin that are held there
 constexpr int kTops = 256;                     // tokens that a chunk lists
 constexpr int kUnit = 38;                      // a bin's sum is in units of 2^-kUnit
 constexpr int kSumBits = 51;                   // and behind them its count
@@ -44,8 +46,9 @@ struct ChunkStat {
   float top;                                   // largest logit of the chunk
   int at;                                      // its lowest index
   double sum;                                  // of the weights relative to top, in pick: of the kept ones to the row's
-  int listed;                                  // tokens in its list: all those of its bins
-  int cut;                                     // up to this one
+  int16_t listed;                              // tokens in its list: all those of its bins
+  int16_t cut;                                 // up to this one
+  int tokens;                                  // that have a weight
 };
 struct Pick {
   uint64_t border;                             // last kept place (below)
@@ -138,15 +141,16 @@ __device__ __forceinline__ int bin_of(float v, double rate4, float top, double t
   return bins_between(top_quarter, quarter(v, rate4), kBins - 1);
 }
 
-// 2^(-b / 4): what a bin's weights are relative to.
+// 2^(-b / 4), also for b below 0: what a bin's weights are relative to.
 __device__ __forceinline__ double bin_scale(int b) {
   const double lower = b & 1 ? 0.84089641525371454303112547623321 : 1.0, half = b & 2 ? 0.70710678118654752440084436210485 : 1.0;
   return __builtin_ldexp(lower * half, -(b >> 2));
 }
-// A bin's sum, from its units.
-__device__ __forceinline__ double bin_sum_of(uint64_t bin, int b) {
-  return __builtin_ldexp(static_cast<double>(bin & kSumMask), -kUnit) * bin_scale(b);
+// A bin's sum in units: a whole number below 2^52 is the low bits of its sum with 2^52.
+__device__ __forceinline__ double bin_units(uint64_t bin) {
+  return __longlong_as_double(static_cast<long long>((bin & kSumMask) | 0x433ull << 52)) - 0x1p52;
 }
+__device__ __forceinline__ double bin_sum_of(uint64_t bin, int b) { return __builtin_ldexp(bin_units(bin), -kUnit) * bin_scale(b); }
 
 // 2^(38 + x / 4) as a whole number, -1 <= x <= 1, in the low 52 bits of the
 // result: the Taylor polynomial of degree 10 of exp(x ln 2 / 4), whose next
@@ -183,7 +187,7 @@ constexpr int kCopies = 4;
 
 __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
   __shared__ float tops[kSWaves];
-  __shared__ int ats[kSWaves], scans[kSWaves], listed, cut;
+  __shared__ int ats[kSWaves], scans[kSWaves], next[kBins], cut, tokens;
   __shared__ double sums[kSWaves];
   __shared__ unsigned long long bins[kBins * kCopies];
   const int tid = threadIdx.x, wave = tid >> 6, c = blockIdx.x, i0 = c * kChunk + 4 * tid;
@@ -226,10 +230,7 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
   if (filtered) {
 #pragma unroll
     for (int k = 0; k < kCopies; ++k) bins[k * kSThreads + tid] = 0;
-    if (tid == 0) {
-      listed = 0;
-      cut = -1;
-    }
+    if (tid == 0) cut = -1;
   }
   __syncthreads();
 #pragma unroll
@@ -269,32 +270,29 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
   const int64_t place = static_cast<int64_t>(r) * a.chunks + c;
   __syncthreads();
   if (filtered) {
-    // the bins of at most kTops tokens together, and these tokens
+    // the bins of at most kTops tokens together, and these tokens bin by bin
     unsigned long long all = 0;
 #pragma unroll
     for (int k = 0; k < kCopies; ++k) all += bins[tid * kCopies + k];
     chunk_bins(a)[place * kBins + tid] = all;
     sum = bin_sum_of(all, tid);
-    int up = wave_scan(static_cast<int>(all >> kSumBits));
+    const int count = static_cast<int>(all >> kSumBits);
+    int up = wave_scan(count);
     if (lane_id() == kWave - 1) scans[wave] = up;
     __syncthreads();
     for (int w = 0; w < wave; ++w) up += scans[w];
+    next[tid] = up - count;
+    if (tid == kBins - 1) tokens = up;
     const uint64_t fits = __ballot(up <= kTops);
     if (lane_id() == 0 && fits) atomicMax(&cut, 64 * wave + 63 - __builtin_clzll(fits));
     __syncthreads();
-    int hits = 0;
-#pragma unroll
-    for (int k = 0; k < kSPer; ++k) hits += any && bin[k] <= cut;
-    int to = wave_scan(hits);
-    int first = 0;
-    if (lane_id() == kWave - 1 && to) first = atomicAdd(&listed, to);
-    to += __builtin_amdgcn_readlane(first, kWave - 1) - hits;
-    if (hits) {
+    if (any) {
       uint64_t* list = chunk_tops(a) + place * kTops;
 #pragma unroll
       for (int k = 0; k < kSPer; ++k)
-        if (bin[k] <= cut) list[to++] = place_of(v[k], i0 + (k / 4) * 4 * kSThreads + k % 4);
+        if (bin[k] <= cut) list[atomicAdd(&next[bin[k]], 1)] = place_of(v[k], i0 + (k / 4) * 4 * kSThreads + k % 4);
     }
+    __syncthreads();
   }
   sum = wave_sum(sum);
   if ((tid & 63) == 0) sums[wave] = sum;
@@ -303,7 +301,9 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
     double all = 0.0;
 #pragma unroll
     for (int w = 0; w < kSWaves; ++w) all += sums[w];
-    chunk_stats(a)[place] = ChunkStat{top, at, all, filtered ? listed : 0, filtered ? cut : -1};
+    const bool lists = filtered && cut >= 0;   // (next has gone on to the end of each listed bin)
+    chunk_stats(a)[place] = ChunkStat{top, at, all, static_cast<int16_t>(lists ? next[cut] : 0), static_cast<int16_t>(lists ? cut : -1),
+                                      filtered ? tokens : 0};
   }
 }
 
@@ -313,24 +313,44 @@ __device__ __forceinline__ double chunk_factor(const Exp2& exp2, float chunk_top
   return weight(exp2, chunk_top, top, rate);
 }
 
+struct Running {                               // sums up to each bin's or cell's end
+  double sum[kBins];
+  int count[kBins];
+};
 struct PickLds {
-  double part_sum[4][kBins];                   // of bins, by quarter of the chunks
-  int part_count[4][kBins];
-  double bin_sum[kBins];                       // of the row's bins, then running sums up to their ends
-  int bin_count[kBins];
-  uint64_t list[kList];
-  double weights[kList];
-  double waves[kDWaves];
+  uint64_t arena[kArena];
+  Running bins, cells;
+  uint64_t few[kRank];
   unsigned long long cell_sum[kBins];
   uint32_t cell_count[kBins];
-  int64_t ahead;
-  double d0, d1, d2;
-  int i0, i1, i2;
+  double waves[kDWaves];
+  int iwaves[kDWaves];
+  int found, n, first, last;
+  double kept;
 };
 struct ChunkShift {                            // of each chunk, in dynamic LDS
-  double factor;                               // from its weights to the row's; below 0: it has none
-  int shift;                                   // from its bins to the row's
-  int pad;
+  union {
+    double factor;                             // from units of its bins to weights of the row's bins; below 0: it has none
+    unsigned long long kept;                   // at the end: of its kept tokens in the border's bin
+  };
+  int16_t shift;                               // from its bins to the row's
+  int16_t cut, listed;                         // of its list
+};
+static_assert(sizeof(ChunkShift) == 16);
+
+// A row at work.
+struct Row {
+  const float* logits;
+  int n;                                       // its number
+  float top;
+  double top_quarter, rate4;
+  Settings s;
+  ChunkStat* stats;
+  const uint64_t* bins;
+  const uint64_t* tops;
+  ChunkShift* chunk;
+  __device__ __forceinline__ int bin(float v) const { return bin_of(v, rate4, top, top_quarter); }
+  __device__ __forceinline__ double weight_of(const Exp2& exp2, float v) const { return weight(exp2, v, top, s.rate); }
 };
 
 // Sum over the workgroup's lanes before this one, and of all.
@@ -350,130 +370,48 @@ __device__ __forceinline__ double block_scan_d(double v, double* lds, double& to
   return before + (up - v);
 }
 
-// Elements of the row whose place is in lo..hi: f(place, value), by all lanes,
-// with eight loads on their way.
-template <class Fn>
-__device__ __forceinline__ void each_between(const SampleArgs& a, const float* row, uint64_t lo, uint64_t hi, Fn f) {
-  constexpr int kAhead = 8;
-  for (int i0 = 4 * static_cast<int>(threadIdx.x); i0 < a.vocab; i0 += 4 * kDThreads * kAhead) {
-    float v[kAhead][4];
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) load_quad(row, i0 + 4 * kDThreads * q, a.vocab, -INFINITY, v[q]);
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float x = taken(v[q][e]);
-        const uint64_t at = place_of(x, i0 + 4 * kDThreads * q + e);
-        if (x > -INFINITY && at >= lo && at <= hi) f(at, x);
-      }
+// Running sums of the first kBins threads' values.
+__device__ __forceinline__ void run_up(double sum, int count, Running& to, PickLds& l) {
+  const int wave = threadIdx.x >> 6;
+  double up = wave_scan(sum);
+  int up_count = wave_scan(count);
+  __syncthreads();
+  if (lane_id() == kWave - 1) {
+    l.waves[wave] = up;
+    l.iwaves[wave] = up_count;
   }
-}
-
-// Ascending, n a power of two; the workgroup.
-__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
-  for (int k = 2; k <= n; k <<= 1)
-    for (int j = k >> 1; j > 0; j >>= 1) {
-      __syncthreads();
-      for (int t = threadIdx.x; t < n / 2; t += kDThreads) {
-        const int i = 2 * t - (t & (j - 1));   // pairs i, i + j
-        const uint64_t x = list[i], y = list[i + j];
-        if ((x > y) == ((i & k) == 0)) {
-          list[i] = y;
-          list[i + j] = x;
-        }
-      }
+  __syncthreads();
+  if (threadIdx.x < kBins) {
+#pragma unroll
+    for (int w = 0; w < kBins / kWave; ++w) {
+      up += w < wave ? l.waves[w] : 0.0;
+      up_count += w < wave ? l.iwaves[w] : 0;
     }
+    to.sum[threadIdx.x] = up;
+    to.count[threadIdx.x] = up_count;
+  }
   __syncthreads();
 }
 
-// The border of a filter among the `count` elements with places lo..hi, before
-// which `ahead` elements of the weight `passed` come: the last place kept by
-// top-k (k > 0: the k-th element) or by top-p (the last before which less than
-// `goal` has passed); `kept`: the weight up to it.
-__device__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const float* row, float top, double rate, uint64_t lo, uint64_t hi,
-                                int64_t count, int64_t ahead, double passed, int k, double goal, PickLds& l, double& kept) {
+// First bin whose running count (k > 0) or sum reaches k or the goal; the
+// last one that has tokens where rounding leaves it unreached.
+__device__ __forceinline__ int crossing(const Running& up, int k, double goal, PickLds& l) {
   const int tid = threadIdx.x;
-  while (count > kList) {
-    // cells of equal width; at the end a cell is one place
-    int shift = 0;
-    while (((hi - lo) >> shift) >= kBins) ++shift;
-    __syncthreads();
-    if (tid < kBins) {
-      l.cell_sum[tid] = 0;
-      l.cell_count[tid] = 0;
-    }
-    __syncthreads();
-    // weights of a row's 2^24 elements at most, in units that their sum stays below 2^63 in
-    int most;
-    (void)__builtin_frexp(weight(exp2, value_at(lo), top, rate), &most);
-    const int unit = 38 - most;
-    each_between(a, row, lo, hi, [&](uint64_t at, float v) QMV_INLINE {
-      const int cell = static_cast<int>((at - lo) >> shift);
-      atomicAdd(&l.cell_sum[cell], static_cast<unsigned long long>(__builtin_ldexp(weight(exp2, v, top, rate), unit) + 0.5));
-      atomicAdd(&l.cell_count[cell], 1u);
-    });
-    __syncthreads();
-    if (tid == 0) {
-      int cell = 0;
-      // where rounding leaves the goal unreached: the last cell that has elements
-      int last = kBins - 1;
-      while (last > 0 && l.cell_count[last] == 0) --last;
-      for (; cell < last; ++cell) {
-        const double sum = __builtin_ldexp(static_cast<double>(l.cell_sum[cell]), -unit);
-        if (l.cell_count[cell] && (k > 0 ? ahead + l.cell_count[cell] >= k : passed + sum >= goal)) break;
-        ahead += l.cell_count[cell];
-        passed += sum;
-      }
-      l.i0 = cell;
-      l.d0 = passed;
-      l.ahead = ahead;
-    }
-    __syncthreads();
-    const uint64_t from = lo + (static_cast<uint64_t>(l.i0) << shift), to = from + ((uint64_t(1) << shift) - 1);
-    lo = from;
-    hi = to < hi ? to : hi;
-    count = l.cell_count[l.i0];
-    ahead = l.ahead;
-    passed = l.d0;
-    __syncthreads();
+  __syncthreads();
+  if (tid == 0) l.found = kBins - 1;
+  __syncthreads();
+  if (tid < kBins) {
+    const int count = up.count[tid];
+    const bool hit = count > 0 && ((k > 0 ? count >= k : up.sum[tid] >= goal) || count == up.count[kBins - 1]);
+    const uint64_t hits = __ballot(hit);
+    if (lane_id() == 0 && hits) atomicMin(&l.found, (tid & ~63) + __builtin_ctzll(hits));
   }
   __syncthreads();
-  if (tid == 0) l.i0 = 0;
-  __syncthreads();
-  each_between(a, row, lo, hi, [&](uint64_t at, float) QMV_INLINE {
-    const int to = atomicAdd(&l.i0, 1);
-    if (to < kList) l.list[to] = at;
-  });
-  __syncthreads();
-  int n = 2;
-  while (n < count) n <<= 1;
-  for (int i = static_cast<int>(count) + tid; i < n; i += kDThreads) l.list[i] = ~uint64_t(0);
-  sort_list(l.list, n);
-  // two neighbours a lane
-  double w[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) w[e] = 2 * tid + e < count ? weight(exp2, value_at(l.list[2 * tid + e]), top, rate) : 0.0;
-  double total;
-  const double before = passed + block_scan_d(w[0] + w[1], l.waves, total);
-  if (tid == 0) l.i1 = 0;
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = 2 * tid + e;
-    const bool in = i < count && (k > 0 ? ahead + i < k : before + (e ? w[0] : 0.0) < goal);
-    if (in) atomicMax(&l.i1, i);
-  }
-  __syncthreads();
-  const int last = l.i1;
-  if (last / 2 == tid) l.d1 = before + w[0] + (last & 1 ? w[1] : 0.0);
-  __syncthreads();
-  kept = l.d1;
-  return l.list[last];
+  return l.found;
 }
 
-// Smallest key whose logit passes, of those up to `most`, which does; one
-// wave, 64 keys at a time.
+// Smallest key whose logit passes, of those up to `most`, which does; a wave
+// for itself, 64 keys at a time.
 template <class Fn>
 __device__ __forceinline__ uint32_t first_key(uint32_t most, Fn passes) {
   uint64_t lo = 0, hi = most;                  // first in lo..hi
@@ -492,83 +430,319 @@ __device__ __forceinline__ uint32_t first_key(uint32_t most, Fn passes) {
   return static_cast<uint32_t>(lo);
 }
 
-// Running sums of the row's bins: of the chunks', each moved to the row's
-// grid. A fourth of the threads takes a fourth of the chunks; chunk bins that
-// the row's last bin takes in are summed by the threads they belong to.
-__device__ __forceinline__ void join_bins(const SampleArgs& a, int r, const ChunkShift* chunk, PickLds& l) {
-  const int tid = threadIdx.x, part = tid / kBins, bin = tid % kBins;
-  const uint64_t* bins = chunk_bins(a) + static_cast<int64_t>(r) * a.chunks * kBins;
-  double sum = 0.0, far_sum = 0.0;
-  int count = 0, far_count = 0;
-#pragma unroll 4
-  for (int c = part; c < a.chunks; c += kDThreads / kBins) {
-    const ChunkShift h = chunk[c];
-    if (h.factor < 0.0) continue;              // uniform in a wave
-    const int from = bin - h.shift;
-    const bool near = from >= 0 && bin < kBins - 1, far = bin + h.shift >= kBins - 1;
-    const uint64_t x = near ? bins[static_cast<int64_t>(c) * kBins + from] : 0, y = far ? bins[static_cast<int64_t>(c) * kBins + bin] : 0;
-    sum += bin_sum_of(x, near ? from : 0) * h.factor;
-    count += static_cast<int>(x >> kSumBits);
-    far_sum += bin_sum_of(y, bin) * h.factor;
-    far_count += static_cast<int>(y >> kSumBits);
-  }
-  // the last bin
-  const double far_wave = wave_sum(far_sum);
-  const int far_wave_count = __builtin_amdgcn_readlane(wave_scan(far_count), kWave - 1);
-  __syncthreads();                             // the row before is done with LDS
-  l.part_sum[part][bin] = sum;
-  l.part_count[part][bin] = count;
-  if (tid < kDWaves) l.cell_count[tid] = 0;
-  __syncthreads();
-  if (lane_id() == 0) {
-    l.waves[tid >> 6] = far_wave;
-    l.cell_count[tid >> 6] = far_wave_count;
-  }
-  __syncthreads();
-  double own = 0.0;
-  int own_count = 0;
-  if (tid < kBins) {
-    own = (l.part_sum[0][tid] + l.part_sum[1][tid]) + (l.part_sum[2][tid] + l.part_sum[3][tid]);
-    own_count = l.part_count[0][tid] + l.part_count[1][tid] + l.part_count[2][tid] + l.part_count[3][tid];
-    if (tid == kBins - 1)
-      for (int w = 0; w < kDWaves; ++w) {
-        own += l.waves[w];
-        own_count += static_cast<int>(l.cell_count[w]);
+// Tokens between two places.
+struct Span {
+  uint64_t lo, hi;
+};
+__device__ __forceinline__ Span bin_span(const Row& row, int b) {
+  const uint32_t most = key_of(row.top);
+  const uint32_t low = first_key(most, [&](float v) QMV_INLINE { return row.bin(v) <= b; });
+  const uint32_t high = b == 0 ? most : first_key(most, [&](float v) QMV_INLINE { return row.bin(v) < b; }) - 1;
+  return Span{first_place(high), last_place(low)};
+}
+
+// Runs of four of the row's values, from i0 on and a step apart, -inf behind
+// its end: all loads before the first use (a branch a run would wait for each).
+template <int N>
+__device__ __forceinline__ void load_runs(const float* row, int i0, int step, int n, float (&v)[N][4]) {
+  const int first = __builtin_amdgcn_readfirstlane(i0);   // (a wave's lanes take 256 values in order)
+  if (first + (N - 1) * step + 4 * kWave <= n) {
+    u32x4 x[N];
+#pragma unroll
+    for (int q = 0; q < N; ++q) x[q] = ld_x4(reinterpret_cast<const uint8_t*>(row + i0 + q * step));
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[q][e] = __uint_as_float(x[q][e]);
+  } else {
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int i = i0 + q * step + e;
+        v[q][e] = row[i < n ? i : n - 1];
       }
+#pragma unroll
+    for (int q = 0; q < N; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[q][e] = i0 + q * step + e < n ? v[q][e] : -INFINITY;
   }
-  double up = wave_scan(own);
-  int up_count = wave_scan(own_count);
-  __syncthreads();
-  if (lane_id() == kWave - 1) {
-    l.waves[tid >> 6] = up;
-    l.cell_count[tid >> 6] = up_count;
+}
+
+// f(place, value) for the row's tokens in a span, by all lanes, with eight
+// loads on their way. Most are outside: their values alone tell.
+template <class Fn>
+__device__ __forceinline__ void each_of_row(const SampleArgs& a, const Row& row, Span g, Fn f) {
+  constexpr int kAhead = 8;
+  const float least = value_at(g.hi), most = value_at(g.lo);
+  for (int i0 = 4 * static_cast<int>(threadIdx.x); i0 < a.vocab; i0 += 4 * kDThreads * kAhead) {
+    float v[kAhead][4];
+    load_runs(row.logits, i0, 4 * kDThreads, a.vocab, v);
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (v[q][e] >= least && v[q][e] <= most) {
+          const float x = taken(v[q][e]);
+          const uint64_t at = place_of(x, i0 + 4 * kDThreads * q + e);
+          if (at >= g.lo && at <= g.hi) f(at, x);
+        }
   }
+}
+
+// The row's tokens in a span, in LDS in any order; their number, `most` at
+// most. A lane marks those of its 32 values first, so that the waves take
+// their places once for all of them (one by one each token would wait for the
+// one before: 47 us for 905 of 128256).
+__device__ __forceinline__ int collect(const SampleArgs& a, const Row& row, Span g, uint64_t* list, int most, PickLds& l) {
+  constexpr int kAhead = 8;
+  const float least = value_at(g.hi), greatest = value_at(g.lo);
+  const bool inside = (g.lo & kLowIndex) != 0 || (g.hi & kLowIndex) != kLowIndex;   // an end among equal logits
   __syncthreads();
-  if (tid < kBins) {
-    for (int w = 0; w < (tid >> 6); ++w) {
-      up += l.waves[w];
-      up_count += static_cast<int>(l.cell_count[w]);
+  if (threadIdx.x == 0) l.n = 0;
+  __syncthreads();
+  for (int i0 = 4 * static_cast<int>(threadIdx.x); i0 - 4 * static_cast<int>(threadIdx.x) < a.vocab; i0 += 4 * kDThreads * kAhead) {
+    float v[kAhead][4];
+    load_runs(row.logits, i0, 4 * kDThreads, a.vocab, v);
+    uint32_t marks = 0;
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) marks |= v[q][e] >= least && v[q][e] <= greatest ? 1u << (4 * q + e) : 0u;
+    if (inside) {                              // uniform
+#pragma unroll
+      for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint64_t at = place_of(taken(v[q][e]), i0 + 4 * kDThreads * q + e);
+          marks &= at < g.lo || at > g.hi ? ~(1u << (4 * q + e)) : ~0u;
+        }
     }
-    l.bin_sum[tid] = up;
-    l.bin_count[tid] = up_count;
+    const int hits = __builtin_popcount(marks), up = wave_scan(hits), all = __builtin_amdgcn_readlane(up, kWave - 1);
+    if (all == 0) continue;
+    int first = 0;
+    if (lane_id() == 0) first = atomicAdd(&l.n, all);
+    int to = __builtin_amdgcn_readfirstlane(first) + up - hits;
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (marks >> (4 * q + e) & 1) {
+          if (to < most) list[to] = place_of(taken(v[q][e]), i0 + 4 * kDThreads * q + e);
+          ++to;
+        }
+  }
+  __syncthreads();
+  return l.n < most ? l.n : most;
+}
+
+// Sorted into `to`, ascending: each goes to the number of those before it.
+__device__ __forceinline__ void sort_few(const uint64_t* list, uint64_t* to, int n, PickLds& l) {
+  const int tid = threadIdx.x;
+  int wide = kWave;
+  while (wide < n) wide <<= 1;
+  const int parts = kDThreads / wide, part = tid / wide, i = tid & (wide - 1), per = (n + parts - 1) / parts;
+  __syncthreads();
+  if (tid < kRank) l.cell_count[tid] = 0;
+  const uint64_t mine = i < n ? list[i] : 0;
+  const int end = (part + 1) * per < n ? (part + 1) * per : n;
+  int before = 0;
+#pragma unroll 4
+  for (int j = part * per; j < end; ++j) before += list[j] < mine;
+  __syncthreads();
+  if (i < n && before) atomicAdd(&l.cell_count[i], static_cast<uint32_t>(before));
+  __syncthreads();
+  if (part == 0 && i < n) to[l.cell_count[i]] = mine;
+  __syncthreads();
+}
+
+// Sorted in place, ascending, n a power of two up to 2 kDThreads * 2. Pairs
+// up to 64 apart stay inside a wave's 128.
+__device__ __forceinline__ void sort_many(uint64_t* list, int n) {
+  int last = 2 * kWave;
+  for (int k = 2; k <= n; k <<= 1)
+    for (int j = k >> 1; j > 0; last = j, j >>= 1) {
+      if (j > kWave || last > kWave) {
+        __syncthreads();
+      } else {
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
+      for (int t = threadIdx.x; t < n / 2; t += kDThreads) {
+        const int i = 2 * t - (t & (j - 1));   // pairs i, i + j
+        const uint64_t x = list[i], y = list[i + j];
+        if ((x > y) == ((i & k) == 0)) {
+          list[i] = y;
+          list[i + j] = x;
+        }
+      }
+    }
+  __syncthreads();
+}
+
+// Running sums of kHalf of the row's bins from `first` on: of the chunks' bins,
+// each moved to the row's grid. Most borders lie in the first half (32
+// octaves), and the other is not read then. A wave takes every eighth chunk, a
+// lane two bins. all, tokens: sum and number of all, where the last bin ends.
+constexpr int kHalf = 2 * kWave;
+__device__ __forceinline__ void join_half(const SampleArgs& a, const Row& row, int half, double all, int tokens, PickLds& l) {
+  constexpr int kAhead = 5;
+  const int wave = threadIdx.x >> 6, lane = lane_id();
+  double sum[2] = {0.0, 0.0};
+  int count[2] = {0, 0};
+  for (int c0 = wave; c0 < a.chunks; c0 += kDWaves * kAhead) {
+    uint64_t x[kAhead][2];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int c = c0 + kDWaves * q < a.chunks ? c0 + kDWaves * q : c0, from = half * kHalf + e * kWave + lane - row.chunk[c].shift;
+        x[q][e] = row.bins[static_cast<int64_t>(c) * kBins + (from > 0 ? from : 0)];
+      }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int c = c0 + kDWaves * q;
+      if (c >= a.chunks) continue;             // uniform
+      const ChunkShift h = row.chunk[c];
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (h.factor >= 0.0 && half * kHalf + e * kWave + lane >= h.shift) {
+          sum[e] = fma(bin_units(x[q][e]), h.factor, sum[e]);
+          count[e] += static_cast<int>(x[q][e] >> kSumBits);
+        }
+    }
+  }
+  double* sums = reinterpret_cast<double*>(l.arena);
+  int* counts = reinterpret_cast<int*>(l.arena + kDWaves * kHalf);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    sums[wave * kHalf + e * kWave + lane] = sum[e];
+    counts[wave * kHalf + e * kWave + lane] = count[e];
+  }
+  __syncthreads();
+  if (wave == 0) {
+    double run = half ? l.bins.sum[kHalf - 1] : 0.0;
+    int run_count = half ? l.bins.count[kHalf - 1] : 0;
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int i = e * kWave + lane, bin = half * kHalf + i;
+      double one = 0.0;
+      int n = 0;
+#pragma unroll
+      for (int w = 0; w < kDWaves; ++w) {
+        one += sums[w * kHalf + i];
+        n += counts[w * kHalf + i];
+      }
+      one = wave_scan(one * bin_scale(bin)) + run;
+      n = wave_scan(n) + run_count;
+      l.bins.sum[bin] = bin == kBins - 1 ? all : one;
+      l.bins.count[bin] = bin == kBins - 1 ? tokens : n;
+      run = __shfl(one, kWave - 1);
+      run_count = __builtin_amdgcn_readlane(n, kWave - 1);
+    }
   }
   __syncthreads();
 }
 
-// First bin whose running count (k > 0) or sum reaches k or the goal; the
-// last one that has tokens where none does.
-__device__ __forceinline__ int crossing(const PickLds& l, int k, double goal, int* slot) {
-  const int tid = threadIdx.x;
-  if (tid == 0) *slot = kBins;
-  __syncthreads();
-  if (tid < kBins) {
-    const int count = l.bin_count[tid], all = l.bin_count[kBins - 1];
-    const bool hit = (k > 0 ? count >= k : l.bin_sum[tid] >= goal) || count == all;
-    const uint64_t hits = __ballot(hit && count > 0);
-    if (lane_id() == 0 && hits) atomicMin(slot, (tid & ~63) + __builtin_ctzll(hits));
+// First bin of the first half whose running count (k > 0) or sum reaches k or
+// the goal, kHalf where none does; every wave for itself.
+__device__ __forceinline__ int crossing_near(const Running& up, int k, double goal) {
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int i = e * kWave + lane_id(), count = up.count[i];
+    const uint64_t hits = __ballot(count > 0 && (k > 0 ? count >= k : up.sum[i] >= goal));
+    if (hits) return e * kWave + __builtin_ctzll(hits);
   }
+  return kHalf;
+}
+
+// The border of a filter in a bin: the last place kept by top-k (k > 0: the
+// k-th token) or by top-p (the last before which less than `goal` has passed);
+// kept: the weight up to it; listed: how many of the bin's tokens the arena
+// holds, which are all of them or 0. The span is cut into cells of equal
+// width until few tokens are left in one.
+__device__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const Row& row, int b, int k, double goal, PickLds& l, double& kept,
+                                int& listed) {
+  const int tid = threadIdx.x;
+  Span g = bin_span(row, b);
+  int ahead = b > 0 ? l.bins.count[b - 1] : 0, count = l.bins.count[b] - ahead;
+  double passed = b > 0 ? l.bins.sum[b - 1] : 0.0;
+  uint64_t* list = l.arena;
+  int n = count <= kArena ? collect(a, row, g, list, kArena, l) : 0;
+  listed = n;
+  while (count > kRank) {
+    int shift = 0;
+    while (((g.hi - g.lo) >> shift) >= kBins) ++shift;
+    __syncthreads();
+    if (tid < kBins) {
+      l.cell_sum[tid] = 0;
+      l.cell_count[tid] = 0;
+    }
+    __syncthreads();
+    // 2^24 tokens at most, none above the weight of the first place
+    int most;
+    (void)__builtin_frexp(row.weight_of(exp2, value_at(g.lo)), &most);
+    const auto add = [&](uint64_t at, float v) QMV_INLINE {
+      const int cell = static_cast<int>((at - g.lo) >> shift);
+      const double w = __builtin_ldexp(row.weight_of(exp2, v), kUnit - most) + 0x1p52;
+      atomicAdd(&l.cell_sum[cell], static_cast<unsigned long long>(__double_as_longlong(w) & ((1ll << 52) - 1)));
+      atomicAdd(&l.cell_count[cell], 1u);
+    };
+    if (n) {
+      for (int i = tid; i < n; i += kDThreads) {
+        const uint64_t at = list[i];
+        if (at >= g.lo && at <= g.hi) add(at, value_at(at));
+      }
+    } else {
+      each_of_row(a, row, g, add);
+    }
+    __syncthreads();
+    run_up(tid < kBins ? __builtin_ldexp(static_cast<double>(l.cell_sum[tid]), most - kUnit) : 0.0,
+           tid < kBins ? static_cast<int>(l.cell_count[tid]) : 0, l.cells, l);
+    const int cell = crossing(l.cells, k > 0 ? k - ahead : 0, goal - passed, l);
+    const int before = cell > 0 ? l.cells.count[cell - 1] : 0;
+    g.lo += static_cast<uint64_t>(cell) << shift;
+    const uint64_t end = g.lo + ((uint64_t(1) << shift) - 1);
+    g.hi = end < g.hi ? end : g.hi;
+    passed += cell > 0 ? l.cells.sum[cell - 1] : 0.0;
+    ahead += before;
+    count = l.cells.count[cell] - before;
+    if (!n && count <= kArena && count > kRank) n = collect(a, row, g, list, kArena, l);
+  }
+  // the few, sorted in the cells' place
+  uint64_t* few = l.few;
+  uint64_t* sorted = reinterpret_cast<uint64_t*>(l.cells.sum);
+  if (n) {
+    __syncthreads();
+    if (tid == 0) l.n = 0;
+    __syncthreads();
+    for (int i = tid; i < n; i += kDThreads) {
+      const uint64_t at = list[i];
+      if (at >= g.lo && at <= g.hi) {
+        const int to = atomicAdd(&l.n, 1);
+        if (to < kRank) few[to] = at;
+      }
+    }
+    __syncthreads();
+  } else {
+    collect(a, row, g, few, kRank, l);
+  }
+  const int m = l.n < kRank ? l.n : kRank;
+  sort_few(few, sorted, m, l);
+  const uint64_t mine = tid < m ? sorted[tid] : 0;
+  const double w = tid < m ? row.weight_of(exp2, value_at(mine)) : 0.0;
+  double total;
+  const double before = passed + block_scan_d(w, l.waves, total);
+  if (tid == 0) l.last = 0;
   __syncthreads();
-  return *slot;
+  const uint64_t ins = __ballot(tid < m && (k > 0 ? ahead + tid < k : before < goal));
+  if (lane_id() == 0 && ins) atomicMax(&l.last, (tid & ~63) + 63 - __builtin_clzll(ins));
+  __syncthreads();
+  const int last = l.last;                     // the first one in any case
+  if (tid == last) l.kept = before + w;
+  __syncthreads();
+  kept = l.kept;
+  return sorted[last];
 }
 
 // Where a row's draw stands.
@@ -578,134 +752,229 @@ struct Drawn {
   int token;
 };
 
-// All `count` tokens up to the border's bin, in LDS: sorted, cut by all
-// filters, and drawn from. all: the sum of the row's weights.
-__device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Settings& s, float top, int count, double all, float u, PickLds& l) {
-  const int tid = threadIdx.x;
-  int n = 2;
-  while (n < count) n <<= 1;
-  for (int i = count + tid; i < n; i += kDThreads) l.list[i] = ~uint64_t(0);
-  sort_list(l.list, n);
-  double w[2], total;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) w[e] = 2 * tid + e < count ? weight(exp2, value_at(l.list[2 * tid + e]), top, s.rate) : 0.0;
+// All `count` tokens (kList at most) up to the border's bin, in the arena:
+// sorted, cut by all filters, and drawn from. all: the sum of the row's weights.
+__device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Row& row, int count, double all, float u, PickLds& l) {
+  constexpr int kPer = kList / kDThreads;
+  const int tid = threadIdx.x, i0 = kPer * tid;
+  const Settings& s = row.s;
+  double* weights = reinterpret_cast<double*>(l.arena + 2 * kList);
+  const auto sorted_list = [&](int n) QMV_INLINE {   // of the arena's first n
+    if (n <= kRank) {
+      sort_few(l.arena, l.arena + kList, n, l);
+      return l.arena + kList;
+    }
+    int wide = kRank;
+    while (wide < n) wide <<= 1;
+    for (int i = n + tid; i < wide; i += kDThreads) l.arena[i] = ~uint64_t(0);
+    sort_many(l.arena, wide);
+    return l.arena;
+  };
+  const uint64_t* list = sorted_list(count);
   const int k = s.k > 0 && s.k < count ? s.k : count;
+  uint64_t at[kPer];
+  double w[kPer], own = 0.0, total;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) w[e] = 2 * tid + e < k ? w[e] : 0.0;
-  const double before = block_scan_d(w[0] + w[1], l.waves, total);
+  for (int e = 0; e < kPer; ++e) {
+    at[e] = i0 + e < k ? list[i0 + e] : 0;
+    w[e] = i0 + e < k ? row.weight_of(exp2, value_at(at[e])) : 0.0;
+    own += w[e];
+  }
+  double before = block_scan_d(own, l.waves, total);
   const double goal = s.p * (s.k > 0 ? total : all);
-  if (tid == 0) l.i0 = 0;
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = 2 * tid + e;
-    const bool in = i < k && (s.p >= 1.0 || before + (e ? w[0] : 0.0) < goal) && w[e] >= s.m;
-    const uint64_t ins = __ballot(in);
-    if (ins && lane_id() == 63 - __builtin_clzll(ins)) atomicMax(&l.i0, i);
-  }
-  __syncthreads();
-  const int last = l.i0;                       // the first token is kept in any case
-  Drawn d;
-  d.border = l.list[last];
-  // the kept ones by their indices
-  n = 2;
-  while (n < last + 1) n <<= 1;
-  __syncthreads();
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = 2 * tid + e;
-    if (i < n) {
-      l.weights[i] = w[e];
-      l.list[i] = i <= last ? (l.list[i] & kLowIndex) << 12 | static_cast<uint64_t>(i) : ~uint64_t(0);
-    }
-  }
-  sort_list(l.list, n);
-  int index[2] = {-1, -1};
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int i = 2 * tid + e;
-    w[e] = 0.0;
-    if (i <= last) {
-      const uint64_t x = l.list[i];
-      w[e] = l.weights[x & 4095];
-      index[e] = static_cast<int>(x >> 12);
-    }
-  }
-  const double up = block_scan_d(w[0] + w[1], l.waves, d.total);
   if (tid == 0) {
-    l.i0 = 0x7fffffff;
-    l.i1 = -1;
+    l.last = 0;
+    l.first = 0x7fffffff;
+    l.found = -1;
   }
   __syncthreads();
-  const double drawn = static_cast<double>(u) * d.total;
-  const bool hit0 = w[0] > 0.0 && up + w[0] > drawn, hit1 = w[1] > 0.0 && up + w[0] + w[1] > drawn;
-  const uint64_t hits = __ballot(hit0 || hit1), some = __ballot(w[0] > 0.0 || w[1] > 0.0);
-  if (hits && lane_id() == __builtin_ctzll(hits)) atomicMin(&l.i0, 2 * tid + (hit0 ? 0 : 1));
-  if (some && lane_id() == 63 - __builtin_clzll(some)) atomicMax(&l.i1, 2 * tid + (w[1] > 0.0 ? 1 : 0));
+  int in = -1;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    if (i0 + e < k && (s.p >= 1.0 || before < goal) && w[e] >= s.m) in = i0 + e;
+    before += w[e];
+  }
+  const uint64_t ins = __ballot(in >= 0);
+  if (ins && lane_id() == 63 - __builtin_clzll(ins)) atomicMax(&l.last, in);
   __syncthreads();
-  const int take = l.i0 != 0x7fffffff ? l.i0 : l.i1;
-  const uint64_t x = l.list[take];
+  const int last = l.last;                     // the first token is kept in any case
+  Drawn d;
+  d.border = list[last];
+  __syncthreads();
+  // the kept ones by their indices
+#pragma unroll
+  for (int e = 0; e < kPer; ++e)
+    if (i0 + e <= last) {
+      weights[i0 + e] = w[e];
+      l.arena[i0 + e] = (at[e] & kLowIndex) << 12 | static_cast<uint64_t>(i0 + e);
+    }
+  __syncthreads();
+  list = sorted_list(last + 1);
+  own = 0.0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    w[e] = i0 + e <= last ? weights[list[i0 + e] & 4095] : 0.0;
+    own += w[e];
+  }
+  double up = block_scan_d(own, l.waves, d.total);
+  const double drawn = static_cast<double>(u) * d.total;
+  int hit = -1, some = -1;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    up += w[e];
+    if (w[e] > 0.0) {
+      some = i0 + e;
+      hit = hit < 0 && up > drawn ? i0 + e : hit;
+    }
+  }
+  const uint64_t hits = __ballot(hit >= 0), somes = __ballot(some >= 0);
+  if (hits && lane_id() == __builtin_ctzll(hits)) atomicMin(&l.first, hit);
+  if (somes && lane_id() == 63 - __builtin_clzll(somes)) atomicMax(&l.found, some);
+  __syncthreads();
+  const uint64_t x = list[l.first != 0x7fffffff ? l.first : l.found];
   d.token = static_cast<int>(x >> 12);
-  d.chosen = l.weights[x & 4095] / d.total;
+  d.chosen = weights[x & 4095] / d.total;
   return d;
 }
 
-// The border by all filters, of a row with more tokens up to it than fit LDS.
-__device__ uint64_t far_border(const SampleArgs& a, const Exp2& exp2, const float* row, const Settings& s, float top, PickLds& l) {
-  const int tid = threadIdx.x;
-  const double top_quarter = quarter(top, 4.0 * s.rate);
-  const uint32_t most = key_of(top);
+// The same of at most 64 tokens, by one wave: each lane has a token.
+__device__ __forceinline__ Drawn draw_wave(const Exp2& exp2, const Row& row, int count, double all, float u, uint64_t* list) {
+  const Settings& s = row.s;
+  const int lane = lane_id();
+  const auto sorted = [&](uint64_t mine, int n) QMV_INLINE {   // the lane's of n in list
+    int before = 0;
+#pragma unroll 8
+    for (int j = 0; j < n; ++j) before += list[j] < mine;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (lane < n) list[before] = mine;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    return lane < n ? list[lane] : 0;
+  };
+  const uint64_t at = sorted(lane < count ? list[lane] : 0, count);
+  const int k = s.k > 0 && s.k < count ? s.k : count;
+  double w = lane < k ? row.weight_of(exp2, value_at(at)) : 0.0;
+  double up = wave_scan(w);
+  const double goal = s.p * (s.k > 0 ? __shfl(up, kWave - 1) : all);
+  const uint64_t ins = __ballot(lane < k && (s.p >= 1.0 || up - w < goal) && w >= s.m) | 1;   // the first in any case
+  const int last = 63 - __builtin_clzll(ins);
+  Drawn d;
+  d.border = __shfl(at, last);
+  // the kept ones by their indices
+  const uint64_t mine = lane <= last ? (at & kLowIndex) << 6 | static_cast<uint64_t>(lane) : 0;
+  if (lane <= last) list[lane] = mine;
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  const uint64_t x = sorted(mine, last + 1);
+  w = __shfl(w, static_cast<int>(x & 63));
+  w = lane <= last ? w : 0.0;
+  up = wave_scan(w);
+  d.total = __shfl(up, kWave - 1);
+  const uint64_t hits = __ballot(w > 0.0 && up > static_cast<double>(u) * d.total), some = __ballot(w > 0.0);
+  const int take = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(some);
+  d.token = static_cast<int>(__shfl(x, take) >> 6);
+  d.chosen = __shfl(w, take) / d.total;
+  return d;
+}
+
+// The border by all filters, of a row with more tokens up to it than kList.
+// listed: tokens of bin `of` that the arena holds.
+__device__ uint64_t far_border(const SampleArgs& a, const Exp2& exp2, const Row& row, PickLds& l, int& listed, int& of) {
+  const Settings& s = row.s;
   uint64_t border = ~uint64_t(0);
-  if (s.m > 0.0)                               // every wave for itself
-    border = last_place(first_key(most, [&](float v) QMV_INLINE { return weight(exp2, v, top, s.rate) >= s.m; }));
-  double total = l.bin_sum[kBins - 1];
+  listed = 0;
+  of = -1;
+  double total = l.bins.sum[kBins - 1];
   for (int turn = 0; turn < 2; ++turn) {       // top-k, then top-p
-    if (turn == 0 ? s.k == 0 || s.k >= l.bin_count[kBins - 1] : s.p >= 1.0) continue;   // uniform
+    if (turn == 0 ? s.k == 0 || s.k >= l.bins.count[kBins - 1] : s.p >= 1.0) continue;   // uniform
     const int k = turn == 0 ? s.k : 0;
     const double goal = s.p * total;
-    const int b = crossing(l, k, goal, &l.i2);
-    const int ahead = b > 0 ? l.bin_count[b - 1] : 0, count = l.bin_count[b] - ahead;
-    const double passed = b > 0 ? l.bin_sum[b - 1] : 0.0;
-    const uint32_t low = first_key(most, [&](float v) QMV_INLINE { return bin_of(v, 4.0 * s.rate, top, top_quarter) <= b; });
-    const uint32_t high = b == 0 ? most : first_key(most, [&](float v) QMV_INLINE { return bin_of(v, 4.0 * s.rate, top, top_quarter) < b; }) - 1;
+    const int b = crossing(l.bins, k, goal, l);
     double kept;
-    const uint64_t found = find_border(a, exp2, row, top, s.rate, first_place(high), last_place(low), count, ahead, passed, k, goal, l, kept);
+    const uint64_t found = find_border(a, exp2, row, b, k, goal, l, kept, listed);
+    of = b;
     if (turn == 0) total = kept;
     border = found < border ? found : border;
     __syncthreads();
   }
-  (void)tid;
+  if (s.m > 0.0) {                             // every wave for itself
+    const uint64_t least =
+        last_place(first_key(key_of(row.top), [&](float v) QMV_INLINE { return row.weight_of(exp2, v) >= s.m; }));
+    border = least < border ? least : border;
+  }
   return border;
 }
 
-// The kept weights of each chunk, and a draw by them: the chunk in which the
-// running sum passes the goal, then its element.
-__device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2, const float* row, ChunkStat* st, const Settings& s, float top,
-                                           uint64_t border, float u, PickLds& l) {
+// The kept weights of each chunk, in its stats.
+__device__ __forceinline__ void kept_sums(const SampleArgs& a, const Exp2& exp2, const Row& row, uint64_t border, int listed, int of, PickLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
-  Drawn d{border, 0.0, 0.0, -1};
-  __syncthreads();
-  if (border != ~uint64_t(0)) {
+  if (border == ~uint64_t(0)) {
+    for (int c = tid; c < a.chunks; c += kDThreads) row.stats[c].sum *= chunk_factor(exp2, row.stats[c].top, row.top, row.s.rate);
+    __syncthreads();
+    return;
+  }
+  const int b = row.bin(value_at(border)), count = l.bins.count[b] - (b > 0 ? l.bins.count[b - 1] : 0);
+  if (count > kArena) {                        // no list of that bin: the row again
     for (int c = wave; c < a.chunks; c += kDWaves) {
       double sum = 0.0;
-#pragma unroll 4
-      for (int j = 0; j < kChunk / (4 * kWave); ++j) {
-        const int i = c * kChunk + 4 * (j * kWave + lane_id());
-        float v[4];
-        load_quad(row, i, a.vocab, -INFINITY, v);
+      for (int j = 0; j < kChunk / (4 * kWave); j += 8) {
+        const int i0 = c * kChunk + 4 * (j * kWave + lane_id());
+        float v[8][4];
+        load_runs(row.logits, i0, 4 * kWave, a.vocab, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x = taken(v[e]);
-          if (place_of(x, i + e) <= border) sum += weight(exp2, x, top, s.rate);
-        }
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float x = taken(v[q][e]);
+            if (place_of(x, i0 + 4 * kWave * q + e) <= border) sum += row.weight_of(exp2, x);
+          }
       }
       sum = wave_sum(sum);
-      if (lane_id() == 0) st[c].sum = sum;
+      if (lane_id() == 0) row.stats[c].sum = sum;
     }
-  } else {
-    for (int c = tid; c < a.chunks; c += kDThreads) st[c].sum *= chunk_factor(exp2, st[c].top, top, s.rate);
+    __syncthreads();
+    return;
+  }
+  // the bins before the border's, and the tokens in that
+  const int n = of == b ? listed : collect(a, row, bin_span(row, b), l.arena, kArena, l);
+  for (int c = wave; c < a.chunks; c += kDWaves) {
+    const ChunkShift h = row.chunk[c];
+    double sum = 0.0;
+    if (h.factor >= 0.0) {
+#pragma unroll
+      for (int j = 0; j < kBins / kWave; ++j) {
+        const int at = j * kWave + lane_id();
+        const uint64_t x = row.bins[static_cast<int64_t>(c) * kBins + at];
+        sum += at + h.shift < b ? bin_units(x) * bin_scale(at + h.shift) : 0.0;
+      }
+      sum = wave_sum(sum) * h.factor;
+    }
+    if (lane_id() == 0) row.stats[c].sum = sum;
   }
   __syncthreads();
+  for (int c = tid; c < a.chunks; c += kDThreads) row.chunk[c].kept = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kDThreads) {
+    const uint64_t at = l.arena[i];
+    if (at <= border) {
+      const double w = __builtin_ldexp(row.weight_of(exp2, value_at(at)), kUnit + (b >> 2)) + 0x1p52;
+      atomicAdd(&row.chunk[(at & kLowIndex) / kChunk].kept, static_cast<unsigned long long>(__double_as_longlong(w) & ((1ll << 52) - 1)));
+    }
+  }
+  __syncthreads();
+  for (int c = tid; c < a.chunks; c += kDThreads)
+    row.stats[c].sum += __builtin_ldexp(static_cast<double>(row.chunk[c].kept), -(kUnit + (b >> 2)));
+  __syncthreads();
+}
+
+// A draw by the chunks' kept weights: the chunk in which the running sum
+// passes the goal, then its element.
+__device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2, const Row& row, uint64_t border, float u, PickLds& l) {
+  constexpr int kPer = kChunk / kDThreads;
+  const int tid = threadIdx.x;
+  const ChunkStat* st = row.stats;
+  Drawn d{border, 0.0, 0.0, -1};
   double sum = 0.0;
   for (int c = lane_id(); c < a.chunks; c += kWave) sum += st[c].sum;
   d.total = wave_sum(sum);
@@ -731,140 +1000,176 @@ __device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2
   }
   const int c = found >= 0 ? found : last;
   if (found < 0) before = last_before;
-  // its elements, a run of four a lane
-  const int i0 = c * kChunk + 4 * tid;
-  float v[4];
-  double w[4], own = 0.0;
-  load_quad(row, i0, a.vocab, -INFINITY, v);
+  // its elements, a run of eight a lane
+  const int i0 = c * kChunk + kPer * tid;
+  float v[kPer];
+  double w[kPer], own = 0.0, all;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    const float x = taken(v[e]);
-    w[e] = place_of(x, i0 + e) <= border ? weight(exp2, x, top, s.rate) : 0.0;
+  for (int q = 0; q < kPer; q += 4) {
+    float four[4];
+    load_quad(row.logits, i0 + q, a.vocab, -INFINITY, four);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[q + e] = taken(four[e]);
+  }
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    w[e] = place_of(v[e], i0 + e) <= border ? row.weight_of(exp2, v[e]) : 0.0;
     own += w[e];
   }
-  double all;
   double up = before + block_scan_d(own, l.waves, all);
   if (tid == 0) {
-    l.i0 = 0x7fffffff;
-    l.i1 = -1;
+    l.first = 0x7fffffff;
+    l.found = -1;
   }
   __syncthreads();
-  int hit = 0x7fffffff, last_hit = -1;
+  int hit = 0x7fffffff, some = -1;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
+  for (int e = 0; e < kPer; ++e) {
     up += w[e];
     if (w[e] > 0.0) {
-      last_hit = i0 + e;
+      some = i0 + e;
       if (up > goal && hit == 0x7fffffff) hit = i0 + e;
     }
   }
-  if (hit != 0x7fffffff) atomicMin(&l.i0, hit);
-  if (last_hit >= 0) atomicMax(&l.i1, last_hit);
+  if (hit != 0x7fffffff) atomicMin(&l.first, hit);
+  if (some >= 0) atomicMax(&l.found, some);
   __syncthreads();
-  d.token = l.i0 != 0x7fffffff ? l.i0 : l.i1;
-  if (d.token >= 0) d.chosen = weight(exp2, taken(row[d.token]), top, s.rate) / d.total;
+  d.token = l.first != 0x7fffffff ? l.first : l.found;
+  if (d.token >= 0) d.chosen = row.weight_of(exp2, taken(row.logits[d.token])) / d.total;
   return d;
 }
 
-// The tokens of bins 0..b in l.list: from the chunks' lists, or from the row
-// where a chunk lists fewer. Returns their number.
-__device__ __forceinline__ int gather(const SampleArgs& a, const float* row, int r, const Settings& s, float top, int b, const ChunkShift* chunk,
-                                      PickLds& l) {
+// The tokens of bins 0..b (kList at most) in the arena: from the chunks'
+// lists, or from the row where a chunk lists fewer. Returns their number.
+__device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int b, PickLds& l) {
+  constexpr int kAhead = 5;                    // lists on their way
   const int tid = threadIdx.x, wave = tid >> 6;
-  const ChunkStat* st = chunk_stats(a) + static_cast<int64_t>(r) * a.chunks;
-  const double top_quarter = quarter(top, 4.0 * s.rate);
   bool covered = true;
-  for (int c = tid; c < a.chunks; c += kDThreads)
-    if (chunk[c].factor >= 0.0 && st[c].cut < kBins - 1 && (b == kBins - 1 || st[c].cut + chunk[c].shift < b)) covered = false;
-  if (tid == 0) l.i0 = 0;
-  if (__syncthreads_and(covered)) {
-    for (int c = wave; c < a.chunks; c += kDWaves) {
-      if (chunk[c].factor < 0.0 || chunk[c].shift > b) continue;
-      const uint64_t* list = chunk_tops(a) + (static_cast<int64_t>(r) * a.chunks + c) * kTops;
-      const int listed = st[c].listed;
+  for (int c = tid; c < a.chunks; c += kDThreads) {
+    const ChunkShift h = row.chunk[c];
+    if (h.factor >= 0.0 && h.cut < kBins - 1 && (b == kBins - 1 || h.cut + h.shift < b)) covered = false;
+  }
+  if (tid == 0) l.n = 0;
+  if (!__syncthreads_and(covered)) {
+    Span all = bin_span(row, b);
+    all.lo = first_place(key_of(row.top));
+    return collect(a, row, all, l.arena, kList, l);
+  }
+  for (int c0 = wave; c0 < a.chunks; c0 += kDWaves * kAhead) {
+    uint64_t x[kAhead];
+    const auto entry = [&](int c, int i) QMV_INLINE { return row.tops[static_cast<int64_t>(c) * kTops + i]; };
 #pragma unroll
-      for (int j = 0; j < kTops / kWave; ++j) {
-        const int i = j * kWave + lane_id();
-        const uint64_t x = i < listed ? list[i] : 0;
-        const bool in = i < listed && bin_of(value_at(x), 4.0 * s.rate, top, top_quarter) <= b;
+    for (int q = 0; q < kAhead; ++q) x[q] = entry(c0 + kDWaves * q < a.chunks ? c0 + kDWaves * q : c0, lane_id());
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int c = c0 + kDWaves * q;
+      if (c >= a.chunks) continue;             // uniform
+      const ChunkShift h = row.chunk[c];
+      const int listed = h.factor >= 0.0 && h.shift <= b ? h.listed : 0;
+      for (int i = lane_id(), more = listed; more > 0; more -= kWave, i += kWave) {
+        if (i != lane_id()) x[q] = i < listed ? entry(c, i) : 0;
+        const bool in = i < listed && row.bin(value_at(x[q])) <= b;
         const uint64_t ins = __ballot(in);
-        if (ins == 0) continue;
+        if (ins == 0) break;
         int first = 0;
-        if (lane_id() == 0) first = atomicAdd(&l.i0, __builtin_popcountll(ins));
-        first = __builtin_amdgcn_readfirstlane(first);
-        const int at = first + __builtin_popcountll(ins & ((uint64_t(1) << lane_id()) - 1));
-        if (in && at < kList) l.list[at] = x;
+        if (lane_id() == 0) first = atomicAdd(&l.n, __builtin_popcountll(ins));
+        const int at = __builtin_amdgcn_readfirstlane(first) + __builtin_popcountll(ins & ((uint64_t(1) << lane_id()) - 1));
+        if (in && at < kList) l.arena[at] = x[q];
+        if (~ins) break;                       // the list goes bin by bin
       }
     }
-  } else {
-    const uint32_t low = first_key(key_of(top), [&](float v) QMV_INLINE { return bin_of(v, 4.0 * s.rate, top, top_quarter) <= b; });
-    each_between(a, row, 0, last_place(low), [&](uint64_t at, float) QMV_INLINE {
-      const int to = atomicAdd(&l.i0, 1);
-      if (to < kList) l.list[to] = at;
-    });
   }
   __syncthreads();
-  const int n = l.i0 < kList ? l.i0 : kList;
-  __syncthreads();
-  return n;
+  return l.n < kList ? l.n : kList;
 }
 
 __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
   __shared__ PickLds l;
   extern __shared__ __align__(16) uint8_t dynamic[];
-  ChunkShift* chunk = reinterpret_cast<ChunkShift*>(dynamic);
   const Exp2 exp2;
-  const int tid = threadIdx.x;
-  const int r = blockIdx.x;
-  const Settings s = settings_of(a, r);
-  const float* row = a.logits + r * a.ldl;
+  const int tid = threadIdx.x, r = blockIdx.x;
+  Row row;
+  row.s = settings_of(a, r);
+  row.n = r;
+  row.logits = a.logits + r * a.ldl;
+  row.stats = chunk_stats(a) + static_cast<int64_t>(r) * a.chunks;
+  row.bins = chunk_bins(a) + static_cast<int64_t>(r) * a.chunks * kBins;
+  row.tops = chunk_tops(a) + static_cast<int64_t>(r) * a.chunks * kTops;
+  row.chunk = reinterpret_cast<ChunkShift*>(dynamic);
+  row.rate4 = 4.0 * row.s.rate;
   const float u = a.u ? a.u[r] : 0.0f;
-  ChunkStat* st = chunk_stats(a) + static_cast<int64_t>(r) * a.chunks;
   float top = -INFINITY;
   int at = 0x7fffffff;
-  if (!s.none) {
-    for (int c = lane_id(); c < a.chunks; c += kWave) take_top(top, at, st[c].top, st[c].at);
+  if (!row.s.none) {
+    for (int c = lane_id(); c < a.chunks; c += kWave) take_top(top, at, row.stats[c].top, row.stats[c].at);
     wave_top(top, at);
   }
+  row.top = top;
+  row.top_quarter = quarter(top, row.rate4);
   Drawn d{0, 0.0, 0.0, -1};
-  if (top == -INFINITY) {                    // uniform
-  } else if (s.greedy) {
+  if (top == -INFINITY) {                      // uniform
+  } else if (row.s.greedy) {
     d = Drawn{place_of(top, at), 1.0, 1.0, at};
-  } else if (!s.filtered()) {
-    d = draw_long(a, exp2, row, st, s, top, ~uint64_t(0), u, l);
+  } else if (!row.s.filtered()) {
+    kept_sums(a, exp2, row, ~uint64_t(0), 0, -1, l);
+    d = draw_long(a, exp2, row, ~uint64_t(0), u, l);
   } else {
-    const double top_quarter = quarter(top, 4.0 * s.rate);
-    for (int c = tid; c < a.chunks; c += kDThreads) {
-      const float ct = st[c].top;
-      const bool has = ct > -INFINITY && (top < INFINITY || ct == top);
-      const int shift = has && top < INFINITY ? bins_between(top_quarter, quarter(ct, 4.0 * s.rate), kBins) : 0;
-      chunk[c] = ChunkShift{has ? chunk_factor(exp2, ct, top, s.rate) : -1.0, shift, 0};
+    double all = 0.0;                          // of the weights, in every wave
+    int tokens = 0;
+    for (int c = lane_id(); c < a.chunks; c += kWave) {
+      const ChunkStat st = row.stats[c];
+      const bool has = st.top > -INFINITY && (top < INFINITY || st.top == top);
+      const double factor = has ? chunk_factor(exp2, st.top, top, row.s.rate) : 0.0;
+      all += st.sum * factor;
+      tokens += has ? st.tokens : 0;
+      if (tid < kWave) {
+        ChunkShift h;
+        const int shift = has && top < INFINITY ? bins_between(row.top_quarter, quarter(st.top, row.rate4), kBins) : 0;
+        h.factor = has ? __builtin_ldexp(factor, -kUnit) * bin_scale(-shift) : -1.0;
+        h.shift = static_cast<int16_t>(shift);
+        h.cut = st.cut;
+        h.listed = st.listed;
+        row.chunk[c] = h;
+      }
     }
+    all = wave_sum(all);
+    tokens = __builtin_amdgcn_readlane(wave_scan(tokens), kWave - 1);
     __syncthreads();
-    join_bins(a, r, chunk, l);
+    join_half(a, row, 0, all, tokens, l);
     // the last bin that can hold the border
-    const double all = l.bin_sum[kBins - 1];
-    int b = kBins - 1;
-    if (s.k > 0) b = crossing(l, s.k, 0.0, &l.i2);
-    else if (s.p < 1.0) b = crossing(l, 0, s.p * all, &l.i2);
-    if (s.m > 0.0 && (s.k == 0 || s.p >= 1.0)) {   // (top-p needs the sum of all k)
-      // w >= m ends in the bin of 4 log2(m), to one by rounding, behind the top's
-      const double end = 4.0 * -log2(s.m) + 2.0;
-      if (end < b) b = static_cast<int>(end);
+    const bool by_weight = row.s.m > 0.0 && (row.s.k == 0 || row.s.p >= 1.0);   // (top-p needs the sum of all k)
+    // w >= m ends in the bin of 4 log2(m), to one by rounding, behind the top's
+    const int end = by_weight ? static_cast<int>(fmin(4.0 * -log2(row.s.m) + 2.0, kBins - 1.0)) : kBins - 1;
+    int b = row.s.k > 0 || row.s.p < 1.0 ? crossing_near(l.bins, row.s.k, row.s.p * all) : kHalf;
+    b = b < end ? b : end;
+    bool joined = false;
+    if (b >= kHalf) {
+      join_half(a, row, 1, all, tokens, l);
+      joined = true;
+      b = kBins - 1;
+      if (row.s.k > 0 || row.s.p < 1.0) b = crossing(l.bins, row.s.k, row.s.p * all, l);
+      b = b < end ? b : end;
     }
-    __syncthreads();
-    if (l.bin_count[b] <= kList) {
-      const int n = gather(a, row, r, s, top, b, chunk, l);
-      d = draw_short(exp2, s, top, n, all, u, l);
+    const int up = l.bins.count[b];
+    if (up <= kList) {
+      const int n = gather(a, row, b, l);
+      if (n <= kWave) {                        // uniform
+        if (tid < kWave) d = draw_wave(exp2, row, n, all, u, l.arena);
+      } else {
+        d = draw_short(exp2, row, n, all, u, l);
+      }
     } else {
-      const uint64_t border = far_border(a, exp2, row, s, top, l);
-      d = draw_long(a, exp2, row, st, s, top, border, u, l);
+      if (!joined) join_half(a, row, 1, all, tokens, l);
+      int listed, of;
+      const uint64_t border = far_border(a, exp2, row, l, listed, of);
+      kept_sums(a, exp2, row, border, listed, of, l);
+      d = draw_long(a, exp2, row, border, u, l);
     }
   }
   if (tid == 0) {
     if (a.tokens) a.tokens[r] = d.token;
     if (a.chosen) a.chosen[r] = static_cast<float>(d.chosen);
-    if (a.probs) picks(a)[r] = Pick{d.border, d.total, s.rate, top, 0};
+    if (a.probs) picks(a)[r] = Pick{d.border, d.total, row.s.rate, top, 0};
   }
 }
 
