@@ -490,11 +490,11 @@ __device__ __forceinline__ void each_of_row(const SampleArgs& a, const Row& row,
   }
 }
 
-// The row's tokens in a span, in LDS in any order; their number, `most` at
-// most. A lane marks those of its 32 values first, so that the waves take
+// The row's tokens in a span (kArena at most), in the arena in any order;
+// returns their number. A lane marks those of its 32 values first, so that the waves take
 // their places once for all of them (one by one each token would wait for the
 // one before: 47 us for 905 of 128256).
-__device__ __forceinline__ int collect(const SampleArgs& a, const Row& row, Span g, uint64_t* list, int most, PickLds& l) {
+__device__ __forceinline__ int collect(const SampleArgs& a, const Row& row, Span g, PickLds& l) {
   constexpr int kAhead = 8;
   const float least = value_at(g.hi), greatest = value_at(g.lo);
   const bool inside = (g.lo & kLowIndex) != 0 || (g.hi & kLowIndex) != kLowIndex;   // an end among equal logits
@@ -528,12 +528,12 @@ __device__ __forceinline__ int collect(const SampleArgs& a, const Row& row, Span
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (marks >> (4 * q + e) & 1) {
-          if (to < most) list[to] = place_of(taken(v[q][e]), i0 + 4 * kDThreads * q + e);
+          if (to < kArena) l.arena[to] = place_of(taken(v[q][e]), i0 + 4 * kDThreads * q + e);
           ++to;
         }
   }
   __syncthreads();
-  return l.n < most ? l.n : most;
+  return l.n < kArena ? l.n : kArena;
 }
 
 // Sorted into `to`, ascending: each goes to the number of those before it.
@@ -667,10 +667,13 @@ __device__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const Row
   Span g = bin_span(row, b);
   int ahead = b > 0 ? l.bins.count[b - 1] : 0, count = l.bins.count[b] - ahead;
   double passed = b > 0 ? l.bins.sum[b - 1] : 0.0;
-  uint64_t* list = l.arena;
-  int n = count <= kArena ? collect(a, row, g, list, kArena, l) : 0;
-  listed = n;
-  while (count > kRank) {
+  const uint64_t* list = l.arena;
+  int n = 0;
+  const int whole = count;
+#pragma unroll 1
+  while (true) {
+    if (n == 0 && count <= kArena) n = collect(a, row, g, l);
+    if (count <= kRank) break;
     int shift = 0;
     while (((g.hi - g.lo) >> shift) >= kBins) ++shift;
     __syncthreads();
@@ -707,26 +710,22 @@ __device__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const Row
     passed += cell > 0 ? l.cells.sum[cell - 1] : 0.0;
     ahead += before;
     count = l.cells.count[cell] - before;
-    if (!n && count <= kArena && count > kRank) n = collect(a, row, g, list, kArena, l);
   }
+  listed = n == whole ? n : 0;
   // the few, sorted in the cells' place
   uint64_t* few = l.few;
   uint64_t* sorted = reinterpret_cast<uint64_t*>(l.cells.sum);
-  if (n) {
-    __syncthreads();
-    if (tid == 0) l.n = 0;
-    __syncthreads();
-    for (int i = tid; i < n; i += kDThreads) {
-      const uint64_t at = list[i];
-      if (at >= g.lo && at <= g.hi) {
-        const int to = atomicAdd(&l.n, 1);
-        if (to < kRank) few[to] = at;
-      }
+  __syncthreads();
+  if (tid == 0) l.n = 0;
+  __syncthreads();
+  for (int i = tid; i < n; i += kDThreads) {
+    const uint64_t at = list[i];
+    if (at >= g.lo && at <= g.hi) {
+      const int to = atomicAdd(&l.n, 1);
+      if (to < kRank) few[to] = at;
     }
-    __syncthreads();
-  } else {
-    collect(a, row, g, few, kRank, l);
   }
+  __syncthreads();
   const int m = l.n < kRank ? l.n : kRank;
   sort_few(few, sorted, m, l);
   const uint64_t mine = tid < m ? sorted[tid] : 0;
@@ -886,6 +885,7 @@ __device__ uint64_t far_border(const SampleArgs& a, const Exp2& exp2, const Row&
   listed = 0;
   of = -1;
   double total = l.bins.sum[kBins - 1];
+#pragma unroll 1
   for (int turn = 0; turn < 2; ++turn) {       // top-k, then top-p
     if (turn == 0 ? s.k == 0 || s.k >= l.bins.count[kBins - 1] : s.p >= 1.0) continue;   // uniform
     const int k = turn == 0 ? s.k : 0;
@@ -915,15 +915,16 @@ __device__ __forceinline__ void kept_sums(const SampleArgs& a, const Exp2& exp2,
     return;
   }
   const int b = row.bin(value_at(border)), count = l.bins.count[b] - (b > 0 ? l.bins.count[b - 1] : 0);
-  if (count > kArena) {                        // no list of that bin: the row again
+  if (of != b || listed != count) {            // no list of that bin: the row again
     for (int c = wave; c < a.chunks; c += kDWaves) {
       double sum = 0.0;
-      for (int j = 0; j < kChunk / (4 * kWave); j += 8) {
+#pragma unroll 1
+      for (int j = 0; j < kChunk / (4 * kWave); j += 4) {
         const int i0 = c * kChunk + 4 * (j * kWave + lane_id());
-        float v[8][4];
+        float v[4][4];
         load_runs(row.logits, i0, 4 * kWave, a.vocab, v);
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
+        for (int q = 0; q < 4; ++q)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const float x = taken(v[q][e]);
@@ -937,7 +938,6 @@ __device__ __forceinline__ void kept_sums(const SampleArgs& a, const Exp2& exp2,
     return;
   }
   // the bins before the border's, and the tokens in that
-  const int n = of == b ? listed : collect(a, row, bin_span(row, b), l.arena, kArena, l);
   for (int c = wave; c < a.chunks; c += kDWaves) {
     const ChunkShift h = row.chunk[c];
     double sum = 0.0;
@@ -955,7 +955,7 @@ __device__ __forceinline__ void kept_sums(const SampleArgs& a, const Exp2& exp2,
   __syncthreads();
   for (int c = tid; c < a.chunks; c += kDThreads) row.chunk[c].kept = 0;
   __syncthreads();
-  for (int i = tid; i < n; i += kDThreads) {
+  for (int i = tid; i < listed; i += kDThreads) {
     const uint64_t at = l.arena[i];
     if (at <= border) {
       const double w = __builtin_ldexp(row.weight_of(exp2, value_at(at)), kUnit + (b >> 2)) + 0x1p52;
@@ -1039,8 +1039,8 @@ __device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2
   return d;
 }
 
-// The tokens of bins 0..b (kList at most) in the arena: from the chunks'
-// lists, or from the row where a chunk lists fewer. Returns their number.
+// The tokens of bins 0..b (kList at most) from the chunks' lists, in the arena.
+// Returns their number, -1 where a chunk lists fewer.
 __device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int b, PickLds& l) {
   constexpr int kAhead = 5;                    // lists on their way
   const int tid = threadIdx.x, wave = tid >> 6;
@@ -1050,11 +1050,7 @@ __device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int b
     if (h.factor >= 0.0 && h.cut < kBins - 1 && (b == kBins - 1 || h.cut + h.shift < b)) covered = false;
   }
   if (tid == 0) l.n = 0;
-  if (!__syncthreads_and(covered)) {
-    Span all = bin_span(row, b);
-    all.lo = first_place(key_of(row.top));
-    return collect(a, row, all, l.arena, kList, l);
-  }
+  if (!__syncthreads_and(covered)) return -1;
   for (int c0 = wave; c0 < a.chunks; c0 += kDWaves * kAhead) {
     uint64_t x[kAhead];
     const auto entry = [&](int c, int i) QMV_INLINE { return row.tops[static_cast<int64_t>(c) * kTops + i]; };
@@ -1135,31 +1131,28 @@ __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
     all = wave_sum(all);
     tokens = __builtin_amdgcn_readlane(wave_scan(tokens), kWave - 1);
     __syncthreads();
-    join_half(a, row, 0, all, tokens, l);
     // the last bin that can hold the border
     const bool by_weight = row.s.m > 0.0 && (row.s.k == 0 || row.s.p >= 1.0);   // (top-p needs the sum of all k)
     // w >= m ends in the bin of 4 log2(m), to one by rounding, behind the top's
     const int end = by_weight ? static_cast<int>(fmin(4.0 * -log2(row.s.m) + 2.0, kBins - 1.0)) : kBins - 1;
-    int b = row.s.k > 0 || row.s.p < 1.0 ? crossing_near(l.bins, row.s.k, row.s.p * all) : kHalf;
-    b = b < end ? b : end;
-    bool joined = false;
-    if (b >= kHalf) {
-      join_half(a, row, 1, all, tokens, l);
-      joined = true;
-      b = kBins - 1;
-      if (row.s.k > 0 || row.s.p < 1.0) b = crossing(l.bins, row.s.k, row.s.p * all, l);
+    const bool by_place = row.s.k > 0 || row.s.p < 1.0;
+    int b = end, n = -1;
+#pragma unroll 1
+    for (int half = 0; half < 2; ++half) {
+      join_half(a, row, half, all, tokens, l);
+      if (half) b = by_place ? crossing(l.bins, row.s.k, row.s.p * all, l) : kBins - 1;
+      else b = by_place ? crossing_near(l.bins, row.s.k, row.s.p * all) : kHalf;
       b = b < end ? b : end;
-    }
-    const int up = l.bins.count[b];
-    if (up <= kList) {
-      const int n = gather(a, row, b, l);
-      if (n <= kWave) {                        // uniform
-        if (tid < kWave) d = draw_wave(exp2, row, n, all, u, l.arena);
-      } else {
-        d = draw_short(exp2, row, n, all, u, l);
+      if (b < kHalf * (half + 1) && l.bins.count[b] <= kList) {
+        n = gather(a, row, b, l);
+        if (n >= 0) break;
       }
+    }
+    if (n > kWave) {                           // uniform
+      d = draw_short(exp2, row, n, all, u, l);
+    } else if (n >= 0) {
+      if (tid < kWave) d = draw_wave(exp2, row, n, all, u, l.arena);
     } else {
-      if (!joined) join_half(a, row, 1, all, tokens, l);
       int listed, of;
       const uint64_t border = far_border(a, exp2, row, l, listed, of);
       kept_sums(a, exp2, row, border, listed, of, l);
