@@ -16,7 +16,8 @@
 //           its end, they are sorted, cut and drawn from in LDS; else the
 //           bin is narrowed until as few are left of it, and the row is
 //           summed again;
-//   probs   the distribution written out, if wanted.
+//   probs   the distribution written out, if wanted, of rows that keep many;
+//           of the others stats writes the zeros and pick what is kept.
 // A chunk's bin is one 64-bit whole number: the count, and the sum in units of
 // 2^-38 of its weights (adding in LDS in any order gives the same bits).
 // Everything else is in 64-bit floating point: with 10^5 logits a running sum
@@ -55,7 +56,7 @@ struct Pick {
   double total;                                // sum of the kept weights; 0: none
   double rate;
   float top;
-  int pad;
+  int written;                                 // the distribution is there already
 };
 
 __device__ __forceinline__ ChunkStat* chunk_stats(const SampleArgs& a) { return reinterpret_cast<ChunkStat*>(a.ws); }
@@ -79,6 +80,7 @@ struct Settings {
   int k;
   bool none, greedy;                           // of no request; of temperature 0
   __device__ __forceinline__ bool filtered() const { return k > 0 || p < 1.0 || m > 0.0; }
+  __device__ __forceinline__ bool plain() const { return !none && !greedy && !filtered(); }
 };
 __device__ __forceinline__ Settings settings_of(const SampleArgs& a, int r) {
   constexpr double kLog2e = 1.4426950408889634073599246810019;
@@ -153,24 +155,25 @@ __device__ __forceinline__ double bin_units(uint64_t bin) {
 __device__ __forceinline__ double bin_sum_of(uint64_t bin, int b) { return __builtin_ldexp(bin_units(bin), -kUnit) * bin_scale(b); }
 
 // 2^(38 + x / 4) as a whole number, -1 <= x <= 1, in the low 52 bits of the
-// result: the Taylor polynomial of degree 10 of exp(x ln 2 / 4), whose next
-// term is below 2 10^-16, in units of 2^-kUnit, added to 2^52.
+// result: the Taylor polynomial of degree 8 of exp(x ln 2 / 4), whose next
+// term is below 4 10^-13 (a ninth of a unit), in units of 2^-kUnit, added to 2^52.
 struct Units {
-  double c[11];
+  static constexpr int kDegree = 8;
+  double c[kDegree + 1];
   __device__ __forceinline__ Units() {
     double v = 0x1p38;
 #pragma unroll
-    for (int i = 0; i <= 10; ++i) {
+    for (int i = 0; i <= kDegree; ++i) {
       c[i] = v + (i == 0 ? 0x1p52 : 0.0);
       v = v * (0.69314718055994530941723212145818 / 4) / (i + 1);
     }
 #pragma unroll
-    for (int i = 0; i <= 10; ++i) asm("" : "+s"(c[i]));
+    for (int i = 0; i <= kDegree; ++i) asm("" : "+s"(c[i]));
   }
   __device__ __forceinline__ long long operator()(double x) const {
-    double p = c[10];
+    double p = c[kDegree];
 #pragma unroll
-    for (int i = 9; i >= 0; --i) p = fma(p, x, c[i]);
+    for (int i = kDegree - 1; i >= 0; --i) p = fma(p, x, c[i]);
     return __double_as_longlong(p);
   }
 };
@@ -194,24 +197,39 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
   const int r = row_of_grid();
   if (r >= a.n_rows) return;
   const Settings s = settings_of(a, r);
-  if (s.none) return;                          // uniform
   const float* row = a.logits + r * a.ldl;
-  float v[kSPer];
-  if ((c + 1) * kChunk <= a.vocab) {         // uniform: all loads at once
+  float v[kSPer];                              // NaN as -inf
+  if ((c + 1) * kChunk <= a.vocab) {           // uniform: all loads at once
 #pragma unroll
     for (int k = 0; k < kSPer; k += 4) {
       const u32x4 x = ld_x4(reinterpret_cast<const uint8_t*>(row + i0 + k * kSThreads));
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[k + e] = taken(__uint_as_float(x[e]));
+      for (int e = 0; e < 4; ++e) v[k + e] = fmaxf(__uint_as_float(x[e]), -INFINITY);
     }
   } else {
 #pragma unroll
     for (int k = 0; k < kSPer; ++k) {
       const int i = i0 + (k / 4) * 4 * kSThreads + k % 4;
       v[k] = row[i < a.vocab ? i : a.vocab - 1];
-      v[k] = i < a.vocab ? taken(v[k]) : -INFINITY;
+      v[k] = i < a.vocab ? fmaxf(v[k], -INFINITY) : -INFINITY;
     }
   }
+  if (a.zeroed && !s.plain()) {                // the distribution's zeros, while the chunk is here
+    float* out = a.probs + r * a.ldp;
+#pragma unroll
+    for (int k = 0; k < kSPer; k += 4) {
+      const int i = i0 + k * kSThreads;
+      if (i + 4 <= a.vocab) {
+        const u32x4 zero{0, 0, 0, 0};
+        __builtin_memcpy(__builtin_assume_aligned(out + i, 4), &zero, 16);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (i + e < a.vocab) out[i + e] = 0.0f;
+      }
+    }
+  }
+  if (s.none) return;                          // uniform
   float top = -INFINITY;
   int at = 0x7fffffff;
 #pragma unroll
@@ -258,10 +276,11 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
 #pragma unroll
     for (int k = 0; k < kSPer; ++k) {
       const double d = static_cast<double>(x[k]);
-      const int b = bins_between(top_quarter, floor(d * rate4), kBins - 1);
+      const double down = fmin(top_quarter - floor(d * rate4), kBins - 1.0);
+      const int b = static_cast<int>(down);
       // 4 log2(w) + b is within +-1 but for the last bin, whose tokens count
       // as 2^-64 of the largest at least: 2^-52 of the sum for all of them
-      const double f = fmax(fma(d - dtop, rate4, static_cast<double>(b)), -1.0);
+      const double f = fmax(fma(d - dtop, rate4, down), -1.0);
       const unsigned long long add = static_cast<unsigned long long>(units(f) + kOne);
       if (x[k] > -INFINITY) atomicAdd(mine + b * kCopies, add);
       bin[k] = x[k] > -INFINITY ? b : kBins;
@@ -290,7 +309,7 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
       uint64_t* list = chunk_tops(a) + place * kTops;
 #pragma unroll
       for (int k = 0; k < kSPer; ++k)
-        if (bin[k] <= cut) list[atomicAdd(&next[bin[k]], 1)] = place_of(v[k], i0 + (k / 4) * 4 * kSThreads + k % 4);
+        if (bin[k] <= cut) list[atomicAdd(&next[bin[k]], 1)] = place_of(taken(v[k]), i0 + (k / 4) * 4 * kSThreads + k % 4);
     }
     __syncthreads();
   }
@@ -656,23 +675,66 @@ __device__ __forceinline__ int crossing_near(const Running& up, int k, double go
   return kHalf;
 }
 
+// The tokens of bins from..b (kArena at most) from the chunks' lists, in the
+// arena. Returns their number, -1 where a chunk lists fewer.
+__device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int from, int b, PickLds& l) {
+  constexpr int kAhead = 5;                    // lists on their way
+  const int tid = threadIdx.x, wave = tid >> 6;
+  bool covered = true;
+  for (int c = tid; c < a.chunks; c += kDThreads) {
+    const ChunkShift h = row.chunk[c];
+    if (h.factor >= 0.0 && h.cut < kBins - 1 && (b == kBins - 1 || h.cut + h.shift < b)) covered = false;
+  }
+  __syncthreads();
+  if (tid == 0) l.n = 0;
+  if (!__syncthreads_and(covered)) return -1;
+  for (int c0 = wave; c0 < a.chunks; c0 += kDWaves * kAhead) {
+    uint64_t x[kAhead];
+    const auto entry = [&](int c, int i) QMV_INLINE { return row.tops[static_cast<int64_t>(c) * kTops + i]; };
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) x[q] = entry(c0 + kDWaves * q < a.chunks ? c0 + kDWaves * q : c0, lane_id());
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int c = c0 + kDWaves * q;
+      if (c >= a.chunks) continue;             // uniform
+      const ChunkShift h = row.chunk[c];
+      const int listed = h.factor >= 0.0 && h.shift <= b ? h.listed : 0;
+      for (int i = lane_id(), more = listed; more > 0; more -= kWave, i += kWave) {
+        if (i != lane_id()) x[q] = i < listed ? entry(c, i) : 0;
+        const int its = i < listed ? row.bin(value_at(x[q])) : kBins;
+        const bool in = its >= from && its <= b;
+        const uint64_t ins = __ballot(in);
+        if (ins) {
+          int first = 0;
+          if (lane_id() == 0) first = atomicAdd(&l.n, __builtin_popcountll(ins));
+          const int at = __builtin_amdgcn_readfirstlane(first) + __builtin_popcountll(ins & ((uint64_t(1) << lane_id()) - 1));
+          if (in && at < kArena) l.arena[at] = x[q];
+        }
+        if (__ballot(its > b)) break;          // the list goes bin by bin
+      }
+    }
+  }
+  __syncthreads();
+  return l.n < kArena ? l.n : kArena;
+}
+
 // The border of a filter in a bin: the last place kept by top-k (k > 0: the
 // k-th token) or by top-p (the last before which less than `goal` has passed);
 // kept: the weight up to it; listed: how many of the bin's tokens the arena
 // holds, which are all of them or 0. The span is cut into cells of equal
 // width until few tokens are left in one.
-__device__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const Row& row, int b, int k, double goal, PickLds& l, double& kept,
+__device__ __forceinline__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const Row& row, int b, int k, double goal, PickLds& l, double& kept,
                                 int& listed) {
   const int tid = threadIdx.x;
   Span g = bin_span(row, b);
   int ahead = b > 0 ? l.bins.count[b - 1] : 0, count = l.bins.count[b] - ahead;
   double passed = b > 0 ? l.bins.sum[b - 1] : 0.0;
   const uint64_t* list = l.arena;
-  int n = 0;
   const int whole = count;
+  int n = whole <= kArena ? gather(a, row, b, b, l) : -1;
 #pragma unroll 1
   while (true) {
-    if (n == 0 && count <= kArena) n = collect(a, row, g, l);
+    if (n < 0 && count <= kArena) n = collect(a, row, g, l);
     if (count <= kRank) break;
     int shift = 0;
     while (((g.hi - g.lo) >> shift) >= kBins) ++shift;
@@ -691,7 +753,7 @@ __device__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const Row
       atomicAdd(&l.cell_sum[cell], static_cast<unsigned long long>(__double_as_longlong(w) & ((1ll << 52) - 1)));
       atomicAdd(&l.cell_count[cell], 1u);
     };
-    if (n) {
+    if (n >= 0) {
       for (int i = tid; i < n; i += kDThreads) {
         const uint64_t at = list[i];
         if (at >= g.lo && at <= g.hi) add(at, value_at(at));
@@ -752,8 +814,9 @@ struct Drawn {
 };
 
 // All `count` tokens (kList at most) up to the border's bin, in the arena:
-// sorted, cut by all filters, and drawn from. all: the sum of the row's weights.
-__device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Row& row, int count, double all, float u, PickLds& l) {
+// sorted, cut by all filters, and drawn from. all: the sum of the row's weights;
+// probs: where the kept ones' probabilities go, if anywhere.
+__device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Row& row, int count, double all, float u, float* probs, PickLds& l) {
   constexpr int kPer = kList / kDThreads;
   const int tid = threadIdx.x, i0 = kPer * tid;
   const Settings& s = row.s;
@@ -816,6 +879,11 @@ __device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Row& row, in
     own += w[e];
   }
   double up = block_scan_d(own, l.waves, d.total);
+  if (probs) {
+#pragma unroll
+    for (int e = 0; e < kPer; ++e)
+      if (i0 + e <= last) probs[list[i0 + e] >> 12] = static_cast<float>(w[e] / d.total);
+  }
   const double drawn = static_cast<double>(u) * d.total;
   int hit = -1, some = -1;
 #pragma unroll
@@ -837,7 +905,7 @@ __device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Row& row, in
 }
 
 // The same of at most 64 tokens, by one wave: each lane has a token.
-__device__ __forceinline__ Drawn draw_wave(const Exp2& exp2, const Row& row, int count, double all, float u, uint64_t* list) {
+__device__ __forceinline__ Drawn draw_wave(const Exp2& exp2, const Row& row, int count, double all, float u, float* probs, uint64_t* list) {
   const Settings& s = row.s;
   const int lane = lane_id();
   const auto sorted = [&](uint64_t mine, int n) QMV_INLINE {   // the lane's of n in list
@@ -872,14 +940,16 @@ __device__ __forceinline__ Drawn draw_wave(const Exp2& exp2, const Row& row, int
   d.total = __shfl(up, kWave - 1);
   const uint64_t hits = __ballot(w > 0.0 && up > static_cast<double>(u) * d.total), some = __ballot(w > 0.0);
   const int take = hits ? __builtin_ctzll(hits) : 63 - __builtin_clzll(some);
+  const double p = w / d.total;
+  if (probs && lane <= last) probs[x >> 6] = static_cast<float>(p);
   d.token = static_cast<int>(__shfl(x, take) >> 6);
-  d.chosen = __shfl(w, take) / d.total;
+  d.chosen = __shfl(p, take);
   return d;
 }
 
 // The border by all filters, of a row with more tokens up to it than kList.
 // listed: tokens of bin `of` that the arena holds.
-__device__ uint64_t far_border(const SampleArgs& a, const Exp2& exp2, const Row& row, PickLds& l, int& listed, int& of) {
+__device__ __forceinline__ uint64_t far_border(const SampleArgs& a, const Exp2& exp2, const Row& row, PickLds& l, int& listed, int& of) {
   const Settings& s = row.s;
   uint64_t border = ~uint64_t(0);
   listed = 0;
@@ -1039,46 +1109,6 @@ __device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2
   return d;
 }
 
-// The tokens of bins 0..b (kList at most) from the chunks' lists, in the arena.
-// Returns their number, -1 where a chunk lists fewer.
-__device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int b, PickLds& l) {
-  constexpr int kAhead = 5;                    // lists on their way
-  const int tid = threadIdx.x, wave = tid >> 6;
-  bool covered = true;
-  for (int c = tid; c < a.chunks; c += kDThreads) {
-    const ChunkShift h = row.chunk[c];
-    if (h.factor >= 0.0 && h.cut < kBins - 1 && (b == kBins - 1 || h.cut + h.shift < b)) covered = false;
-  }
-  if (tid == 0) l.n = 0;
-  if (!__syncthreads_and(covered)) return -1;
-  for (int c0 = wave; c0 < a.chunks; c0 += kDWaves * kAhead) {
-    uint64_t x[kAhead];
-    const auto entry = [&](int c, int i) QMV_INLINE { return row.tops[static_cast<int64_t>(c) * kTops + i]; };
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) x[q] = entry(c0 + kDWaves * q < a.chunks ? c0 + kDWaves * q : c0, lane_id());
-#pragma unroll
-    for (int q = 0; q < kAhead; ++q) {
-      const int c = c0 + kDWaves * q;
-      if (c >= a.chunks) continue;             // uniform
-      const ChunkShift h = row.chunk[c];
-      const int listed = h.factor >= 0.0 && h.shift <= b ? h.listed : 0;
-      for (int i = lane_id(), more = listed; more > 0; more -= kWave, i += kWave) {
-        if (i != lane_id()) x[q] = i < listed ? entry(c, i) : 0;
-        const bool in = i < listed && row.bin(value_at(x[q])) <= b;
-        const uint64_t ins = __ballot(in);
-        if (ins == 0) break;
-        int first = 0;
-        if (lane_id() == 0) first = atomicAdd(&l.n, __builtin_popcountll(ins));
-        const int at = __builtin_amdgcn_readfirstlane(first) + __builtin_popcountll(ins & ((uint64_t(1) << lane_id()) - 1));
-        if (in && at < kList) l.arena[at] = x[q];
-        if (~ins) break;                       // the list goes bin by bin
-      }
-    }
-  }
-  __syncthreads();
-  return l.n < kList ? l.n : kList;
-}
-
 __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
   __shared__ PickLds l;
   extern __shared__ __align__(16) uint8_t dynamic[];
@@ -1099,13 +1129,17 @@ __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
   if (!row.s.none) {
     for (int c = lane_id(); c < a.chunks; c += kWave) take_top(top, at, row.stats[c].top, row.stats[c].at);
     wave_top(top, at);
+    top = taken(top);
   }
   row.top = top;
   row.top_quarter = quarter(top, row.rate4);
   Drawn d{0, 0.0, 0.0, -1};
+  float* probs = a.zeroed ? a.probs + r * a.ldp : nullptr;
+  bool written = a.zeroed && !row.s.plain();   // else the last launch writes the distribution
   if (top == -INFINITY) {                      // uniform
   } else if (row.s.greedy) {
     d = Drawn{place_of(top, at), 1.0, 1.0, at};
+    if (probs && tid == 0) probs[at] = 1.0f;
   } else if (!row.s.filtered()) {
     kept_sums(a, exp2, row, ~uint64_t(0), 0, -1, l);
     d = draw_long(a, exp2, row, ~uint64_t(0), u, l);
@@ -1144,15 +1178,16 @@ __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
       else b = by_place ? crossing_near(l.bins, row.s.k, row.s.p * all) : kHalf;
       b = b < end ? b : end;
       if (b < kHalf * (half + 1) && l.bins.count[b] <= kList) {
-        n = gather(a, row, b, l);
+        n = gather(a, row, 0, b, l);
         if (n >= 0) break;
       }
     }
     if (n > kWave) {                           // uniform
-      d = draw_short(exp2, row, n, all, u, l);
+      d = draw_short(exp2, row, n, all, u, probs, l);
     } else if (n >= 0) {
-      if (tid < kWave) d = draw_wave(exp2, row, n, all, u, l.arena);
+      if (tid < kWave) d = draw_wave(exp2, row, n, all, u, probs, l.arena);
     } else {
+      written = false;
       int listed, of;
       const uint64_t border = far_border(a, exp2, row, l, listed, of);
       kept_sums(a, exp2, row, border, listed, of, l);
@@ -1162,7 +1197,7 @@ __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
   if (tid == 0) {
     if (a.tokens) a.tokens[r] = d.token;
     if (a.chosen) a.chosen[r] = static_cast<float>(d.chosen);
-    if (a.probs) picks(a)[r] = Pick{d.border, d.total, row.s.rate, top, 0};
+    if (a.probs) picks(a)[r] = Pick{d.border, d.total, row.s.rate, top, written};
   }
 }
 
@@ -1171,6 +1206,7 @@ __global__ void __launch_bounds__(kSThreads) sample_probs_kernel(SampleArgs a) {
   const int r = row_of_grid();
   if (r >= a.n_rows) return;
   const Pick pick = picks(a)[r];
+  if (pick.written) return;                    // uniform
   const float* row = a.logits + r * a.ldl;
   float* out = a.probs + r * a.ldp;
   float v[kSPer];

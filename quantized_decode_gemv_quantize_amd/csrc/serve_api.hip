@@ -217,6 +217,7 @@ int mmvq_sample(const float* logits, int64_t ldl, int vocab, int n_rows, const m
   a.vocab = vocab;
   a.n_rows = n_rows;
   a.n_seqs = n_seqs;
+  a.zeroed = probs && probs != logits;
   sample_bytes(n_rows, vocab, &a.chunks);
   a.ws = static_cast<uint8_t*>(workspace);
   const hipStream_t st = static_cast<hipStream_t>(stream);

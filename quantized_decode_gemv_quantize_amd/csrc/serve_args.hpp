@@ -80,6 +80,7 @@ struct SampleArgs {
   float* probs;
   int64_t ldl, ldp;
   int vocab, n_rows, n_seqs, chunks;
+  bool zeroed;             // probs are no part of logits: written on the way
   uint8_t* ws;
 };
 
