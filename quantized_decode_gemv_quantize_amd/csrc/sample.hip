@@ -12,10 +12,9 @@
 //           sum over bins of a quarter octave of the weight, and the chunk's
 //           tokens in its first bins (at most kTops);
 //   pick    a workgroup a row: the chunks' histograms joined, and the bin in
-//           which the border lies. Where no more than kList tokens come up to
-//           its end, they are sorted, cut and drawn from in LDS; else the
-//           bin is narrowed until as few are left of it, and the row is
-//           summed again;
+//           which the border lies. Where no more than kArena tokens come up
+//           to its end, they are cut and drawn from in LDS, sorted if they
+//           are few; else the bin is narrowed until few are left of it;
 //   probs   the distribution written out, if wanted, of rows that keep many;
 //           of the others stats writes the zeros and pick what is kept.
 // A chunk's bin is one 64-bit whole number: the count, and the sum in units of
@@ -35,9 +34,8 @@ constexpr int kChunk = kSThreads * kSPer;
 constexpr int kBins = 256;                     // the last one: everything below
 constexpr int kDThreads = 512;
 constexpr int kDWaves = kDThreads / kWave;
-constexpr int kRank = 256;                     // tokens that are sorted by counting those before each
-constexpr int kList = 2048;                    // tokens that are sorted, cut and drawn from in LDS
-constexpr int kArena = 3 * kList;              // tokens of one bin that are held there
+constexpr int kRank = 256;                     // tokens that are sorted, each by counting those before it
+constexpr int kArena = 6144;                   // tokens that are cut and drawn from in LDS
 constexpr int kTops = 256;                     // tokens that a chunk lists
 constexpr int kUnit = 38;                      // a bin's sum is in units of 2^-kUnit
 constexpr int kSumBits = 51;                   // and behind them its count
@@ -575,30 +573,6 @@ __device__ __forceinline__ void sort_few(const uint64_t* list, uint64_t* to, int
   __syncthreads();
 }
 
-// Sorted in place, ascending, n a power of two up to 2 kDThreads * 2. Pairs
-// up to 64 apart stay inside a wave's 128.
-__device__ __forceinline__ void sort_many(uint64_t* list, int n) {
-  int last = 2 * kWave;
-  for (int k = 2; k <= n; k <<= 1)
-    for (int j = k >> 1; j > 0; last = j, j >>= 1) {
-      if (j > kWave || last > kWave) {
-        __syncthreads();
-      } else {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-      }
-      for (int t = threadIdx.x; t < n / 2; t += kDThreads) {
-        const int i = 2 * t - (t & (j - 1));   // pairs i, i + j
-        const uint64_t x = list[i], y = list[i + j];
-        if ((x > y) == ((i & k) == 0)) {
-          list[i] = y;
-          list[i + j] = x;
-        }
-      }
-    }
-  __syncthreads();
-}
-
 // Running sums of kHalf of the row's bins from `first` on: of the chunks' bins,
 // each moved to the row's grid. Most borders lie in the first half (32
 // octaves), and the other is not read then. A wave takes every eighth chunk, a
@@ -718,26 +692,37 @@ __device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int f
   return l.n < kArena ? l.n : kArena;
 }
 
-// The border of a filter in a bin: the last place kept by top-k (k > 0: the
-// k-th token) or by top-p (the last before which less than `goal` has passed);
-// kept: the weight up to it; listed: how many of the bin's tokens the arena
-// holds, which are all of them or 0. The span is cut into cells of equal
-// width until few tokens are left in one.
-__device__ __forceinline__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const Row& row, int b, int k, double goal, PickLds& l, double& kept,
-                                int& listed) {
-  const int tid = threadIdx.x;
-  Span g = bin_span(row, b);
-  int ahead = b > 0 ? l.bins.count[b - 1] : 0, count = l.bins.count[b] - ahead;
-  double passed = b > 0 ? l.bins.sum[b - 1] : 0.0;
+// Whole units of a weight up to 1, as the low bits of a sum with 2^52.
+constexpr int kFine = 49;                      // 2^13 of them stay below 2^62
+__device__ __forceinline__ unsigned long long fine_units(double w) {
+  return static_cast<unsigned long long>(__double_as_longlong(__builtin_ldexp(w, kFine) + 0x1p52)) & ((1ull << 52) - 1);
+}
+
+// Where the border of a filter is looked for: `count` tokens, behind `ahead`
+// others of the weight `passed`; n of them, all, are in the arena (-1: not yet).
+struct Search {
+  Span g;
+  int count, ahead, n;
+  double passed;
+};
+
+// The last place kept by top-k (k > 0: the k-th token) or by top-p (the last
+// before which less than `goal` has passed); kept: the weight up to it. The
+// span is cut into cells of equal width until few tokens are left in one. On
+// return s.n tells whether all its tokens are in the arena.
+__device__ __forceinline__ uint64_t find_border(const SampleArgs& a, const Exp2& exp2, const Row& row, Search& s, int k, double goal, PickLds& l,
+                                                double& kept) {
+  const int tid = threadIdx.x, whole = s.count;
+  Span g = s.g;
+  int count = s.count, ahead = s.ahead, n = s.n;
+  double passed = s.passed;
   const uint64_t* list = l.arena;
-  const int whole = count;
-  int n = whole <= kArena ? gather(a, row, b, b, l) : -1;
 #pragma unroll 1
   while (true) {
     if (n < 0 && count <= kArena) n = collect(a, row, g, l);
     if (count <= kRank) break;
-    int shift = 0;
-    while (((g.hi - g.lo) >> shift) >= kBins) ++shift;
+    const uint64_t wide = g.hi - g.lo;
+    const int bits = 64 - __builtin_clzll(wide | 1), shift = bits > 8 ? bits - 8 : 0;   // at most kBins cells
     __syncthreads();
     if (tid < kBins) {
       l.cell_sum[tid] = 0;
@@ -773,7 +758,7 @@ __device__ __forceinline__ uint64_t find_border(const SampleArgs& a, const Exp2&
     ahead += before;
     count = l.cells.count[cell] - before;
   }
-  listed = n == whole ? n : 0;
+  s.n = n == whole ? n : -1;
   // the few, sorted in the cells' place
   uint64_t* few = l.few;
   uint64_t* sorted = reinterpret_cast<uint64_t*>(l.cells.sum);
@@ -813,94 +798,49 @@ struct Drawn {
   int token;
 };
 
-// All `count` tokens (kList at most) up to the border's bin, in the arena:
+// All `count` tokens (kRank at most) up to the border's bin, in the arena:
 // sorted, cut by all filters, and drawn from. all: the sum of the row's weights;
 // probs: where the kept ones' probabilities go, if anywhere.
 __device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Row& row, int count, double all, float u, float* probs, PickLds& l) {
-  constexpr int kPer = kList / kDThreads;
-  const int tid = threadIdx.x, i0 = kPer * tid;
+  const int tid = threadIdx.x;
   const Settings& s = row.s;
-  double* weights = reinterpret_cast<double*>(l.arena + 2 * kList);
-  const auto sorted_list = [&](int n) QMV_INLINE {   // of the arena's first n
-    if (n <= kRank) {
-      sort_few(l.arena, l.arena + kList, n, l);
-      return l.arena + kList;
-    }
-    int wide = kRank;
-    while (wide < n) wide <<= 1;
-    for (int i = n + tid; i < wide; i += kDThreads) l.arena[i] = ~uint64_t(0);
-    sort_many(l.arena, wide);
-    return l.arena;
-  };
-  const uint64_t* list = sorted_list(count);
+  uint64_t* sorted = l.arena + kRank;
+  double* weights = reinterpret_cast<double*>(l.arena + 2 * kRank);
+  sort_few(l.arena, sorted, count, l);
   const int k = s.k > 0 && s.k < count ? s.k : count;
-  uint64_t at[kPer];
-  double w[kPer], own = 0.0, total;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    at[e] = i0 + e < k ? list[i0 + e] : 0;
-    w[e] = i0 + e < k ? row.weight_of(exp2, value_at(at[e])) : 0.0;
-    own += w[e];
-  }
-  double before = block_scan_d(own, l.waves, total);
-  const double goal = s.p * (s.k > 0 ? total : all);
+  const uint64_t at = tid < k ? sorted[tid] : 0;
+  double w = tid < k ? row.weight_of(exp2, value_at(at)) : 0.0, total;
+  const double before = block_scan_d(w, l.waves, total), goal = s.p * (s.k > 0 ? total : all);
   if (tid == 0) {
     l.last = 0;
     l.first = 0x7fffffff;
     l.found = -1;
   }
   __syncthreads();
-  int in = -1;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    if (i0 + e < k && (s.p >= 1.0 || before < goal) && w[e] >= s.m) in = i0 + e;
-    before += w[e];
-  }
-  const uint64_t ins = __ballot(in >= 0);
-  if (ins && lane_id() == 63 - __builtin_clzll(ins)) atomicMax(&l.last, in);
+  const uint64_t ins = __ballot(tid < k && (s.p >= 1.0 || before < goal) && w >= s.m);
+  if (ins && lane_id() == 0) atomicMax(&l.last, (tid & ~63) + 63 - __builtin_clzll(ins));
   __syncthreads();
   const int last = l.last;                     // the first token is kept in any case
   Drawn d;
-  d.border = list[last];
-  __syncthreads();
+  d.border = sorted[last];
   // the kept ones by their indices
-#pragma unroll
-  for (int e = 0; e < kPer; ++e)
-    if (i0 + e <= last) {
-      weights[i0 + e] = w[e];
-      l.arena[i0 + e] = (at[e] & kLowIndex) << 12 | static_cast<uint64_t>(i0 + e);
-    }
+  if (tid <= last) {
+    weights[tid] = w;
+    l.arena[tid] = (at & kLowIndex) << 12 | static_cast<uint64_t>(tid);
+  }
+  __syncthreads();                             // (the border is read)
+  sort_few(l.arena, sorted, last + 1, l);
+  const uint64_t x = tid <= last ? sorted[tid] : 0;
+  w = tid <= last ? weights[x & 4095] : 0.0;
+  const double up = block_scan_d(w, l.waves, d.total) + w;
+  if (probs && tid <= last) probs[x >> 12] = static_cast<float>(w / d.total);
+  const uint64_t hits = __ballot(w > 0.0 && up > static_cast<double>(u) * d.total), some = __ballot(w > 0.0);
+  if (hits && lane_id() == 0) atomicMin(&l.first, (tid & ~63) + __builtin_ctzll(hits));
+  if (some && lane_id() == 0) atomicMax(&l.found, (tid & ~63) + 63 - __builtin_clzll(some));
   __syncthreads();
-  list = sorted_list(last + 1);
-  own = 0.0;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    w[e] = i0 + e <= last ? weights[list[i0 + e] & 4095] : 0.0;
-    own += w[e];
-  }
-  double up = block_scan_d(own, l.waves, d.total);
-  if (probs) {
-#pragma unroll
-    for (int e = 0; e < kPer; ++e)
-      if (i0 + e <= last) probs[list[i0 + e] >> 12] = static_cast<float>(w[e] / d.total);
-  }
-  const double drawn = static_cast<double>(u) * d.total;
-  int hit = -1, some = -1;
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) {
-    up += w[e];
-    if (w[e] > 0.0) {
-      some = i0 + e;
-      hit = hit < 0 && up > drawn ? i0 + e : hit;
-    }
-  }
-  const uint64_t hits = __ballot(hit >= 0), somes = __ballot(some >= 0);
-  if (hits && lane_id() == __builtin_ctzll(hits)) atomicMin(&l.first, hit);
-  if (somes && lane_id() == 63 - __builtin_clzll(somes)) atomicMax(&l.found, some);
-  __syncthreads();
-  const uint64_t x = list[l.first != 0x7fffffff ? l.first : l.found];
-  d.token = static_cast<int>(x >> 12);
-  d.chosen = weights[x & 4095] / d.total;
+  const uint64_t take = sorted[l.first != 0x7fffffff ? l.first : l.found];
+  d.token = static_cast<int>(take >> 12);
+  d.chosen = weights[take & 4095] / d.total;
   return d;
 }
 
@@ -947,23 +887,30 @@ __device__ __forceinline__ Drawn draw_wave(const Exp2& exp2, const Row& row, int
   return d;
 }
 
-// The border by all filters, of a row with more tokens up to it than kList.
-// listed: tokens of bin `of` that the arena holds.
-__device__ __forceinline__ uint64_t far_border(const SampleArgs& a, const Exp2& exp2, const Row& row, PickLds& l, int& listed, int& of) {
+// The border by all filters. listed: tokens in the arena, all up to the border
+// (0: none there); else of: the bin whose tokens are there in the end, -1 for none.
+__device__ __forceinline__ uint64_t far_border(const SampleArgs& a, const Exp2& exp2, const Row& row, double all, int tokens, int listed, int& of,
+                                               int& of_listed, PickLds& l) {
   const Settings& s = row.s;
   uint64_t border = ~uint64_t(0);
-  listed = 0;
   of = -1;
-  double total = l.bins.sum[kBins - 1];
+  of_listed = 0;
+  double total = all;
 #pragma unroll 1
   for (int turn = 0; turn < 2; ++turn) {       // top-k, then top-p
-    if (turn == 0 ? s.k == 0 || s.k >= l.bins.count[kBins - 1] : s.p >= 1.0) continue;   // uniform
+    if (turn == 0 ? s.k == 0 || s.k >= tokens : s.p >= 1.0) continue;   // uniform
     const int k = turn == 0 ? s.k : 0;
     const double goal = s.p * total;
-    const int b = crossing(l.bins, k, goal, l);
+    Search search{Span{first_place(key_of(row.top)), ~uint64_t(0)}, listed, 0, listed, 0.0};
+    if (listed == 0) {
+      of = crossing(l.bins, k, goal, l);
+      const int ahead = of > 0 ? l.bins.count[of - 1] : 0, count = l.bins.count[of] - ahead;
+      const double passed = of > 0 ? l.bins.sum[of - 1] : 0.0;
+      search = Search{bin_span(row, of), count, ahead, count <= kArena ? gather(a, row, of, of, l) : -1, passed};
+    }
     double kept;
-    const uint64_t found = find_border(a, exp2, row, b, k, goal, l, kept, listed);
-    of = b;
+    const uint64_t found = find_border(a, exp2, row, search, k, goal, l, kept);
+    of_listed = search.n;
     if (turn == 0) total = kept;
     border = found < border ? found : border;
     __syncthreads();
@@ -974,6 +921,91 @@ __device__ __forceinline__ uint64_t far_border(const SampleArgs& a, const Exp2& 
     border = least < border ? least : border;
   }
   return border;
+}
+
+// A draw from the arena's n tokens up to the border: their weights summed over
+// cells of indices, until few are left in the one in which the running sum
+// passes the goal.
+__device__ __forceinline__ Drawn draw_list(const Exp2& exp2, const Row& row, int n, uint64_t border, int vocab, float u, float* probs, PickLds& l) {
+  const int tid = threadIdx.x;
+  Drawn d{border, 0.0, 0.0, -1};
+  int lo = 0, shift = 32 - __builtin_clz(static_cast<uint32_t>(vocab)) - 8;
+  shift = shift > 0 ? shift : 0;
+  double passed = 0.0, drawn = -1.0;
+#pragma unroll 1
+  while (true) {
+    __syncthreads();
+    if (tid < kBins) {
+      l.cell_sum[tid] = 0;
+      l.cell_count[tid] = 0;
+    }
+    if (tid == 0) {
+      l.first = kBins;
+      l.last = 0;
+    }
+    __syncthreads();
+    for (int i = tid; i < n; i += kDThreads) {
+      const uint64_t at = l.arena[i];
+      const int index = static_cast<int>(at & kLowIndex) - lo;
+      if (at <= border && index >= 0 && index >> shift < kBins) {
+        atomicAdd(&l.cell_sum[index >> shift], fine_units(row.weight_of(exp2, value_at(at))));
+        atomicAdd(&l.cell_count[index >> shift], 1u);
+      }
+    }
+    __syncthreads();
+    run_up(tid < kBins ? __builtin_ldexp(static_cast<double>(l.cell_sum[tid]), -kFine) : 0.0, 0, l.cells, l);
+    if (drawn < 0.0) {                         // the first time
+      d.total = l.cells.sum[kBins - 1];
+      drawn = static_cast<double>(u) * d.total;
+    }
+    if (tid < kBins) {
+      const bool some = l.cell_sum[tid] > 0;
+      const uint64_t hits = __ballot(some && passed + l.cells.sum[tid] > drawn), somes = __ballot(some);
+      if (lane_id() == 0 && hits) atomicMin(&l.first, (tid & ~63) + __builtin_ctzll(hits));
+      if (lane_id() == 0 && somes) atomicMax(&l.last, (tid & ~63) + 63 - __builtin_clzll(somes));
+    }
+    __syncthreads();
+    const int cell = l.first < kBins ? l.first : l.last;
+    lo += cell << shift;
+    passed += cell > 0 ? l.cells.sum[cell - 1] : 0.0;
+    if (l.cell_count[cell] <= kRank) break;    // (a cell of one index has one)
+    shift = shift > 8 ? shift - 8 : 0;
+  }
+  // the few by their indices
+  uint64_t* sorted = reinterpret_cast<uint64_t*>(l.cells.sum);
+  __syncthreads();
+  if (tid == 0) {
+    l.n = 0;
+    l.first = kRank;
+    l.last = 0;
+  }
+  __syncthreads();
+  for (int i = tid; i < n; i += kDThreads) {
+    const uint64_t at = l.arena[i];
+    const int index = static_cast<int>(at & kLowIndex) - lo;
+    if (at <= border) {
+      if (probs) probs[at & kLowIndex] = static_cast<float>(row.weight_of(exp2, value_at(at)) / d.total);
+      if (index >= 0 && index >> shift == 0) {
+        const int to = atomicAdd(&l.n, 1);
+        if (to < kRank) l.few[to] = (at & kLowIndex) << 32 | at >> kIndexBits;
+      }
+    }
+  }
+  __syncthreads();
+  const int m = l.n < kRank ? l.n : kRank;
+  sort_few(l.few, sorted, m, l);
+  const uint64_t x = tid < m ? sorted[tid] : 0;
+  const double w = tid < m ? row.weight_of(exp2, value_of(~static_cast<uint32_t>(x))) : 0.0;
+  double all;
+  const double up = passed + block_scan_d(w, l.waves, all) + w;
+  const uint64_t hits = __ballot(w > 0.0 && up > drawn), some = __ballot(w > 0.0);
+  if (hits && lane_id() == 0) atomicMin(&l.first, (tid & ~63) + __builtin_ctzll(hits));
+  if (some && lane_id() == 0) atomicMax(&l.last, (tid & ~63) + 63 - __builtin_clzll(some));
+  __syncthreads();
+  const uint64_t take = sorted[l.first < kRank ? l.first : l.last];
+  d.token = static_cast<int>(take >> 32);
+  d.chosen = row.weight_of(exp2, value_of(~static_cast<uint32_t>(take))) / d.total;
+  return d;
 }
 
 // The kept weights of each chunk, in its stats.
@@ -1177,21 +1209,25 @@ __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
       if (half) b = by_place ? crossing(l.bins, row.s.k, row.s.p * all, l) : kBins - 1;
       else b = by_place ? crossing_near(l.bins, row.s.k, row.s.p * all) : kHalf;
       b = b < end ? b : end;
-      if (b < kHalf * (half + 1) && l.bins.count[b] <= kList) {
+      if (b < kHalf * (half + 1) && l.bins.count[b] <= kArena) {
         n = gather(a, row, 0, b, l);
         if (n >= 0) break;
       }
     }
-    if (n > kWave) {                           // uniform
-      d = draw_short(exp2, row, n, all, u, probs, l);
-    } else if (n >= 0) {
+    if (n >= 0 && n <= kWave) {                // uniform
       if (tid < kWave) d = draw_wave(exp2, row, n, all, u, probs, l.arena);
+    } else if (n >= 0 && n <= kRank) {
+      d = draw_short(exp2, row, n, all, u, probs, l);
     } else {
-      written = false;
-      int listed, of;
-      const uint64_t border = far_border(a, exp2, row, l, listed, of);
-      kept_sums(a, exp2, row, border, listed, of, l);
-      d = draw_long(a, exp2, row, border, u, l);
+      int of, of_listed;
+      const uint64_t border = far_border(a, exp2, row, all, tokens, n > 0 ? n : 0, of, of_listed, l);
+      if (n > 0) {
+        d = draw_list(exp2, row, n, border, a.vocab, u, probs, l);
+      } else {
+        written = false;
+        kept_sums(a, exp2, row, border, of_listed, of, l);
+        d = draw_long(a, exp2, row, border, u, l);
+      }
     }
   }
   if (tid == 0) {
