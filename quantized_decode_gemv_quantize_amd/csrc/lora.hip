@@ -3,9 +3,9 @@
 //   v = A_a x[t] (r numbers a row), out[t] = base[t] + scale_a * B_a v
 //
 // Two launches: shrink (v, in ranges of K) and expand (v of all ranges
-// summed, B_a v, the addition). Up to 16 rows of one adapter, out of 64
-// consecutive ones, share its weights: the tile of a 16x16x32 bf16 matrix
-// product, whose other side is 16 rows of A or B. Rows of one adapter are
+// summed, B_a v, the addition). Up to 16 rows of one adapter (32 in large
+// batches), out of 64 consecutive ones, share its weights: a side of 16x16x32
+// bf16 matrix products, whose other side is 16 rows of A or B. Rows of one adapter are
 // found in the ids of the 64 by a ballot, so that nothing has to be sorted
 // or listed first; single tokens of as many adapters leave 15 of a tile's 16
 // columns empty, but then the weights are all there is to read, and the
@@ -24,11 +24,10 @@ namespace qmv {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kLThreads = 256;
-constexpr int kLWaves = kLThreads / kWave;
 constexpr int kLBlock = 64;                    // consecutive rows among which tiles are formed
-constexpr int kLTile = 16;                     // rows of a tile
 constexpr int kLStep = 32;                     // of K, or ranks, a matrix product
+constexpr int kLColumns = 16;                  // rows of x a matrix product
+constexpr int kAWaves = 8, kBWaves = 4;        // of a workgroup of shrink and of expand
 
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -57,43 +56,44 @@ __device__ __forceinline__ void split8(const float (&v)[8], u32x4 (&part)[N]) {
   }
 }
 
-// Eight consecutive weights at element i, as bf16 parts; those from `valid` on 0.
+// Eight consecutive weights: as they are stored, and as bf16 parts.
 template <int TYPE>
 struct Weights {
   static constexpr int kParts = TYPE == MMVQ_BF16 ? 1 : TYPE == MMVQ_F16 ? 2 : 3;
   static constexpr int kBytes = TYPE == MMVQ_F32 ? 4 : 2;
-  static __device__ __forceinline__ void load(const uint8_t* m, int64_t i, int valid, u32x4 (&part)[kParts]) {
-    const uint8_t* p = m + i * kBytes;
-    float v[8];
-    if constexpr (TYPE == MMVQ_F32) {
-      const u32x4 a = ld_a16_x4(p), b = ld_a16_x4(p + 16);
+  static constexpr int kQuads = TYPE == MMVQ_F32 ? 2 : 1;
+  u32x4 raw[kQuads];
+  __device__ __forceinline__ void load(const uint8_t* m, int64_t i) {
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q) raw[q] = ld_a16_x4(m + i * kBytes + 16 * q);
+  }
+  // Those from `valid` on become 0 (8 and more: none).
+  __device__ __forceinline__ void cut(int valid) {
+#pragma unroll
+    for (int q = 0; q < kQuads; ++q)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[e] = __uint_as_float(a[e]);
-        v[e + 4] = __uint_as_float(b[e]);
+        if constexpr (TYPE == MMVQ_F32) raw[q][e] = 4 * q + e < valid ? raw[q][e] : 0u;
+        else raw[q][e] &= (2 * e < valid ? 0x0000FFFFu : 0u) | (2 * e + 1 < valid ? 0xFFFF0000u : 0u);
       }
+  }
+  __device__ __forceinline__ void split(u32x4 (&part)[kParts]) const {
+    if constexpr (TYPE == MMVQ_BF16) {
+      part[0] = raw[0];
     } else {
-      const u32x4 a = ld_a16_x4(p);
-      if constexpr (TYPE == MMVQ_BF16) {
-        part[0] = a;
-        if (valid < 8) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            part[0][e] = a[e] & ((2 * e < valid ? 0x0000FFFFu : 0u) | (2 * e + 1 < valid ? 0xFFFF0000u : 0u));
-        }
-        return;
-      }
+      float v[8];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        v[2 * e] = h2f(a[e]);
-        v[2 * e + 1] = h2f(a[e] >> 16);
+        if constexpr (TYPE == MMVQ_F32) {
+          v[e] = __uint_as_float(raw[0][e]);
+          v[e + 4] = __uint_as_float(raw[1][e]);
+        } else {
+          v[2 * e] = h2f(raw[0][e]);
+          v[2 * e + 1] = h2f(raw[0][e] >> 16);
+        }
       }
+      split8<kParts>(v, part);
     }
-    if (valid < 8) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = e < valid ? v[e] : 0.0f;
-    }
-    split8<kParts>(v, part);
   }
 };
 
@@ -109,11 +109,12 @@ __device__ __forceinline__ f32x4 multiply(const u32x4 (&w)[PARTS], const u32x4 (
 }
 
 // The tile that row `lead` of a block of 64 leads, the same in every wave.
+template <int CT>
 struct Tile {
   int adapter;             // -1: none
   int rank;
   int count;               // rows; 0: none
-  int row;                 // of the lane's column (lane % 16), valid below count
+  int row[CT];             // of the lane's columns lane % 16 + 16 c; the first one's behind count
   float scale;
 };
 
@@ -130,17 +131,23 @@ __device__ __forceinline__ int block_ids(const LoraArgs& a, int block) {
   return t < a.n ? adapter_of(a, t) : -2;
 }
 
-__device__ __forceinline__ Tile tile_of(const LoraArgs& a, int block, int ids, int lead) {
-  Tile tile{__builtin_amdgcn_readlane(ids, lead), 0, 0, 0, 0.0f};
+template <int CT>
+__device__ __forceinline__ Tile<CT> tile_of(const LoraArgs& a, int block, int ids, int lead) {
+  constexpr int kRows = kLColumns * CT;
+  Tile<CT> tile{__builtin_amdgcn_readlane(ids, lead), 0, 0, {}, 0.0f};
   const uint64_t same = __ballot(ids == tile.adapter);
   const int ahead = __builtin_popcountll(same & ((uint64_t(1) << lead) - 1));
-  if (tile.adapter == -2 || ahead % kLTile) return tile;
+  if (tile.adapter == -2 || ahead % kRows) return tile;
   const int left = __builtin_popcountll(same) - ahead;
-  tile.count = left < kLTile ? left : kLTile;
+  tile.count = left < kRows ? left : kRows;
   const int lane = lane_id(), mine = __builtin_popcountll(same & ((uint64_t(1) << lane) - 1)) - ahead;
-  const bool member = ids == tile.adapter && mine >= 0 && mine < kLTile;
-  const int pushed = __builtin_amdgcn_ds_permute(4 * (member ? mine : kWave - 1), block * kLBlock + lane);
-  tile.row = __shfl(pushed, lane % kLTile);
+  const bool member = ids == tile.adapter && mine >= 0 && mine < kRows;
+  const int pushed = __builtin_amdgcn_ds_permute(4 * (member ? mine : kWave - 1), lane);
+#pragma unroll
+  for (int c = 0; c < CT; ++c) {
+    const int column = lane % kLColumns + kLColumns * c;
+    tile.row[c] = block * kLBlock + __shfl(pushed, column < tile.count ? column : 0);
+  }
   if (tile.adapter >= 0) {
     const int r = a.rank ? a.rank[tile.adapter] : a.max_rank;
     tile.rank = r < 0 ? 0 : r > a.max_rank ? a.max_rank : r;
@@ -159,175 +166,268 @@ __device__ __forceinline__ void values8(const float* p, float (&v)[8]) {
   }
 }
 
-// v of a tile over a range of K, up to 16 RT ranks at a time. The four waves
-// share the range.
-template <int TYPE, int RT>
-__global__ void __launch_bounds__(kLThreads) lora_shrink_kernel(LoraArgs a) {
+// v of a tile over a range of K, 16 RT ranks at a time. The waves share the
+// range. Columns behind the tile's count and ranks behind the adapter's repeat
+// real ones, so that no load waits for a condition; what comes of them is
+// not stored, or not used.
+template <int TYPE, int RT, int CT>
+__global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a) {
   using W = Weights<TYPE>;
-  __shared__ f32x4 lds[kLWaves][RT][kWave];
+  constexpr int kRegs = 8 * CT + 4 * W::kQuads * RT, kAhead = kRegs <= 24 ? 4 : kRegs <= 48 ? 2 : 1;   // steps on their way
+  __shared__ f32x4 lds[kAWaves][RT][kWave];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / 16;
-  const int block = blockIdx.x, per_y = kLBlock / gridDim.y, split = blockIdx.z;
+  const int block = blockIdx.x, split = blockIdx.z;
   const int ids = block_ids(a, block);
-  const int steps = static_cast<int>((a.K + kLStep - 1) / kLStep);
-  const int s0 = (split * kLWaves + wave) * a.steps, s1 = s0 + a.steps < steps ? s0 + a.steps : steps;
-  for (int lead = blockIdx.y * per_y; lead < static_cast<int>(blockIdx.y + 1) * per_y; ++lead) {
-    const Tile tile = tile_of(a, block, ids, lead);
+  const int steps = static_cast<int>((a.K + kLStep - 1) / kLStep), whole = static_cast<int>(a.K / kLStep);
+  const int s0 = (split * kAWaves + wave) * a.steps, s1 = s0 + a.steps < steps ? s0 + a.steps : steps;
+  for (int lead = blockIdx.y * a.leads, end = lead + a.leads; lead < end; ++lead) {
+    const Tile<CT> tile = tile_of<CT>(a, block, ids, lead);
     if (tile.count == 0 || tile.rank == 0) continue;       // uniform
-    const bool live = lane % 16 < tile.count;
-    const float* x = a.x + (live ? tile.row : 0) * a.ldx;
+    const float* x[CT];
+#pragma unroll
+    for (int c = 0; c < CT; ++c) x[c] = a.x + tile.row[c] * a.ldx + 8 * g;
     const uint8_t* A = a.A + tile.adapter * a.stride_a * W::kBytes;
     for (int r0 = 0; r0 < tile.rank; r0 += 16 * RT) {
-      f32x4 acc[RT];
+      f32x4 acc[RT][CT];
+      int64_t w0[RT];                          // element of the lane's rank
 #pragma unroll
-      for (int t = 0; t < RT; ++t) acc[t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 2
-      for (int s = s0; s < s1; ++s) {
-        const int k = s * kLStep + 8 * g;
-        float v[8];
+      for (int t = 0; t < RT; ++t) {
+        const int j = r0 + 16 * t + lane % 16;
+        w0[t] = (j < tile.rank ? j : tile.rank - 1) * a.K + 8 * g;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] = 0.0f;
-        if (live && k < a.K) values8(x + k, v);
-        u32x4 w[RT][W::kParts], xp[3];
+        for (int c = 0; c < CT; ++c) acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      }
+      const auto products = [&](const float (&v)[CT][8], W (&w)[RT]) QMV_INLINE {
+        u32x4 xp[CT][3];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) split8<3>(v[c], xp[c]);
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+          if (RT == 1 || r0 + 16 * t < tile.rank) {        // uniform
+            u32x4 wp[W::kParts];
+            w[t].split(wp);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[t][c] = multiply<W::kParts>(wp, xp[c], acc[t][c]);
+          }
+      };
+      int s = s0;
+      for (const int last = s1 < whole ? s1 : whole; s < last; s += kAhead) {
+        float v[kAhead][CT][8];
+        W w[kAhead][RT];
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q) {
+          const int k = (s + q < last ? s + q : last - 1) * kLStep;
+#pragma unroll
+          for (int c = 0; c < CT; ++c) values8(x[c] + k, v[q][c]);
+#pragma unroll
+          for (int t = 0; t < RT; ++t)
+            if (RT == 1 || r0 + 16 * t < tile.rank) w[q][t].load(A, w0[t] + k);
+        }
+#pragma unroll
+        for (int q = 0; q < kAhead; ++q)
+          if (s + q < last) products(v[q], w[q]);           // uniform
+      }
+      if (whole < s1 && s0 <= whole) {                     // the rest of K: 8, 16 or 24 values
+        float v[1][CT][8];
+        W w[1][RT];
+        const int k = whole * kLStep, back = k + 8 * g < a.K ? 0 : 8 * g;   // lanes behind it repeat the first's, times 0
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          values8(x[c] + k - back, v[0][c]);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) v[0][c][e] = back ? 0.0f : v[0][c][e];
+        }
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          const int j = r0 + 16 * t + lane % 16;
-#pragma unroll
-          for (int p = 0; p < W::kParts; ++p) w[t][p] = u32x4{0, 0, 0, 0};
-          if (j < tile.rank && k < a.K) W::load(A, j * a.K + k, 8, w[t]);
+          w[0][t].load(A, w0[t] + k - back);
+          w[0][t].cut(back ? 0 : 8);
         }
-        split8<3>(v, xp);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) acc[t] = multiply<W::kParts>(w[t], xp, acc[t]);
+        products(v[0], w[0]);
       }
-      __syncthreads();                         // the sums before are read
 #pragma unroll
-      for (int t = 0; t < RT; ++t) lds[wave][t][lane] = acc[t];
-      __syncthreads();
-      for (int t = wave; t < RT; t += kLWaves) {
-        const int j = r0 + 16 * t + 4 * g;
-        f32x4 sum = lds[0][t][lane];
+      for (int c = 0; c < CT; ++c) {
+        __syncthreads();                       // the sums before are read
 #pragma unroll
-        for (int w = 1; w < kLWaves; ++w) sum += lds[w][t][lane];
-        if (live && j < a.max_rank)
-          *reinterpret_cast<f32x4*>(a.part + (static_cast<int64_t>(split) * a.n + tile.row) * a.max_rank + j) = sum;
+        for (int t = 0; t < RT; ++t) lds[wave][t][lane] = acc[t][c];
+        __syncthreads();
+        for (int t = wave; t < RT; t += kAWaves) {
+          const int j = r0 + 16 * t + 4 * g;
+          f32x4 sum = lds[0][t][lane];
+#pragma unroll
+          for (int w = 1; w < kAWaves; ++w) sum += lds[w][t][lane];
+          if (lane % kLColumns + kLColumns * c < tile.count && j < a.max_rank)
+            *reinterpret_cast<f32x4*>(a.part + (static_cast<int64_t>(split) * a.n + tile.row[c]) * a.max_rank + j) = sum;
+        }
       }
     }
   }
 }
 
 // base + scale * B v of a tile, for a slice of M; up to 32 RC ranks.
-template <int TYPE, int RC>
-__global__ void __launch_bounds__(kLThreads) lora_expand_kernel(LoraArgs a) {
+template <int TYPE, int RC, int CT>
+__global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a) {
   using W = Weights<TYPE>;
+  constexpr int kAhead = RC * W::kQuads * (CT + 1) <= 4 ? 4 : RC * W::kQuads <= 4 ? 2 : 1;   // tiles of 16 outputs on their way
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / 16;
-  const int block = blockIdx.x, per_y = kLBlock / gridDim.y;
+  const int block = blockIdx.x;
   const int ids = block_ids(a, block);
-  const int64_t m_step = static_cast<int64_t>(gridDim.z) * kLWaves * 16, m_first = (static_cast<int64_t>(blockIdx.z) * kLWaves + wave) * 16;
-  for (int lead = blockIdx.y * per_y; lead < static_cast<int>(blockIdx.y + 1) * per_y; ++lead) {
-    const Tile tile = tile_of(a, block, ids, lead);
+  constexpr int kPiece = 16 * kAhead;          // outputs a wave takes at a time, side by side
+  const int64_t m_first = (static_cast<int64_t>(blockIdx.z) * kBWaves + wave) * kPiece, m_step = static_cast<int64_t>(gridDim.z) * kBWaves * kPiece;
+  for (int lead = blockIdx.y * a.leads, end = lead + a.leads; lead < end; ++lead) {
+    const Tile<CT> tile = tile_of<CT>(a, block, ids, lead);
     if (tile.count == 0 || (tile.rank == 0 && a.base == a.out)) continue;   // uniform
-    const bool live = lane % 16 < tile.count;
-    u32x4 v[RC][3];
+    const float* base[CT];
+    float* out[CT];
+    bool live[CT];
 #pragma unroll
-    for (int c = 0; c < RC; ++c) {
-      const int j = kLStep * c + 8 * g;
-      float sum[8];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-      if (live && j < tile.rank)
-        for (int s = 0; s < a.splits; ++s) {
-          float one[8];
-          values8(a.part + (static_cast<int64_t>(s) * a.n + tile.row) * a.max_rank + j, one);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) sum[e] += one[e];
-        }
-      split8<3>(sum, v[c]);
+    for (int c = 0; c < CT; ++c) {
+      live[c] = lane % kLColumns + kLColumns * c < tile.count;
+      base[c] = a.base + tile.row[c] * a.ldb + 4 * g;
+      out[c] = a.out + tile.row[c] * a.ldo + 4 * g;
     }
     const uint8_t* B = a.B + (tile.adapter < 0 ? 0 : tile.adapter) * a.stride_b * W::kBytes;
-    const float* base = a.base + (live ? tile.row : 0) * a.ldb;
-    float* out = a.out + (live ? tile.row : 0) * a.ldo;
-    for (int64_t m0 = m_first; m0 < a.M; m0 += m_step) {
-      const int64_t m = m0 + lane % 16, o = m0 + 4 * g;
-      f32x4 acc{0.0f, 0.0f, 0.0f, 0.0f};
+    W w[kAhead][RC];
+    f32x4 old[kAhead][CT];
+    const auto fetch = [&](int64_t m0) QMV_INLINE {
 #pragma unroll
-      for (int c = 0; c < RC; ++c) {
-        const int j = kLStep * c + 8 * g;
-        if (kLStep * c < tile.rank) {          // uniform
-          u32x4 w[W::kParts];
+      for (int t = 0; t < kAhead; ++t) {
+        const int64_t m = m0 + 16 * t + lane % 16, row = (m < a.M ? m : a.M - 1) * a.max_rank;
 #pragma unroll
-          for (int p = 0; p < W::kParts; ++p) w[p] = u32x4{0, 0, 0, 0};
-          if (m < a.M && j < tile.rank) W::load(B, m * a.max_rank + j, tile.rank - j, w);
-          acc = multiply<W::kParts>(w, v[c], acc);
+        for (int q = 0; q < RC; ++q) {
+          const int j = kLStep * q + 8 * g;
+          if (kLStep * q < tile.rank) w[t][q].load(B, row + (j < a.max_rank ? j : 0));   // uniform
         }
+#pragma unroll
+        for (int c = 0; c < CT; ++c)
+          if (live[c] && m0 + 16 * t + 4 * g + 4 <= a.M) {
+            const u32x4 b = ld_x4(reinterpret_cast<const uint8_t*>(base[c] + m0 + 16 * t));
+            old[t][c] = f32x4{__uint_as_float(b[0]), __uint_as_float(b[1]), __uint_as_float(b[2]), __uint_as_float(b[3])};
+          }
       }
-      if (live && o + 4 <= a.M) {
-        const u32x4 b = ld_x4(reinterpret_cast<const uint8_t*>(base + o));
-        f32x4 y;
+    };
+    if (m_first < a.M) fetch(m_first);         // on their way while v is summed
+    u32x4 v[CT][RC][3];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(b[e]) + tile.scale * acc[e];
-        __builtin_memcpy(__builtin_assume_aligned(out + o, 4), &y, 16);
-      } else if (live) {
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (o + e < a.M) out[o + e] = base[o + e] + tile.scale * acc[e];
+      for (int q = 0; q < RC; ++q) {
+        const int j = kLStep * q + 8 * g;
+        float sum[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
+        if (j < tile.rank) {
+          const float* part = a.part + static_cast<int64_t>(tile.row[c]) * a.max_rank + j;
+          const int64_t step = static_cast<int64_t>(a.n) * a.max_rank;
+#pragma unroll 4
+          for (int s = 0; s < a.splits; ++s) {
+            float one[8];
+            values8(part + s * step, one);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) sum[e] += one[e];
+          }
+        }
+        // (ranks behind the adapter's have sums of others' weights)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum[e] = j + e < tile.rank ? sum[e] : 0.0f;
+        split8<3>(sum, v[c][q]);
+      }
+    const bool cuts = tile.rank % kLStep != 0;   // uniform
+    for (int64_t m0 = m_first; m0 < a.M; m0 += m_step) {
+      if (m0 > m_first) fetch(m0);
+#pragma unroll
+      for (int t = 0; t < kAhead; ++t) {
+        f32x4 acc[CT];
+#pragma unroll
+        for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < RC; ++q) {
+          if (kLStep * q < tile.rank) {        // uniform
+            if (cuts) w[t][q].cut(tile.rank - kLStep * q - 8 * g);
+            u32x4 wp[W::kParts];
+            w[t][q].split(wp);
+#pragma unroll
+            for (int c = 0; c < CT; ++c) acc[c] = multiply<W::kParts>(wp, v[c][q], acc[c]);
+          }
+        }
+        const int64_t o = m0 + 16 * t;
+#pragma unroll
+        for (int c = 0; c < CT; ++c) {
+          if (live[c] && o + 4 * g + 4 <= a.M) {
+            f32x4 y;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[e] = old[t][c][e] + tile.scale * acc[c][e];
+            __builtin_memcpy(__builtin_assume_aligned(out[c] + o, 4), &y, 16);
+          } else if (live[c]) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (o + 4 * g + e < a.M) out[c][o + e] = base[c][o + e] + tile.scale * acc[c][e];
+          }
+        }
       }
     }
   }
 }
 
-// Launch shape. Ranges of K until the chip is filled, of two products a wave
-// at least; slices of M likewise, of 64 outputs at least.
+// Launch shape. How many tiles there are the host cannot see: it counts on
+// rows of their own adapters in one block of rows, of one adapter beyond.
+// Ranges of K until the chip is filled, of two products a wave at least, and
+// slices of M likewise. Of many rows tiles take 32, which halves the reads of
+// the weights.
 struct LoraShape {
-  int blocks, leads, splits, steps, slices;
+  int blocks, leads, groups, splits, steps, slices, ct;
 };
-inline LoraShape lora_shape(int64_t n, int64_t K, int64_t M) {
+inline LoraShape lora_shape(int64_t n, int64_t K, int64_t M, int max_rank) {
   LoraShape s;
+  s.ct = n >= 1024 && max_rank <= 64 ? 2 : 1;
   s.blocks = static_cast<int>((n + kLBlock - 1) / kLBlock);
-  s.leads = s.blocks <= 8 ? 64 : s.blocks <= 32 ? 16 : 4;
-  const int64_t tiles = (n + kLTile - 1) / kLTile, want = (4 * kCus + tiles - 1) / tiles;
-  const int64_t steps = (K + kLStep - 1) / kLStep, most = (steps + 2 * kLWaves - 1) / (2 * kLWaves);
+  s.leads = s.blocks <= 8 ? 1 : s.blocks <= 32 ? 4 : kLColumns * s.ct;   // rows of a block that a workgroup looks for tiles at
+  const int rows = n < kLBlock ? static_cast<int>(n) : kLBlock;
+  s.groups = (rows + s.leads - 1) / s.leads;
+  int64_t tiles = (n + kLColumns * s.ct - 1) / (kLColumns * s.ct);
+  if (tiles < rows) tiles = rows;
+  const int64_t want = (2 * kCus + tiles - 1) / tiles;
+  const int64_t steps = (K + kLStep - 1) / kLStep, most = (steps + 2 * kAWaves - 1) / (2 * kAWaves);
   int64_t splits = want < most ? want : most;
   if (splits > 16) splits = 16;
-  s.steps = static_cast<int>((steps + splits * kLWaves - 1) / (splits * kLWaves));
-  s.splits = static_cast<int>((steps + static_cast<int64_t>(s.steps) * kLWaves - 1) / (s.steps * kLWaves));
-  const int64_t groups = (M + 63) / 64;
-  s.slices = static_cast<int>(want < groups ? want : groups);
+  s.steps = static_cast<int>((steps + splits * kAWaves - 1) / (splits * kAWaves));
+  s.splits = static_cast<int>((steps + static_cast<int64_t>(s.steps) * kAWaves - 1) / (s.steps * kAWaves));
+  const int64_t pieces = (M + 32 * kBWaves - 1) / (32 * kBWaves);
+  s.slices = static_cast<int>(2 * want < pieces ? 2 * want : pieces);
   if (s.slices > 64) s.slices = 64;
   return s;
 }
 
 int64_t lora_bytes(int64_t n, int64_t K, int64_t M, int max_rank) {
   if (n == 0) return 0;
-  return lora_shape(n, K, M).splits * n * max_rank * static_cast<int64_t>(sizeof(float));
+  return lora_shape(n, K, M, max_rank).splits * n * max_rank * static_cast<int64_t>(sizeof(float));
 }
 
-template <int TYPE, int RT>
+template <int TYPE, int RT, int RC, int CT>
 int launch_ranks(const LoraArgs& a, const LoraShape& s, hipStream_t st) {
-  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, RT>), dim3(s.blocks, s.leads, s.splits), dim3(kLThreads), 0, st, a);
+  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, RT, CT>), dim3(s.blocks, s.groups, s.splits), dim3(kAWaves * kWave), 0, st, a);
   const int rc = check_launch();
   if (rc) return rc;
-  constexpr int RC = (RT + 1) / 2;
-  const dim3 grid(s.blocks, s.leads, s.slices);
-  if constexpr (RT == 8) {
-    if (a.max_rank > 128) {
-      hipLaunchKernelGGL((lora_expand_kernel<TYPE, 2 * RC>), grid, dim3(kLThreads), 0, st, a);
-      return check_launch();
-    }
-  }
-  hipLaunchKernelGGL((lora_expand_kernel<TYPE, RC>), grid, dim3(kLThreads), 0, st, a);
+  hipLaunchKernelGGL((lora_expand_kernel<TYPE, RC, CT>), dim3(s.blocks, s.groups, s.slices), dim3(kBWaves * kWave), 0, st, a);
   return check_launch();
 }
 
 template <int TYPE>
 int launch_type(const LoraArgs& given, hipStream_t st) {
   LoraArgs a = given;
-  const LoraShape s = lora_shape(a.n, a.K, a.M);
+  const LoraShape s = lora_shape(a.n, a.K, a.M, a.max_rank);
   a.splits = s.splits;
   a.steps = s.steps;
-  if (a.max_rank <= 16) return launch_ranks<TYPE, 1>(a, s, st);
-  if (a.max_rank <= 32) return launch_ranks<TYPE, 2>(a, s, st);
-  if (a.max_rank <= 64) return launch_ranks<TYPE, 4>(a, s, st);
-  return launch_ranks<TYPE, 8>(a, s, st);
+  a.leads = s.leads;
+  if (s.ct == 2) {
+    if (a.max_rank <= 16) return launch_ranks<TYPE, 1, 1, 2>(a, s, st);
+    if (a.max_rank <= 32) return launch_ranks<TYPE, 2, 1, 2>(a, s, st);
+    return launch_ranks<TYPE, 4, 2, 2>(a, s, st);
+  }
+  if (a.max_rank <= 16) return launch_ranks<TYPE, 1, 1, 1>(a, s, st);
+  if (a.max_rank <= 32) return launch_ranks<TYPE, 2, 1, 1>(a, s, st);
+  if (a.max_rank <= 64) return launch_ranks<TYPE, 4, 2, 1>(a, s, st);
+  if (a.max_rank <= 128) return launch_ranks<TYPE, 8, 4, 1>(a, s, st);
+  return launch_ranks<TYPE, 8, 8, 1>(a, s, st);
 }
 
 int launch_lora(int type, const LoraArgs& a, hipStream_t st) {
