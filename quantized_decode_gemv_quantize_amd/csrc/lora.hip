@@ -28,6 +28,9 @@ constexpr int kLBlock = 64;                    // consecutive rows among which t
 constexpr int kLStep = 32;                     // of K, or ranks, a matrix product
 constexpr int kLColumns = 16;                  // rows of x a matrix product
 constexpr int kAWaves = 8, kBWaves = 4;        // of a workgroup of shrink and of expand
+constexpr int kChunk = kAWaves * kLStep;       // of K that a workgroup of shrink takes at a time
+constexpr int kPiece = kBWaves * 64;           // outputs that one of expand takes at a time
+constexpr int kPad = 4;                        // floats behind a row of either in LDS: rows a bank group apart
 
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -109,12 +112,11 @@ __device__ __forceinline__ f32x4 multiply(const u32x4 (&w)[PARTS], const u32x4 (
 }
 
 // The tile that row `lead` of a block of 64 leads, the same in every wave.
-template <int CT>
 struct Tile {
   int adapter;             // -1: none
   int rank;
   int count;               // rows; 0: none
-  int row[CT];             // of the lane's columns lane % 16 + 16 c; the first one's behind count
+  int row;                 // in lane i that of row i of the tile, the first one's behind count
   float scale;
 };
 
@@ -132,9 +134,9 @@ __device__ __forceinline__ int block_ids(const LoraArgs& a, int block) {
 }
 
 template <int CT>
-__device__ __forceinline__ Tile<CT> tile_of(const LoraArgs& a, int block, int ids, int lead) {
+__device__ __forceinline__ Tile tile_of(const LoraArgs& a, int block, int ids, int lead) {
   constexpr int kRows = kLColumns * CT;
-  Tile<CT> tile{__builtin_amdgcn_readlane(ids, lead), 0, 0, {}, 0.0f};
+  Tile tile{__builtin_amdgcn_readlane(ids, lead), 0, 0, 0, 0.0f};
   const uint64_t same = __ballot(ids == tile.adapter);
   const int ahead = __builtin_popcountll(same & ((uint64_t(1) << lead) - 1));
   if (tile.adapter == -2 || ahead % kRows) return tile;
@@ -143,11 +145,7 @@ __device__ __forceinline__ Tile<CT> tile_of(const LoraArgs& a, int block, int id
   const int lane = lane_id(), mine = __builtin_popcountll(same & ((uint64_t(1) << lane) - 1)) - ahead;
   const bool member = ids == tile.adapter && mine >= 0 && mine < kRows;
   const int pushed = __builtin_amdgcn_ds_permute(4 * (member ? mine : kWave - 1), lane);
-#pragma unroll
-  for (int c = 0; c < CT; ++c) {
-    const int column = lane % kLColumns + kLColumns * c;
-    tile.row[c] = block * kLBlock + __shfl(pushed, column < tile.count ? column : 0);
-  }
+  tile.row = block * kLBlock + __shfl(pushed, lane < tile.count ? lane : 0);
   if (tile.adapter >= 0) {
     const int r = a.rank ? a.rank[tile.adapter] : a.max_rank;
     tile.rank = r < 0 ? 0 : r > a.max_rank ? a.max_rank : r;
@@ -156,36 +154,44 @@ __device__ __forceinline__ Tile<CT> tile_of(const LoraArgs& a, int block, int id
   return tile;
 }
 
-// Eight fp32 values at element i of a row (4-byte aligned).
-__device__ __forceinline__ void values8(const float* p, float (&v)[8]) {
-  const u32x4 a = ld_x4(reinterpret_cast<const uint8_t*>(p)), b = ld_x4(reinterpret_cast<const uint8_t*>(p + 4));
+__device__ __forceinline__ f32x4 ld_f4(const float* p) {   // 4-byte aligned
+  return __builtin_bit_cast(f32x4, ld_x4(reinterpret_cast<const uint8_t*>(p)));
+}
+__device__ __forceinline__ void eight(f32x4 a, f32x4 b, float (&v)[8]) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) {
-    v[e] = __uint_as_float(a[e]);
-    v[e + 4] = __uint_as_float(b[e]);
+    v[e] = a[e];
+    v[e + 4] = b[e];
   }
 }
 
-// v of a tile over a range of K, 16 RT ranks at a time. The waves share the
-// range. Columns behind the tile's count and ranks behind the adapter's repeat
-// real ones, so that no load waits for a condition; what comes of them is
-// not stored, or not used.
+// v of a tile over a range of K, 16 RT ranks at a time. The workgroup takes
+// kChunk of K after the other: rows of x go through LDS, as a row's values side
+// by side are what memory reads best and 8 of each of 16 rows what the
+// products take; each wave multiplies 32 of the chunk. The next chunk's loads
+// are on their way meanwhile. Columns behind the tile's count and ranks
+// behind the adapter's repeat real ones, so that no load waits for a condition;
+// what comes of them is not stored, or not used.
 template <int TYPE, int RT, int CT>
 __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a) {
   using W = Weights<TYPE>;
-  constexpr int kRegs = 8 * CT + 4 * W::kQuads * RT, kAhead = kRegs <= 24 ? 4 : kRegs <= 48 ? 2 : 1;   // steps on their way
-  __shared__ f32x4 lds[kAWaves][RT][kWave];
+  constexpr int kRows = kLColumns * CT, kPer = kRows / kAWaves, kLine = kChunk + kPad;
+  __shared__ union {
+    float x[2][kRows][kLine];
+    f32x4 sums[kAWaves][RT][kWave];
+  } lds;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / 16;
   const int block = blockIdx.x, split = blockIdx.z;
   const int ids = block_ids(a, block);
-  const int steps = static_cast<int>((a.K + kLStep - 1) / kLStep), whole = static_cast<int>(a.K / kLStep);
-  const int s0 = (split * kAWaves + wave) * a.steps, s1 = s0 + a.steps < steps ? s0 + a.steps : steps;
+  const int chunks = static_cast<int>((a.K + kChunk - 1) / kChunk);
+  const int c0 = split * a.steps, c1 = c0 + a.steps < chunks ? c0 + a.steps : chunks;
   for (int lead = blockIdx.y * a.leads, end = lead + a.leads; lead < end; ++lead) {
-    const Tile<CT> tile = tile_of<CT>(a, block, ids, lead);
+    const Tile tile = tile_of<CT>(a, block, ids, lead);
     if (tile.count == 0 || tile.rank == 0) continue;       // uniform
-    const float* x[CT];
+    const float* x[kPer];                      // the wave's rows of the tile
 #pragma unroll
-    for (int c = 0; c < CT; ++c) x[c] = a.x + tile.row[c] * a.ldx + 8 * g;
+    for (int i = 0; i < kPer; ++i)
+      x[i] = a.x + static_cast<int64_t>(__builtin_amdgcn_readlane(tile.row, wave + kAWaves * i)) * a.ldx + 4 * lane;
     const uint8_t* A = a.A + tile.adapter * a.stride_a * W::kBytes;
     for (int r0 = 0; r0 < tile.rank; r0 += 16 * RT) {
       f32x4 acc[RT][CT];
@@ -193,185 +199,185 @@ __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
         const int j = r0 + 16 * t + lane % 16;
-        w0[t] = (j < tile.rank ? j : tile.rank - 1) * a.K + 8 * g;
+        w0[t] = (j < tile.rank ? j : tile.rank - 1) * a.K;
 #pragma unroll
         for (int c = 0; c < CT; ++c) acc[t][c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       }
-      const auto products = [&](const float (&v)[CT][8], W (&w)[RT]) QMV_INLINE {
-        u32x4 xp[CT][3];
+      f32x4 next[kPer];
+      W w[RT];
+      const auto fetch = [&](int chunk) QMV_INLINE {       // values behind K are 0 and meet real weights
+        const int64_t k = static_cast<int64_t>(chunk) * kChunk, kw = k + kLStep * wave + 8 * g;
 #pragma unroll
-        for (int c = 0; c < CT; ++c) split8<3>(v[c], xp[c]);
+        for (int i = 0; i < kPer; ++i)
+          if (wave + kAWaves * i < tile.count)             // uniform
+            next[i] = k + 4 * lane < a.K ? ld_f4(x[i] + k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-          if (RT == 1 || r0 + 16 * t < tile.rank) {        // uniform
-            u32x4 wp[W::kParts];
-            w[t].split(wp);
-#pragma unroll
-            for (int c = 0; c < CT; ++c) acc[t][c] = multiply<W::kParts>(wp, xp[c], acc[t][c]);
-          }
+          if (RT == 1 || r0 + 16 * t < tile.rank) w[t].load(A, w0[t] + (kw < a.K ? kw : 0));
       };
-      int s = s0;
-      for (const int last = s1 < whole ? s1 : whole; s < last; s += kAhead) {
-        float v[kAhead][CT][8];
-        W w[kAhead][RT];
+      if (c0 < c1) fetch(c0);
+      for (int c = c0; c < c1; ++c) {
+        float(*at)[kLine] = lds.x[c & 1];
 #pragma unroll
-        for (int q = 0; q < kAhead; ++q) {
-          const int k = (s + q < last ? s + q : last - 1) * kLStep;
+        for (int i = 0; i < kPer; ++i)
+          if (wave + kAWaves * i < tile.count) *reinterpret_cast<f32x4*>(&at[wave + kAWaves * i][4 * lane]) = next[i];
+        u32x4 wp[RT][W::kParts];
 #pragma unroll
-          for (int c = 0; c < CT; ++c) values8(x[c] + k, v[q][c]);
+        for (int t = 0; t < RT; ++t)
+          if (RT == 1 || r0 + 16 * t < tile.rank) w[t].split(wp[t]);
+        if (c + 1 < c1) fetch(c + 1);
+        __syncthreads();                       // (the buffer was read two chunks ago, before the last barrier)
+#pragma unroll
+        for (int q = 0; q < CT; ++q) {
+          const int column = lane % kLColumns + kLColumns * q;
+          const float* from = &at[column < tile.count ? column : 0][kLStep * wave + 8 * g];
+          float v[8];
+          eight(*reinterpret_cast<const f32x4*>(from), *reinterpret_cast<const f32x4*>(from + 4), v);
+          u32x4 xp[3];
+          split8<3>(v, xp);
 #pragma unroll
           for (int t = 0; t < RT; ++t)
-            if (RT == 1 || r0 + 16 * t < tile.rank) w[q][t].load(A, w0[t] + k);
+            if (RT == 1 || r0 + 16 * t < tile.rank) acc[t][q] = multiply<W::kParts>(wp[t], xp, acc[t][q]);
         }
-#pragma unroll
-        for (int q = 0; q < kAhead; ++q)
-          if (s + q < last) products(v[q], w[q]);           // uniform
-      }
-      if (whole < s1 && s0 <= whole) {                     // the rest of K: 8, 16 or 24 values
-        float v[1][CT][8];
-        W w[1][RT];
-        const int k = whole * kLStep, back = k + 8 * g < a.K ? 0 : 8 * g;   // lanes behind it repeat the first's, times 0
-#pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          values8(x[c] + k - back, v[0][c]);
-#pragma unroll
-          for (int e = 0; e < 8; ++e) v[0][c][e] = back ? 0.0f : v[0][c][e];
-        }
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          w[0][t].load(A, w0[t] + k - back);
-          w[0][t].cut(back ? 0 : 8);
-        }
-        products(v[0], w[0]);
       }
 #pragma unroll
       for (int c = 0; c < CT; ++c) {
-        __syncthreads();                       // the sums before are read
+        __syncthreads();                       // LDS is read
 #pragma unroll
-        for (int t = 0; t < RT; ++t) lds[wave][t][lane] = acc[t][c];
+        for (int t = 0; t < RT; ++t) lds.sums[wave][t][lane] = acc[t][c];
         __syncthreads();
+        const int column = lane % kLColumns + kLColumns * c, row = __shfl(tile.row, column);
         for (int t = wave; t < RT; t += kAWaves) {
           const int j = r0 + 16 * t + 4 * g;
-          f32x4 sum = lds[0][t][lane];
+          f32x4 sum = lds.sums[0][t][lane];
 #pragma unroll
-          for (int w = 1; w < kAWaves; ++w) sum += lds[w][t][lane];
-          if (lane % kLColumns + kLColumns * c < tile.count && j < a.max_rank)
-            *reinterpret_cast<f32x4*>(a.part + (static_cast<int64_t>(split) * a.n + tile.row[c]) * a.max_rank + j) = sum;
+          for (int w = 1; w < kAWaves; ++w) sum += lds.sums[w][t][lane];
+          if (column < tile.count && j < a.max_rank)
+            *reinterpret_cast<f32x4*>(a.part + (static_cast<int64_t>(split) * a.n + row) * a.max_rank + j) = sum;
         }
       }
+      __syncthreads();                         // the sums are read
     }
   }
 }
 
-// base + scale * B v of a tile, for a slice of M; up to 32 RC ranks.
+// base + scale * B v of a tile, for a slice of M; up to 32 RC ranks. The
+// workgroup takes kPiece outputs after the other; products go to LDS, and each
+// wave adds whole rows of them to base: 1 KB side by side a load and a store,
+// where the products' own layout has 64 bytes of each of 16 rows.
 template <int TYPE, int RC, int CT>
 __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a) {
   using W = Weights<TYPE>;
-  constexpr int kAhead = RC * W::kQuads * (CT + 1) <= 4 ? 4 : RC * W::kQuads <= 4 ? 2 : 1;   // tiles of 16 outputs on their way
+  constexpr int kRows = kLColumns * CT, kPer = kRows / kBWaves, kTiles = kPiece / kBWaves / 16, kLine = kPiece + kPad;
+  __shared__ float lds[kRows][kLine];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / 16;
   const int block = blockIdx.x;
   const int ids = block_ids(a, block);
-  constexpr int kPiece = 16 * kAhead;          // outputs a wave takes at a time, side by side
-  const int64_t m_first = (static_cast<int64_t>(blockIdx.z) * kBWaves + wave) * kPiece, m_step = static_cast<int64_t>(gridDim.z) * kBWaves * kPiece;
+  const int64_t m_first = static_cast<int64_t>(blockIdx.z) * kPiece, m_step = static_cast<int64_t>(gridDim.z) * kPiece;
   for (int lead = blockIdx.y * a.leads, end = lead + a.leads; lead < end; ++lead) {
-    const Tile<CT> tile = tile_of<CT>(a, block, ids, lead);
+    const Tile tile = tile_of<CT>(a, block, ids, lead);
     if (tile.count == 0 || (tile.rank == 0 && a.base == a.out)) continue;   // uniform
-    const float* base[CT];
-    float* out[CT];
-    bool live[CT];
-#pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      live[c] = lane % kLColumns + kLColumns * c < tile.count;
-      base[c] = a.base + tile.row[c] * a.ldb + 4 * g;
-      out[c] = a.out + tile.row[c] * a.ldo + 4 * g;
-    }
     const uint8_t* B = a.B + (tile.adapter < 0 ? 0 : tile.adapter) * a.stride_b * W::kBytes;
-    W w[kAhead][RC];
-    f32x4 old[kAhead][CT];
+    W w[kTiles][RC];
     const auto fetch = [&](int64_t m0) QMV_INLINE {
 #pragma unroll
-      for (int t = 0; t < kAhead; ++t) {
-        const int64_t m = m0 + 16 * t + lane % 16, row = (m < a.M ? m : a.M - 1) * a.max_rank;
+      for (int t = 0; t < kTiles; ++t) {
+        const int64_t m = m0 + 64 * wave + 16 * t + lane % 16, row = (m < a.M ? m : a.M - 1) * a.max_rank;
 #pragma unroll
         for (int q = 0; q < RC; ++q) {
           const int j = kLStep * q + 8 * g;
           if (kLStep * q < tile.rank) w[t][q].load(B, row + (j < a.max_rank ? j : 0));   // uniform
         }
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-          if (live[c] && m0 + 16 * t + 4 * g + 4 <= a.M) {
-            const u32x4 b = ld_x4(reinterpret_cast<const uint8_t*>(base[c] + m0 + 16 * t));
-            old[t][c] = f32x4{__uint_as_float(b[0]), __uint_as_float(b[1]), __uint_as_float(b[2]), __uint_as_float(b[3])};
-          }
       }
     };
     if (m_first < a.M) fetch(m_first);         // on their way while v is summed
     u32x4 v[CT][RC][3];
 #pragma unroll
-    for (int c = 0; c < CT; ++c)
+    for (int c = 0; c < CT; ++c) {
+      const float* part = a.part + static_cast<int64_t>(__shfl(tile.row, lane % kLColumns + kLColumns * c)) * a.max_rank;
+      const int64_t step = static_cast<int64_t>(a.n) * a.max_rank;
 #pragma unroll
       for (int q = 0; q < RC; ++q) {
         const int j = kLStep * q + 8 * g;
         float sum[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-        if (j < tile.rank) {
-          const float* part = a.part + static_cast<int64_t>(tile.row[c]) * a.max_rank + j;
-          const int64_t step = static_cast<int64_t>(a.n) * a.max_rank;
+        if (j < tile.rank)
 #pragma unroll 4
           for (int s = 0; s < a.splits; ++s) {
             float one[8];
-            values8(part + s * step, one);
+            eight(ld_f4(part + s * step + j), ld_f4(part + s * step + j + 4), one);
 #pragma unroll
             for (int e = 0; e < 8; ++e) sum[e] += one[e];
           }
-        }
         // (ranks behind the adapter's have sums of others' weights)
 #pragma unroll
         for (int e = 0; e < 8; ++e) sum[e] = j + e < tile.rank ? sum[e] : 0.0f;
         split8<3>(sum, v[c][q]);
       }
+    }
     const bool cuts = tile.rank % kLStep != 0;   // uniform
     for (int64_t m0 = m_first; m0 < a.M; m0 += m_step) {
-      if (m0 > m_first) fetch(m0);
+      const int64_t o = m0 + 4 * lane;
+      f32x4 old[kPer];
+      const float* base[kPer];
+      float* out[kPer];
 #pragma unroll
-      for (int t = 0; t < kAhead; ++t) {
-        f32x4 acc[CT];
+      for (int i = 0; i < kPer; ++i) {
+        const int64_t row = __builtin_amdgcn_readlane(tile.row, wave + kBWaves * i);
+        base[i] = a.base + row * a.ldb + o;
+        out[i] = a.out + row * a.ldo + o;
+        if (wave + kBWaves * i < tile.count && o + 4 <= a.M) old[i] = ld_f4(base[i]);
+      }
+      if (tile.rank > 0) {                     // uniform
 #pragma unroll
-        for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        for (int t = 0; t < kTiles; ++t) {
+          f32x4 acc[CT];
 #pragma unroll
-        for (int q = 0; q < RC; ++q) {
-          if (kLStep * q < tile.rank) {        // uniform
-            if (cuts) w[t][q].cut(tile.rank - kLStep * q - 8 * g);
-            u32x4 wp[W::kParts];
-            w[t][q].split(wp);
+          for (int c = 0; c < CT; ++c) acc[c] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-            for (int c = 0; c < CT; ++c) acc[c] = multiply<W::kParts>(wp, v[c][q], acc[c]);
+          for (int q = 0; q < RC; ++q) {
+            if (kLStep * q < tile.rank) {      // uniform
+              if (cuts) w[t][q].cut(tile.rank - kLStep * q - 8 * g);
+              u32x4 wp[W::kParts];
+              w[t][q].split(wp);
+#pragma unroll
+              for (int c = 0; c < CT; ++c) acc[c] = multiply<W::kParts>(wp, v[c][q], acc[c]);
+            }
           }
+#pragma unroll
+          for (int c = 0; c < CT; ++c)
+            if (lane % kLColumns + kLColumns * c < tile.count)
+              *reinterpret_cast<f32x4*>(&lds[lane % kLColumns + kLColumns * c][64 * wave + 16 * t + 4 * g]) = acc[c];
         }
-        const int64_t o = m0 + 16 * t;
+        if (m0 + m_step < a.M) fetch(m0 + m_step);
+        __syncthreads();
+      }
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          if (live[c] && o + 4 * g + 4 <= a.M) {
-            f32x4 y;
+      for (int i = 0; i < kPer; ++i) {
+        if (wave + kBWaves * i >= tile.count) continue;    // uniform
+        f32x4 add{0.0f, 0.0f, 0.0f, 0.0f};
+        if (tile.rank > 0) add = *reinterpret_cast<const f32x4*>(&lds[wave + kBWaves * i][4 * lane]);
+        if (o + 4 <= a.M) {
+          f32x4 y;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = old[t][c][e] + tile.scale * acc[c][e];
-            __builtin_memcpy(__builtin_assume_aligned(out[c] + o, 4), &y, 16);
-          } else if (live[c]) {
+          for (int e = 0; e < 4; ++e) y[e] = tile.rank > 0 ? old[i][e] + tile.scale * add[e] : old[i][e];
+          __builtin_memcpy(__builtin_assume_aligned(out[i], 4), &y, 16);
+        } else {
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (o + 4 * g + e < a.M) out[c][o + e] = base[c][o + e] + tile.scale * acc[c][e];
-          }
+          for (int e = 0; e < 4; ++e)
+            if (o + e < a.M) out[i][e] = tile.rank > 0 ? base[i][e] + tile.scale * add[e] : base[i][e];
         }
       }
+      if (tile.rank > 0) __syncthreads();      // LDS is read
     }
   }
 }
 
 // Launch shape. How many tiles there are the host cannot see: it counts on
 // rows of their own adapters in one block of rows, of one adapter beyond.
-// Ranges of K until the chip is filled, of two products a wave at least, and
-// slices of M likewise. Of many rows tiles take 32, which halves the reads of
+// Ranges of K until the chip is filled, of two chunks at least, and slices of M
+// likewise. Of many rows tiles take 32, which halves the reads of
 // the weights.
 struct LoraShape {
   int blocks, leads, groups, splits, steps, slices, ct;
@@ -386,12 +392,12 @@ inline LoraShape lora_shape(int64_t n, int64_t K, int64_t M, int max_rank) {
   int64_t tiles = (n + kLColumns * s.ct - 1) / (kLColumns * s.ct);
   if (tiles < rows) tiles = rows;
   const int64_t want = (2 * kCus + tiles - 1) / tiles;
-  const int64_t steps = (K + kLStep - 1) / kLStep, most = (steps + 2 * kAWaves - 1) / (2 * kAWaves);
+  const int64_t chunks = (K + kChunk - 1) / kChunk, most = (chunks + 1) / 2;
   int64_t splits = want < most ? want : most;
   if (splits > 16) splits = 16;
-  s.steps = static_cast<int>((steps + splits * kAWaves - 1) / (splits * kAWaves));
-  s.splits = static_cast<int>((steps + static_cast<int64_t>(s.steps) * kAWaves - 1) / (s.steps * kAWaves));
-  const int64_t pieces = (M + 32 * kBWaves - 1) / (32 * kBWaves);
+  s.steps = static_cast<int>((chunks + splits - 1) / splits);
+  s.splits = static_cast<int>((chunks + s.steps - 1) / s.steps);
+  const int64_t pieces = (M + kPiece - 1) / kPiece;
   s.slices = static_cast<int>(2 * want < pieces ? 2 * want : pieces);
   if (s.slices > 64) s.slices = 64;
   return s;

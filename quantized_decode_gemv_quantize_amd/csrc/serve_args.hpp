@@ -63,7 +63,7 @@ struct LoraArgs {
   const int32_t* adapter;
   int64_t stride_a, stride_b, ldx, ldb, ldo, K, M;
   int n, n_seqs, n_adapters, max_rank;
-  int splits, steps;       // ranges of K, and a wave's part of one in steps
+  int splits, steps;       // ranges of K, and chunks of one
   int leads;               // rows of a block that a workgroup looks for tiles at
   float* part;             // [split][row][max_rank]
 };
