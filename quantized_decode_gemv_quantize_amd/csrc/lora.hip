@@ -268,8 +268,9 @@ __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a
 template <int TYPE, int RC, int CT>
 __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a) {
   using W = Weights<TYPE>;
-  constexpr int kRows = kLColumns * CT, kPer = kRows / kBWaves, kTiles = kPiece / kBWaves / 16, kLine = kPiece + kPad;
-  __shared__ float lds[kRows][kLine];
+  constexpr int kRuns = kPiece / (4 * kWave);   // of a row: four outputs a lane
+  constexpr int kRows = kLColumns * CT, kPer = kRows * kRuns / kBWaves, kTiles = kPiece / kBWaves / 16, kLine = kPiece + kPad;
+  __shared__ float lds[kRows][kLine], sums[kRows][kLStep * RC + kPad];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / 16;
   const int block = blockIdx.x;
   const int ids = block_ids(a, block);
@@ -291,43 +292,46 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
       }
     };
     if (m_first < a.M) fetch(m_first);         // on their way while v is summed
+    // v: each four ranks of a row summed by one thread, 0 behind the adapter's rank (the sums there are others')
+    constexpr int kRanks = kLStep * RC, kQuads = kRanks / 4;
+    for (int i = static_cast<int>(threadIdx.x); i < kRows * kQuads; i += kBWaves * kWave) {
+      const int c = i / kQuads, j = i % kQuads * 4;
+      const float* part = a.part + static_cast<int64_t>(__shfl(tile.row, c)) * a.max_rank + j;
+      const int64_t step = static_cast<int64_t>(a.n) * a.max_rank;
+      f32x4 sum{0.0f, 0.0f, 0.0f, 0.0f};
+      if (c < tile.count && j < tile.rank)
+#pragma unroll 8
+        for (int s = 0; s < a.splits; ++s) sum += ld_f4(part + s * step);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) sum[e] = j + e < tile.rank ? sum[e] : 0.0f;
+      *reinterpret_cast<f32x4*>(&sums[c][j]) = sum;
+    }
+    __syncthreads();
     u32x4 v[CT][RC][3];
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const float* part = a.part + static_cast<int64_t>(__shfl(tile.row, lane % kLColumns + kLColumns * c)) * a.max_rank;
-      const int64_t step = static_cast<int64_t>(a.n) * a.max_rank;
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int q = 0; q < RC; ++q) {
-        const int j = kLStep * q + 8 * g;
-        float sum[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = 0.0f;
-        if (j < tile.rank)
-#pragma unroll 4
-          for (int s = 0; s < a.splits; ++s) {
-            float one[8];
-            eight(ld_f4(part + s * step + j), ld_f4(part + s * step + j + 4), one);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) sum[e] += one[e];
-          }
-        // (ranks behind the adapter's have sums of others' weights)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum[e] = j + e < tile.rank ? sum[e] : 0.0f;
-        split8<3>(sum, v[c][q]);
+        const float* from = &sums[lane % kLColumns + kLColumns * c][kLStep * q + 8 * g];
+        float one[8];
+        eight(*reinterpret_cast<const f32x4*>(from), *reinterpret_cast<const f32x4*>(from + 4), one);
+        split8<3>(one, v[c][q]);
       }
-    }
+    __syncthreads();                           // (the next tile's sums)
     const bool cuts = tile.rank % kLStep != 0;   // uniform
     for (int64_t m0 = m_first; m0 < a.M; m0 += m_step) {
-      const int64_t o = m0 + 4 * lane;
       f32x4 old[kPer];
       const float* base[kPer];
       float* out[kPer];
+      int64_t o[kPer];
 #pragma unroll
-      for (int i = 0; i < kPer; ++i) {
-        const int64_t row = __builtin_amdgcn_readlane(tile.row, wave + kBWaves * i);
-        base[i] = a.base + row * a.ldb + o;
-        out[i] = a.out + row * a.ldo + o;
-        if (wave + kBWaves * i < tile.count && o + 4 <= a.M) old[i] = ld_f4(base[i]);
+      for (int i = 0; i < kPer; ++i) {         // the wave's runs of rows
+        const int run = wave + kBWaves * i;
+        const int64_t row = __builtin_amdgcn_readlane(tile.row, run / kRuns);
+        o[i] = m0 + run % kRuns * 4 * kWave + 4 * lane;
+        base[i] = a.base + row * a.ldb + o[i];
+        out[i] = a.out + row * a.ldo + o[i];
+        if (run / kRuns < tile.count && o[i] + 4 <= a.M) old[i] = ld_f4(base[i]);
       }
       if (tile.rank > 0) {                     // uniform
 #pragma unroll
@@ -355,10 +359,11 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
       }
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        if (wave + kBWaves * i >= tile.count) continue;    // uniform
+        const int run = wave + kBWaves * i;
+        if (run / kRuns >= tile.count) continue;           // uniform
         f32x4 add{0.0f, 0.0f, 0.0f, 0.0f};
-        if (tile.rank > 0) add = *reinterpret_cast<const f32x4*>(&lds[wave + kBWaves * i][4 * lane]);
-        if (o + 4 <= a.M) {
+        if (tile.rank > 0) add = *reinterpret_cast<const f32x4*>(&lds[run / kRuns][run % kRuns * 4 * kWave + 4 * lane]);
+        if (o[i] + 4 <= a.M) {
           f32x4 y;
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = tile.rank > 0 ? old[i][e] + tile.scale * add[e] : old[i][e];
@@ -366,7 +371,7 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
-            if (o + e < a.M) out[i][e] = tile.rank > 0 ? base[i][e] + tile.scale * add[e] : base[i][e];
+            if (o[i] + e < a.M) out[i][e] = tile.rank > 0 ? base[i][e] + tile.scale * add[e] : base[i][e];
         }
       }
       if (tile.rank > 0) __syncthreads();      // LDS is read
@@ -376,9 +381,13 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
 
 // Launch shape. How many tiles there are the host cannot see: it counts on
 // rows of their own adapters in one block of rows, of one adapter beyond.
-// Ranges of K until the chip is filled, of two chunks at least, and slices of M
-// likewise. Of many rows tiles take 32, which halves the reads of
-// the weights.
+// K is cut until every compute unit has a workgroup, in ranges of two chunks
+// at least, or two of them in ranges of four (64 rows of their own, K = 4096:
+// 4 ranges 34.6 us, 8 of two chunks 37.6; one row: 8.5 and 7.5; 4000 rows of
+// 14336: 5 ranges 98, 3 108). M is cut until every compute unit has two: 64 rows
+// by 14336 in 8 slices 34.6 us, in 4 50, in 16 54; 4000 by 4096 in 5 115, in 3
+// 129, in 10 126. Of many rows tiles take 32, which halves the reads of the
+// weights.
 struct LoraShape {
   int blocks, leads, groups, splits, steps, slices, ct;
 };
@@ -391,14 +400,16 @@ inline LoraShape lora_shape(int64_t n, int64_t K, int64_t M, int max_rank) {
   s.groups = (rows + s.leads - 1) / s.leads;
   int64_t tiles = (n + kLColumns * s.ct - 1) / (kLColumns * s.ct);
   if (tiles < rows) tiles = rows;
-  const int64_t want = (2 * kCus + tiles - 1) / tiles;
-  const int64_t chunks = (K + kChunk - 1) / kChunk, most = (chunks + 1) / 2;
-  int64_t splits = want < most ? want : most;
+  const auto fill = [&](int64_t groups) { return (groups + tiles - 1) / tiles; };
+  const int64_t chunks = (K + kChunk - 1) / kChunk, one = fill(kCus), two = fill(2 * kCus);
+  const int64_t few = (chunks + 1) / 2 < one ? (chunks + 1) / 2 : one, some = (chunks + 3) / 4;
+  int64_t splits = few > some ? few : some;
+  if (splits > two) splits = two;
   if (splits > 16) splits = 16;
   s.steps = static_cast<int>((chunks + splits - 1) / splits);
   s.splits = static_cast<int>((chunks + s.steps - 1) / s.steps);
   const int64_t pieces = (M + kPiece - 1) / kPiece;
-  s.slices = static_cast<int>(2 * want < pieces ? 2 * want : pieces);
+  s.slices = static_cast<int>(two < pieces ? two : pieces);
   if (s.slices > 64) s.slices = 64;
   return s;
 }
