@@ -182,15 +182,15 @@ static_assert(kUnit == 38);
 constexpr int kGridRows = 1 << 15;
 __device__ __forceinline__ int row_of_grid() { return static_cast<int>(blockIdx.z) * kGridRows + static_cast<int>(blockIdx.y); }
 
-// Histogram of a chunk. Lanes add to one of kCopies copies, so that those of
-// one bin meet less often (one copy 106 us, NN for four, for 256 rows of 151669).
-constexpr int kCopies = 4;
-
+// Bound by vector instructions (22 a filtered logit, most of them 64-bit) and
+// by the latencies of its steps; the LDS additions of lanes that meet in a bin
+// are hidden behind them (four copies of the bins to keep them apart gained
+// nothing: 57.3 and 58.6 us for 256 rows of 151669).
 __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
   __shared__ float tops[kSWaves];
-  __shared__ int ats[kSWaves], scans[kSWaves], next[kBins], cut, tokens;
+  __shared__ int ats[kSWaves], scans[kSWaves], next[kBins], ends[kBins], cut;
   __shared__ double sums[kSWaves];
-  __shared__ unsigned long long bins[kBins * kCopies];
+  __shared__ unsigned long long bins[kBins];
   const int tid = threadIdx.x, wave = tid >> 6, c = blockIdx.x, i0 = c * kChunk + 4 * tid;
   const int r = row_of_grid();
   if (r >= a.n_rows) return;
@@ -212,7 +212,9 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
       v[k] = i < a.vocab ? fmaxf(v[k], -INFINITY) : -INFINITY;
     }
   }
-  if (a.zeroed && !s.plain()) {                // the distribution's zeros, while the chunk is here
+  // (stores come last: a barrier would wait for those before it)
+  const auto zeros = [&]() QMV_INLINE {
+    if (!a.zeroed || s.plain()) return;        // the distribution's, while the chunk is here
     float* out = a.probs + r * a.ldp;
 #pragma unroll
     for (int k = 0; k < kSPer; k += 4) {
@@ -226,8 +228,11 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
           if (i + e < a.vocab) out[i + e] = 0.0f;
       }
     }
+  };
+  if (s.none) {                                // uniform
+    zeros();
+    return;
   }
-  if (s.none) return;                          // uniform
   float top = -INFINITY;
   int at = 0x7fffffff;
 #pragma unroll
@@ -244,8 +249,7 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
     ats[wave] = at;
   }
   if (filtered) {
-#pragma unroll
-    for (int k = 0; k < kCopies; ++k) bins[k * kSThreads + tid] = 0;
+    bins[tid] = 0;
     if (tid == 0) cut = -1;
   }
   __syncthreads();
@@ -261,16 +265,14 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
 #pragma unroll
     for (int k = 0; k < kSPer; ++k) x[k] = v[k] == top ? 0.0f : -INFINITY;
   }
-  const double dtop = top < INFINITY ? static_cast<double>(top) : 0.0;
+  const double dtop = top < INFINITY ? static_cast<double>(top) : 0.0, rate4 = 4.0 * s.rate, top_quarter = floor(dtop * rate4);
   if (any && !filtered) {
     const Exp2 exp2;                         // (in scalar registers that the other branch has no use for)
 #pragma unroll
     for (int k = 0; k < kSPer; ++k) sum += exp2((static_cast<double>(x[k]) - dtop) * s.rate);
   } else if (any) {
     const Units units;
-    unsigned long long* mine = bins + (tid & (kCopies - 1));
     constexpr long long kOne = (1ll << kSumBits) - (0x433ll << 52);   // a count, without the exponent of 2^52
-    const double rate4 = 4.0 * s.rate, top_quarter = floor(dtop * rate4);
 #pragma unroll
     for (int k = 0; k < kSPer; ++k) {
       const double d = static_cast<double>(x[k]);
@@ -280,18 +282,15 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
       // as 2^-64 of the largest at least: 2^-52 of the sum for all of them
       const double f = fmax(fma(d - dtop, rate4, down), -1.0);
       const unsigned long long add = static_cast<unsigned long long>(units(f) + kOne);
-      if (x[k] > -INFINITY) atomicAdd(mine + b * kCopies, add);
+      if (x[k] > -INFINITY) atomicAdd(&bins[b], add);
       bin[k] = x[k] > -INFINITY ? b : kBins;
     }
   }
-  const int64_t place = static_cast<int64_t>(r) * a.chunks + c;
   __syncthreads();
+  unsigned long long all = 0;
   if (filtered) {
-    // the bins of at most kTops tokens together, and these tokens bin by bin
-    unsigned long long all = 0;
-#pragma unroll
-    for (int k = 0; k < kCopies; ++k) all += bins[tid * kCopies + k];
-    chunk_bins(a)[place * kBins + tid] = all;
+    // the bins of at most kTops tokens together
+    all = bins[tid];
     sum = bin_sum_of(all, tid);
     const int count = static_cast<int>(all >> kSumBits);
     int up = wave_scan(count);
@@ -299,29 +298,42 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
     __syncthreads();
     for (int w = 0; w < wave; ++w) up += scans[w];
     next[tid] = up - count;
-    if (tid == kBins - 1) tokens = up;
+    ends[tid] = up;
     const uint64_t fits = __ballot(up <= kTops);
     if (lane_id() == 0 && fits) atomicMax(&cut, 64 * wave + 63 - __builtin_clzll(fits));
-    __syncthreads();
-    if (any) {
-      uint64_t* list = chunk_tops(a) + place * kTops;
-#pragma unroll
-      for (int k = 0; k < kSPer; ++k)
-        if (bin[k] <= cut) list[atomicAdd(&next[bin[k]], 1)] = place_of(taken(v[k]), i0 + (k / 4) * 4 * kSThreads + k % 4);
-    }
-    __syncthreads();
   }
   sum = wave_sum(sum);
   if ((tid & 63) == 0) sums[wave] = sum;
   __syncthreads();
+  const int64_t place = static_cast<int64_t>(r) * a.chunks + c;
   if (tid == 0) {
-    double all = 0.0;
+    double whole = 0.0;
 #pragma unroll
-    for (int w = 0; w < kSWaves; ++w) all += sums[w];
-    const bool lists = filtered && cut >= 0;   // (next has gone on to the end of each listed bin)
-    chunk_stats(a)[place] = ChunkStat{top, at, all, static_cast<int16_t>(lists ? next[cut] : 0), static_cast<int16_t>(lists ? cut : -1),
-                                      filtered ? tokens : 0};
+    for (int w = 0; w < kSWaves; ++w) whole += sums[w];
+    const bool lists = filtered && cut >= 0;
+    chunk_stats(a)[place] = ChunkStat{top, at, whole, static_cast<int16_t>(lists ? ends[cut] : 0), static_cast<int16_t>(lists ? cut : -1),
+                                      filtered ? ends[kBins - 1] : 0};
   }
+  if (filtered) {
+    chunk_bins(a)[place * kBins + tid] = all;
+    if (any) {                                 // their tokens, bin by bin
+      uint64_t* list = chunk_tops(a) + place * kTops;
+      // a lane's one after the other: few have more than four
+      const int last = cut;
+      uint32_t marks = 0;
+#pragma unroll
+      for (int k = 0; k < kSPer; ++k) marks |= bin[k] <= last ? 1u << k : 0u;
+      while (marks) {
+        const int k = __builtin_ctz(marks);
+        marks &= marks - 1;
+        const int i = i0 + (k / 4) * 4 * kSThreads + k % 4;
+        const float mine = fmaxf(row[i], -INFINITY);       // (out of registers, it would be 16 selects)
+        const int b = bin_of(mine, rate4, top, top_quarter);
+        list[atomicAdd(&next[b], 1)] = place_of(taken(mine), i);
+      }
+    }
+  }
+  zeros();
 }
 
 // exp(chunk_top - top) in weights, the factor between the chunk's sums and the row's.
