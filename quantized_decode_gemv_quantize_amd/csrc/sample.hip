@@ -35,7 +35,7 @@ constexpr int kBins = 256;                     // the last one: everything below
 constexpr int kDThreads = 512;
 constexpr int kDWaves = kDThreads / kWave;
 constexpr int kRank = 256;                     // tokens that are sorted, each by counting those before it
-constexpr int kArena = 6144;                   // tokens that are cut and drawn from in LDS
+constexpr int kArena = 5120;                   // tokens that are cut and drawn from in LDS
 constexpr int kTops = 256;                     // tokens that a chunk lists
 constexpr int kUnit = 38;                      // a bin's sum is in units of 2^-kUnit
 constexpr int kSumBits = 51;                   // and behind them its count
@@ -347,14 +347,16 @@ struct Running {                               // sums up to each bin's or cell'
   int count[kBins];
 };
 struct PickLds {
-  uint64_t arena[kArena];
-  Running bins, cells;
-  uint64_t few[kRank];
+  uint64_t arena[kArena];                      // places
+  double weights[kArena];                      // of those, once they are asked for
+  Running bins;
+  uint64_t few[kRank], sorted[kRank];
   unsigned long long cell_sum[kBins];
   uint32_t cell_count[kBins];
   double waves[kDWaves];
   int iwaves[kDWaves];
   int found, n, first, last;
+  uint32_t low;
   double kept;
 };
 struct ChunkShift {                            // of each chunk, in dynamic LDS
@@ -397,29 +399,6 @@ __device__ __forceinline__ double block_scan_d(double v, double* lds, double& to
     total += lds[w];
   }
   return before + (up - v);
-}
-
-// Running sums of the first kBins threads' values.
-__device__ __forceinline__ void run_up(double sum, int count, Running& to, PickLds& l) {
-  const int wave = threadIdx.x >> 6;
-  double up = wave_scan(sum);
-  int up_count = wave_scan(count);
-  __syncthreads();
-  if (lane_id() == kWave - 1) {
-    l.waves[wave] = up;
-    l.iwaves[wave] = up_count;
-  }
-  __syncthreads();
-  if (threadIdx.x < kBins) {
-#pragma unroll
-    for (int w = 0; w < kBins / kWave; ++w) {
-      up += w < wave ? l.waves[w] : 0.0;
-      up_count += w < wave ? l.iwaves[w] : 0;
-    }
-    to.sum[threadIdx.x] = up;
-    to.count[threadIdx.x] = up_count;
-  }
-  __syncthreads();
 }
 
 // First bin whose running count (k > 0) or sum reaches k or the goal; the
@@ -706,8 +685,100 @@ __device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int f
 
 // Whole units of a weight up to 1, as the low bits of a sum with 2^52.
 constexpr int kFine = 49;                      // 2^13 of them stay below 2^62
-__device__ __forceinline__ unsigned long long fine_units(double w) {
-  return static_cast<unsigned long long>(__double_as_longlong(__builtin_ldexp(w, kFine) + 0x1p52)) & ((1ull << 52) - 1);
+__device__ __forceinline__ unsigned long long units_of(double w, int unit) {
+  return static_cast<unsigned long long>(__double_as_longlong(__builtin_ldexp(w, unit) + 0x1p52)) & ((1ull << 52) - 1);
+}
+
+// The weights of the arena's n tokens, and the key of the lowest.
+__device__ __forceinline__ void weigh(const Exp2& exp2, const Row& row, int n, PickLds& l) {
+  constexpr int kAhead = 4;
+  uint32_t low = 0xFFFFFFFFu;
+  __syncthreads();
+  if (threadIdx.x == 0) l.low = 0xFFFFFFFFu;
+  __syncthreads();
+  for (int i0 = threadIdx.x; i0 < n; i0 += kDThreads * kAhead) {
+    double w[kAhead];
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q) {
+      const int i = i0 + kDThreads * q;
+      const float v = value_at(l.arena[i < n ? i : i0]);
+      w[q] = row.weight_of(exp2, v);
+      low = key_of(v) < low ? key_of(v) : low;
+    }
+#pragma unroll
+    for (int q = 0; q < kAhead; ++q)
+      if (i0 + kDThreads * q < n) l.weights[i0 + kDThreads * q] = w[q];
+  }
+  for (int mask = kWave / 2; mask > 0; mask >>= 1) {
+    const uint32_t other = static_cast<uint32_t>(__shfl_xor(static_cast<int>(low), mask));
+    low = other < low ? other : low;
+  }
+  if (lane_id() == 0) atomicMin(&l.low, low);
+  __syncthreads();
+}
+
+// Cells of tokens: their sums in units, and their number.
+__device__ __forceinline__ void clear_cells(PickLds& l) {
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kDThreads) {
+    l.cell_sum[i] = 0;
+    l.cell_count[i] = 0;
+  }
+  __syncthreads();
+}
+__device__ __forceinline__ void add_to_cell(PickLds& l, int cell, unsigned long long units) {
+  atomicAdd(&l.cell_sum[cell], units);
+  atomicAdd(&l.cell_count[cell], 1u);
+}
+struct CellFound {
+  int cell, count, ahead;                      // tokens in it and before it
+  double passed, total;                        // weight before it, and of all
+};
+// The first cell that hit(running sum, running count) holds for, the last one
+// that has a weight (by_weight) or tokens where it holds for none. Every wave
+// for itself, so that nothing has to be handed on.
+template <class Hit>
+__device__ __forceinline__ CellFound find_cell(const PickLds& l, int unit, bool by_weight, Hit hit) {
+  constexpr int kPer = kBins / kWave;
+  double sum[kPer], own = 0.0;
+  int count[kPer], own_count = 0;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    sum[e] = __builtin_ldexp(static_cast<double>(l.cell_sum[kPer * lane_id() + e]), -unit);
+    count[e] = static_cast<int>(l.cell_count[kPer * lane_id() + e]);
+    own += sum[e];
+    own_count += count[e];
+  }
+  const double up = wave_scan(own), start = up - own;
+  const int up_count = wave_scan(own_count), start_count = up_count - own_count;
+  double run = start;
+  int run_count = start_count, first = kPer, last = -1;
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) {
+    run += sum[e];
+    run_count += count[e];
+    const bool some = by_weight ? sum[e] > 0.0 : count[e] > 0;
+    first = first == kPer && some && hit(run, run_count) ? e : first;
+    last = some ? e : last;
+  }
+  const uint64_t hits = __ballot(first < kPer), somes = __ballot(last >= 0);
+  const int lane = hits ? __builtin_ctzll(hits) : somes ? 63 - __builtin_clzll(somes) : 0;
+  const int e = __builtin_amdgcn_readlane(hits ? first : last < 0 ? 0 : last, lane);
+  CellFound f;
+  f.cell = kPer * lane + e;
+  double passed = start;
+  int ahead = start_count, mine = count[0];
+#pragma unroll
+  for (int i = 0; i < kPer - 1; ++i) {
+    passed += i < e ? sum[i] : 0.0;
+    ahead += i < e ? count[i] : 0;
+    mine = i + 1 == e ? count[i + 1] : mine;
+  }
+  f.passed = __shfl(passed, lane);
+  f.ahead = __builtin_amdgcn_readlane(ahead, lane);
+  f.count = __builtin_amdgcn_readlane(mine, lane);
+  f.total = __shfl(up, kWave - 1);
+  return f;
 }
 
 // Where the border of a filter is looked for: `count` tokens, behind `ahead`
@@ -716,6 +787,7 @@ struct Search {
   Span g;
   int count, ahead, n;
   double passed;
+  bool weighed;
 };
 
 // The last place kept by top-k (k > 0: the k-th token) or by top-p (the last
@@ -728,66 +800,60 @@ __device__ __forceinline__ uint64_t find_border(const SampleArgs& a, const Exp2&
   Span g = s.g;
   int count = s.count, ahead = s.ahead, n = s.n;
   double passed = s.passed;
-  const uint64_t* list = l.arena;
+  bool weighed = s.weighed;
 #pragma unroll 1
   while (true) {
     if (n < 0 && count <= kArena) n = collect(a, row, g, l);
     if (count <= kRank) break;
+    if (n >= 0 && !weighed) {
+      weigh(exp2, row, n, l);
+      weighed = true;
+    }
     const uint64_t wide = g.hi - g.lo;
     const int bits = 64 - __builtin_clzll(wide | 1), shift = bits > 8 ? bits - 8 : 0;   // at most kBins cells
-    __syncthreads();
-    if (tid < kBins) {
-      l.cell_sum[tid] = 0;
-      l.cell_count[tid] = 0;
-    }
-    __syncthreads();
     // 2^24 tokens at most, none above the weight of the first place
     int most;
     (void)__builtin_frexp(row.weight_of(exp2, value_at(g.lo)), &most);
-    const auto add = [&](uint64_t at, float v) QMV_INLINE {
-      const int cell = static_cast<int>((at - g.lo) >> shift);
-      const double w = __builtin_ldexp(row.weight_of(exp2, v), kUnit - most) + 0x1p52;
-      atomicAdd(&l.cell_sum[cell], static_cast<unsigned long long>(__double_as_longlong(w) & ((1ll << 52) - 1)));
-      atomicAdd(&l.cell_count[cell], 1u);
-    };
+    const int unit = kUnit - most;
+    clear_cells(l);
     if (n >= 0) {
       for (int i = tid; i < n; i += kDThreads) {
-        const uint64_t at = list[i];
-        if (at >= g.lo && at <= g.hi) add(at, value_at(at));
+        const uint64_t at = l.arena[i];
+        if (at >= g.lo && at <= g.hi) add_to_cell(l, static_cast<int>((at - g.lo) >> shift), units_of(l.weights[i], unit));
       }
     } else {
-      each_of_row(a, row, g, add);
+      each_of_row(a, row, g, [&](uint64_t at, float v) QMV_INLINE {
+        add_to_cell(l, static_cast<int>((at - g.lo) >> shift), units_of(row.weight_of(exp2, v), unit));
+      });
     }
     __syncthreads();
-    run_up(tid < kBins ? __builtin_ldexp(static_cast<double>(l.cell_sum[tid]), most - kUnit) : 0.0,
-           tid < kBins ? static_cast<int>(l.cell_count[tid]) : 0, l.cells, l);
-    const int cell = crossing(l.cells, k > 0 ? k - ahead : 0, goal - passed, l);
-    const int before = cell > 0 ? l.cells.count[cell - 1] : 0;
-    g.lo += static_cast<uint64_t>(cell) << shift;
+    const CellFound f = find_cell(l, unit, false, [&](double sum, int tokens) QMV_INLINE {
+      return k > 0 ? ahead + tokens >= k : passed + sum >= goal;
+    });
+    g.lo += static_cast<uint64_t>(f.cell) << shift;
     const uint64_t end = g.lo + ((uint64_t(1) << shift) - 1);
     g.hi = end < g.hi ? end : g.hi;
-    passed += cell > 0 ? l.cells.sum[cell - 1] : 0.0;
-    ahead += before;
-    count = l.cells.count[cell] - before;
+    passed += f.passed;
+    ahead += f.ahead;
+    count = f.count;
   }
   s.n = n == whole ? n : -1;
-  // the few, sorted in the cells' place
-  uint64_t* few = l.few;
-  uint64_t* sorted = reinterpret_cast<uint64_t*>(l.cells.sum);
+  s.weighed = weighed;
+  // the few, sorted
   __syncthreads();
   if (tid == 0) l.n = 0;
   __syncthreads();
   for (int i = tid; i < n; i += kDThreads) {
-    const uint64_t at = list[i];
+    const uint64_t at = l.arena[i];
     if (at >= g.lo && at <= g.hi) {
       const int to = atomicAdd(&l.n, 1);
-      if (to < kRank) few[to] = at;
+      if (to < kRank) l.few[to] = at;
     }
   }
   __syncthreads();
   const int m = l.n < kRank ? l.n : kRank;
-  sort_few(few, sorted, m, l);
-  const uint64_t mine = tid < m ? sorted[tid] : 0;
+  sort_few(l.few, l.sorted, m, l);
+  const uint64_t mine = tid < m ? l.sorted[tid] : 0;
   const double w = tid < m ? row.weight_of(exp2, value_at(mine)) : 0.0;
   double total;
   const double before = passed + block_scan_d(w, l.waves, total);
@@ -800,7 +866,7 @@ __device__ __forceinline__ uint64_t find_border(const SampleArgs& a, const Exp2&
   if (tid == last) l.kept = before + w;
   __syncthreads();
   kept = l.kept;
-  return sorted[last];
+  return l.sorted[last];
 }
 
 // Where a row's draw stands.
@@ -816,8 +882,8 @@ struct Drawn {
 __device__ __forceinline__ Drawn draw_short(const Exp2& exp2, const Row& row, int count, double all, float u, float* probs, PickLds& l) {
   const int tid = threadIdx.x;
   const Settings& s = row.s;
-  uint64_t* sorted = l.arena + kRank;
-  double* weights = reinterpret_cast<double*>(l.arena + 2 * kRank);
+  uint64_t* sorted = l.sorted;
+  double* weights = l.weights;
   sort_few(l.arena, sorted, count, l);
   const int k = s.k > 0 && s.k < count ? s.k : count;
   const uint64_t at = tid < k ? sorted[tid] : 0;
@@ -913,12 +979,12 @@ __device__ __forceinline__ uint64_t far_border(const SampleArgs& a, const Exp2& 
     if (turn == 0 ? s.k == 0 || s.k >= tokens : s.p >= 1.0) continue;   // uniform
     const int k = turn == 0 ? s.k : 0;
     const double goal = s.p * total;
-    Search search{Span{first_place(key_of(row.top)), ~uint64_t(0)}, listed, 0, listed, 0.0};
+    Search search{Span{first_place(key_of(row.top)), last_place(l.low)}, listed, 0, listed, 0.0, listed > 0};
     if (listed == 0) {
       of = crossing(l.bins, k, goal, l);
       const int ahead = of > 0 ? l.bins.count[of - 1] : 0, count = l.bins.count[of] - ahead;
       const double passed = of > 0 ? l.bins.sum[of - 1] : 0.0;
-      search = Search{bin_span(row, of), count, ahead, count <= kArena ? gather(a, row, of, of, l) : -1, passed};
+      search = Search{bin_span(row, of), count, ahead, count <= kArena ? gather(a, row, of, of, l) : -1, passed, false};
     }
     double kept;
     const uint64_t found = find_border(a, exp2, row, search, k, goal, l, kept);
@@ -946,45 +1012,25 @@ __device__ __forceinline__ Drawn draw_list(const Exp2& exp2, const Row& row, int
   double passed = 0.0, drawn = -1.0;
 #pragma unroll 1
   while (true) {
-    __syncthreads();
-    if (tid < kBins) {
-      l.cell_sum[tid] = 0;
-      l.cell_count[tid] = 0;
-    }
-    if (tid == 0) {
-      l.first = kBins;
-      l.last = 0;
-    }
-    __syncthreads();
+    clear_cells(l);
     for (int i = tid; i < n; i += kDThreads) {
       const uint64_t at = l.arena[i];
       const int index = static_cast<int>(at & kLowIndex) - lo;
-      if (at <= border && index >= 0 && index >> shift < kBins) {
-        atomicAdd(&l.cell_sum[index >> shift], fine_units(row.weight_of(exp2, value_at(at))));
-        atomicAdd(&l.cell_count[index >> shift], 1u);
-      }
+      if (at <= border && index >= 0 && index >> shift < kBins) add_to_cell(l, index >> shift, units_of(l.weights[i], kFine));
     }
     __syncthreads();
-    run_up(tid < kBins ? __builtin_ldexp(static_cast<double>(l.cell_sum[tid]), -kFine) : 0.0, 0, l.cells, l);
-    if (drawn < 0.0) {                         // the first time
-      d.total = l.cells.sum[kBins - 1];
+    CellFound f = find_cell(l, kFine, true, [&](double sum, int) QMV_INLINE { return drawn >= 0.0 && passed + sum > drawn; });
+    if (drawn < 0.0) {                         // the first time: the number goes by the sum
+      d.total = f.total;
       drawn = static_cast<double>(u) * d.total;
+      f = find_cell(l, kFine, true, [&](double sum, int) QMV_INLINE { return passed + sum > drawn; });
     }
-    if (tid < kBins) {
-      const bool some = l.cell_sum[tid] > 0;
-      const uint64_t hits = __ballot(some && passed + l.cells.sum[tid] > drawn), somes = __ballot(some);
-      if (lane_id() == 0 && hits) atomicMin(&l.first, (tid & ~63) + __builtin_ctzll(hits));
-      if (lane_id() == 0 && somes) atomicMax(&l.last, (tid & ~63) + 63 - __builtin_clzll(somes));
-    }
-    __syncthreads();
-    const int cell = l.first < kBins ? l.first : l.last;
-    lo += cell << shift;
-    passed += cell > 0 ? l.cells.sum[cell - 1] : 0.0;
-    if (l.cell_count[cell] <= kRank) break;    // (a cell of one index has one)
+    lo += f.cell << shift;
+    passed += f.passed;
+    if (f.count <= kRank) break;               // (a cell of one index has one)
     shift = shift > 8 ? shift - 8 : 0;
   }
   // the few by their indices
-  uint64_t* sorted = reinterpret_cast<uint64_t*>(l.cells.sum);
   __syncthreads();
   if (tid == 0) {
     l.n = 0;
@@ -992,31 +1038,32 @@ __device__ __forceinline__ Drawn draw_list(const Exp2& exp2, const Row& row, int
     l.last = 0;
   }
   __syncthreads();
+  const double share = 1.0 / d.total;
   for (int i = tid; i < n; i += kDThreads) {
     const uint64_t at = l.arena[i];
     const int index = static_cast<int>(at & kLowIndex) - lo;
     if (at <= border) {
-      if (probs) probs[at & kLowIndex] = static_cast<float>(row.weight_of(exp2, value_at(at)) / d.total);
+      if (probs) probs[at & kLowIndex] = static_cast<float>(l.weights[i] * share);
       if (index >= 0 && index >> shift == 0) {
         const int to = atomicAdd(&l.n, 1);
-        if (to < kRank) l.few[to] = (at & kLowIndex) << 32 | at >> kIndexBits;
+        if (to < kRank) l.few[to] = (at & kLowIndex) << 32 | static_cast<uint64_t>(i);
       }
     }
   }
   __syncthreads();
   const int m = l.n < kRank ? l.n : kRank;
-  sort_few(l.few, sorted, m, l);
-  const uint64_t x = tid < m ? sorted[tid] : 0;
-  const double w = tid < m ? row.weight_of(exp2, value_of(~static_cast<uint32_t>(x))) : 0.0;
+  sort_few(l.few, l.sorted, m, l);
+  const uint64_t x = tid < m ? l.sorted[tid] : 0;
+  const double w = tid < m ? l.weights[x & 0xFFFFFFFFu] : 0.0;
   double all;
   const double up = passed + block_scan_d(w, l.waves, all) + w;
   const uint64_t hits = __ballot(w > 0.0 && up > drawn), some = __ballot(w > 0.0);
   if (hits && lane_id() == 0) atomicMin(&l.first, (tid & ~63) + __builtin_ctzll(hits));
   if (some && lane_id() == 0) atomicMax(&l.last, (tid & ~63) + 63 - __builtin_clzll(some));
   __syncthreads();
-  const uint64_t take = sorted[l.first < kRank ? l.first : l.last];
+  const uint64_t take = l.sorted[l.first < kRank ? l.first : l.last];
   d.token = static_cast<int>(take >> 32);
-  d.chosen = row.weight_of(exp2, value_of(~static_cast<uint32_t>(take))) / d.total;
+  d.chosen = l.weights[take & 0xFFFFFFFFu] / d.total;
   return d;
 }
 
@@ -1232,6 +1279,7 @@ __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
       d = draw_short(exp2, row, n, all, u, probs, l);
     } else {
       int of, of_listed;
+      if (n > 0) weigh(exp2, row, n, l);
       const uint64_t border = far_border(a, exp2, row, all, tokens, n > 0 ? n : 0, of, of_listed, l);
       if (n > 0) {
         d = draw_list(exp2, row, n, border, a.vocab, u, probs, l);
