@@ -94,7 +94,8 @@ int mmvq_kv_release(const mmvq_kv_pool *pool, int n_seqs, const int32_t *keep,
 int mmvq_kv_plan_workspace(int n_seqs, int64_t *bytes);
 
 /* A step of n_new[s] new tokens for each request s behind the cached[s] that
- * it has in the cache (values below 0 count as 0), in n_rows rows:
+ * it has in the cache (values below 0 count as 0, lengths above 2^30 as that),
+ * in n_rows rows:
  *   token_start  n_seqs + 1 entries: request s has the rows token_start[s] ..
  *                token_start[s+1]-1, the requests one after the other from
  *                row 0 (new tokens that n_rows leaves no room for are cut);

@@ -24,13 +24,7 @@ namespace qmv {
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kLBlock = 64;                    // consecutive rows among which tiles are formed
-constexpr int kLStep = 32;                     // of K, or ranks, a matrix product
-constexpr int kLColumns = 16;                  // rows of x a matrix product
-constexpr int kAWaves = 8, kBWaves = 4;        // of a workgroup of shrink and of expand
-constexpr int kChunk = kAWaves * kLStep;       // of K that a workgroup of shrink takes at a time
-constexpr int kPiece = kBWaves * 64;           // outputs that one of expand takes at a time
-constexpr int kPad = 4;                        // floats behind a row of either in LDS: rows a bank group apart
+constexpr int kPad = 4;                        // floats behind a row in LDS: rows a bank group apart
 
 __device__ __forceinline__ f32x4 mfma_bf16(u32x4 a, u32x4 b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
@@ -166,7 +160,7 @@ __device__ __forceinline__ void eight(f32x4 a, f32x4 b, float (&v)[8]) {
 }
 
 // v of a tile over a range of K, 16 RT ranks at a time. The workgroup takes
-// kChunk of K after the other: rows of x go through LDS, as a row's values side
+// kLoraChunk of K after the other: rows of x go through LDS, as a row's values side
 // by side are what memory reads best and 8 of each of 16 rows what the
 // products take; each wave multiplies 32 of the chunk. The next chunk's loads
 // are on their way meanwhile. Columns behind the tile's count and ranks
@@ -175,7 +169,7 @@ __device__ __forceinline__ void eight(f32x4 a, f32x4 b, float (&v)[8]) {
 template <int TYPE, int RT, int CT>
 __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a) {
   using W = Weights<TYPE>;
-  constexpr int kRows = kLColumns * CT, kPer = kRows / kAWaves, kLine = kChunk + kPad;
+  constexpr int kRows = kLColumns * CT, kPer = kRows / kAWaves, kLine = kLoraChunk + kPad;
   __shared__ union {
     float x[2][kRows][kLine];
     f32x4 sums[kAWaves][RT][kWave];
@@ -183,7 +177,7 @@ __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / 16;
   const int block = blockIdx.x, split = blockIdx.z;
   const int ids = block_ids(a, block);
-  const int chunks = static_cast<int>((a.K + kChunk - 1) / kChunk);
+  const int chunks = static_cast<int>((a.K + kLoraChunk - 1) / kLoraChunk);
   const int c0 = split * a.steps, c1 = c0 + a.steps < chunks ? c0 + a.steps : chunks;
   for (int lead = blockIdx.y * a.leads, end = lead + a.leads; lead < end; ++lead) {
     const Tile tile = tile_of<CT>(a, block, ids, lead);
@@ -206,7 +200,7 @@ __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a
       f32x4 next[kPer];
       W w[RT];
       const auto fetch = [&](int chunk) QMV_INLINE {       // values behind K are 0 and meet real weights
-        const int64_t k = static_cast<int64_t>(chunk) * kChunk, kw = k + kLStep * wave + 8 * g;
+        const int64_t k = static_cast<int64_t>(chunk) * kLoraChunk, kw = k + kLStep * wave + 8 * g;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
           if (wave + kAWaves * i < tile.count)             // uniform
@@ -262,19 +256,19 @@ __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a
 }
 
 // base + scale * B v of a tile, for a slice of M; up to 32 RC ranks. The
-// workgroup takes kPiece outputs after the other; products go to LDS, and each
+// workgroup takes kLoraPiece outputs after the other; products go to LDS, and each
 // wave adds whole rows of them to base: 1 KB side by side a load and a store,
 // where the products' own layout has 64 bytes of each of 16 rows.
 template <int TYPE, int RC, int CT>
 __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a) {
   using W = Weights<TYPE>;
-  constexpr int kRuns = kPiece / (4 * kWave);   // of a row: four outputs a lane
-  constexpr int kRows = kLColumns * CT, kPer = kRows * kRuns / kBWaves, kTiles = kPiece / kBWaves / 16, kLine = kPiece + kPad;
+  constexpr int kRuns = kLoraPiece / (4 * kWave);   // of a row: four outputs a lane
+  constexpr int kRows = kLColumns * CT, kPer = kRows * kRuns / kBWaves, kTiles = kLoraPiece / kBWaves / 16, kLine = kLoraPiece + kPad;
   __shared__ float lds[kRows][kLine], sums[kRows][kLStep * RC + kPad];
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / 16;
   const int block = blockIdx.x;
   const int ids = block_ids(a, block);
-  const int64_t m_first = static_cast<int64_t>(blockIdx.z) * kPiece, m_step = static_cast<int64_t>(gridDim.z) * kPiece;
+  const int64_t m_first = static_cast<int64_t>(blockIdx.z) * kLoraPiece, m_step = static_cast<int64_t>(gridDim.z) * kLoraPiece;
   for (int lead = blockIdx.y * a.leads, end = lead + a.leads; lead < end; ++lead) {
     const Tile tile = tile_of<CT>(a, block, ids, lead);
     if (tile.count == 0 || (tile.rank == 0 && a.base == a.out)) continue;   // uniform
@@ -377,41 +371,6 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
       if (tile.rank > 0) __syncthreads();      // LDS is read
     }
   }
-}
-
-// Launch shape. How many tiles there are the host cannot see: it counts on
-// rows of their own adapters in one block of rows, of one adapter beyond.
-// K is cut until every compute unit has a workgroup, in ranges of two chunks
-// at least, or two of them in ranges of four (64 rows of their own, K = 4096:
-// 4 ranges 34.6 us, 8 of two chunks 37.6; one row: 8.5 and 7.5; 4000 rows of
-// 14336: 5 ranges 98, 3 108). M is cut until every compute unit has two: 64 rows
-// by 14336 in 8 slices 34.6 us, in 4 50, in 16 54; 4000 by 4096 in 5 115, in 3
-// 129, in 10 126. Of many rows tiles take 32, which halves the reads of the
-// weights.
-struct LoraShape {
-  int blocks, leads, groups, splits, steps, slices, ct;
-};
-inline LoraShape lora_shape(int64_t n, int64_t K, int64_t M, int max_rank) {
-  LoraShape s;
-  s.ct = n >= 1024 && max_rank <= 64 ? 2 : 1;
-  s.blocks = static_cast<int>((n + kLBlock - 1) / kLBlock);
-  s.leads = s.blocks <= 8 ? 1 : s.blocks <= 32 ? 4 : kLColumns * s.ct;   // rows of a block that a workgroup looks for tiles at
-  const int rows = n < kLBlock ? static_cast<int>(n) : kLBlock;
-  s.groups = (rows + s.leads - 1) / s.leads;
-  int64_t tiles = (n + kLColumns * s.ct - 1) / (kLColumns * s.ct);
-  if (tiles < rows) tiles = rows;
-  const auto fill = [&](int64_t groups) { return (groups + tiles - 1) / tiles; };
-  const int64_t chunks = (K + kChunk - 1) / kChunk, one = fill(kCus), two = fill(2 * kCus);
-  const int64_t few = (chunks + 1) / 2 < one ? (chunks + 1) / 2 : one, some = (chunks + 3) / 4;
-  int64_t splits = few > some ? few : some;
-  if (splits > two) splits = two;
-  if (splits > 16) splits = 16;
-  s.steps = static_cast<int>((chunks + splits - 1) / splits);
-  s.splits = static_cast<int>((chunks + s.steps - 1) / s.steps);
-  const int64_t pieces = (M + kPiece - 1) / kPiece;
-  s.slices = static_cast<int>(two < pieces ? two : pieces);
-  if (s.slices > 64) s.slices = 64;
-  return s;
 }
 
 int64_t lora_bytes(int64_t n, int64_t K, int64_t M, int max_rank) {

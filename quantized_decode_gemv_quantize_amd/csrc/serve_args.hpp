@@ -6,7 +6,7 @@
 #include <stdint.h>
 
 #include "../../include/mmvq_serve.h"
-#include "decode_plan.hpp"
+#include "serve_plan.hpp"
 
 namespace qmv {
 

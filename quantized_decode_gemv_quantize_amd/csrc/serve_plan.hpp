@@ -1,0 +1,53 @@
+// serve_plan.hpp - launch arithmetic of the operators of a step over many
+// requests, shared by the launchers, the kernels and the host model of the tests.
+#pragma once
+
+#include "decode_plan.hpp"
+
+namespace qmv {
+
+constexpr int kLBlock = 64;                    // consecutive rows among which tiles are formed
+constexpr int kLStep = 32;                     // of K, or ranks, a matrix product
+constexpr int kLColumns = 16;                  // rows of x a matrix product
+constexpr int kAWaves = 8, kBWaves = 4;        // of a workgroup of shrink and of expand
+constexpr int kLoraChunk = kAWaves * kLStep;       // of K that a workgroup of shrink takes at a time
+constexpr int kLoraPiece = kBWaves * 64;           // outputs that one of expand takes at a time
+
+// Launch shape. How many tiles there are the host cannot see: it counts on
+// rows of their own adapters in one block of rows, of one adapter beyond.
+// K is cut until every compute unit has a workgroup, in ranges of two chunks
+// at least, or two of them in ranges of four (64 rows of their own, K = 4096:
+// 4 ranges 34.6 us, 8 of two chunks 37.6; one row: 8.5 and 7.5; 4000 rows of
+// 14336: 5 ranges 98, 3 108). M is cut until every compute unit has two: 64 rows
+// by 14336 in 8 slices 34.6 us, in 4 50, in 16 54; 4000 by 4096 in 5 115, in 3
+// 129, in 10 126. Of many rows tiles take 32, which halves the reads of the
+// weights. A workgroup looks for tiles at four rows of each block where there
+// are several: most of one at each row would find none (512 rows of 8 adapters
+// 46 -> 37 us, 512 of their own 53 -> 56).
+struct LoraShape {
+  int blocks, leads, groups, splits, steps, slices, ct;
+};
+inline LoraShape lora_shape(int64_t n, int64_t K, int64_t M, int max_rank) {
+  LoraShape s;
+  s.ct = n >= 1024 && max_rank <= 64 ? 2 : 1;
+  s.blocks = static_cast<int>((n + kLBlock - 1) / kLBlock);
+  s.leads = s.blocks == 1 ? 1 : s.blocks <= 32 ? 4 : kLColumns * s.ct;   // rows of a block that a workgroup looks for tiles at
+  const int rows = n < kLBlock ? static_cast<int>(n) : kLBlock;
+  s.groups = (rows + s.leads - 1) / s.leads;
+  int64_t tiles = (n + kLColumns * s.ct - 1) / (kLColumns * s.ct);
+  if (tiles < rows) tiles = rows;
+  const auto fill = [&](int64_t groups) { return (groups + tiles - 1) / tiles; };
+  const int64_t chunks = (K + kLoraChunk - 1) / kLoraChunk, one = fill(kCus), two = fill(2 * kCus);
+  const int64_t few = (chunks + 1) / 2 < one ? (chunks + 1) / 2 : one, some = (chunks + 3) / 4;
+  int64_t splits = few > some ? few : some;
+  if (splits > two) splits = two;
+  if (splits > 16) splits = 16;
+  s.steps = static_cast<int>((chunks + splits - 1) / splits);
+  s.splits = static_cast<int>((chunks + s.steps - 1) / s.steps);
+  const int64_t pieces = (M + kLoraPiece - 1) / kLoraPiece;
+  s.slices = static_cast<int>(two < pieces ? two : pieces);
+  if (s.slices > 64) s.slices = 64;
+  return s;
+}
+
+}  // namespace qmv

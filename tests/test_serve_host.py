@@ -3,6 +3,9 @@ exported, the host-only queries, and every refusal (arguments are checked
 before any device is touched)."""
 import ctypes
 import gc
+import os
+import shutil
+import subprocess
 import weakref
 
 import pytest
@@ -178,3 +181,18 @@ def test_descriptors_keep_their_tensors():
         del made
         gc.collect()
         assert all(r() is None for r in refs)
+
+
+def test_launch_arithmetic(tmp_path):
+    """Rows, ranges of K and slices of M of an adapters' launch, over sizes up to the limits."""
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    clang = next((c for c in ("/opt/rocm/llvm/bin/clang++", shutil.which("clang++")) if c and os.path.exists(c)), None)
+    if clang is None:
+        pytest.skip("clang++ (host) not available")
+    exe = tmp_path / "serve"
+    subprocess.check_call([clang, "-std=c++17", "-O2", "-Wall", "-DQMV_HOST_MODEL", "-I",
+                           os.path.join(root, "quantized_decode_gemv_quantize_amd", "csrc"), "-o", str(exe),
+                           os.path.join(root, "tests", "host_model", "serve.cpp")])
+    res = subprocess.run([str(exe)], capture_output=True, text=True, timeout=300)
+    assert res.returncode == 0, res.stdout[-4000:]
+    assert "0 failing check(s)" in res.stdout
