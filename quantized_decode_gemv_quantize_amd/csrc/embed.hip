@@ -7,6 +7,7 @@
 // one (d q + m, d sc q - dmin m) go through 64 bits. Every byte of a row is
 // read once and every output written once; the writes are most of it.
 #include "launch.hpp"
+#include "past.hpp"
 #include "serve_args.hpp"
 
 namespace qmv {
@@ -140,7 +141,7 @@ __global__ void __launch_bounds__(kEThreads) embed_kernel(EmbedArgs a) {
     for (int k = 0; k < kEQuads; ++k) {
       const int i = first + 4 * kWave * k;
       if (i + 4 <= a.K) {
-        __builtin_memcpy(__builtin_assume_aligned(out + i, 4), y[k], 16);
+        store_four(out + i, y[k], a.past);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -156,6 +157,7 @@ int launch_embed(int type, const EmbedArgs& given, hipStream_t st) {
   EmbedArgs a = given;
   a.pieces = (a.K + kEPiece - 1) / kEPiece;
   a.units = a.n * a.pieces;
+  a.past = past_caches(a.n, a.K);
   const int64_t blocks = (a.units + kEWaves - 1) / kEWaves;
   const dim3 grid(static_cast<unsigned>(blocks < kMaxEmbedGrid ? blocks : kMaxEmbedGrid)), block(kEThreads);
   switch (type) {

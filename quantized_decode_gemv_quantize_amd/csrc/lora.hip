@@ -17,6 +17,7 @@
 // three (2^-28 of the whole) are formed: fp32 products, for three, six or
 // eight matrix instructions where one of fp32 takes the time of sixteen.
 #include "launch.hpp"
+#include "past.hpp"
 #include "serve_args.hpp"
 
 namespace qmv {
@@ -166,7 +167,9 @@ __device__ __forceinline__ void eight(f32x4 a, f32x4 b, float (&v)[8]) {
 // are on their way meanwhile. Columns behind the tile's count and ranks
 // behind the adapter's repeat real ones, so that no load waits for a condition;
 // what comes of them is not stored, or not used.
-template <int TYPE, int RT, int CT>
+// PAST: x passes the caches by (a branch about each load instead: 109 us for
+// the prompts' 101).
+template <int TYPE, int RT, int CT, bool PAST>
 __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a) {
   using W = Weights<TYPE>;
   constexpr int kRows = kLColumns * CT, kPer = kRows / kAWaves, kLine = kLoraChunk + kPad;
@@ -199,12 +202,13 @@ __global__ void __launch_bounds__(kAWaves * kWave) lora_shrink_kernel(LoraArgs a
       }
       f32x4 next[kPer];
       W w[RT];
+      const auto ld_row = [&](const float* p) QMV_INLINE { return PAST ? __builtin_bit_cast(f32x4, load_past(p)) : ld_f4(p); };
       const auto fetch = [&](int chunk) QMV_INLINE {       // values behind K are 0 and meet real weights
         const int64_t k = static_cast<int64_t>(chunk) * kLoraChunk, kw = k + kLStep * wave + 8 * g;
 #pragma unroll
         for (int i = 0; i < kPer; ++i)
           if (wave + kAWaves * i < tile.count)             // uniform
-            next[i] = k + 4 * lane < a.K ? ld_f4(x[i] + k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+            next[i] = k + 4 * lane < a.K ? ld_row(x[i] + k) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int t = 0; t < RT; ++t)
           if (RT == 1 || r0 + 16 * t < tile.rank) w[t].load(A, w0[t] + (kw < a.K ? kw : 0));
@@ -358,10 +362,10 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
         f32x4 add{0.0f, 0.0f, 0.0f, 0.0f};
         if (tile.rank > 0) add = *reinterpret_cast<const f32x4*>(&lds[run / kRuns][run % kRuns * 4 * kWave + 4 * lane]);
         if (o[i] + 4 <= a.M) {
-          f32x4 y;
+          float y[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) y[e] = tile.rank > 0 ? old[i][e] + tile.scale * add[e] : old[i][e];
-          __builtin_memcpy(__builtin_assume_aligned(out[i], 4), &y, 16);
+          store_four(out[i], y, CT == 2 && a.past);   // (single tokens: the branch alone 34.8 -> 35.3 us for 64 rows)
         } else {
 #pragma unroll
           for (int e = 0; e < 4; ++e)
@@ -380,7 +384,9 @@ int64_t lora_bytes(int64_t n, int64_t K, int64_t M, int max_rank) {
 
 template <int TYPE, int RT, int RC, int CT>
 int launch_ranks(const LoraArgs& a, const LoraShape& s, hipStream_t st) {
-  hipLaunchKernelGGL((lora_shrink_kernel<TYPE, RT, CT>), dim3(s.blocks, s.groups, s.splits), dim3(kAWaves * kWave), 0, st, a);
+  const dim3 grid(s.blocks, s.groups, s.splits), block(kAWaves * kWave);
+  if (CT == 2 && past_caches(a.n, a.K)) hipLaunchKernelGGL((lora_shrink_kernel<TYPE, RT, CT, CT == 2>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((lora_shrink_kernel<TYPE, RT, CT, false>), grid, block, 0, st, a);
   const int rc = check_launch();
   if (rc) return rc;
   hipLaunchKernelGGL((lora_expand_kernel<TYPE, RC, CT>), dim3(s.blocks, s.groups, s.slices), dim3(kBWaves * kWave), 0, st, a);
@@ -394,6 +400,7 @@ int launch_type(const LoraArgs& given, hipStream_t st) {
   a.splits = s.splits;
   a.steps = s.steps;
   a.leads = s.leads;
+  a.past = past_caches(a.n, a.M);
   if (s.ct == 2) {
     if (a.max_rank <= 16) return launch_ranks<TYPE, 1, 1, 2>(a, s, st);
     if (a.max_rank <= 32) return launch_ranks<TYPE, 2, 1, 2>(a, s, st);

@@ -23,6 +23,7 @@
 // in 32 bits moves a border by more than many tokens' probability.
 #include "draw.hpp"
 #include "launch.hpp"
+#include "past.hpp"
 #include "serve_args.hpp"
 
 namespace qmv {
@@ -220,8 +221,7 @@ __global__ void __launch_bounds__(kSThreads) sample_stats_kernel(SampleArgs a) {
     for (int k = 0; k < kSPer; k += 4) {
       const int i = i0 + k * kSThreads;
       if (i + 4 <= a.vocab) {
-        const u32x4 zero{0, 0, 0, 0};
-        __builtin_memcpy(__builtin_assume_aligned(out + i, 4), &zero, 16);
+        store_four(out + i, {0.0f, 0.0f, 0.0f, 0.0f}, a.past);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -342,7 +342,7 @@ __device__ __forceinline__ double chunk_factor(const Exp2& exp2, float chunk_top
   return weight(exp2, chunk_top, top, rate);
 }
 
-struct Running {                               // sums up to each bin's or cell's end
+struct Running {                               // sums up to each bin's end
   double sum[kBins];
   int count[kBins];
 };
@@ -354,7 +354,6 @@ struct PickLds {
   unsigned long long cell_sum[kBins];
   uint32_t cell_count[kBins];
   double waves[kDWaves];
-  int iwaves[kDWaves];
   int found, n, first, last;
   uint32_t low;
   double kept;
@@ -1325,7 +1324,7 @@ __global__ void __launch_bounds__(kSThreads) sample_probs_kernel(SampleArgs a) {
       p[e] = in ? static_cast<float>(weight(exp2, v[k + e], pick.top, pick.rate) / pick.total) : 0.0f;
     }
     if (i + 4 <= a.vocab) {
-      __builtin_memcpy(__builtin_assume_aligned(out + i, 4), p, 16);
+      store_four(out + i, p, a.past);
     } else {
 #pragma unroll
       for (int e = 0; e < 4; ++e)
@@ -1334,7 +1333,9 @@ __global__ void __launch_bounds__(kSThreads) sample_probs_kernel(SampleArgs a) {
   }
 }
 
-int launch_sample(const SampleArgs& a, hipStream_t st) {
+int launch_sample(const SampleArgs& given, hipStream_t st) {
+  SampleArgs a = given;
+  a.past = past_caches(a.n_rows, a.vocab);
   const unsigned chunks = static_cast<unsigned>(a.chunks), rows = static_cast<unsigned>(a.n_rows);
   const dim3 grid(chunks, rows < kGridRows ? rows : kGridRows, (rows + kGridRows - 1) / kGridRows);
   hipLaunchKernelGGL(sample_stats_kernel, grid, dim3(kSThreads), 0, st, a);

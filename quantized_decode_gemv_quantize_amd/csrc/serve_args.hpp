@@ -18,6 +18,7 @@ struct EmbedArgs {
   int vocab, K;
   float scale;
   int pieces;              // of a row
+  bool past;               // out passes the caches by
 };
 
 struct PoolArgs {
@@ -65,6 +66,7 @@ struct LoraArgs {
   int n, n_seqs, n_adapters, max_rank;
   int splits, steps;       // ranges of K, and chunks of one
   int leads;               // rows of a block that a workgroup looks for tiles at
+  bool past;               // out passes the caches by
   float* part;             // [split][row][max_rank]
 };
 
@@ -82,6 +84,7 @@ struct SampleArgs {
   int64_t ldl, ldp;
   int vocab, n_rows, n_seqs, chunks;
   bool zeroed;             // probs are no part of logits: written on the way
+  bool past;               // probs pass the caches by
   uint8_t* ws;
 };
 
