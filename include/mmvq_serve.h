@@ -94,8 +94,8 @@ int mmvq_kv_release(const mmvq_kv_pool *pool, int n_seqs, const int32_t *keep,
 int mmvq_kv_plan_workspace(int n_seqs, int64_t *bytes);
 
 /* A step of n_new[s] new tokens for each request s behind the cached[s] that
- * it has in the cache (values below 0 count as 0, lengths above 2^30 as that),
- * in n_rows rows:
+ * it has in the cache (values below 0 count as 0, cached ones above 2^30 as
+ * 2^30), in n_rows rows:
  *   token_start  n_seqs + 1 entries: request s has the rows token_start[s] ..
  *                token_start[s+1]-1, the requests one after the other from
  *                row 0 (new tokens that n_rows leaves no room for are cut);
@@ -201,8 +201,11 @@ int mmvq_sample_workspace(int n_rows, int vocab, int64_t *bytes);
  * -inf and NaN logits have the weight 0; where a row has +inf logits these
  * have 1 and all others 0. A row without any weight, or of no request
  * (row_seq outside 0..n_seqs-1): token -1, chosen 0, probs 0. An infinite
- * temperature gives equal weights. All sums, exponentials and comparisons are
- * in 64 bits; u in [0, 1).
+ * temperature gives equal weights. Exponentials, sums and comparisons are in
+ * 64 bits; in the sums that p is measured against each weight is rounded by
+ * at most 2^-38 of itself, or 2^-64 of w_top, so that where the sum before a
+ * token is that near to p times all of them, it may count either way.
+ * u in [0, 1).
  * Requires 0 <= n_rows <= 2^20, 1 <= vocab <= 2^24, n_seqs >= 0, ldl and ldp
  * >= vocab; 4-byte aligned. params NULL: all off. */
 int mmvq_sample(const float *logits, int64_t ldl, int vocab, int n_rows,

@@ -5,7 +5,12 @@
 // A product of a block's scale and a code fits fp32 (at most 23 bits), so the
 // formats without an offset take one fp32 product with `scale`. Those with
 // one (d q + m, d sc q - dmin m) go through 64 bits. Every byte of a row is
-// read once and every output written once; the writes are most of it.
+// read once and every output written once; the writes are most of it and bound
+// it: 4096 rows of 4096 take 13.5 (Q4_1) to 16.3 us (Q5_K), 15.0 from Q4_K (5.1
+// TB/s), 24.3 from F32 (5.5 TB/s). One row is a launch's latency and two loads',
+// 2.9 us. A wave takes kEPiece values of a row, in runs of four a lane, so that
+// a store is 1 KB side by side and a short row does not leave a workgroup
+// idle; what the lanes of a block share comes from the caches.
 #include "launch.hpp"
 #include "past.hpp"
 #include "serve_args.hpp"

@@ -11,6 +11,12 @@
 // columns empty, but then the weights are all there is to read, and the
 // products wait for them anyway.
 //
+// Bound by memory where there are many rows, by the chain of two launches, the
+// ids, the ranks and the first loads where there are few: one row of 4096 by
+// 4096 3.9 + 5.3 us. Adapters are rows of max_rank, of which a lower rank uses the
+// front: B's lines are fetched whole, 64 rows of their own adapters of ranks 8
+// to 64 read 77 MB for the 47 that count (expand 24 us, 3.3 TB/s).
+//
 // fp32 values enter a product as three bf16 parts by truncation, x = x1 + x2 +
 // x3 exactly (8 bits each); weights as one (bf16), two (fp16: 11 bits) or
 // three (fp32). All products of parts but that of the two last of three and
@@ -272,7 +278,9 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), g = lane / 16;
   const int block = blockIdx.x;
   const int ids = block_ids(a, block);
-  const int64_t m_first = static_cast<int64_t>(blockIdx.z) * kLoraPiece, m_step = static_cast<int64_t>(gridDim.z) * kLoraPiece;
+  // (pieces of a slice one after the other: 1% less than every gridDim.z-th)
+  const int64_t slice = static_cast<int64_t>(a.pieces) * kLoraPiece, m_first = blockIdx.z * slice;
+  const int64_t m_end = m_first + slice < a.M ? m_first + slice : a.M;
   for (int lead = blockIdx.y * a.leads, end = lead + a.leads; lead < end; ++lead) {
     const Tile tile = tile_of<CT>(a, block, ids, lead);
     if (tile.count == 0 || (tile.rank == 0 && a.base == a.out)) continue;   // uniform
@@ -289,7 +297,7 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
         }
       }
     };
-    if (m_first < a.M) fetch(m_first);         // on their way while v is summed
+    if (m_first < m_end) fetch(m_first);       // on their way while v is summed
     // v: each four ranks of a row summed by one thread, 0 behind the adapter's rank (the sums there are others')
     constexpr int kRanks = kLStep * RC, kQuads = kRanks / 4;
     for (int i = static_cast<int>(threadIdx.x); i < kRows * kQuads; i += kBWaves * kWave) {
@@ -317,7 +325,7 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
       }
     __syncthreads();                           // (the next tile's sums)
     const bool cuts = tile.rank % kLStep != 0;   // uniform
-    for (int64_t m0 = m_first; m0 < a.M; m0 += m_step) {
+    for (int64_t m0 = m_first; m0 < m_end; m0 += kLoraPiece) {
       f32x4 old[kPer];
       const float* base[kPer];
       float* out[kPer];
@@ -352,7 +360,7 @@ __global__ void __launch_bounds__(kBWaves * kWave) lora_expand_kernel(LoraArgs a
             if (lane % kLColumns + kLColumns * c < tile.count)
               *reinterpret_cast<f32x4*>(&lds[lane % kLColumns + kLColumns * c][64 * wave + 16 * t + 4 * g]) = acc[c];
         }
-        if (m0 + m_step < a.M) fetch(m0 + m_step);
+        if (m0 + kLoraPiece < m_end) fetch(m0 + kLoraPiece);
         __syncthreads();
       }
 #pragma unroll
@@ -400,6 +408,7 @@ int launch_type(const LoraArgs& given, hipStream_t st) {
   a.splits = s.splits;
   a.steps = s.steps;
   a.leads = s.leads;
+  a.pieces = s.pieces;
   a.past = past_caches(a.n, a.M);
   if (s.ct == 2) {
     if (a.max_rank <= 16) return launch_ranks<TYPE, 1, 1, 2>(a, s, st);

@@ -9,7 +9,8 @@
 // their request by bisection in the running sums, in LDS up to 1024 requests.
 // All of it is a chain of latencies: two scans, ten steps of a bisection, a
 // table entry. Up to kPlanRows rows one workgroup does everything in one
-// launch; more rows take a second launch over all of them.
+// launch (64 requests, 318 rows: 4.0 us); more rows take a second launch over
+// all of them (512 requests, 58 336 rows, 0.9 MB of maps: 2.7 + 5.5 us).
 #include "draw.hpp"
 #include "launch.hpp"
 #include "serve_args.hpp"
@@ -214,7 +215,9 @@ __device__ __forceinline__ void given_up(const ReleaseArgs& a, int s, int& from,
 
 // One workgroup; the requests that give pages up are listed, and each of
 // them is a wave's: first their pages are counted, and with the counts'
-// running sum they are put behind the free ones in order.
+// running sum they are put behind the free ones in order. A chain of
+// latencies, too, six barriers and two walks of a table row: 3.1 us for 3 of 64
+// requests with up to 250 pages, 5.5 for 40 of 512 with up to 187.
 __global__ void __launch_bounds__(kPThreads) release_kernel(ReleaseArgs a) {
   __shared__ int lds[2][kPWaves];
   __shared__ int list[kPThreads], from[kPThreads], to[kPThreads], count[kPThreads];

@@ -18,7 +18,8 @@
 //   probs   the distribution written out, if wanted, of rows that keep many;
 //           of the others stats writes the zeros and pick what is kept.
 // A chunk's bin is one 64-bit whole number: the count, and the sum in units of
-// 2^-38 of its weights (adding in LDS in any order gives the same bits).
+// 2^-38 of 2^(-b/4) for bin b (adding in LDS in any order gives the same bits,
+// and one addition a token is what the bins can bear).
 // Everything else is in 64-bit floating point: with 10^5 logits a running sum
 // in 32 bits moves a border by more than many tokens' probability.
 #include "draw.hpp"

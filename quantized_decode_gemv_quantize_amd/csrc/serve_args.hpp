@@ -65,6 +65,7 @@ struct LoraArgs {
   int64_t stride_a, stride_b, ldx, ldb, ldo, K, M;
   int n, n_seqs, n_adapters, max_rank;
   int splits, steps;       // ranges of K, and chunks of one
+  int pieces;              // of M, of a slice
   int leads;               // rows of a block that a workgroup looks for tiles at
   bool past;               // out passes the caches by
   float* part;             // [split][row][max_rank]

@@ -35,7 +35,7 @@ inline bool past_caches(int64_t rows, int64_t length) {
 // are several: most of one at each row would find none (512 rows of 8 adapters
 // 46 -> 37 us, 512 of their own 53 -> 56).
 struct LoraShape {
-  int blocks, leads, groups, splits, steps, slices, ct;
+  int blocks, leads, groups, splits, steps, slices, pieces, ct;
 };
 inline LoraShape lora_shape(int64_t n, int64_t K, int64_t M, int max_rank) {
   LoraShape s;
@@ -55,8 +55,10 @@ inline LoraShape lora_shape(int64_t n, int64_t K, int64_t M, int max_rank) {
   s.steps = static_cast<int>((chunks + splits - 1) / splits);
   s.splits = static_cast<int>((chunks + s.steps - 1) / s.steps);
   const int64_t pieces = (M + kLoraPiece - 1) / kLoraPiece;
-  s.slices = static_cast<int>(two < pieces ? two : pieces);
-  if (s.slices > 64) s.slices = 64;
+  int64_t slices = two < pieces ? two : pieces;
+  if (slices > 64) slices = 64;
+  s.pieces = static_cast<int>((pieces + slices - 1) / slices);
+  s.slices = static_cast<int>((pieces + s.pieces - 1) / s.pieces);
   return s;
 }
 

@@ -28,6 +28,8 @@ int main() {
           const int64_t chunks = (K + kLoraChunk - 1) / kLoraChunk;
           CHECK(s.splits >= 1 && s.splits <= 16 && s.steps >= 1, "splits %d steps %d", s.splits, s.steps);
           CHECK(static_cast<int64_t>(s.splits) * s.steps >= chunks && static_cast<int64_t>(s.splits - 1) * s.steps < chunks, "K %ld splits %d steps %d", (long)K, s.splits, s.steps);
+          CHECK(s.pieces >= 1 && static_cast<int64_t>(s.slices) * s.pieces * kLoraPiece >= M &&
+                static_cast<int64_t>(s.slices - 1) * s.pieces * kLoraPiece < M, "M %ld slices %d pieces %d", (long)M, s.slices, s.pieces);
           CHECK(s.slices >= 1 && s.slices <= 64 && static_cast<int64_t>(s.slices - 1) * kLoraPiece < M, "M %ld slices %d", (long)M, s.slices);
           CHECK(s.ct == 1 || (s.ct == 2 && rank <= 64), "ct %d rank %d", s.ct, rank);
           CHECK(static_cast<int64_t>(s.blocks) * s.groups * (s.splits > s.slices ? s.splits : s.slices) < (int64_t(1) << 31), "grid");
