@@ -1305,24 +1305,19 @@ __global__ void __launch_bounds__(kSThreads) sample_probs_kernel(SampleArgs a) {
   if (pick.written) return;                    // uniform
   const float* row = a.logits + r * a.ldl;
   float* out = a.probs + r * a.ldp;
-  float v[kSPer];
+  float v[kSPer / 4][4];
   const int i0 = blockIdx.x * kChunk + 4 * static_cast<int>(threadIdx.x);
+  load_runs(row, i0, 4 * kSThreads, a.vocab, v);
+  // (a product with the rounded 1 / total, 2^-53 off: a quotient each is most of the kernel's instructions)
+  const double share = pick.total > 0.0 ? 1.0 / pick.total : 0.0;
 #pragma unroll
-  for (int k = 0; k < kSPer; k += 4) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int i = i0 + k * kSThreads + e;
-      v[k + e] = i < a.vocab ? taken(row[i]) : -INFINITY;
-    }
-  }
-#pragma unroll
-  for (int k = 0; k < kSPer; k += 4) {
-    const int i = i0 + k * kSThreads;
+  for (int k = 0; k < kSPer / 4; ++k) {
+    const int i = i0 + 4 * k * kSThreads;
     float p[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const bool in = pick.total > 0.0 && place_of(v[k + e], i + e) <= pick.border;
-      p[e] = in ? static_cast<float>(weight(exp2, v[k + e], pick.top, pick.rate) / pick.total) : 0.0f;
+      const float x = taken(v[k][e]);
+      p[e] = place_of(x, i + e) <= pick.border ? static_cast<float>(weight(exp2, x, pick.top, pick.rate) * share) : 0.0f;
     }
     if (i + 4 <= a.vocab) {
       store_four(out + i, p, a.past);
