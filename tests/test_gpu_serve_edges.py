@@ -212,3 +212,49 @@ def test_two_steps_in_one_graph():
             assert np.array_equal(host(start[i]), want[0]) and np.array_equal(host(slot[i]), want[4])
             at = want[1].astype(np.int64)
         assert np.array_equal(host(cached), at) and np.array_equal(host(table), pool.table) and host(n_free)[0] == pool.n_free
+
+
+@pytest.mark.parametrize("kind", [B.F32, B.F16, B.BF16])
+def test_embed_rows_beyond_the_caches(kind):
+    """More than 32 MB of rows, of an odd length and with a gap between them."""
+    import torch
+    n, K, vocab, ldo = 9001, 1001, 50, 1006
+    t = {B.F32: torch.float32, B.F16: torch.float16, B.BF16: torch.bfloat16}[kind]
+    table = torch.randn(vocab, K, generator=torch.Generator().manual_seed(2)).to(t).to("cuda:0")
+    ids = torch.arange(n, device="cuda:0", dtype=torch.int32) * 7 % (vocab + 1) - 1
+    out = nan(n, ldo)
+    announce(f"embed {n} rows of {K}")
+    B.mmvq_embed(table, kind, vocab, K, ids, n, 0.75, out, ldo)
+    want = torch.where((ids >= 0)[:, None], table.float()[ids.clamp(min=0).long()] * 0.75, 0.0)
+    assert torch.equal(out[:, :K], want) and bool(out[:, K:].isnan().all())
+
+
+@pytest.mark.parametrize("kind,r", [(B.BF16, 16), (B.F16, 32), (B.F32, 64)])
+def test_lora_rows_beyond_the_caches(kind, r):
+    """More than 32 MB of x and of out, odd M, gaps between rows, in place and not."""
+    import torch
+    n, K, M, count = 2100, 4104, 4099, 3
+    t = {B.F32: torch.float32, B.F16: torch.float16, B.BF16: torch.bfloat16}[kind]
+    gen = torch.Generator().manual_seed(r)
+    a = (torch.randn(count, r, K, generator=gen) / 64).to(t).to("cuda:0")
+    b = torch.randn(count, M, r, generator=gen).to(t).to("cuda:0")
+    s = B.lora_set(a, b, kind, count, K, M, r)
+    x, base = torch.randn(n, K + 4, generator=gen).to("cuda:0"), torch.randn(n, M + 1, generator=gen).to("cuda:0")
+    ids = (torch.arange(n, device="cuda:0") // 700).int()
+    ids[5::97] = -1
+    dt, xs = torch.float64, x[:, :K].double()
+    want, size = base[:, :M].double(), base[:, :M].double().abs()
+    for i in range(count):
+        of = ids == i
+        v, va = xs[of] @ a[i].to(dt).t().contiguous(), xs[of].abs() @ a[i].to(dt).abs().t().contiguous()
+        want[of] += v @ b[i].to(dt).t().contiguous()
+        size[of] += va @ b[i].to(dt).abs().t().contiguous()
+    # fp32 sums of K / 32 products' sums and r of them, in runs of at most 16 and trees: some 40 roundings a term
+    tol = 64 * 2.0 ** -24 * size
+    ws = garbage(B.mmvq_lora_workspace(s, n))
+    out = nan(n, M + 3)
+    announce(f"lora {n} rows type {kind} rank {r}")
+    B.mmvq_lora(s, x, K + 4, n, None, ids, n, base, M + 1, out, M + 3, ws, ws.numel())
+    assert bool(((out[:, :M].double() - want).abs() <= tol).all()) and bool(out[:, M:].isnan().all())
+    B.mmvq_lora(s, x, K + 4, n, None, ids, n, base, M + 1, base, M + 1, ws, ws.numel())
+    assert torch.equal(base[:, :M], out[:, :M])
