@@ -665,7 +665,8 @@ __device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int f
       const int c = c0 + kDWaves * q;
       if (c >= a.chunks) continue;             // uniform
       const ChunkShift h = row.chunk[c];
-      const int listed = h.factor >= 0.0 && h.shift <= b ? h.listed : 0;
+      // (a chunk from kBins on has all its tokens in the row's last bin)
+      const int listed = h.factor >= 0.0 && (h.shift <= b || b == kBins - 1) ? h.listed : 0;
       for (int i = lane_id(), more = listed; more > 0; more -= kWave, i += kWave) {
         if (i != lane_id()) x[q] = i < listed ? entry(c, i) : 0;
         const int its = i < listed ? row.bin(value_at(x[q])) : kBins;
