@@ -1149,7 +1149,8 @@ __device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2
   for (int c0 = 0; c0 < a.chunks && found < 0; c0 += kWave) {
     const int c = c0 + lane_id();
     const double w = c < a.chunks ? st[c].sum : 0.0, up = wave_scan(w) + run;
-    const uint64_t hit = __ballot(up > goal), some = __ballot(w > 0.0);
+    // (a chunk without weight may have the larger sum by rounding alone: the scan adds in another order at each lane)
+    const uint64_t hit = __ballot(w > 0.0 && up > goal), some = __ballot(w > 0.0);
     if (some) {
       const int i = 63 - __builtin_clzll(some);
       last = c0 + i;

@@ -1,0 +1,24 @@
+"""Draws by a number between two running sums of chunks that differ by rounding
+alone."""
+import numpy as np
+import pytest
+
+import draw_borders
+from gpu_helpers import dev, host
+from quantized_decode_gemv_quantize_amd import binding as B
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("seed", range(4))
+def test_sample_draws_no_chunk_without_weight(seed):
+    """A running sum that is larger at an entirely masked chunk than at the one before it, by rounding alone, with
+    the number between the two."""
+    import torch
+    z, allowed = draw_borders.logits_row(seed)
+    V = len(z)
+    tokens, chosen = torch.full((1,), -5, dtype=torch.int32, device="cuda:0"), torch.full((1,), -5.0, device="cuda:0")
+    ws = torch.full((B.mmvq_sample_workspace(1, V),), 0xA5, dtype=torch.uint8, device="cuda:0")
+    B.mmvq_sample(dev(z[None]), V, V, 1, None, None, 1, dev(np.array([0.5], np.float32)), tokens, chosen, None, V, ws, ws.numel())
+    got = int(host(tokens)[0])
+    assert got in allowed and abs(host(chosen)[0] - np.exp(z[got].astype(np.float64)) / np.exp(z.astype(np.float64)).sum()) < 1e-6
