@@ -352,7 +352,8 @@ __device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const
       const SeqSum o = c0 == 0 ? own : c < a.chunks ? sums(c) : none;
       const double w = use ? o.rest : o.all;
       const double up = wave_scan(w) + run;
-      const uint64_t hit = __ballot(up > goal), some = __ballot(w > 0.0);
+      // (a chunk without weight may have the larger sum by rounding alone: the scan adds in another order at each lane)
+      const uint64_t hit = __ballot(w > 0.0 && up > goal), some = __ballot(w > 0.0);
       if (some) {
         const int i = 63 - __builtin_clzll(some);
         last = c0 + i;

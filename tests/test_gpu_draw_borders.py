@@ -22,3 +22,20 @@ def test_sample_draws_no_chunk_without_weight(seed):
     B.mmvq_sample(dev(z[None]), V, V, 1, None, None, 1, dev(np.array([0.5], np.float32)), tokens, chosen, None, V, ws, ws.numel())
     got = int(host(tokens)[0])
     assert got in allowed and abs(host(chosen)[0] - np.exp(z[got].astype(np.float64)) / np.exp(z.astype(np.float64)).sum()) < 1e-6
+
+
+@pytest.mark.parametrize("with_draft", [False, True])
+@pytest.mark.parametrize("seed", range(4))
+def test_verify_draws_no_chunk_without_weight(seed, with_draft):
+    """A sequence of one row, from which the next token is drawn: one with a weight, though the running sum is
+    larger at a chunk without any than at the one before it."""
+    import torch
+    z, allowed = draw_borders.weights_row(seed)
+    V = len(z)
+    count, out = (torch.full((1, n), -5, dtype=torch.int32, device="cuda:0") for n in (1, 2))
+    ws = torch.full((B.mmvq_verify_workspace(1, 1, V),), 0xA5, dtype=torch.uint8, device="cuda:0")
+    drafted, half = dev(np.zeros(1, np.int32)), dev(np.array([0.5], np.float32))
+    B.mmvq_verify_draft(dev(z[None]), V, V, B.TARGET_WEIGHTS, None, drafted, dev(z[None]) if with_draft else None, V,
+                        dev(np.array([0, 1], np.int32)), 1, 1, half, half, count, out, 2, ws, ws.numel())
+    got = host(out)[0]
+    assert host(count)[0, 0] == 0 and got[0] in allowed and got[1] == -1
