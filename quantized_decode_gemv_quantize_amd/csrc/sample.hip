@@ -354,7 +354,7 @@ struct PickLds {
   double weights[kArena];                      // of those, once they are asked for
   Running bins;
   uint64_t few[kRank], sorted[kRank];
-  unsigned long long cell_sum[kBins];
+  unsigned long long cell_sum[kBins], cell_rest[kBins];
   uint32_t cell_count[kBins];
   double waves[kDWaves];
   int found, n, first, last;
@@ -687,7 +687,6 @@ __device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int f
 }
 
 // Whole units of a weight up to 1, as the low bits of a sum with 2^52.
-constexpr int kFine = 49;                      // 2^13 of them stay below 2^62
 __device__ __forceinline__ unsigned long long units_of(double w, int unit) {
   return static_cast<unsigned long long>(__double_as_longlong(__builtin_ldexp(w, unit) + 0x1p52)) & ((1ull << 52) - 1);
 }
@@ -725,6 +724,7 @@ __device__ __forceinline__ void clear_cells(PickLds& l) {
   __syncthreads();
   for (int i = threadIdx.x; i < kBins; i += kDThreads) {
     l.cell_sum[i] = 0;
+    l.cell_rest[i] = 0;
     l.cell_count[i] = 0;
   }
   __syncthreads();
@@ -733,13 +733,24 @@ __device__ __forceinline__ void add_to_cell(PickLds& l, int cell, unsigned long 
   atomicAdd(&l.cell_sum[cell], units);
   atomicAdd(&l.cell_count[cell], 1u);
 }
+// For the draw: weights up to 2^scale (larger ones count as that) in whole
+// units of 2^(scale - kFine) and what is left in units of 2^(scale - 2 kFine),
+// so that sums in any order are those of 64 bits. The arena's 2^13 tokens at
+// most stay below 2^62 of either.
+constexpr int kFine = 49;
+__device__ __forceinline__ void add_weight(PickLds& l, int cell, double w, int scale) {
+  const double x = fmin(__builtin_ldexp(w, kFine - scale), 0x1p49), whole = floor(x);
+  add_to_cell(l, cell, units_of(whole, 0));
+  atomicAdd(&l.cell_rest[cell], units_of(x - whole, kFine));
+}
+static_assert(kFine == 49 && kArena <= 1 << 13);
 struct CellFound {
   int cell, count, ahead;                      // tokens in it and before it
   double passed, total;                        // weight before it, and of all
 };
 // The first cell that hit(running sum, running count) holds for, the last one
-// that has a weight (by_weight) or tokens where it holds for none. Every wave
-// for itself, so that nothing has to be handed on.
+// that has a weight (by_weight, of add_weight) or tokens where it holds for
+// none. Every wave for itself, so that nothing has to be handed on.
 template <class Hit>
 __device__ __forceinline__ CellFound find_cell(const PickLds& l, int unit, bool by_weight, Hit hit) {
   constexpr int kPer = kBins / kWave;
@@ -748,6 +759,7 @@ __device__ __forceinline__ CellFound find_cell(const PickLds& l, int unit, bool 
 #pragma unroll
   for (int e = 0; e < kPer; ++e) {
     sum[e] = __builtin_ldexp(static_cast<double>(l.cell_sum[kPer * lane_id() + e]), -unit);
+    if (by_weight) sum[e] += __builtin_ldexp(static_cast<double>(l.cell_rest[kPer * lane_id() + e]), -unit - kFine);
     count[e] = static_cast<int>(l.cell_count[kPer * lane_id() + e]);
     own += sum[e];
     own_count += count[e];
@@ -1006,27 +1018,39 @@ __device__ __forceinline__ uint64_t far_border(const SampleArgs& a, const Exp2& 
 
 // A draw from the arena's n tokens up to the border: their weights summed over
 // cells of indices, until few are left in the one in which the running sum
-// passes the goal.
+// passes the goal. Against a goal far below the largest weight (u = 0, above
+// all) they are summed again, in units of the goal's size: a token that weighs
+// more passes it, however much more.
 __device__ __forceinline__ Drawn draw_list(const Exp2& exp2, const Row& row, int n, uint64_t border, int vocab, float u, float* probs, PickLds& l) {
+  constexpr int kLeast = -1000;                // 2^-1074, the smallest weight, is a number of its units
   const int tid = threadIdx.x;
   Drawn d{border, 0.0, 0.0, -1};
   int lo = 0, shift = 32 - __builtin_clz(static_cast<uint32_t>(vocab)) - 8;
   shift = shift > 0 ? shift : 0;
-  double passed = 0.0, drawn = -1.0;
+  double passed = 0.0, drawn = 0.0;
+  int scale = 0;
+  bool known = false;
 #pragma unroll 1
   while (true) {
     clear_cells(l);
     for (int i = tid; i < n; i += kDThreads) {
       const uint64_t at = l.arena[i];
       const int index = static_cast<int>(at & kLowIndex) - lo;
-      if (at <= border && index >= 0 && index >> shift < kBins) add_to_cell(l, index >> shift, units_of(l.weights[i], kFine));
+      if (at <= border && index >= 0 && index >> shift < kBins) add_weight(l, index >> shift, l.weights[i], scale);
     }
     __syncthreads();
-    CellFound f = find_cell(l, kFine, true, [&](double sum, int) QMV_INLINE { return drawn >= 0.0 && passed + sum > drawn; });
-    if (drawn < 0.0) {                         // the first time: the number goes by the sum
+    const auto passes = [&](double sum, int) QMV_INLINE { return known && passed + sum > drawn; };
+    CellFound f = find_cell(l, kFine - scale, true, passes);
+    if (!known) {                              // the first time: the number goes by the sum
+      known = true;
       d.total = f.total;
       drawn = static_cast<double>(u) * d.total;
-      f = find_cell(l, kFine, true, [&](double sum, int) QMV_INLINE { return passed + sum > drawn; });
+      if (drawn < 0x1p-32) {
+        scale = kLeast;
+        if (drawn > 0x1p-999) (void)__builtin_frexp(drawn, &scale);
+        continue;
+      }
+      f = find_cell(l, kFine, true, passes);
     }
     lo += f.cell << shift;
     passed += f.passed;

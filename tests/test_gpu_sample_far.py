@@ -33,3 +33,28 @@ def test_sample_chunks_far_below_the_top(counts, fall):
     z = np.stack([far_row(V, counts, tops, rng) for _ in k])
     for u in (rng.random(len(k)), np.full(len(k), 1 - 2.0 ** -24)):
         check_sample(z, u, T, k, p, m)
+
+
+def peaks_over_floor(V, depth, rng):
+    """Logits of a few likely tokens in the second half over a broad floor `depth` below."""
+    z = (rng.standard_normal(V) * 0.5 - depth).astype(np.float32)
+    z[rng.integers(V // 2, V, 5)] = rng.standard_normal(5)
+    return z
+
+
+SMALLEST = np.array([0.0, 1e-38, 1e-30, 1e-18, 2.0 ** -40, 2.0 ** -24, 0.25], np.float32)
+
+
+@pytest.mark.parametrize("n", [300, 2000, 5000])
+@pytest.mark.parametrize("depth", [20.0, 36.0, 60.0])
+def test_sample_small_numbers_among_listed_tokens(n, depth):
+    """The first token whose running sum passes u * total, also where that and all weights before it are far below
+    2^-50 of the largest; u = 0 draws the first kept token."""
+    announce(f"small numbers, {n} tokens, depth {depth}")
+    rng = np.random.default_rng(n + int(depth))
+    z = np.full((len(SMALLEST), 9000), -np.inf, np.float32)
+    for row in z:
+        at = np.sort(rng.choice(9000, n, replace=False))
+        row[at] = peaks_over_floor(n, depth, rng)
+    check_sample(z, SMALLEST, 1.0, [n + 1] * len(SMALLEST))
+    check_sample(z, SMALLEST, 1.0, n - n // 7)
