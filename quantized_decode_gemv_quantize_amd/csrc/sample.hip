@@ -1103,7 +1103,9 @@ __device__ __forceinline__ void kept_sums(const SampleArgs& a, const Exp2& exp2,
     return;
   }
   const int b = row.bin(value_at(border)), count = l.bins.count[b] - (b > 0 ? l.bins.count[b - 1] : 0);
-  if (of != b || listed != count) {            // no list of that bin: the row again
+  // no list of that bin: the row again; also for the last bin, whose weights are
+  // too unlike for its units (a chunk that has no others would count as without weight)
+  if (of != b || listed != count || b == kBins - 1) {
     for (int c = wave; c < a.chunks; c += kDWaves) {
       double sum = 0.0;
 #pragma unroll 1

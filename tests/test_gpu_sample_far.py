@@ -58,3 +58,15 @@ def test_sample_small_numbers_among_listed_tokens(n, depth):
         row[at] = peaks_over_floor(n, depth, rng)
     check_sample(z, SMALLEST, 1.0, [n + 1] * len(SMALLEST))
     check_sample(z, SMALLEST, 1.0, n - n // 7)
+
+
+@pytest.mark.parametrize("V,depth", [(9000, 200.0), (20000, 60.0), (20000, 90.0), (20000, 700.0)])
+def test_sample_small_numbers_among_many_tokens(V, depth):
+    """The same with the border among more tokens than are listed, all of them in the last bin of the weight: a
+    chunk of the row that holds nothing else is drawn from by u = 0."""
+    announce(f"small numbers, V {V}, depth {depth}")
+    rng = np.random.default_rng(V + int(depth))
+    z = np.stack([peaks_over_floor(V, depth, rng) for _ in SMALLEST])
+    for k in (2000, V - V // 7, V - 1):
+        check_sample(z, SMALLEST, 1.0, k)
+    check_sample(z, SMALLEST, 1.0, V - 1, 1.0, 1e-30)
