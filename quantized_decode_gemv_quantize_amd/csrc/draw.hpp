@@ -68,6 +68,10 @@ __device__ __forceinline__ double wave_scan(double v) {
   return v;
 }
 
+// The sums before each lane, from the inclusive ones. (Those less the lane's own
+// value would lose in it what is far smaller.)
+__device__ __forceinline__ double wave_before(double up) { return dpp_zero_d<0x138, 0xF>(up); }   // wave_shr:1
+
 template <int CTRL, int ROWS>
 __device__ __forceinline__ int dpp_zero_i(int v) {
   return __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xF, false);

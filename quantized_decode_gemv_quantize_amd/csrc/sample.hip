@@ -400,7 +400,7 @@ __device__ __forceinline__ double block_scan_d(double v, double* lds, double& to
     before += w < wave ? lds[w] : 0.0;
     total += lds[w];
   }
-  return before + (up - v);
+  return before + wave_before(up);
 }
 
 // First bin whose running count (k > 0) or sum reaches k or the goal; the
@@ -764,7 +764,7 @@ __device__ __forceinline__ CellFound find_cell(const PickLds& l, int unit, bool 
     own += sum[e];
     own_count += count[e];
   }
-  const double up = wave_scan(own), start = up - own;
+  const double up = wave_scan(own), start = wave_before(up);
   const int up_count = wave_scan(own_count), start_count = up_count - own_count;
   double run = start;
   int run_count = start_count, first = kPer, last = -1;
@@ -1174,18 +1174,18 @@ __device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2
   int found = -1, last = 0;
   for (int c0 = 0; c0 < a.chunks && found < 0; c0 += kWave) {
     const int c = c0 + lane_id();
-    const double w = c < a.chunks ? st[c].sum : 0.0, up = wave_scan(w) + run;
+    const double w = c < a.chunks ? st[c].sum : 0.0, sums = wave_scan(w), up = sums + run, ahead = wave_before(sums) + run;
     // (a chunk without weight may have the larger sum by rounding alone: the scan adds in another order at each lane)
     const uint64_t hit = __ballot(w > 0.0 && up > goal), some = __ballot(w > 0.0);
     if (some) {
       const int i = 63 - __builtin_clzll(some);
       last = c0 + i;
-      last_before = __shfl(up - w, i);
+      last_before = __shfl(ahead, i);
     }
     if (hit) {
       const int i = __builtin_ctzll(hit);
       found = c0 + i;
-      before = __shfl(up - w, i);
+      before = __shfl(ahead, i);
     }
     run = __shfl(up, kWave - 1);
   }

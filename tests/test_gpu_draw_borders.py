@@ -1,11 +1,12 @@
-"""Draws by a number between two running sums of chunks that differ by rounding
-alone."""
+"""Draws by numbers between two running sums that lie close together: chunks'
+sums that differ by rounding alone, small sums before a large weight."""
 import numpy as np
 import pytest
 
 import draw_borders
 from gpu_helpers import dev, host
 from quantized_decode_gemv_quantize_amd import binding as B
+from test_gpu_serve import check_sample
 
 pytestmark = pytest.mark.gpu
 
@@ -39,3 +40,18 @@ def test_verify_draws_no_chunk_without_weight(seed, with_draft):
                         dev(np.array([0, 1], np.int32)), 1, 1, half, half, count, out, 2, ws, ws.numel())
     got = host(out)[0]
     assert host(count)[0, 0] == 0 and got[0] in allowed and got[1] == -1
+
+
+# weights 1e-20, 1.5e-20, 1 at these places of a row, and u between the first and the first two
+PLACES = [(0, 4096, 5000), (0, 8, 9), (4000, 4100, 4101), (3, 8192, 8193), (64, 512, 517), (0, 270336, 270337)]
+
+
+@pytest.mark.parametrize("at", PLACES)
+@pytest.mark.parametrize("kw", [dict(), dict(k=3), dict(k=8193), dict(m=1e-25)])
+def test_sample_small_sums_before_a_large_weight(at, kw):
+    """What lies before a chunk or a lane is not lost in that one's own sum."""
+    z = np.full((1, max(at) + 1000), -np.inf, np.float32)
+    z[0, list(at)] = np.log([1e-20, 1.5e-20, 1.0])
+    check_sample(z, [2e-20], 1.0, **kw)
+    z[0, ~np.isfinite(z[0])] = -100.0            # all others far below
+    check_sample(z, [2e-20], 1.0, **kw)
