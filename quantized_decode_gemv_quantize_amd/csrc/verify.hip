@@ -351,18 +351,18 @@ __device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const
       const int c = c0 + lane_id();
       const SeqSum o = c0 == 0 ? own : c < a.chunks ? sums(c) : none;
       const double w = use ? o.rest : o.all;
-      const double up = wave_scan(w) + run;
+      const double row_up = wave_scan(w), up = row_up + run, ahead = wave_before(row_up) + run;
       // (a chunk without weight may have the larger sum by rounding alone: the scan adds in another order at each lane)
       const uint64_t hit = __ballot(w > 0.0 && up > goal), some = __ballot(w > 0.0);
       if (some) {
         const int i = 63 - __builtin_clzll(some);
         last = c0 + i;
-        last_before = __shfl(up - w, i);
+        last_before = __shfl(ahead, i);
       }
       if (hit) {
         const int i = __builtin_ctzll(hit);
         found = c0 + i;
-        before = __shfl(up - w, i);
+        before = __shfl(ahead, i);
       }
       run = __shfl(up, kWave - 1);
     }
@@ -395,7 +395,7 @@ __device__ __forceinline__ int draw(const VerifyArgs& a, const Exp2& exp2, const
   const double up = wave_scan(own);
   if ((tid & 63) == 63) l.wsum[wave] = up;
   __syncthreads();
-  double run = l.before + (up - own);
+  double run = l.before + wave_before(up);
   for (int v = 0; v < wave; ++v) run += l.wsum[v];
   int hit = 0x7fffffff, last = -1;
 #pragma unroll

@@ -55,3 +55,18 @@ def test_sample_small_sums_before_a_large_weight(at, kw):
     check_sample(z, [2e-20], 1.0, **kw)
     z[0, ~np.isfinite(z[0])] = -100.0            # all others far below
     check_sample(z, [2e-20], 1.0, **kw)
+
+
+@pytest.mark.parametrize("with_draft", [False, True])
+@pytest.mark.parametrize("at", PLACES)
+def test_verify_small_sums_before_a_large_weight(at, with_draft):
+    import torch
+    V = max(at) + 1000
+    z = np.zeros((1, V), np.float32)
+    z[0, list(at)] = [1e-20, 1.5e-20, 1.0]
+    count, out = (torch.full((1, n), -5, dtype=torch.int32, device="cuda:0") for n in (1, 2))
+    ws = torch.full((B.mmvq_verify_workspace(1, 1, V),), 0xA5, dtype=torch.uint8, device="cuda:0")
+    u = dev(np.array([2e-20], np.float32))
+    B.mmvq_verify_draft(dev(z), V, V, B.TARGET_WEIGHTS, None, dev(np.zeros(1, np.int32)), dev(z) if with_draft else None, V,
+                        dev(np.array([0, 1], np.int32)), 1, 1, u, u, count, out, 2, ws, ws.numel())
+    assert host(count)[0, 0] == 0 and host(out).tolist() == [[at[1], -1]]
