@@ -143,7 +143,7 @@ int mmvq_lora(const mmvq_lora_set* set, const float* x, int64_t ldx, int64_t n, 
   if (rc) return rc;
   if (n != 0 && (!set->A || !set->B || !x || !base || !out || !workspace || (n_seqs > 0 && !adapter))) return MMVQ_ERR_NULL;
   if (ldx < set->K || ldx > kMaxElems || ldb < set->M || ldb > kMaxElems || ldo < set->M || ldo > kMaxElems || n_seqs < 0 ||
-      n_seqs > kMaxSeqs || (!row_seq && n_seqs < n) || (base == out && base && ldb != ldo) ||
+      (!row_seq && n_seqs < n) || (base == out && base && ldb != ldo) ||
       workspace_bytes < lora_bytes(n, set->K, set->M, set->max_rank))
     return MMVQ_ERR_SHAPE;
   if (!aligned(set->A, 16) || !aligned(set->B, 16) || !aligned(set->rank, 4) || !aligned(set->scale, 4) || !aligned(x, 4) ||
