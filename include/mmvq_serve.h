@@ -159,8 +159,9 @@ int mmvq_lora_workspace(const mmvq_lora_set *set, int64_t n, int64_t *bytes);
  * be out itself (same pointer and stride): the projection's own output, to
  * which the adapters' is added. Rows of x, base and out at + t*ld floats.
  * Products are those of fp32 values (x in three bf16 parts, which hold all
- * its bits; weights in one to three), sums fp32. x and the weights must be
- * finite; a row's own values that are not reach no other row.
+ * its bits but those below 2^-133, the last that bf16 has; weights in one to
+ * three), sums fp32. x and the weights must be finite; a row's own values that
+ * are not reach no other row.
  * Consecutive rows of one adapter share its weights: rows are best ordered
  * by request. Requires 0 <= n <= 2^20, ldx >= K, ldb and ldo >= M, buffers
  * without overlap but for base; 4-byte aligned. */
