@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kEThreads) embed_kernel(EmbedArgs a) {
     for (int k = 0; k < kEQuads; ++k) {
       const int i = first + 4 * kWave * k;
       if (i + 4 <= a.K) {
-        store_four(out + i, y[k], a.past);
+        if (a.through) store_four_through(out + i, y[k]);
+        else store_four(out + i, y[k], a.past);
       } else {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -162,7 +163,8 @@ int launch_embed(int type, const EmbedArgs& given, hipStream_t st) {
   EmbedArgs a = given;
   a.pieces = (a.K + kEPiece - 1) / kEPiece;
   a.units = a.n * a.pieces;
-  a.past = past_caches(a.n, a.K);
+  a.past = past_caches(a.n, a.K, kEmbedPast);
+  a.through = !a.past && past_caches(a.n, a.K, kL2);
   const int64_t blocks = (a.units + kEWaves - 1) / kEWaves;
   const dim3 grid(static_cast<unsigned>(blocks < kMaxEmbedGrid ? blocks : kMaxEmbedGrid)), block(kEThreads);
   switch (type) {

@@ -1369,7 +1369,7 @@ __global__ void __launch_bounds__(kSThreads) sample_probs_kernel(SampleArgs a) {
 
 int launch_sample(const SampleArgs& given, hipStream_t st) {
   SampleArgs a = given;
-  a.past = past_caches(a.n_rows, a.vocab);
+  a.past = past_caches(a.n_rows, a.vocab, kL2);
   const unsigned chunks = static_cast<unsigned>(a.chunks), rows = static_cast<unsigned>(a.n_rows);
   const dim3 grid(chunks, rows < kGridRows ? rows : kGridRows, (rows + kGridRows - 1) / kGridRows);
   hipLaunchKernelGGL(sample_stats_kernel, grid, dim3(kSThreads), 0, st, a);

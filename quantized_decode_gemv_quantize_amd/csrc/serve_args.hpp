@@ -18,7 +18,7 @@ struct EmbedArgs {
   int vocab, K;
   float scale;
   int pieces;              // of a row
-  bool past;               // out passes the caches by
+  bool past, through;      // out passes the caches by, or the L2 only
 };
 
 struct PoolArgs {

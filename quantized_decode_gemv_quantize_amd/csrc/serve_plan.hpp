@@ -13,15 +13,18 @@ constexpr int kAWaves = 8, kBWaves = 4;        // of a workgroup of shrink and o
 constexpr int kLoraChunk = kAWaves * kLStep;   // of K that a workgroup of shrink takes at a time
 constexpr int kLoraPiece = kBWaves * 64;       // outputs that one of expand takes at a time
 
-// Whether rows of floats pass the caches by: more than the L2 of all eight
-// dies hold, of which the next reader would find only the end. Stores of 67 MB
-// of embedding rows 18.0 -> 15.0 us, x and out of 4000 adapter rows (229 and 66
-// MB) 115 -> 100, zeros of 128 distributions (66 MB) 64 -> 57; but 8 MB of
-// embedding rows 4.8 -> 5.0.
-inline bool past_caches(int64_t rows, int64_t length) {
-  constexpr int64_t kCaches = 32 << 20;
-  return rows * length * 4 > kCaches;
-}
+// Whether rows of floats are more than so many bytes, from which on they pass
+// caches by: the L2 of all eight dies hold 32 MB, the last-level cache 256 MB,
+// beside all else that the rows' reader needs.
+inline bool past_caches(int64_t rows, int64_t length, int64_t bytes) { return rows * length * 4 > bytes; }
+constexpr int64_t kL2 = int64_t(32) << 20;
+
+// Embedding rows, stored as usual, through the L2 and past all caches: us alone
+// and with the norm that reads them. 49 MB 15.1, 12.4, 11.2 and 41.8, 40.7,
+// 44.1; 67 MB 17.4, 15.2, 13.2 and 52.4, 51.3, 56.1; 98 MB 24.9, 20.7, 18.6 and
+// 75.0, 75.0, 79.3; 134 MB 31.4, 28.8, 24.9 and 118, 119, 104. (8 MB past the
+// caches 4.8 -> 5.0 alone.)
+constexpr int64_t kEmbedPast = int64_t(104) << 20;
 
 // Launch shape. How many tiles there are the host cannot see: it counts on
 // rows of their own adapters in one block of rows, of one adapter beyond.
