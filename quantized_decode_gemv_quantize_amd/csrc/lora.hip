@@ -395,7 +395,7 @@ int64_t lora_bytes(int64_t n, int64_t K, int64_t M, int max_rank) {
 template <int TYPE, int RT, int RC, int CT>
 int launch_ranks(const LoraArgs& a, const LoraShape& s, hipStream_t st) {
   const dim3 grid(s.blocks, s.groups, s.splits), block(kAWaves * kWave);
-  if (CT == 2 && past_caches(a.n, a.K, kL2)) hipLaunchKernelGGL((lora_shrink_kernel<TYPE, RT, CT, CT == 2>), grid, block, 0, st, a);
+  if (CT == 2 && past_caches(a.n, a.K, kLoraPast)) hipLaunchKernelGGL((lora_shrink_kernel<TYPE, RT, CT, CT == 2>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((lora_shrink_kernel<TYPE, RT, CT, false>), grid, block, 0, st, a);
   const int rc = check_launch();
   if (rc) return rc;
@@ -411,7 +411,7 @@ int launch_type(const LoraArgs& given, hipStream_t st) {
   a.steps = s.steps;
   a.leads = s.leads;
   a.pieces = s.pieces;
-  a.past = past_caches(a.n, a.M, kL2);
+  a.past = past_caches(a.n, a.M, kL2) && !past_caches(a.n, a.M, kLoraOut);
   if (s.ct == 2) {
     if (a.max_rank <= 16) return launch_ranks<TYPE, 1, 1, 2>(a, s, st);
     if (a.max_rank <= 32) return launch_ranks<TYPE, 2, 1, 2>(a, s, st);

@@ -26,6 +26,21 @@ constexpr int64_t kL2 = int64_t(32) << 20;
 // caches 4.8 -> 5.0 alone.)
 constexpr int64_t kEmbedPast = int64_t(104) << 20;
 
+// Adapters' x, read past the caches from there on, and as usual before: us
+// alone, and with the norm behind the projection and another reader of x. 34 MB
+// (2100 rows of 4096) 49.8, 47.7 and 93.5, 91.7; 63 MB (1100 of 14336) 50.3, 45.4
+// and 90.2, 88.6; 67 MB (4096 of 4096) 63.5, 65.9 and 155, 161; 86 MB (1500 of
+// 14336) 77.6, 72 and 129, 132; 235 MB (4096 of 14336) 105, 127 and 252, 262.
+constexpr int64_t kLoraPast = int64_t(63) << 20;
+
+// Their out, stored as usual and past the caches: us alone, with the norm that
+// adds it to the residual, with a norm of it. 52 MB (2100 rows of 4096 by 6144)
+// 64.5, 56.5 and 106, 107 and 86.9, 88.0; 67 MB (4096 of 14336 by 4096) 115, 106
+// and 166, 167 and 143, 149; 134 MB (8192 of 4096 by 4096) 126, 124 and 222, 225
+// and 188, 189; 235 MB (4096 of 4096 by 14336) 171, 168 and 332, 342 and 250,
+// 256. So past the caches from 32 MB up to there; in place it is all one.
+constexpr int64_t kLoraOut = int64_t(104) << 20;
+
 // Launch shape. How many tiles there are the host cannot see: it counts on
 // rows of their own adapters in one block of rows, of one adapter beyond.
 // K is cut until every compute unit has a workgroup, in ranges of two chunks
