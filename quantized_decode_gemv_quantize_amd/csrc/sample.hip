@@ -374,7 +374,6 @@ static_assert(sizeof(ChunkShift) == 16);
 // A row at work.
 struct Row {
   const float* logits;
-  int n;                                       // its number
   float top;
   double top_quarter, rate4;
   Settings s;
@@ -1243,7 +1242,6 @@ __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
   const int tid = threadIdx.x, r = blockIdx.x;
   Row row;
   row.s = settings_of(a, r);
-  row.n = r;
   row.logits = a.logits + r * a.ldl;
   row.stats = chunk_stats(a) + static_cast<int64_t>(r) * a.chunks;
   row.bins = chunk_bins(a) + static_cast<int64_t>(r) * a.chunks * kBins;
