@@ -164,7 +164,7 @@ int launch_embed(int type, const EmbedArgs& given, hipStream_t st) {
   a.pieces = (a.K + kEPiece - 1) / kEPiece;
   a.units = a.n * a.pieces;
   a.past = past_caches(a.n, a.K, kEmbedPast);
-  a.through = !a.past && past_caches(a.n, a.K, kL2);
+  a.through = !a.past && past_caches(a.n, a.K, kL2) && a.ldo % 32 == 0 && reinterpret_cast<uintptr_t>(a.out) % 128 == 0;
   const int64_t blocks = (a.units + kEWaves - 1) / kEWaves;
   const dim3 grid(static_cast<unsigned>(blocks < kMaxEmbedGrid ? blocks : kMaxEmbedGrid)), block(kEThreads);
   switch (type) {

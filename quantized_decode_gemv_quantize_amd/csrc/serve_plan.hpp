@@ -20,10 +20,14 @@ inline bool past_caches(int64_t rows, int64_t length, int64_t bytes) { return ro
 constexpr int64_t kL2 = int64_t(32) << 20;
 
 // Embedding rows, stored as usual, through the L2 and past all caches: us alone
-// and with the norm that reads them. 49 MB 15.1, 12.4, 11.2 and 41.8, 40.7,
-// 44.1; 67 MB 17.4, 15.2, 13.2 and 52.4, 51.3, 56.1; 98 MB 24.9, 20.7, 18.6 and
-// 75.0, 75.0, 79.3; 134 MB 31.4, 28.8, 24.9 and 118, 119, 104. (8 MB past the
-// caches 4.8 -> 5.0 alone.)
+// and with the norm that makes q8_1 columns of them. Q4_K rows of 4096, 49 MB
+// 15.1, 12.4, 11.2 and 41.8, 40.7, 44.1; 67 MB 17.4, 15.2, 13.2 and 52.4, 51.3,
+// 56.1; 98 MB 24.9, 20.7, 18.6 and 75.0, 75.0, 79.3; 134 MB 31.4, 28.8, 24.9 and
+// 118, 119, 104 (110, 120, 121 where the norm makes fp32 rows). BF16 rows of
+// 2565, which end inside a line of 128 bytes, 62 MB 17.1, 17.4, 16.5 and, with
+// fp32 rows of a norm, 55.6, 63.7, 62.2; 92 MB 24.4, 39.0, 23.8 and 90.0, 96.4,
+// 92.8. So through the L2 from 32 MB on where rows are whole lines, and past
+// the caches from here on. (8 MB past the caches 4.8 -> 5.0 alone.)
 constexpr int64_t kEmbedPast = int64_t(104) << 20;
 
 // Adapters' x, read past the caches from there on, and as usual before: us

@@ -10,11 +10,12 @@ pytestmark = pytest.mark.gpu
 
 @pytest.mark.parametrize("kind", [B.F32, B.BF16])
 @pytest.mark.parametrize("n", [2001, 20011, 40009])
-def test_embed_stores(kind, n):
-    """8, 80 and 160 MB, rows of an odd length with a gap, read by the next launch on the stream; with scales in a
-    replayed graph."""
+@pytest.mark.parametrize("ldo", [1003, 1024])
+def test_embed_stores(kind, n, ldo):
+    """8, 80 and 160 MB, rows of an odd length with a gap that begin inside lines of 128 bytes and at them, read by
+    the next launch on the stream; with scales in a replayed graph."""
     import torch
-    K, vocab, ldo = 1001, 50, 1003
+    K, vocab = 1001, 50
     t = torch.float32 if kind == B.F32 else torch.bfloat16
     table = torch.randn(vocab, K, generator=torch.Generator().manual_seed(n)).to(t).to("cuda:0")
     ids = torch.arange(n, device="cuda:0", dtype=torch.int32) * 7 % (vocab + 1) - 1
