@@ -50,8 +50,8 @@ extern "C" {
  * MMVQ_F16 is in mmvq_decode.h. */
 enum { MMVQ_F32 = 0, MMVQ_BF16 = 30 };
 
-/* out[t*ldo + i] = scale * W[ids[t]][i], i < K, rounded to fp32 once, for n
- * tokens. table: vocab rows back to back, of a weight format of mmvq.h (so a
+/* out[t*ldo + i] = scale * W[ids[t]][i], i < K, for n tokens, rounded to fp32
+ * (formats with an offset, d q + m, from 64 bits, 2^-52 off). table: vocab rows back to back, of a weight format of mmvq.h (so a
  * tied LM head serves as it is; K a multiple of the type's block) or F32, F16
  * or BF16 (any K). A token outside 0..vocab-1 gives a row of zeros.
  * Requires 1 <= K <= 2^24, 1 <= vocab < 2^31, n >= 0, n*K <= 2^40, ldo >= K;
@@ -203,9 +203,12 @@ int mmvq_sample_workspace(int n_rows, int vocab, int64_t *bytes);
  * have 1 and all others 0. A row without any weight, or of no request
  * (row_seq outside 0..n_seqs-1): token -1, chosen 0, probs 0. An infinite
  * temperature gives equal weights. Exponentials, sums and comparisons are in
- * 64 bits; in the sums that p is measured against each weight is rounded by
- * at most 2^-38 of itself, or 2^-64 of w_top, so that where the sum before a
- * token is that near to p times all of them, it may count either way.
+ * 64 bits, but for two kinds of sums. In those that p is measured against each
+ * weight is rounded by at most 2^-38 of itself, or 2^-64 of w_top; and so it is
+ * in those that u is measured against and that chosen and probs are divided by,
+ * where more than 5120 tokens of a filtered row come up to the last kept one and
+ * those that weigh like it. Where the sum before a token is that near to p or to
+ * u times all of them, it may count either way.
  * u in [0, 1).
  * Requires 0 <= n_rows <= 2^20, 1 <= vocab <= 2^24, n_seqs >= 0, ldl and ldp
  * >= vocab; 4-byte aligned. params NULL: all off. */

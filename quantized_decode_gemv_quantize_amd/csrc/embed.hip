@@ -1,14 +1,14 @@
 // embed.hip - rows of an embedding table, in any weight format.
 //
-//   out[t][i] = scale * W[ids[t]][i], rounded to fp32 once
+//   out[t][i] = scale * W[ids[t]][i], in fp32
 //
 // A product of a block's scale and a code fits fp32 (at most 23 bits), so the
-// formats without an offset take one fp32 product with `scale`. Those with
-// one (d q + m, d sc q - dmin m) go through 64 bits. Every byte of a row is
-// read once and every output written once; the writes are most of it and bound
-// it: 4096 rows of 4096 take 13.5 (Q4_1) to 16.3 us (Q5_K), 15.0 from Q4_K (5.1
-// TB/s), 24.3 from F32 (5.5 TB/s). One row is a launch's latency and two loads',
-// 2.9 us. A wave takes kEPiece values of a row, in runs of four a lane, so that
+// formats without an offset take one fp32 product with `scale`, which rounds
+// once. Those with one (d q + m, d sc q - dmin m) go through 64 bits and round
+// those, 2^-52 off, to fp32. Every byte of a row is read once and every output
+// written once; the writes are most of it and bound it: 4096 rows of 4096 take
+// 11.9 (Q4_0) to 15.9 us (Q5_K), 15.2 from Q4_K (5.0 TB/s), 30.3 from F32 (4.4
+// TB/s). One row is a launch's latency and two loads', 3 us. A wave takes kEPiece values of a row, in runs of four a lane, so that
 // a store is 1 KB side by side and a short row does not leave a workgroup
 // idle; what the lanes of a block share comes from the caches.
 #include "launch.hpp"

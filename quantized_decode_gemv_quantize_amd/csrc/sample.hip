@@ -37,8 +37,14 @@ constexpr int kBins = 256;                     // the last one: everything below
 constexpr int kDThreads = 512;
 constexpr int kDWaves = kDThreads / kWave;
 constexpr int kRank = 256;                     // tokens that are sorted, each by counting those before it
-constexpr int kArena = 5120;                   // tokens that are cut and drawn from in LDS
-constexpr int kTops = 256;                     // tokens that a chunk lists
+// Tokens that are cut and drawn from in LDS: what fits beside the descriptors of
+// 2^24 logits' chunks. With 2560 256 rows of top-p (128256 logits) 113 -> 141 us
+// and 128 with distributions 102 -> 185, the others 0.4 to 1 less.
+constexpr int kArena = 5120;
+// Tokens that a chunk lists. With 128 64 rows of top-p 56.7 -> 61.7 us, 256 of
+// min-p 67.1 -> 63.8, one row 0.3 less; with 512 56.7 -> 52.5, 67.1 -> 71.7, one
+// row 0.6 more.
+constexpr int kTops = 256;
 constexpr int kUnit = 38;                      // a bin's sum is in units of 2^-kUnit
 constexpr int kSumBits = 51;                   // and behind them its count
 constexpr uint64_t kSumMask = (uint64_t(1) << kSumBits) - 1;
@@ -184,8 +190,9 @@ static_assert(kUnit == 38);
 constexpr int kGridRows = 1 << 15;
 __device__ __forceinline__ int row_of_grid() { return static_cast<int>(blockIdx.z) * kGridRows + static_cast<int>(blockIdx.y); }
 
-// Bound by vector instructions (22 a filtered logit, most of them 64-bit) and
-// by the latencies of its steps; the LDS additions of lanes that meet in a bin
+// Bound by vector instructions (44 to 56 a logit of filtered rows, of which 22,
+// most of them 64-bit, form its bin and add to it, and most others list a
+// chunk's tokens) and by the latencies of its steps; the LDS additions of lanes that meet in a bin
 // are hidden behind them (four copies of the bins to keep them apart gained
 // nothing: 57.3 and 58.6 us for 256 rows of 151669). 64 rows of 128256 take 18 us
 // (33 MB, 1.8 TB/s), 256 of 151669 54 (155 MB, 2.9), 128 whose distributions' zeros
@@ -571,6 +578,9 @@ __device__ __forceinline__ void sort_few(const uint64_t* list, uint64_t* to, int
 // lane two bins. all, tokens: sum and number of all, where the last bin ends.
 constexpr int kHalf = 2 * kWave;
 __device__ __forceinline__ void join_half(const SampleArgs& a, const Row& row, int half, double all, int tokens, PickLds& l) {
+  // chunks of a wave on their way: 40 of all eight, 163840 logits, in one round
+  // (3 or 8: 64 rows of 128256 with all filters 34.7 -> 35.0 and 35.5 us; 1 row of
+  // 200064, two rounds, 21.1, with 3 20.8)
   constexpr int kAhead = 5;
   const int wave = threadIdx.x >> 6, lane = lane_id();
   double sum[2] = {0.0, 0.0};
@@ -644,7 +654,7 @@ __device__ __forceinline__ int crossing_near(const Running& up, int k, double go
 // The tokens of bins from..b (kArena at most) from the chunks' lists, in the
 // arena. Returns their number, -1 where a chunk lists fewer.
 __device__ __forceinline__ int gather(const SampleArgs& a, const Row& row, int from, int b, PickLds& l) {
-  constexpr int kAhead = 5;                    // lists on their way
+  constexpr int kAhead = 5;                    // lists on their way, as in join_half
   const int tid = threadIdx.x, wave = tid >> 6;
   bool covered = true;
   for (int c = tid; c < a.chunks; c += kDThreads) {
@@ -1093,7 +1103,9 @@ __device__ __forceinline__ Drawn draw_list(const Exp2& exp2, const Row& row, int
   return d;
 }
 
-// The kept weights of each chunk, in its stats.
+// The kept weights of each chunk, in its stats. From the bins they are good to
+// 2^-38 of each weight. (Always from the row itself, in 64 bits: 64 rows of top-p
+// 57 -> 84 us, 128 with distributions 102 -> 142.)
 __device__ __forceinline__ void kept_sums(const SampleArgs& a, const Exp2& exp2, const Row& row, uint64_t border, int listed, int of, PickLds& l) {
   const int tid = threadIdx.x, wave = tid >> 6;
   if (border == ~uint64_t(0)) {
@@ -1231,10 +1243,12 @@ __device__ __forceinline__ Drawn draw_long(const SampleArgs& a, const Exp2& exp2
 
 // A chain of latencies: the chunks' tops, their bins, the crossing, the lists,
 // ranks, a scan. Over 128256 logits: 10 us for a row with few tokens up to its
-// border's bin, 17 for 64 rows of mixed filters, 35 for 128 rows of top-p where the
-// slowest has thousands (weights, cells and barriers in LDS), 62 where it has to be
-// read again, which one workgroup does in 23 us (22 GB/s). A wave has the registers
-// of two a SIMD: with 1024 threads a call of 128 rows takes 76 us for 63.
+// border's bin, 17 for 64 rows of mixed filters, 36 for 128 rows of top-p where the
+// slowest has thousands (weights, cells and barriers in LDS), 60 where it has to be
+// read again, which one workgroup does in 23 us (22 GB/s); 160 where the border's
+// bin alone has more than kArena (temperature 2, top-p 0.95) and it is read more than
+// once. A wave has the registers of two a SIMD: with 1024 threads a call of 128 rows
+// takes 76 us for 63.
 __global__ void __launch_bounds__(kDThreads) sample_pick_kernel(SampleArgs a) {
   __shared__ PickLds l;
   extern __shared__ __align__(16) uint8_t dynamic[];
@@ -1367,6 +1381,9 @@ __global__ void __launch_bounds__(kSThreads) sample_probs_kernel(SampleArgs a) {
 
 int launch_sample(const SampleArgs& given, hipStream_t st) {
   SampleArgs a = given;
+  // (Distributions of top-p rows stored as usual and past the caches, us alone and
+  // with mmvq_verify_draft behind: 49 MB 53.5, 53.0 and 73.1, 73.5; 66 MB 66.7, 60.0
+  // and 88.0, 87.6; 99 MB 84.0, 80.8 and 112, 113; 131 MB 107, 98 and 135, 132.)
   a.past = past_caches(a.n_rows, a.vocab, kL2);
   const unsigned chunks = static_cast<unsigned>(a.chunks), rows = static_cast<unsigned>(a.n_rows);
   const dim3 grid(chunks, rows < kGridRows ? rows : kGridRows, (rows + kGridRows - 1) / kGridRows);

@@ -47,15 +47,23 @@ constexpr int64_t kLoraOut = int64_t(104) << 20;
 
 // Launch shape. How many tiles there are the host cannot see: it counts on
 // rows of their own adapters in one block of rows, of one adapter beyond.
-// K is cut until every compute unit has a workgroup, in ranges of two chunks
+// K is cut towards a workgroup for every compute unit, in ranges of two chunks
 // at least, or two of them in ranges of four (64 rows of their own, K = 4096:
 // 4 ranges 34.6 us, 8 of two chunks 37.6; one row: 8.5 and 7.5; 4000 rows of
-// 14336: 5 ranges 98, 3 108). M is cut until every compute unit has two: 64 rows
-// by 14336 in 8 slices 34.6 us, in 4 50, in 16 54; 4000 by 4096 in 5 115, in 3
-// 129, in 10 126. Of many rows tiles take 32, which halves the reads of the
-// weights. A workgroup looks for tiles at four rows of each block where there
-// are several: most of one at each row would find none (512 rows of 8 adapters
-// 46 -> 37 us, 512 of their own 53 -> 56).
+// 14336: 5 ranges 98, 3 108). M is cut towards two for every compute unit, in
+// pieces of 256: 64 rows by 14336 in 8 slices 34.6 us, in 4 50, in 16 54; 4000 by
+// 4096 in 5 115, in 3 129, in 10 126. Few rows do not fill the chip so: one of 4096
+// by 4096 has 8 workgroups and then 16, which at high ranks stream its adapter
+// at some 250 GB/s (rank 128 in fp32 27 us).
+// From 1024 rows on tiles take 32, which halves the reads of the weights, but
+// also the tiles to share them out by, and counts double where rows have adapters
+// of their own. Tiles of 16 and of 32, 8 requests, us: 4096 by 4096, bf16 of rank
+// 16, 1024 rows 26, 33, 2048 41, 45, 4096 73, 62, 8192 125, 131; fp32 of rank 64 88, 84
+// and 104, 102 and 187, 142 and 327, 264; 4096 by 14336, bf16 of rank 16 62, 57 and
+// 91, 87 and 185, 165 and 344, 340; 2048 rows of 1024 requests 86, 118.
+// A workgroup looks for tiles at four rows of each block where there are several:
+// most of one at each row would find none (512 rows of 8 adapters 46 -> 37 us,
+// 512 of their own 53 -> 56).
 struct LoraShape {
   int blocks, leads, groups, splits, steps, slices, pieces, ct;
 };
