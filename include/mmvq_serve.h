@@ -206,9 +206,10 @@ int mmvq_sample_workspace(int n_rows, int vocab, int64_t *bytes);
  * 64 bits, but for two kinds of sums. In those that p is measured against each
  * weight is rounded by at most 2^-38 of itself, or 2^-64 of w_top; and so it is
  * in those that u is measured against and that chosen and probs are divided by,
- * where more than 5120 tokens of a filtered row come up to the last kept one and
- * those that weigh like it. Where the sum before a token is that near to p or to
- * u times all of them, it may count either way.
+ * where many tokens of a filtered row (more than 5120, or than 256 of 4096
+ * neighbours) come up to the last kept one and those that weigh like it. Where
+ * the sum before a token is that near to p or to u times all of them, it may
+ * count either way.
  * u in [0, 1).
  * Requires 0 <= n_rows <= 2^20, 1 <= vocab <= 2^24, n_seqs >= 0, ldl and ldp
  * >= vocab; 4-byte aligned. params NULL: all off. */
