@@ -21,9 +21,10 @@
 //
 // fp32 values enter a product as three bf16 parts by truncation, x = x1 + x2 +
 // x3 exactly (8 bits each; what lies below 2^-133, bf16's last bit, is lost);
-// weights as one (bf16), two (fp16: 11 bits) or three (fp32). All products of parts but that of the two last of three and
-// three (2^-28 of the whole) are formed: fp32 products, for three, six or
-// eight matrix instructions where one of fp32 takes the time of sixteen.
+// weights as one (bf16), two (fp16: 11 bits) or three (fp32). All products of
+// parts but that of the two last of three and three (2^-28 of the whole) are
+// formed: fp32 products, for three, six or eight matrix instructions where one of
+// fp32 takes the time of sixteen.
 #include "launch.hpp"
 #include "past.hpp"
 #include "serve_args.hpp"

@@ -20,7 +20,8 @@
 // A chunk's bin is one 64-bit whole number: the count, and the sum in units of
 // 2^-38 of 2^(-b/4) for bin b (adding in LDS in any order gives the same bits,
 // and one addition a token is what the bins can bear).
-// Everything else is in 64-bit floating point: with 10^5 logits a running sum
+// Cells of the search for a border hold such sums, too. Everything else is in 64
+// bits or more: with 10^5 logits a running sum
 // in 32 bits moves a border by more than many tokens' probability.
 #include "draw.hpp"
 #include "launch.hpp"
